@@ -249,7 +249,7 @@ def prepare(case, seed):
         from attention_backward_flashattention_gb300 import binding
         s["cache"] = binding.PagedCache(s["k_cache"], s["v_cache"], s["k_scale"], s["v_scale"])
         if c["op"] == "decode":
-            s["workspace"] = binding.decode_workspace(s["cache"], c["batch"], c["hq"])
+            s["workspace"] = binding.decode_workspace(s["q"].device)
         else:
             s["rot"] = binding.Rotation(s["inv_freq"], begin=c["begin"],
                                         interleaved=c["interleaved"])
