@@ -28,16 +28,22 @@ ATTN_ERR_CUDA = -4
 ATTN_ERR_TIMEOUT = -5
 ATTN_ERR_INTERNAL = -6
 ATTN_ERR_SCRATCH_TOO_SMALL = -7
+ATTN_ERR_BAD_PAGE = -8
+ATTN_ERR_WORKSPACE_NOT_READY = -9
 LAYOUT_BTHD = 0
 LAYOUT_PACKED_QKV = 1
 MAX_VARLEN_SEQS = 1024
+ROPE_HALVES, ROPE_PAIRS = 0, 1
+CACHE_BF16, CACHE_E4M3 = 0, 1
 
 EXPORTED = ("attn_fwd", "attn_bwd_workspace_size", "attn_bwd", "attn_bwd_status",
             "attn_fwd_status", "attn_strerror", "attn_varlen_order", "attn_debug_set_wait_bias",
             "attn_profile_main_kernel", "attn_profile_aux_kernels", "attn_bwd_noalloc",
             "attn_bwd_noalloc_status", "attn_step_host_scratch_size", "attn_step_host",
             "attn_step_host_status", "attn_fwd_window", "attn_bwd_window", "attn_fwd_ex",
-            "attn_bwd_ex", "attn_debug_cache_stats", "attn_debug_set_bwd_variant")
+            "attn_bwd_ex", "attn_debug_cache_stats", "attn_debug_set_bwd_variant",
+            "attn_rope_rates", "attn_rope", "attn_cache_append", "attn_cache_status",
+            "attn_decode", "attn_decode_workspace_size", "attn_decode_workspace_init")
 BLOCK = 128  # rows per block of a block-sparse mask
 
 _lock = threading.Lock()
@@ -48,6 +54,21 @@ class AttnError(RuntimeError):
     def __init__(self, code: int, where: str):
         super().__init__(f"{where}: {strerror(code)} ({code})")
         self.code = code
+
+
+class _RotationStruct(ctypes.Structure):
+    """attn_rotation of include/attn.h."""
+    _fields_ = [("rates", ctypes.c_void_p), ("begin", ctypes.c_int), ("dim", ctypes.c_int),
+                ("style", ctypes.c_int)]
+
+
+class _CacheStruct(ctypes.Structure):
+    """attn_paged_cache of include/attn.h."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale")] + \
+               [(f"{s}_{n}_stride", ctypes.c_longlong) for s in "kv"
+                for n in ("page", "token", "head")] + \
+               [(n, ctypes.c_int) for n in ("type", "num_pages", "page_size", "heads", "dqk",
+                                            "dv")]
 
 
 def load():
@@ -110,6 +131,21 @@ def load():
         lib.attn_step_host.restype = I
         lib.attn_step_host_status.argtypes = [P, I, I, I, I, I, I, I, P]
         lib.attn_step_host_status.restype = I
+        L = ctypes.c_longlong
+        lib.attn_rope_rates.argtypes = [P, I, P]
+        lib.attn_rope_rates.restype = I
+        lib.attn_rope.argtypes = [P, P, P, P, I, I, I, I, I, I, L, L, L, L, P, I, I, P, P, P]
+        lib.attn_rope.restype = I
+        lib.attn_cache_append.argtypes = [P, P, I, L, P, I, I, P, P, L, P, L, P, L, P, L, I, P, P]
+        lib.attn_cache_append.restype = I
+        lib.attn_cache_status.argtypes = [P]
+        lib.attn_cache_status.restype = I
+        lib.attn_decode_workspace_size.argtypes = []
+        lib.attn_decode_workspace_size.restype = SZ
+        lib.attn_decode_workspace_init.argtypes = [P, SZ, P]
+        lib.attn_decode_workspace_init.restype = I
+        lib.attn_decode.argtypes = [P, P, I, L, P, I, P, L, P, P, I, I, F, P, SZ, P]
+        lib.attn_decode.restype = I
         _lib = lib
         return lib
 
@@ -329,6 +365,65 @@ def attn_varlen_order(cu_seqlens) -> list:
     return list(out)[:n]
 
 
+def attn_rope_rates(rates_rad) -> list:
+    """Fixed-point form (turns per position, times 2^64) of rates in radians per position."""
+    vals = [float(r) for r in rates_rad]
+    src = (ctypes.c_double * max(len(vals), 1))(*vals)
+    out = (ctypes.c_ulonglong * max(len(vals), 1))()
+    rc = load().attn_rope_rates(ctypes.cast(src, ctypes.c_void_p), len(vals),
+                                ctypes.cast(out, ctypes.c_void_p))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope_rates")
+    return list(out)[:len(vals)]
+
+
+def _struct(x):
+    """Address of a ctypes structure (or of a Rotation's or PagedCache's), or None."""
+    if x is None:
+        return None
+    return ctypes.addressof(getattr(x, "struct", x))
+
+
+def attn_rope(q, k, q_out, k_out, B, Hq, Hk, Tq, Tk, d, q_row, k_row, q_out_row, k_out_row,
+              rotation, inverse=False, pos0=0, cu_seqlens_q=None, cu_seqlens_k=None,
+              stream=None) -> int:
+    cq, ck = _HostInts(cu_seqlens_q), _HostInts(cu_seqlens_k)
+    return load().attn_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B, Hq, Hk, Tq, Tk, d,
+                            q_row, k_row, q_out_row, k_out_row, _struct(rotation), int(inverse),
+                            int(pos0), cq.ptr, ck.ptr, _stream(stream))
+
+
+def attn_cache_append(cache, block_table, max_pages, table_stride, lens, B, T, cu_seqlens, k,
+                      k_row, v, v_row, q, q_row, q_out, q_out_row, Hq, rotation=None,
+                      stream=None) -> int:
+    cu = _HostInts(cu_seqlens)
+    return load().attn_cache_append(_struct(cache), _ptr(block_table), max_pages, table_stride,
+                                    _ptr(lens), B, T, cu.ptr, _ptr(k), k_row, _ptr(v), v_row,
+                                    _ptr(q), q_row, _ptr(q_out), q_out_row, Hq,
+                                    _struct(rotation), _stream(stream))
+
+
+def attn_cache_status(stream=None) -> int:
+    return load().attn_cache_status(_stream(stream))
+
+
+def attn_decode_workspace_size() -> int:
+    return int(load().attn_decode_workspace_size())
+
+
+def attn_decode_workspace_init(workspace, workspace_bytes, stream=None) -> int:
+    return load().attn_decode_workspace_init(_ptr(workspace), int(workspace_bytes),
+                                             _stream(stream))
+
+
+def attn_decode(cache, block_table, max_pages, table_stride, lens, B, q, q_row, o, lse, Hq,
+                window_left, scale, workspace, workspace_bytes, stream=None) -> int:
+    return load().attn_decode(_struct(cache), _ptr(block_table), max_pages, table_stride,
+                              _ptr(lens), B, _ptr(q), q_row, _ptr(o), _ptr(lse), Hq,
+                              int(window_left), float(scale), _ptr(workspace),
+                              int(workspace_bytes), _stream(stream))
+
+
 # ----------------------------------------------------------------------------
 # Conveniences: shapes from tensors, outputs allocated with torch
 # ----------------------------------------------------------------------------
@@ -441,3 +536,262 @@ def step_host(q, k, v, dO, causal=False, scale=None, deterministic=False, heads_
     if own:
         cs.synchronize()
     return dq, dk, dvt, o
+
+
+# ----------------------------------------------------------------------------
+# Position rotation, paged cache, decode
+# ----------------------------------------------------------------------------
+class Rotation:
+    """The position rotation of a head's columns begin .. begin + 2 * len(inv_freq) - 1.
+
+    inv_freq: the angle (radians) that each pair of columns turns per position, a
+    float64 tensor or sequence (any frequencies: base 10000, rescaled ones, ...).
+    interleaved: pairs are adjacent columns; else they lie dim/2 apart."""
+
+    def __init__(self, inv_freq, begin=0, interleaved=False, device=None):
+        if device is None:
+            device = inv_freq.device if getattr(inv_freq, "is_cuda", False) else "cuda"
+        vals = inv_freq.double().tolist() if isinstance(inv_freq, torch.Tensor) else inv_freq
+        words = attn_rope_rates(vals)
+        signed = [w - (1 << 64) if w >> 63 else w for w in words]
+        self.rates = torch.tensor(signed, dtype=torch.int64, device=device)
+        self.begin, self.dim, self.interleaved = int(begin), 2 * len(words), bool(interleaved)
+        self.struct = _RotationStruct(self.rates.data_ptr(), self.begin, self.dim,
+                                      ROPE_PAIRS if interleaved else ROPE_HALVES)
+
+
+class PagedCache:
+    """A paged key / value cache over the caller's tensors.
+
+    k_cache (pages, page_size, heads, dqk) and v_cache (pages, page_size, heads, dv),
+    bf16 or float8_e4m3fn, with any strides whose columns are adjacent (a cache kept
+    as (pages, heads, page_size, d) is passed transposed).  k_scale, v_scale: fp32
+    per key head, the value of one stored unit of an e4m3 cache (None: 1)."""
+
+    def __init__(self, k_cache, v_cache, k_scale=None, v_scale=None):
+        if k_cache.dim() != 4 or v_cache.dim() != 4 or k_cache.shape[:3] != v_cache.shape[:3]:
+            raise ValueError("k_cache and v_cache must be (pages, page_size, heads, d) with the "
+                             "same pages, page_size and heads")
+        kinds = {torch.bfloat16: CACHE_BF16, torch.float8_e4m3fn: CACHE_E4M3}
+        if k_cache.dtype not in kinds or v_cache.dtype != k_cache.dtype:
+            raise ValueError("the caches must both be bfloat16 or both float8_e4m3fn")
+        pages, page_size, heads, dqk = k_cache.shape
+        for t in (k_cache, v_cache):
+            if t.stride(3) != 1:
+                raise ValueError("the columns of a cache row must be adjacent")
+            if t.device != k_cache.device:
+                raise ValueError("the caches must be on one device")
+        for t in (k_scale, v_scale):
+            if t is not None and (t.dtype != torch.float32 or t.numel() != heads
+                                  or not t.is_contiguous() or t.device != k_cache.device):
+                raise ValueError("k_scale and v_scale must be contiguous fp32, one per key head, "
+                                 "on the cache's device")
+        self.k_cache, self.v_cache, self.k_scale, self.v_scale = k_cache, v_cache, k_scale, v_scale
+        self.device = k_cache.device
+        self.page_size, self.heads, self.dqk, self.dv = page_size, heads, dqk, v_cache.shape[3]
+        self.struct = _CacheStruct(
+            k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
+            *k_cache.stride()[:3], *v_cache.stride()[:3], kinds[k_cache.dtype], pages, page_size,
+            heads, dqk, self.dv)
+
+
+class _On:
+    """Runs a call on its tensors' device and stream: outputs are allocated, and the kernel
+    launched, on `stream` (None: the device's current stream)."""
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.stack = []
+        index = device.index if device.index is not None else torch.cuda.current_device()
+        if index != torch.cuda.current_device():
+            self.stack.append(torch.cuda.device(index))
+        if stream is not None:
+            if not isinstance(stream, torch.cuda.Stream):
+                stream = torch.cuda.ExternalStream(int(stream), device=index)
+            self.stack.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.stack:
+            c.__enter__()
+
+    def __exit__(self, *exc):
+        for c in reversed(self.stack):
+            c.__exit__(*exc)
+
+
+def _rows(t, name, heads=None, d=None):
+    """Distance in elements between the token rows of a bf16 (..., H, d) tensor whose leading
+    dimensions are evenly spaced rows of dense heads."""
+    if t.dtype != torch.bfloat16:
+        raise ValueError(f"{name} must be bfloat16")
+    shape, stride = t.shape, t.stride()
+    if t.dim() < 3 or (heads is not None and shape[-2] != heads) or (d is not None
+                                                                   and shape[-1] != d):
+        raise ValueError(f"{name} must be (rows, heads, d)")
+    if (shape[-1] > 1 and stride[-1] != 1) or (shape[-2] > 1 and stride[-2] != shape[-1]):
+        raise ValueError(f"the heads of a row of {name} must be adjacent")
+    row, span = 0, 1  # span: rows below the dimension at hand
+    for n, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
+        if n == 1:
+            continue
+        if row == 0:
+            row = s
+        elif s != row * span:
+            raise ValueError(f"the rows of {name} must be evenly spaced")
+        span *= n
+    return row if row else shape[-2] * shape[-1]
+
+
+def _same_device(device, **tensors):
+    # (the kernels would read a host pointer as a device address)
+    if device.type != "cuda":
+        raise ValueError("tensors must be on a CUDA device")
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+
+
+def rope(q, k, rotation, inverse=False, pos0=0, cu_seqlens=None, cu_seqlens_k=None, out=None,
+         stream=None):
+    """(q, k) rotated by their positions, as bf16 tensors (either may be None).
+
+    q (B,Tq,Hq,d), k (B,Tk,Hk,d), or (sum T, H, d) with host offsets; slots of a packed
+    buffer work as they are.  Positions: key j of a sequence at pos0 + j, and the queries
+    are its last ones, as in forward().  inverse=True turns the other way, which is the
+    gradient: gradients of the rotated tensors in, of the unrotated ones out.  out: (q_out,
+    k_out), which may be the inputs themselves."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k are both None")
+    varlen = cu_seqlens is not None
+    for name, t in (("q", q), ("k", k)):
+        if t is not None and t.dim() != (3 if varlen else 4):
+            raise ValueError(f"{name} must have {3 if varlen else 4} dimensions")
+        if t is not None and (t.shape[-1] != x.shape[-1]
+                              or (not varlen and t.shape[0] != x.shape[0])):
+            raise ValueError("q and k must agree in batch and head size")
+    B = len(cu_seqlens) - 1 if varlen else x.shape[0]
+    at = 0 if varlen else 1
+    Tq = x.shape[at] if q is None else q.shape[at]
+    Tk = x.shape[at] if k is None else k.shape[at]
+    q_out, k_out = out if out is not None else (None, None)
+    if out is not None:
+        for name, t, o in (("q", q, q_out), ("k", k, k_out)):
+            if (t is None) != (o is None) or (o is not None and o.shape != t.shape):
+                raise ValueError(f"out must hold a tensor like {name}")
+    rows = [0 if t is None else _rows(t, n) for t, n in
+            ((q, "q"), (k, "k"), (q_out, "out[0]"), (k_out, "out[1]"))]
+    _same_device(x.device, k=k, q_out=q_out, k_out=k_out, rates=rotation.rates)
+    with _On(x.device, stream):
+        if out is None:
+            q_out, k_out = (None if t is None else
+                            torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
+                            for t in (q, k))
+        if x.numel() == 0:
+            return q_out, k_out
+        rc = attn_rope(q, k, q_out, k_out, B, 0 if q is None else q.shape[-2],
+                       0 if k is None else k.shape[-2], Tq, Tk, x.shape[-1], *rows, rotation,
+                       inverse, pos0, cu_seqlens, cu_seqlens_k)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_rope")
+    return q_out, k_out
+
+
+def _check_tables(cache, block_table, lens):
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or (
+            block_table.shape[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError("block_table must be int32 (sequences, pages) with adjacent entries")
+    if lens.dtype != torch.int32 or lens.dim() != 1 or not lens.is_contiguous() \
+            or lens.shape[0] != block_table.shape[0]:
+        raise ValueError("lens must be contiguous int32, one per row of block_table")
+    if block_table.device != cache.device or lens.device != cache.device:
+        raise ValueError(f"block_table and lens must be on {cache.device}")
+    width = block_table.shape[1]
+    return width, max(block_table.stride(0), width)
+
+
+def cache_append(cache, k, v, block_table, lens, q=None, rotation=None, cu_seqlens=None,
+                 q_out=None, stream=None):
+    """Appends new tokens' keys (T,heads,dqk) and values (T,heads,dv) to a PagedCache.
+
+    lens: device int32, each sequence's length with the new tokens counted; block_table:
+    device int32 (sequences, pages).  Without cu_seqlens (host offsets of the new rows) every
+    sequence brings T / sequences tokens.  k is rotated to its position if a rotation is
+    given, and so is q (T,Hq,dqk), which is returned (in q_out, which may be q)."""
+    width, stride = _check_tables(cache, block_table, lens)
+    B, T = lens.shape[0], k.shape[0]
+    k_row = _rows(k, "k", cache.heads, cache.dqk)
+    v_row = _rows(v, "v", cache.heads, cache.dv)
+    if k.dim() != 3 or v.dim() != 3 or v.shape[0] != T:
+        raise ValueError("k and v must be (T, heads, d) with the same T")
+    if cu_seqlens is not None and len(cu_seqlens) != B + 1:
+        raise ValueError("cu_seqlens must have one entry more than there are sequences")
+    q_row = out_row = Hq = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T:
+            raise ValueError("q must be (T, heads, dqk)")
+        q_row, Hq = _rows(q, "q", None, cache.dqk), q.shape[1]
+    if q_out is not None:
+        if q is None or q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+        out_row = _rows(q_out, "q_out")
+    _same_device(cache.device, k=k, v=v, q=q, q_out=q_out,
+                 rates=None if rotation is None else rotation.rates)
+    with _On(cache.device, stream):
+        if q is not None and q_out is None:
+            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        rc = attn_cache_append(cache, block_table, width, stride, lens, B, T, cu_seqlens, k,
+                               k_row, v, v_row, q, q_row, q_out, out_row, Hq, rotation)
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_cache_append")
+    return q_out
+
+
+def decode_workspace(device=None, stream=None):
+    """A workspace for decode(), initialised on `stream`; calls that share one must be
+    ordered on the GPU."""
+    device = torch.device("cuda" if device is None else device)
+    with _On(device, stream):
+        ws = torch.empty(attn_decode_workspace_size(), dtype=torch.uint8, device=device)
+        rc = attn_decode_workspace_init(ws, ws.numel())
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode_workspace_init")
+    return ws
+
+
+def decode(cache, q, block_table, lens, scale=None, window_left=-1, with_lse=True,
+           workspace=None, out=None, stream=None):
+    """Attention of one new token per sequence over a PagedCache: o (B,Hq,dv) bf16 and the
+    log-sum-exp (B,Hq) fp32 (None unless with_lse).
+
+    q (B,Hq,dqk) bf16, Hq a multiple of the cache's heads; lens counts the new token, whose
+    key is in the cache already.  window_left >= 0: only the last window_left + 1 keys.
+    workspace: from decode_workspace() (None: one is made and initialised for this call).
+    out: (o, lse) to write to (lse may be None)."""
+    width, stride = _check_tables(cache, block_table, lens)
+    B = lens.shape[0]
+    q_row = _rows(q, "q", None, cache.dqk)
+    if q.dim() != 3 or q.shape[0] != B:
+        raise ValueError("q must be (sequences, heads, dqk)")
+    Hq = q.shape[1]
+    o, lse = out if out is not None else (None, None)
+    if out is not None and (o.dtype != torch.bfloat16 or o.shape != (B, Hq, cache.dv)
+                            or not o.is_contiguous()):
+        raise ValueError("out[0] must be contiguous bfloat16 (sequences, heads, dv)")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, Hq)
+                            or not lse.is_contiguous()):
+        raise ValueError("out[1] must be contiguous float32 (sequences, heads)")
+    _same_device(cache.device, q=q, workspace=workspace, o=o, lse=lse)
+    scale = 1.0 / math.sqrt(cache.dqk) if scale is None else scale
+    with _On(cache.device, stream):
+        if out is None:
+            o = torch.empty((B, Hq, cache.dv), dtype=torch.bfloat16, device=q.device)
+            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if with_lse else None
+        if workspace is None:
+            workspace = decode_workspace(cache.device)
+        rc = attn_decode(cache, block_table, width, stride, lens, B, q, q_row, o, lse, Hq,
+                         window_left, scale, workspace,
+                         workspace.numel() * workspace.element_size())
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_decode")
+    return o, lse

@@ -325,6 +325,8 @@ const char* attn_strerror(int code) {
     case ATTN_ERR_TIMEOUT: return "device wait timed out";
     case ATTN_ERR_INTERNAL: return "internal kernel set-up error";
     case ATTN_ERR_SCRATCH_TOO_SMALL: return "problem needs more than the built-in 32 MiB scratch";
+    case ATTN_ERR_BAD_PAGE: return "length or page index outside the paged cache";
+    case ATTN_ERR_WORKSPACE_NOT_READY: return "decode workspace was not initialised";
     default: return "unknown error";
   }
 }

@@ -79,6 +79,8 @@ extern "C" {
 #define ATTN_ERR_TIMEOUT (-5)             /* a kernel's bounded wait gave up */
 #define ATTN_ERR_INTERNAL (-6)            /* a kernel found its launch set-up unusable */
 #define ATTN_ERR_SCRATCH_TOO_SMALL (-7)   /* attn_bwd_noalloc: problem exceeds its scratch */
+#define ATTN_ERR_BAD_PAGE (-8)            /* a length or page index outside the paged cache */
+#define ATTN_ERR_WORKSPACE_NOT_READY (-9) /* attn_decode: workspace was not initialised */
 
 #define ATTN_LAYOUT_BTHD 0
 #define ATTN_LAYOUT_PACKED_QKV 1
@@ -339,6 +341,155 @@ int attn_step_host(const void* q, const void* k, const void* v, const void* dO, 
  */
 int attn_step_host_status(const void* scratch, int B, int H, int T, int dqk, int dv,
                           int heads_per_group, int deterministic, void* stream);
+
+/*
+ * Position rotation and the paged key / value cache: what a model needs around
+ * the attention above to see positions (training and serving) and to generate
+ * token by token (serving).  No counterpart on the pages.
+ */
+
+/*
+ * The rotation of a head's columns begin .. begin + dim - 1, in pairs (a, b):
+ * at position p pair i turns by the angle p * w_i,
+ *     a' = a cos(p w_i) - b sin(p w_i),   b' = a sin(p w_i) + b cos(p w_i);
+ * the other columns pass unchanged.  style: which columns form pair i,
+ * ATTN_ROPE_HALVES: (begin + i, begin + dim/2 + i); ATTN_ROPE_PAIRS:
+ * (begin + 2i, begin + 2i + 1).  begin and dim are multiples of 16 (dim > 0).
+ * rates: DEVICE array of dim/2 words from attn_rope_rates(); 8-byte aligned.
+ */
+#define ATTN_ROPE_HALVES 0
+#define ATTN_ROPE_PAIRS 1
+typedef struct attn_rotation {
+  const unsigned long long* rates;
+  int begin, dim, style;
+} attn_rotation;
+
+/*
+ * Host helper (no GPU needed): converts n angular rates w_i (radians per
+ * position, finite, of any size) to the fixed-point form that the kernels
+ * read: the fraction of a turn per position, times 2^64.  A position times
+ * that word, modulo 2^64, is the angle modulo one turn, so an angle is as exact
+ * at position two billion as at position one.  Copy the words to the device
+ * once.  Returns ATTN_ERR_INVALID_ARG for NULL, n <= 0 or a rate that is not
+ * finite.
+ */
+int attn_rope_rates(const double* rates_rad, int n, unsigned long long* out);
+
+/*
+ * Rotates q and k by their positions: q (B,Tq,Hq,d) and k (B,Tk,Hk,d) bf16
+ * into q_out and k_out.  Either of q and k may be NULL (with its output); an
+ * output may be its input (in place), and must not overlap it otherwise.
+ * Positions are those of attn_fwd: key j of a sequence is at pos0 + j, query
+ * i at pos0 + i + (Tk - Tq) (pass Tk = Tq when only q is given and its
+ * positions start at pos0).  Variable length: cu_seqlens_q / cu_seqlens_k as in
+ * attn_fwd_ex (host; Tq and Tk are then totals, at most ATTN_MAX_VARLEN_SEQS
+ * sequences), sequence by sequence.  A query in front of the first key
+ * (Lq > Lk) has a negative position, which turns the other way.  *_row: elements between token rows
+ * of each tensor, a multiple of 8 and at least H*d (0: H*d); a slot of a packed
+ * (B,T,3,H,d) buffer has 3*H*d.  inverse = 1 turns the other way: the gradient
+ * with respect to the unrotated tensor from the gradient with respect to the
+ * rotated one.  d is 64, 128 or 192; pos0 >= 0 and every position below 2^31.
+ * Computed in fp32 and rounded to bf16 once.
+ */
+int attn_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int Hq, int Hk,
+              int Tq, int Tk, int d, long long q_row, long long k_row, long long q_out_row,
+              long long k_out_row, const attn_rotation* rotation, int inverse, int pos0,
+              const int* cu_seqlens_q, const int* cu_seqlens_k, void* stream);
+
+/*
+ * A paged cache of keys and values.  k and v (device) hold num_pages pages of
+ * page_size tokens for each of `heads` key heads, dqk and dv columns wide;
+ * element (page, token, head, c) of k is at page * k_page_stride + token *
+ * k_token_stride + head * k_head_stride + c, in elements (v likewise), so
+ * (pages, tokens, heads, d), (pages, heads, tokens, d) and one buffer that
+ * holds both k and v are all described by strides.  Bases and strides are
+ * multiples of 16 bytes; distinct elements must not overlap.
+ * type ATTN_CACHE_BF16: bf16.  ATTN_CACHE_E4M3: 8-bit floats, each standing
+ * for its value times k_scale[head] / v_scale[head] (device fp32, one positive
+ * value per key head; NULL: 1).
+ *
+ * Which pages a sequence uses is in its row of a block table (device int32,
+ * B rows of max_pages entries, table_stride entries apart): its token t is
+ * token t % page_size of page table[t / page_size].  Entries past a sequence's
+ * length are not read.
+ *
+ * lens (device int32, B): the number of tokens of each sequence INCLUDING the
+ * ones that this step appends.  The same array serves attn_cache_append and
+ * attn_decode of one step.  A length of 0 marks an unused row.
+ *
+ * A device-side error (a length that exceeds max_pages * page_size, a page
+ * index outside 0 .. num_pages - 1) faults nothing: such tokens are not written
+ * and not attended, and attn_cache_status() reports ATTN_ERR_BAD_PAGE.
+ */
+#define ATTN_CACHE_BF16 0
+#define ATTN_CACHE_E4M3 1
+typedef struct attn_paged_cache {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  long long k_page_stride, k_token_stride, k_head_stride;
+  long long v_page_stride, v_token_stride, v_head_stride;
+  int type, num_pages, page_size, heads, dqk, dv;
+} attn_paged_cache;
+
+/*
+ * Appends new tokens to the cache: k (T,heads,dqk) and v (T,heads,dv) bf16,
+ * rows k_row and v_row elements apart (multiple of 8; 0: dense).  Without
+ * cu_seqlens every sequence brings T / B tokens (T a multiple of B); with it
+ * (host, B + 1 offsets, as in attn_fwd) sequence b brings rows cu_seqlens[b] ..
+ * cu_seqlens[b+1] - 1.  The i-th of n new tokens of sequence b takes position
+ * lens[b] - n + i; a token whose position is negative (an unused row) is
+ * ignored, and nothing of it is written.
+ * rotation: NULL, or the rotation applied to k on the way (at the token's
+ * position).  q, q_out: NULL, or the same tokens' queries (T,Hq,dqk) bf16, rows
+ * q_row / q_out_row elements apart, rotated into q_out (in place if equal;
+ * copied without a rotation).
+ * e4m3 caches keep x / scale rounded to nearest even and saturated at +-448
+ * (NaN stays NaN).  Two new tokens must not fall on the same cache slot.
+ */
+int attn_cache_append(const attn_paged_cache* cache, const int* block_table, int max_pages,
+                      long long table_stride, const int* lens, int B, int T,
+                      const int* cu_seqlens, const void* k, long long k_row, const void* v,
+                      long long v_row, const void* q, long long q_row, void* q_out,
+                      long long q_out_row, int Hq, const attn_rotation* rotation, void* stream);
+
+/*
+ * Attention of one new token per sequence over the cache: q (B,Hq,dqk) bf16
+ * (rows q_row elements apart; 0: dense), o (B,Hq,dv) bf16, lse (B,Hq) fp32 or
+ * NULL.  Query head h uses key head h / (Hq / heads); Hq is a multiple of
+ * `heads`.  The token sits at position lens[b] - 1 and sees the keys 0 ..
+ * lens[b] - 1, or with window_left >= 0 only lens[b] - 1 - window_left ..
+ * lens[b] - 1 (-1: no window).  A row that sees no key (lens[b] <= 0), or
+ * whose scores are all -inf, gets O = 0 and LSE = -inf.  Keys and values that
+ * a row does not see never touch it, whatever their bits; one that it sees
+ * and that is not finite makes the row not finite.
+ *
+ * The work is split over the keys of all sequences alike, in equal shares; the
+ * parts of a row are joined by the last of its CTAs to finish, in a fixed
+ * order: results do not depend on timing (they do on the shares, so on the
+ * other lengths of the batch).
+ *
+ * workspace: attn_decode_workspace_size() bytes, 256-byte aligned, initialised
+ * ONCE with attn_decode_workspace_init() before its first use; each call
+ * leaves it ready for the next, of any sizes.  Calls that share a workspace,
+ * captured graphs included, must be ordered on the GPU.  A workspace that was
+ * not initialised writes nothing, and attn_cache_status() reports
+ * ATTN_ERR_WORKSPACE_NOT_READY.
+ */
+size_t attn_decode_workspace_size(void);
+int attn_decode_workspace_init(void* workspace, size_t workspace_bytes, void* stream);
+int attn_decode(const attn_paged_cache* cache, const int* block_table, int max_pages,
+                long long table_stride, const int* lens, int B, const void* q, long long q_row,
+                void* o, float* lse, int Hq, int window_left, float scale, void* workspace,
+                size_t workspace_bytes, void* stream);
+
+/*
+ * Synchronises `stream`, returns the sticky device status of attn_cache_append
+ * and attn_decode on the current device (ATTN_OK, ATTN_ERR_BAD_PAGE or
+ * ATTN_ERR_WORKSPACE_NOT_READY; the first since the last read) and clears it.
+ */
+int attn_cache_status(void* stream);
 
 /* Static text for an ATTN_* code. */
 const char* attn_strerror(int code);
