@@ -10,6 +10,7 @@ kernels: there is no CPU path, and a missing library raises at first use.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -158,8 +159,14 @@ def _ptr(x):
     return int(x)
 
 
+# the current stream's handle without a Stream object (a tenth of the time, where it exists)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(s):
     if s is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(s, torch.cuda.Stream):
         return s.cuda_stream
@@ -587,7 +594,6 @@ class PagedCache:
                 raise ValueError("k_scale and v_scale must be contiguous fp32, one per key head, "
                                  "on the cache's device")
         self.k_cache, self.v_cache, self.k_scale, self.v_scale = k_cache, v_cache, k_scale, v_scale
-        self.device = k_cache.device
         self.page_size, self.heads, self.dqk, self.dv = page_size, heads, dqk, v_cache.shape[3]
         self.struct = _CacheStruct(
             k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
@@ -596,13 +602,11 @@ class PagedCache:
 
 
 class _On:
-    """Runs a call on its tensors' device and stream: outputs are allocated, and the kernel
-    launched, on `stream` (None: the device's current stream)."""
+    """Runs a call on a device and stream: outputs are allocated, and the kernel launched, on
+    `stream` (None: the device's current stream)."""
 
-    def __init__(self, device, stream):
-        self.device = device
+    def __init__(self, index, stream):
         self.stack = []
-        index = device.index if device.index is not None else torch.cuda.current_device()
         if index != torch.cuda.current_device():
             self.stack.append(torch.cuda.device(index))
         if stream is not None:
@@ -619,15 +623,28 @@ class _On:
             c.__exit__(*exc)
 
 
+_HERE_NOW = contextlib.nullcontext()
+
+
+def _on(index, stream):
+    """_On(index, stream), or nothing to enter where that is where the caller is."""
+    if stream is None and index == torch.cuda.current_device():
+        return _HERE_NOW
+    return _On(index, stream)
+
+
 def _rows(t, name, heads=None, d=None):
     """Distance in elements between the token rows of a bf16 (..., H, d) tensor whose leading
     dimensions are evenly spaced rows of dense heads."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be bfloat16")
-    shape, stride = t.shape, t.stride()
-    if t.dim() < 3 or (heads is not None and shape[-2] != heads) or (d is not None
-                                                                   and shape[-1] != d):
+    shape = t.shape
+    if len(shape) < 3 or (heads is not None and shape[-2] != heads) or (d is not None
+                                                                      and shape[-1] != d):
         raise ValueError(f"{name} must be (rows, heads, d)")
+    if t.is_contiguous():
+        return shape[-2] * shape[-1]
+    stride = t.stride()
     if (shape[-1] > 1 and stride[-1] != 1) or (shape[-2] > 1 and stride[-2] != shape[-1]):
         raise ValueError(f"the heads of a row of {name} must be adjacent")
     row, span = 0, 1  # span: rows below the dimension at hand
@@ -642,13 +659,16 @@ def _rows(t, name, heads=None, d=None):
     return row if row else shape[-2] * shape[-1]
 
 
-def _same_device(device, **tensors):
-    # (the kernels would read a host pointer as a device address)
-    if device.type != "cuda":
+def _device_of(t, *others):
+    """The CUDA device that all of these are on (None entries are passed over).  The kernels
+    would read a host pointer as a device address."""
+    index = t.get_device()
+    if index < 0:
         raise ValueError("tensors must be on a CUDA device")
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}")
+    for o in others:
+        if o is not None and o.get_device() != index:
+            raise ValueError(f"tensors must be on one CUDA device (cuda:{index})")
+    return index
 
 
 def rope(q, k, rotation, inverse=False, pos0=0, cu_seqlens=None, cu_seqlens_k=None, out=None,
@@ -681,12 +701,14 @@ def rope(q, k, rotation, inverse=False, pos0=0, cu_seqlens=None, cu_seqlens_k=No
                 raise ValueError(f"out must hold a tensor like {name}")
     rows = [0 if t is None else _rows(t, n) for t, n in
             ((q, "q"), (k, "k"), (q_out, "out[0]"), (k_out, "out[1]"))]
-    _same_device(x.device, k=k, q_out=q_out, k_out=k_out, rates=rotation.rates)
-    with _On(x.device, stream):
+    index = _device_of(x, k, q_out, k_out, rotation.rates)
+    with _on(index, stream):
         if out is None:
-            q_out, k_out = (None if t is None else
-                            torch.empty(t.shape, dtype=torch.bfloat16, device=t.device)
-                            for t in (q, k))
+            q_out = None if q is None else torch.empty(q.shape, dtype=torch.bfloat16,
+                                                       device=q.device)
+            k_out = None if k is None else torch.empty(k.shape, dtype=torch.bfloat16,
+                                                       device=k.device)
+            rows[2:] = 0, 0  # dense
         if x.numel() == 0:
             return q_out, k_out
         rc = attn_rope(q, k, q_out, k_out, B, 0 if q is None else q.shape[-2],
@@ -698,16 +720,18 @@ def rope(q, k, rotation, inverse=False, pos0=0, cu_seqlens=None, cu_seqlens_k=No
 
 
 def _check_tables(cache, block_table, lens):
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or (
-            block_table.shape[1] > 1 and block_table.stride(1) != 1):
+    """(sequences, table width, table stride)."""
+    if block_table.dtype is not torch.int32 or len(block_table.shape) != 2:
         raise ValueError("block_table must be int32 (sequences, pages) with adjacent entries")
-    if lens.dtype != torch.int32 or lens.dim() != 1 or not lens.is_contiguous() \
-            or lens.shape[0] != block_table.shape[0]:
+    B, width = block_table.shape
+    stride = width
+    if not block_table.is_contiguous():
+        if width > 1 and block_table.stride(1) != 1:
+            raise ValueError("block_table must be int32 (sequences, pages) with adjacent entries")
+        stride = max(block_table.stride(0), width)
+    if lens.dtype is not torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
         raise ValueError("lens must be contiguous int32, one per row of block_table")
-    if block_table.device != cache.device or lens.device != cache.device:
-        raise ValueError(f"block_table and lens must be on {cache.device}")
-    width = block_table.shape[1]
-    return width, max(block_table.stride(0), width)
+    return B, width, stride
 
 
 def cache_append(cache, k, v, block_table, lens, q=None, rotation=None, cu_seqlens=None,
@@ -718,8 +742,8 @@ def cache_append(cache, k, v, block_table, lens, q=None, rotation=None, cu_seqle
     device int32 (sequences, pages).  Without cu_seqlens (host offsets of the new rows) every
     sequence brings T / sequences tokens.  k is rotated to its position if a rotation is
     given, and so is q (T,Hq,dqk), which is returned (in q_out, which may be q)."""
-    width, stride = _check_tables(cache, block_table, lens)
-    B, T = lens.shape[0], k.shape[0]
+    B, width, stride = _check_tables(cache, block_table, lens)
+    T = k.shape[0]
     k_row = _rows(k, "k", cache.heads, cache.dqk)
     v_row = _rows(v, "v", cache.heads, cache.dv)
     if k.dim() != 3 or v.dim() != 3 or v.shape[0] != T:
@@ -735,9 +759,9 @@ def cache_append(cache, k, v, block_table, lens, q=None, rotation=None, cu_seqle
         if q is None or q_out.shape != q.shape:
             raise ValueError("q_out must have q's shape")
         out_row = _rows(q_out, "q_out")
-    _same_device(cache.device, k=k, v=v, q=q, q_out=q_out,
-                 rates=None if rotation is None else rotation.rates)
-    with _On(cache.device, stream):
+    index = _device_of(cache.k_cache, k, v, q, q_out, block_table, lens,
+                       None if rotation is None else rotation.rates)
+    with _on(index, stream):
         if q is not None and q_out is None:
             q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
         rc = attn_cache_append(cache, block_table, width, stride, lens, B, T, cu_seqlens, k,
@@ -751,7 +775,10 @@ def decode_workspace(device=None, stream=None):
     """A workspace for decode(), initialised on `stream`; calls that share one must be
     ordered on the GPU."""
     device = torch.device("cuda" if device is None else device)
-    with _On(device, stream):
+    if device.type != "cuda":
+        raise ValueError("a decode workspace must be on a CUDA device")
+    index = torch.cuda.current_device() if device.index is None else device.index
+    with _on(index, stream):
         ws = torch.empty(attn_decode_workspace_size(), dtype=torch.uint8, device=device)
         rc = attn_decode_workspace_init(ws, ws.numel())
     if rc != ATTN_OK:
@@ -768,27 +795,28 @@ def decode(cache, q, block_table, lens, scale=None, window_left=-1, with_lse=Tru
     key is in the cache already.  window_left >= 0: only the last window_left + 1 keys.
     workspace: from decode_workspace() (None: one is made and initialised for this call).
     out: (o, lse) to write to (lse may be None)."""
-    width, stride = _check_tables(cache, block_table, lens)
-    B = lens.shape[0]
+    B, width, stride = _check_tables(cache, block_table, lens)
     q_row = _rows(q, "q", None, cache.dqk)
-    if q.dim() != 3 or q.shape[0] != B:
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != B:
         raise ValueError("q must be (sequences, heads, dqk)")
-    Hq = q.shape[1]
+    Hq = shape[1]
     o, lse = out if out is not None else (None, None)
-    if out is not None and (o.dtype != torch.bfloat16 or o.shape != (B, Hq, cache.dv)
+    if out is not None and (o.dtype is not torch.bfloat16 or o.shape != (B, Hq, cache.dv)
                             or not o.is_contiguous()):
         raise ValueError("out[0] must be contiguous bfloat16 (sequences, heads, dv)")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (B, Hq)
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, Hq)
                             or not lse.is_contiguous()):
         raise ValueError("out[1] must be contiguous float32 (sequences, heads)")
-    _same_device(cache.device, q=q, workspace=workspace, o=o, lse=lse)
-    scale = 1.0 / math.sqrt(cache.dqk) if scale is None else scale
-    with _On(cache.device, stream):
+    index = _device_of(cache.k_cache, q, block_table, lens, workspace, o, lse)
+    if scale is None:
+        scale = 1.0 / math.sqrt(cache.dqk)
+    with _on(index, stream):
         if out is None:
             o = torch.empty((B, Hq, cache.dv), dtype=torch.bfloat16, device=q.device)
             lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if with_lse else None
         if workspace is None:
-            workspace = decode_workspace(cache.device)
+            workspace = decode_workspace(index)
         rc = attn_decode(cache, block_table, width, stride, lens, B, q, q_row, o, lse, Hq,
                          window_left, scale, workspace,
                          workspace.numel() * workspace.element_size())

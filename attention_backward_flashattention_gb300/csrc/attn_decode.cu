@@ -11,32 +11,35 @@
 // about it:
 //   * A work item is a (sequence, key head, tile of at most 16 of the query
 //     heads that share it), so one read serves the whole group.
-//   * The keys of all items, in tiles of 64, are one line that is cut into
-//     equal shares, one per CTA, whatever the lengths are: the grid is fixed (a captured
-//     call follows the lengths on the device), no CTA has more than one tile
-//     more than another, and a CTA writes at most two unfinished items.
-//   * Each warp runs on its own: it takes 16 of a tile's 64 keys through a
-//     ring of asynchronous 16-byte copies in shared memory that only it uses (no
-//     block barrier until an item ends), multiplies with m16n8k16 (query rows
-//     x 16 keys x 16 columns), and keeps m, l and O of its keys in registers.
-//   * The four warps join in shared memory when the item or the share ends.
-//     An item that lies in one share is then finished; else the part goes to the
-//     workspace, and the CTA that arrives last joins the parts in the order of
-//     their CTAs.  Over sixteen parts are joined in two levels, so that one
-//     CTA never reads more than about two dozen.
+//   * The keys of all items, in tiles, are one line that is cut into pieces
+//     whose places depend on the lengths alone: a first piece per CTA, then
+//     smaller ones that the CTAs claim as they get done (make_line).  The grid
+//     is fixed, so a captured call follows the lengths on the device.
+//   * Each warp runs on its own: it takes a step of 16 keys (32 of an e4m3 cache)
+//     of each tile through a ring of asynchronous 16-byte copies in shared
+//     memory that only it uses (no block barrier until an item ends).  The
+//     products are m16n8k16 with the keys (then the value columns) as the 16 rows
+//     and the query heads as the 8 columns, so a group of eight heads fills
+//     them; m, l and O of the warp's keys stay in registers.
+//   * The warps join in shared memory when the item or the piece ends.  The next
+//     item is known by then, and its first steps are on their way before the
+//     join is done.  An item that lies in one piece is then finished; else the
+//     part goes to the workspace, and the CTA that arrives last joins the parts
+//     in the order of their pieces.  Over kJoinParts parts are joined in levels.
 // Legacy matrix instructions are enough here: at the measured 6.8 TB/s a bf16
-// cache brings 3.4 T elements a second, 109 TFLOP/s of 16-row products.
+// cache brings 3.4 T elements a second, 54 TFLOP/s of products with 8 columns.
+// (Their e4m3 form is no use on this GPU: it is carried out as conversions to
+// fp16 of both operands around each instruction, and measured half as fast as
+// converting the cache's side once.)
 //
 // Precision.  Scores, m, l and O are fp32.  The probabilities enter the second
 // product as bf16 (its other operand is bf16), as a rounded value plus the
-// rounded rest, so they carry 16 bits: with at most eight query rows the rest
-// takes the eight idle rows of the same instruction and costs nothing; above
-// that it takes a second instruction.  Rounded once, they would add as much
-// error to O as its own rounding to bf16 does.  An e4m3 cache is widened to fp16 (exact),
-// and so are the queries, scaled per row by a power of two to a largest value
-// in [1, 2) (exact but for elements below 2^-14 of the row's largest, which
-// lose bits below 2^-24 of it); the probabilities are fp16 (11 bits against
-// the cache's 4).
+// rounded rest, in two instructions: 16 bits.  Rounded once, they would add as
+// much error to O as its own rounding to bf16 does.  An e4m3 cache is widened to
+// fp16 (exact), and so are the queries, scaled per row by a power of two to a
+// largest value in [1, 2) (exact but for elements below 2^-14 of the row's
+// largest, which lose bits below 2^-24 of it); the probabilities are fp16 (11
+// bits against the cache's 4).
 #include <algorithm>
 #include <cstring>
 
@@ -47,10 +50,6 @@ namespace attn {
 
 namespace {
 
-constexpr int kWarps = kDecodeWarps;
-constexpr int kThreads = kWarps * 32;
-constexpr int kSub = kStepKeys;
-constexpr int kKeys = kTileKeys;
 
 struct DecodeParams {
   CacheView cache;
@@ -62,7 +61,7 @@ struct DecodeParams {
   int items_per_seq;  // key heads x row tiles
   int window;
   float scale_log2;
-  const uint32_t* header;
+  DecodeHeader* header;
   int* counters;
   float* ml;
   float* acc;
@@ -70,8 +69,11 @@ struct DecodeParams {
 };
 
 // ---- instructions -----------------------------------------------------------
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
-  // a source size of 0 writes zeros and reads nothing
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// take == false: writes zeros and reads nothing (a source size of 0).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(take ? 16 : 0)
                : "memory");
@@ -103,6 +105,7 @@ __device__ __forceinline__ uint4 ldsm_t(uint32_t a) {
                : "memory");
   return v;
 }
+// d += a b, a 16 x 16 (rows g and g + 8 of this thread), b 16 x 8.
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -117,14 +120,20 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t w) {  // the low two bytes
+// The transpose of an 8 x 8 matrix of 16-bit elements (two of a row in each thread).
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t f16x2_lo(uint32_t w) {  // e4m3 bytes 0 and 1
   uint32_t r;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
       : "=r"(r)
       : "r"(w));
   return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2_hi(uint32_t w) {  // the high two bytes
+__device__ __forceinline__ uint32_t f16x2_hi(uint32_t w) {  // e4m3 bytes 2 and 3
   uint32_t r;
   asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
       : "=r"(r)
@@ -136,63 +145,94 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+// Adds 1; what the CTA wrote before (and a barrier ordered) is seen by who adds
+// later, and what was written before earlier additions is seen here.
+__device__ __forceinline__ int arrive(int* counter) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  return old;
+}
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // ---- sizes of one variant ---------------------------------------------------
-// R: query rows held (8 or 16).  Shared memory per warp: a ring of kStages
-// steps, each 16 key rows and 16 value rows.
+// R: query rows held (8 or 16).  Two CTAs on an SM.  Shared memory: a ring of
+// kStages steps for each warp, kStep key rows and value rows each, and the O of half
+// the warps, for their join.  Six warps where their rings fit and the registers
+// of eight query rows do (12 warps on an SM: 168 each); else four.
 template <int DQK, int DV, bool E4M3, int R>
 struct Cfg {
+  static constexpr int kStep = E4M3 ? 32 : 16;
   static constexpr int kElt = E4M3 ? 1 : 2;
   static constexpr int kRowK = DQK * kElt, kRowV = DV * kElt;
-  static constexpr int kStepK = kSub * kRowK, kStep = kSub * (kRowK + kRowV);
-  // Bytes a warp keeps in flight: with three CTAs on an SM, 12 warps.
-  static constexpr int kStages = kStep > 8192 ? 2 : (16384 / kStep > 6 ? 6 : 16384 / kStep);
-  static constexpr int kRing = kStages * kStep;
-  static constexpr int kJoin = R * DV * 4;  // a warp's O when the warps join (same memory)
-  static constexpr int kWarpBytes = kRing > kJoin ? kRing : kJoin;
-  static constexpr int kSmem = kWarps * kWarpBytes;
-  static constexpr int kCtasPerSm = kSmem <= 66 * 1024 ? 3 : 2;
-  static_assert(kWarpBytes % 128 == 0, "rings start on a bank-aligned boundary");
+  static constexpr int kBytesK = kStep * kRowK, kBytes = kStep * (kRowK + kRowV);
+  static constexpr int kStages = kBytes > 8192 ? 2 : (16384 / kBytes > 4 ? 4 : 16384 / kBytes);
+  static constexpr int kRing = kStages * kBytes;
+  static constexpr int kPitch = DV + 4;  // (the rows' distance keeps them on different banks)
+  static constexpr int kJoin = R * kPitch * 4;
+  static constexpr int kWarps = R == 8 && 6 * kRing + 3 * kJoin <= 111 * 1024 ? 6 : 4;
+  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kHalf = kWarps / 2;
+  static constexpr int kTile = kWarps * kStep;
+  static constexpr int kSmem = kWarps * kRing + kHalf * kJoin;
+  static_assert(kRing % 128 == 0, "rings start on a bank-aligned boundary");
+  static_assert(kHalf * kJoin >= kJoinParts * R * 8, "room for the parts joined at a time");
 };
 
-// Where 16-byte chunk c of row r is kept, so that the reads below touch every
-// bank once (per quarter warp).  Keys are read eight rows apart in pairs: chunk 4j + t
-// of rows 2i and 2i + 1; rows that are a multiple of 128 bytes long need the
-// halves of a 128-byte line exchanged on odd rows.
+// The 16-byte chunk c of row r is kept in place c ^ swizzle(r), so that the reads
+// below touch every bank once (per quarter warp): keys two rows at a time, four
+// chunks of each (key_chunk); bf16 values by ldmatrix, one chunk of eight rows; e4m3
+// values a chunk and the next of rows 0, 2, 4 and 6.
 template <int ROW>
-__device__ __forceinline__ uint32_t key_at(int r, int c) {
-  return r * ROW + ((ROW % 128 == 0 ? c ^ ((r & 1) << 2) : c) << 4);
+__device__ __forceinline__ int swizzle(int r) {
+  return ROW % 128 == 0 ? r & 7 : ROW == 64 ? (r >> 1) & 3 : 0;
 }
-// Values: bf16 by ldmatrix, one chunk of eight rows; e4m3 a chunk of rows 0, 2, 4, 6.
-template <int ROW, bool E4M3>
-__device__ __forceinline__ uint32_t value_at(int r, int c) {
-  if constexpr (!E4M3) return r * ROW + ((c ^ (r & 7)) << 4);
-  if constexpr (ROW >= 128) return r * ROW + ((c ^ (((r >> 1) & 3) << 1)) << 4);
-  return r * ROW + ((c ^ ((r >> 1) & 3)) << 4);
+// The chunk of a key row that thread t of four reads j-th.
+template <int ROW>
+__device__ __forceinline__ constexpr int key_chunk(int j, int t) {
+  return ROW % 128 == 0 ? 8 * (j >> 1) + 2 * t + (j & 1) : 4 * j + t;
 }
 
-// Copies 16 rows of ROW bytes; row r is `off` (held by lane r) bytes from base,
-// and is taken if bit r of `rows` is set (else zeros).
-template <int ROW, bool KEYS, bool E4M3>
+// Copies STEP rows of ROW bytes, those whose bit of `rows` is set (else zeros).
+// IN_PAGE: row 0 is `off` bytes from base and the others follow `token` units of 16
+// bytes apart; else row r is at lane r's `off`.
+template <int STEP, int ROW, bool IN_PAGE>
 __device__ __forceinline__ void copy_rows(uint32_t dst, const char* base, int64_t off,
-                                          uint32_t rows) {
+                                          uint32_t token, uint32_t rows) {
   constexpr int kChunks = ROW / 16;
   constexpr int kWide = kChunks % 8 == 0 ? 8 : 4;  // lanes side by side on one row
   constexpr int kRows = 32 / kWide;                // rows of one instruction
-  const int lane = lane_id();
+  int lane;  // (read anew, so that what follows from it is not kept in registers)
+  asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
+  const int r0 = lane / kWide, c0 = lane % kWide;
+  // the places of the first two instructions' chunks: those of the others lie
+  // a constant behind the one of the same parity
+  const uint32_t at0 = dst + r0 * ROW + ((c0 ^ swizzle<ROW>(r0)) << 4);
+  const uint32_t at1 = dst + r0 * ROW + ((c0 ^ swizzle<ROW>(r0 + kRows)) << 4);
+  const char* src = base + off * (IN_PAGE ? 1 : 0) +
+                    ((int64_t)((IN_PAGE ? (uint64_t)r0 * token : 0) + c0) << 4);
+  const int64_t apart = (int64_t)((uint64_t)token * kRows << 4);
+  if (rows == (STEP == 32 ? ~0u : (1u << STEP) - 1u)) {
 #pragma unroll
-  for (int i = 0; i < kSub / kRows; ++i) {
-    const int r = i * kRows + lane / kWide;
-    const int64_t o = __shfl_sync(0xffffffffu, off, r);
-    const bool take = (rows >> r) & 1;
-    const char* src = take ? base + o : base;
+    for (int i = 0; i < STEP / kRows; ++i) {
+      const char* from = src;
+      if constexpr (IN_PAGE) src += apart;
+      else from += __shfl_sync(0xffffffffu, off, i * kRows + r0);
 #pragma unroll
-    for (int p = 0; p < kChunks / kWide; ++p) {
-      const int c = p * kWide + lane % kWide;
-      const uint32_t at = KEYS ? key_at<ROW>(r, c) : value_at<ROW, E4M3>(r, c);
-      cp_async16(dst + at, src + (take ? c * 16 : 0), take);
+      for (int p = 0; p < kChunks / kWide; ++p)
+        cp_async16(((i & 1) ? at1 : at0) + i * kRows * ROW + p * kWide * 16, from + p * kWide * 16);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < STEP / kRows; ++i) {
+      const char* from = src;
+      if constexpr (IN_PAGE) src += apart;
+      else from += __shfl_sync(0xffffffffu, off, i * kRows + r0);
+      const bool take = (rows >> (i * kRows + r0)) & 1;
+#pragma unroll
+      for (int p = 0; p < kChunks / kWide; ++p)
+        cp_async16_or_zero(((i & 1) ? at1 : at0) + i * kRows * ROW + p * kWide * 16,
+                           take ? from + p * kWide * 16 : base, take);
     }
   }
 }
@@ -220,543 +260,672 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 }
 
 // Sums the parts in their order, to the slot `slot_out` or (slot_out < 0) to the
-// outputs.  wgt and tot: shared memory.
-template <int DV, int R>
-__device__ void join_parts(const DecodeParams& P, const Joined& j, int rows, int slot_out, int b,
-                           int head, float v_scale, float (*wgt)[R], float2* tot) {
+// outputs.  `tmp`: shared memory for count() * R float2.
+template <int DV, int R, int kThreads>
+__device__ __forceinline__ void join_parts(const DecodeParams& P, const Joined& j, int rows,
+                                           int slot_out, int b, int head, float v_scale,
+                                           float2* tmp) {
+  constexpr int kBatch = kJoinParts;  // loads on their way at once
   const int tid = threadIdx.x;
   const int n = j.count();
   const float2* ml = reinterpret_cast<const float2*>(P.ml);
-  if (tid < rows) {
-    float m = -INFINITY;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, __ldcg(ml + j.slot(i) * kMaxTileRows + tid).x);
-    const float z = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int i = 0; i < n; ++i) {
-      const float2 x = __ldcg(ml + j.slot(i) * kMaxTileRows + tid);
-      const float f = ex2(x.x - z);
-      wgt[i][tid] = f;
-      l += x.y * f;
-    }
-    tot[tid] = make_float2(m, l);
-  }
-  __syncthreads();
-  for (int e = tid; e < rows * DV / 4; e += kThreads) {
-    const int row = e / (DV / 4), c = (e - row * (DV / 4)) * 4;
+  for (int x = tid; x < n * R; x += kThreads)
+    if (x % R < rows) tmp[x] = __ldcg(ml + j.slot(x / R) * kMaxTileRows + x % R);
+  bool ready = false;
+  for (int e = tid; e - tid < rows * DV / 4; e += kThreads) {  // (all threads take every turn)
+    const bool mine = e < rows * DV / 4;
+    const int row = mine ? e / (DV / 4) : 0, c = (e % (DV / 4)) * 4;
+    float m = -INFINITY, z = 0.f, l = 0.f;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(
-          P.acc + ((int64_t)j.slot(i) * kMaxTileRows + row) * DV + c));
-      const float f = wgt[i][row];
-      s.x += x.x * f;
-      s.y += x.y * f;
-      s.z += x.z * f;
-      s.w += x.w * f;
+    for (int i0 = 0; i0 < n; i0 += kBatch) {
+      float4 x[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (mine && i0 + i < n)
+          x[i] = __ldcg(reinterpret_cast<const float4*>(
+              P.acc + ((int64_t)j.slot(i0 + i) * kMaxTileRows + row) * DV + c));
+      if (!ready) {  // the first loads are on their way
+        __syncthreads();
+        ready = true;
+      }
+      if (i0 == 0) {
+        for (int i = 0; i < n; ++i) m = fmaxf(m, tmp[i * R + row].x);
+        z = m == -INFINITY ? 0.f : m;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (mine && i0 + i < n) {
+          const float2 w = tmp[(i0 + i) * R + row];
+          const float f = ex2(w.x - z);
+          l += w.y * f;
+          s.x += x[i].x * f;
+          s.y += x[i].y * f;
+          s.z += x[i].z * f;
+          s.w += x[i].w * f;
+        }
+      }
     }
-    const float2 t = tot[row];
+    if (!mine) continue;
     if (slot_out >= 0) {
       __stcg(reinterpret_cast<float4*>(
                  P.acc + ((int64_t)slot_out * kMaxTileRows + row) * DV + c),
              s);
       if (c == 0)
-        __stcg(reinterpret_cast<float2*>(P.ml) + slot_out * kMaxTileRows + row, t);
+        __stcg(reinterpret_cast<float2*>(P.ml) + slot_out * kMaxTileRows + row,
+               make_float2(m, l));
     } else {
-      const float inv = t.y == 0.f ? 0.f : v_scale / t.y;
+      const float inv = l == 0.f ? 0.f : v_scale / l;
       store_row4<DV>(P, b, head, row, c, s, inv);
-      if (c == 0 && P.lse) P.lse[(int64_t)b * P.Hq + head + row] = lse_of(t.x, t.y);
+      if (c == 0 && P.lse) P.lse[(int64_t)b * P.Hq + head + row] = lse_of(m, l);
     }
   }
 }
 
+// ---- walking the line ----------------------------------------------------------
+// What a CTA works on: part of one item (the tiles tile0 .. tile1 - 1 of it).
+struct Item {
+  const int* table;              // the sequence's pages
+  const char *k_base, *v_base;   // the key head's columns of the cache
+  int b, kvh, head, rows;
+  int tile0, tile1;
+  KeyRange keys;
+  ItemParts parts;
+  int my_part;
+  int more;                      // 0: nothing is left, and the rest is not set
+};
+// Where it is on the line.
+struct Walk {
+  long long at, stop;  // next tile of the piece, and its end
+  long long seq_at;    // first tile of sequence b on the line
+  int b, piece;
+};
+
+// The next item with tiles, of this piece or of one claimed now.  One thread calls
+// it.  before[i]: tiles in front of the sequences i * chunk ..
+template <int STEP, int TILE>
+__device__ __noinline__ void next_item(const DecodeParams& P, const Line& line,
+                                       const long long* before, int threads, int chunk, Walk& k,
+                                       Item* w) {
+  auto range = [&](int b, int& len) {
+    len = __ldg(P.cache.lens + b);
+    return key_range(P.cache, P.window, len, STEP, TILE);
+  };
+  for (;;) {
+    while (k.at < k.stop) {
+      int len;
+      const KeyRange keys = range(k.b, len);
+      const long long all = (long long)keys.tiles * P.items_per_seq;
+      if (k.at >= k.seq_at + all) {
+        k.seq_at += all;
+        ++k.b;
+        continue;
+      }
+      if (len > keys.end) atomicCAS(P.status, 0, kStatusBadPage);
+      const int item = (int)div_line(k.at - k.seq_at, keys.tiles);
+      const long long item_at = k.seq_at + (long long)item * keys.tiles;
+      const int tile0 = (int)(snap(line, k.at, item_at, keys.tiles) - item_at);
+      k.at = item_at + keys.tiles;
+      const int tile1 =
+          k.stop >= k.at ? keys.tiles : (int)(snap(line, k.stop, item_at, keys.tiles) - item_at);
+      if (tile0 >= tile1) continue;
+      const int kvh = item / P.row_tiles, first = (item - kvh * P.row_tiles) * P.tile_rows;
+      w->table = P.cache.table + k.b * P.cache.table_stride;
+      w->k_base = P.cache.k.base + kvh * P.cache.k.head;
+      w->v_base = P.cache.v.base + kvh * P.cache.v.head;
+      w->b = k.b;
+      w->kvh = kvh;
+      w->head = kvh * P.group + first;
+      w->rows = min(P.tile_rows, P.group - first);
+      w->tile0 = tile0;
+      w->tile1 = tile1;
+      w->keys = keys;
+      w->parts = item_parts(line, item_at, keys.tiles);
+      w->my_part = k.piece - w->parts.first;
+      w->more = 1;
+      return;
+    }
+    if (k.piece >= 0) {  // (-1: the first piece is still to come)
+      if (line.pieces == line.n) break;  // a piece for each: nothing is claimed
+      k.piece = line.n + atomicAdd(&P.header->claimed, 1);
+    } else {
+      k.piece = blockIdx.x;
+    }
+    if (k.piece >= line.pieces) break;
+    k.at = cut(line, k.piece);
+    k.stop = cut(line, k.piece + 1);
+    int lo = 0, hi = threads - 1;  // the last i with before[i] <= at
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (before[mid] <= k.at) lo = mid; else hi = mid - 1;
+    }
+    k.b = lo * chunk;
+    k.seq_at = before[lo];
+  }
+  w->more = 0;
+}
+
 // ---- the kernel -------------------------------------------------------------
-template <int DQK, int DV, bool E4M3, int R>
-__global__ void __launch_bounds__(kThreads, Cfg<DQK, DV, E4M3, R>::kCtasPerSm)
+// IN_PAGE: pages hold whole steps (page_size is a multiple of the step), so a
+// step's rows are evenly spaced and one page index serves it.
+template <int DQK, int DV, bool E4M3, int R, bool IN_PAGE>
+__global__ void __launch_bounds__(Cfg<DQK, DV, E4M3, R>::kThreads, 2)
 decode_kernel(const __grid_constant__ DecodeParams P) {
   using C = Cfg<DQK, DV, E4M3, R>;
-  constexpr int kNT = DV / 8;       // column tiles of O
-  constexpr int kQ = DQK / 8;       // registers of one query row per thread
-  constexpr bool kHi = R > 8;       // rows 8 .. 15 hold queries
+  constexpr int kStep = C::kStep, kKeys = C::kTile, kWarps = C::kWarps, kThreads = C::kThreads;
+  constexpr int kQT = R / 8;         // tiles of eight query rows
+  constexpr int kKT = kStep / 16;    // tiles of sixteen keys
+  constexpr int kVT = DV / 16;       // tiles of sixteen value columns
+  constexpr int kQ = DQK / 8;        // registers of a tile's queries
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ long long s_prefix;
-  __shared__ long long s_sum[kWarps];
-  __shared__ int s_b;
-  __shared__ uint32_t s_rows[kWarps][C::kStages];  // which keys of a step take part
-  __shared__ float2 s_ml[kWarps][R];
-  __shared__ float2 s_tot[R];
-  constexpr int kMostJoined = kMaxDecodeCtas / kJoinParts + 1;  // groups of one item
-  static_assert(kMostJoined >= kJoinParts, "room for a group's parts");
-  __shared__ float s_wgt[kMostJoined][R];
+  __shared__ Line s_line;
+  __shared__ long long s_sum[kWarps], s_before[kThreads];
+  __shared__ Walk s_walk;
+  __shared__ Item s_items[2];
   __shared__ int s_last;
+  __shared__ uint32_t s_rows[kWarps][C::kStages];  // which keys of a step take part
+  __shared__ float2 s_ml[kWarps][R], s_ml2[C::kHalf][R];
 
   const int tid = threadIdx.x, lane = lane_id(), warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
+  float* const joined = reinterpret_cast<float*>(smem + kWarps * C::kRing);
 
   // The line: tiles of every sequence, times its items.  Each thread sums the
-  // tiles of consecutive sequences; the one whose sequences hold this CTA's
-  // first tile finds where.
-  if (__ldg(P.header) != kDecodeReady) {
-    if (tid == 0) atomicCAS(P.status, 0, kStatusNotReady);
-    return;
-  }
+  // tiles of consecutive sequences.
+  const uint32_t ready = *reinterpret_cast<const volatile uint32_t*>(&P.header->ready);
   const int chunk = (P.B + kThreads - 1) / kThreads;
   const int b_lo = min(tid * chunk, P.B), b_hi = min(b_lo + chunk, P.B);
   long long mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += key_range(P.cache, P.window, __ldg(P.cache.lens + b)).tiles;
-  long long upto = mine;  // inclusive prefix over the warp
+  for (int b = b_lo; b < b_hi; ++b)
+    mine += key_range(P.cache, P.window, __ldg(P.cache.lens + b), kStep, kKeys).tiles;
+  long long before = mine;  // inclusive prefix over the warp
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, upto, d);
-    if (lane >= d) upto += x;
+    const long long x = __shfl_up_sync(0xffffffffu, before, d);
+    if (lane >= d) before += x;
   }
-  if (lane == 31) s_sum[warp] = upto;
+  if (lane == 31) s_sum[warp] = before;
+  before -= mine;
   __syncthreads();
-  long long before = upto - mine, all = 0;
+  long long all = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += s_sum[w];
     all += s_sum[w];
   }
-  const long long total = all * P.items_per_seq;
-  const int n_cta = (int)min((long long)gridDim.x, total);
-  if ((int)blockIdx.x >= n_cta) return;
-  long long at = share(blockIdx.x, total, n_cta);
-  const long long stop = share(blockIdx.x + 1, total, n_cta);
-  if (b_lo < b_hi && at >= before * P.items_per_seq &&
-      at < (before + mine) * P.items_per_seq) {
-    long long x = before;
-    int b = b_lo;
-    for (;; ++b) {
-      const int nt = key_range(P.cache, P.window, __ldg(P.cache.lens + b)).tiles;
-      if (at < (x + nt) * P.items_per_seq || b + 1 >= b_hi) break;
-      x += nt;
+  if (ready != kDecodeReady) {
+    if (tid == 0) atomicCAS(P.status, 0, kStatusNotReady);
+    return;
+  }
+  // (threads without sequences: in front of nothing, behind every tile)
+  s_before[tid] = before * P.items_per_seq;
+  __syncthreads();
+  if (tid == 0) {
+    s_line = make_line(all * P.items_per_seq, (long long)P.B * P.items_per_seq, gridDim.x);
+    s_items[0].more = 0;
+    if ((int)blockIdx.x < s_line.n) {
+      s_walk.piece = -1;
+      s_walk.at = s_walk.stop = 0;
+      next_item<kStep, kKeys>(P, s_line, s_before, kThreads, chunk, s_walk, &s_items[0]);
     }
-    s_b = b;
-    s_prefix = x * P.items_per_seq;
   }
   __syncthreads();
-  int b = s_b;
-  long long seq_at = s_prefix;  // first tile of sequence b on the line
+  if ((int)blockIdx.x >= s_line.n) return;
+  const uint32_t ring = smem_u32(smem) + warp * C::kRing;
 
-  const uint32_t ring = smem_u32(smem) + warp * C::kWarpBytes;
-
-  while (at < stop) {
-    const int len = __ldg(P.cache.lens + b);
-    const KeyRange rg = key_range(P.cache, P.window, len);
-    if (at >= seq_at + (long long)rg.tiles * P.items_per_seq) {  // next sequence
-      seq_at += (long long)rg.tiles * P.items_per_seq;
-      ++b;
-      continue;
+  // Where a step of an item lies.  (What is the same for all steps of an item is
+  // read from shared memory each time: registers are scarce.)  Step i of this warp
+  // covers keys key0 + i * kKeys ..; page_of: the page of this lane's key of step i
+  // (IN_PAGE: of the step).
+  const Item* it = &s_items[0];
+  int key0 = 0, steps = 0, page = 0;
+  auto key_of = [&](int i) { return key0 + i * kKeys + (IN_PAGE ? 0 : lane & (kStep - 1)); };
+  auto wanted = [&](int key) { return IN_PAGE || (key >= it->keys.first && key < it->keys.end); };
+  auto page_of = [&](int i) {
+    const int key = key_of(i);
+    return i < steps && wanted(key) ? __ldg(it->table + div_page(P.cache, key)) : 0;
+  };
+  constexpr uint32_t kAllRows = kStep == 32 ? ~0u : (1u << kStep) - 1u;
+  // Copies step i's keys; what its values take (copy_values) is in take and in_page.
+  uint32_t take = 0;
+  int in_page = 0;
+  auto copy_keys = [&](int i, int st, int page) {
+    const int key = key_of(i);
+    const bool ok = wanted(key) && page_in(P.cache, page);
+    if (!ok && wanted(key)) atomicCAS(P.status, 0, kStatusBadPage);
+    if constexpr (IN_PAGE) {
+      take = key >= it->keys.first && key + kStep <= it->keys.end ? kAllRows
+                                                                  : seen_bits(it->keys, key, kStep);
+      if (!ok) take = 0;
+    } else {
+      take = __ballot_sync(0xffffffffu, ok) & kAllRows;
     }
-    if (len > rg.end && tid == 0) atomicCAS(P.status, 0, kStatusBadPage);
-    const int item = (int)((at - seq_at) / rg.tiles);
-    const long long item_at = seq_at + (long long)item * rg.tiles;
-    const int tile0 = (int)(at - item_at);
-    const int tile1 = (int)min((long long)rg.tiles, stop - item_at);
-    at = item_at + tile1;
-    const int kvh = item / P.row_tiles;
-    const int rt = item - kvh * P.row_tiles;
-    const int rows = min(P.tile_rows, P.group - rt * P.tile_rows);
-    const int head = kvh * P.group + rt * P.tile_rows;
-
-    // this warp's steps: step i covers keys key0 + i * kKeys ..
-    const int key0 = rg.origin + tile0 * kKeys + warp * kSub;
-    const int steps = key0 < rg.end ? min(tile1 - tile0, (rg.end - key0 + kKeys - 1) / kKeys) : 0;
-
-    const int* table = P.cache.table + b * P.cache.table_stride;
-    const char* kbase = P.cache.k.base + kvh * P.cache.k.head;
-    const char* vbase = P.cache.v.base + kvh * P.cache.v.head;
-    int64_t koff = 0, voff = 0, voff_next = 0;
-    uint32_t rows_next = 0;
-    // lane r's key of step i (r = lane % 16), whether it is one that is seen, and its page
-    auto key_of = [&](int i) { return key0 + i * kKeys + (lane & 15); };
-    auto wanted = [&](int key) { return key >= rg.first && key < rg.end; };
-    auto page_of = [&](int i) {
-      const int key = key_of(i);
-      return i < steps && wanted(key) ? __ldg(table + div_page(P.cache, key)) : 0;
-    };
-    auto locate = [&](int i, int page) {  // koff, voff_next, rows_next of step i
-      const int key = key_of(i);
-      const bool ok = wanted(key) && page_in(P.cache, page);
-      if (!ok && wanted(key)) atomicCAS(P.status, 0, kStatusBadPage);
-      koff = ok ? token_at(P.cache, P.cache.k, page, key) : 0;
-      voff_next = ok ? token_at(P.cache, P.cache.v, page, key) : 0;
-      rows_next = __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
-    };
-    int page = page_of(0);
-
-    // queries, as the first operand's registers: the columns of a step of 16
-    // are the ones that a thread reads of a key row in one 16-byte load
-    uint32_t qa[kQ], qb[kHi ? kQ : 1];
-    float c_lo = P.scale_log2, c_hi = P.scale_log2;
-    if (E4M3 && P.cache.k.scale) {
-      const float ks = __ldg(P.cache.k.scale + kvh);
-      c_lo *= ks;
-      c_hi *= ks;
+    if (lane == 0) s_rows[warp][st] = take;
+    in_page = key - div_page(P.cache, key) * P.cache.page_size;
+    copy_rows<kStep, C::kRowK, IN_PAGE>(ring + st * C::kBytes, it->k_base,
+                                        ok ? token_at(P.cache.k, page, in_page) : 0,
+                                        P.cache.k.token, take);
+  };
+  auto copy_values = [&](int i, int st, int page) {
+    const bool ok = wanted(key_of(i)) && page_in(P.cache, page);
+    copy_rows<kStep, C::kRowV, IN_PAGE>(ring + st * C::kBytes + C::kBytesK, it->v_base,
+                                        ok ? token_at(P.cache.v, page, in_page) : 0,
+                                        P.cache.v.token, take);
+  };
+  auto begin_item = [&](const Item* item) {  // the page of its first step
+    it = item;
+    steps = 0;
+    if (it->more) {
+      key0 = it->keys.origin + it->tile0 * kKeys + warp * kStep;
+      if (key0 < it->keys.end)
+        steps = min(it->tile1 - it->tile0, (it->keys.end - key0 + kKeys - 1) / kKeys);
     }
-    {
-      const uint16_t* qp = P.q + b * P.q_row + (int64_t)head * DQK;
-      auto load_row = [&](int row, uint32_t* dst, float& c) {
-        constexpr int kCol = E4M3 ? 16 : 8;  // columns a thread takes at a time
-#pragma unroll
-        for (int j = 0; j < DQK / (4 * kCol); ++j) {
-#pragma unroll
-          for (int h = 0; h < kCol / 8; ++h) {
-            const uint4 w = row < rows ? __ldg(reinterpret_cast<const uint4*>(
-                                             qp + row * DQK + (4 * j + t4) * kCol + h * 8))
-                                       : make_uint4(0, 0, 0, 0);
-            uint32_t* d = dst + (j * (kCol / 8) + h) * 4;
-            d[0] = w.x;
-            d[1] = w.y;
-            d[2] = w.z;
-            d[3] = w.w;
-          }
-        }
-        if constexpr (E4M3) {  // to fp16, by a power of two
-          float big = 0.f;
-#pragma unroll
-          for (int i = 0; i < kQ; ++i) big = fmaxf(big, fmaxf(fabsf(bf_lo(dst[i])), fabsf(bf_hi(dst[i]))));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          // 2^e <= big < 2^(e+1); rows of zeros, subnormals or infinities stay as they are
-          const int e = (int)(__float_as_uint(big) >> 23) - 127;
-          const bool plain = e < -100 || e > 100;
-          const float down = plain ? 1.f : __uint_as_float((uint32_t)(127 - e) << 23);
-          c *= plain ? 1.f : __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll
-          for (int i = 0; i < kQ; ++i) dst[i] = pack_f16(bf_lo(dst[i]) * down, bf_hi(dst[i]) * down);
-        }
-      };
-      load_row(g, qa, c_lo);
-      if constexpr (kHi) load_row(g + 8, qb, c_hi);
-    }
-
-    float acc[kNT][4];
-#pragma unroll
-    for (int i = 0; i < kNT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-    float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
-
-    // fill the ring: groups K0 V0 K1 V1 ...
-#pragma unroll
+    page = page_of(0);
+  };
+  auto fill_ring = [&]() {  // groups K0 V0 K1 V1 ...
+#pragma unroll 1
     for (int i = 0; i < C::kStages; ++i) {
+      const int now = page;
       if (i < steps) {
-        locate(i, page);
         page = page_of(i + 1);
-        if (lane == 0) s_rows[warp][i] = rows_next;
-        copy_rows<C::kRowK, true, E4M3>(ring + i * C::kStep, kbase, koff, rows_next);
-        cp_commit();
-        copy_rows<C::kRowV, false, E4M3>(ring + i * C::kStep + C::kStepK, vbase, voff_next, rows_next);
-        cp_commit();
-      } else {
-        cp_commit();
-        cp_commit();
-      }
-    }
-
-    int stage = 0;
-    for (int i = 0; i < steps; ++i) {
-      const uint32_t ks = ring + stage * C::kStep, vs = ks + C::kStepK;
-      cp_wait<2 * C::kStages - 1>();
-      __syncwarp();
-      const uint32_t seen = s_rows[warp][stage];
-      float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-      if constexpr (E4M3) {
-#pragma unroll
-        for (int j = 0; j < DQK / 64; ++j) {
-          const uint4 k0 = lds128(ks + key_at<C::kRowK>(g, 4 * j + t4));
-          const uint4 k1 = lds128(ks + key_at<C::kRowK>(g + 8, 4 * j + t4));
-          const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            const int x = j * 8 + h * 2;
-            const uint32_t a1 = kHi ? qb[kHi ? x : 0] : 0u, a3 = kHi ? qb[kHi ? x + 1 : 0] : 0u;
-            mma16816<true>(s0, qa[x], a1, qa[x + 1], a3, e4m3x2_to_f16x2(w0[h]),
-                           e4m3x2_to_f16x2_hi(w0[h]));
-            mma16816<true>(s1, qa[x], a1, qa[x + 1], a3, e4m3x2_to_f16x2(w1[h]),
-                           e4m3x2_to_f16x2_hi(w1[h]));
-          }
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < DQK / 32; ++j) {
-          const uint4 k0 = lds128(ks + key_at<C::kRowK>(g, 4 * j + t4));
-          const uint4 k1 = lds128(ks + key_at<C::kRowK>(g + 8, 4 * j + t4));
-          const int x = j * 4;
-          const uint32_t h0 = kHi ? qb[kHi ? x : 0] : 0u, h1 = kHi ? qb[kHi ? x + 1 : 0] : 0u,
-                         h2 = kHi ? qb[kHi ? x + 2 : 0] : 0u, h3 = kHi ? qb[kHi ? x + 3 : 0] : 0u;
-          mma16816<false>(s0, qa[x], h0, qa[x + 1], h1, k0.x, k0.y);
-          mma16816<false>(s1, qa[x], h0, qa[x + 1], h1, k1.x, k1.y);
-          mma16816<false>(s0, qa[x + 2], h2, qa[x + 3], h3, k0.z, k0.w);
-          mma16816<false>(s1, qa[x + 2], h2, qa[x + 3], h3, k1.z, k1.w);
-        }
-      }
-      __syncwarp();  // every lane has read the keys
-      const int next = i + C::kStages;
-      if (next < steps) {
-        locate(next, page);
-        page = page_of(next + 1);
-        if (lane == 0) s_rows[warp][stage] = rows_next;
-        copy_rows<C::kRowK, true, E4M3>(ks, kbase, koff, rows_next);
-        voff = voff_next;
+        copy_keys(i, i, now);
       }
       cp_commit();
-
-      // running maximum and sum; keys that take no part are -inf
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool in0 = (seen >> (2 * t4 + e)) & 1, in1 = (seen >> (8 + 2 * t4 + e)) & 1;
-        s0[e] = in0 ? s0[e] * c_lo : -INFINITY;
-        s1[e] = in1 ? s1[e] * c_lo : -INFINITY;
-        if constexpr (kHi) {
-          s0[2 + e] = in0 ? s0[2 + e] * c_hi : -INFINITY;
-          s1[2 + e] = in1 ? s1[2 + e] * c_hi : -INFINITY;
-        }
-      }
-      float x_lo = fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s1[0], s1[1]));
-      float x_hi = kHi ? fmaxf(fmaxf(s0[2], s0[3]), fmaxf(s1[2], s1[3])) : -INFINITY;
-      x_lo = fmaxf(x_lo, __shfl_xor_sync(0xffffffffu, x_lo, 1));
-      x_lo = fmaxf(x_lo, __shfl_xor_sync(0xffffffffu, x_lo, 2));
-      if constexpr (kHi) {
-        x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 1));
-        x_hi = fmaxf(x_hi, __shfl_xor_sync(0xffffffffu, x_hi, 2));
-      }
-      if (__any_sync(0xffffffffu, x_lo > m_lo || x_hi > m_hi)) {
-        const float n_lo = fmaxf(m_lo, x_lo), n_hi = fmaxf(m_hi, x_hi);
-        const float f_lo = m_lo == -INFINITY ? 0.f : ex2(m_lo - n_lo);
-        const float f_hi = m_hi == -INFINITY ? 0.f : ex2(m_hi - n_hi);
-        m_lo = n_lo;
-        m_hi = n_hi;
-        l_lo *= f_lo;
-        l_hi *= f_hi;
-        // without queries in rows 8 .. 15 those rows are the rest of rows 0 .. 7
-        const float r_hi = kHi ? f_hi : f_lo;
-#pragma unroll
-        for (int n = 0; n < kNT; ++n) {
-          acc[n][0] *= f_lo;
-          acc[n][1] *= f_lo;
-          acc[n][2] *= r_hi;
-          acc[n][3] *= r_hi;
-        }
-      }
-      const float z_lo = m_lo == -INFINITY ? 0.f : m_lo, z_hi = m_hi == -INFINITY ? 0.f : m_hi;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s0[e] = ex2(s0[e] - z_lo);
-        s1[e] = ex2(s1[e] - z_lo);
-        l_lo += s0[e] + s1[e];
-        if constexpr (kHi) {
-          s0[2 + e] = ex2(s0[2 + e] - z_hi);
-          s1[2 + e] = ex2(s1[2 + e] - z_hi);
-          l_hi += s0[2 + e] + s1[2 + e];
-        }
-      }
-      // the second product's first operand
-      uint32_t pa[4], pr[4];
-      if constexpr (E4M3) {
-        pa[0] = pack_f16(s0[0], s0[1]);
-        pa[2] = pack_f16(s1[0], s1[1]);
-        pa[1] = kHi ? pack_f16(s0[2], s0[3]) : 0u;
-        pa[3] = kHi ? pack_f16(s1[2], s1[3]) : 0u;
-      } else {
-        pa[0] = pack_bf16(s0[0], s0[1]);
-        pa[2] = pack_bf16(s1[0], s1[1]);
-        const uint32_t r0 = pack_bf16(s0[0] - bf_lo(pa[0]), s0[1] - bf_hi(pa[0]));
-        const uint32_t r2 = pack_bf16(s1[0] - bf_lo(pa[2]), s1[1] - bf_hi(pa[2]));
-        if constexpr (kHi) {
-          pa[1] = pack_bf16(s0[2], s0[3]);
-          pa[3] = pack_bf16(s1[2], s1[3]);
-          pr[0] = r0;
-          pr[2] = r2;
-          pr[1] = pack_bf16(s0[2] - bf_lo(pa[1]), s0[3] - bf_hi(pa[1]));
-          pr[3] = pack_bf16(s1[2] - bf_lo(pa[3]), s1[3] - bf_hi(pa[3]));
-        } else {
-          pa[1] = r0;
-          pa[3] = r2;
-        }
-      }
-
-      cp_wait<2 * C::kStages - 1>();
-      __syncwarp();
-      if constexpr (E4M3) {
-        // a thread reads DV / 8 columns of the four keys that its probabilities
-        // belong to; column tile n holds columns n, DV/8 + n, 2 DV/8 + n, ...
-        constexpr int kW = DV / 32;  // words of one key
-        uint32_t w[4][kW];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int key = 2 * t4 + (r & 1) + (r >> 1) * 8;
-          if constexpr (DV == 128) {
-            const uint4 x = lds128(vs + value_at<C::kRowV, true>(key, g));
-            w[r][0] = x.x;
-            w[r][1] = x.y;
-            w[r][kW > 2 ? 2 : 0] = x.z;
-            w[r][kW > 2 ? 3 : 0] = x.w;
-          } else {
-            const uint2 x = lds64(vs + value_at<C::kRowV, true>(key, g >> 1) + (g & 1) * 8);
-            w[r][0] = x.x;
-            w[r][1] = x.y;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < kW; ++j) {
-          const uint32_t a01 = __byte_perm(w[0][j], w[1][j], 0x5140),
-                         a23 = __byte_perm(w[0][j], w[1][j], 0x7362),
-                         b01 = __byte_perm(w[2][j], w[3][j], 0x5140),
-                         b23 = __byte_perm(w[2][j], w[3][j], 0x7362);
-          mma16816<true>(acc[4 * j], pa[0], pa[1], pa[2], pa[3], e4m3x2_to_f16x2(a01),
-                         e4m3x2_to_f16x2(b01));
-          mma16816<true>(acc[4 * j + 1], pa[0], pa[1], pa[2], pa[3], e4m3x2_to_f16x2_hi(a01),
-                         e4m3x2_to_f16x2_hi(b01));
-          mma16816<true>(acc[4 * j + 2], pa[0], pa[1], pa[2], pa[3], e4m3x2_to_f16x2(a23),
-                         e4m3x2_to_f16x2(b23));
-          mma16816<true>(acc[4 * j + 3], pa[0], pa[1], pa[2], pa[3], e4m3x2_to_f16x2_hi(a23),
-                         e4m3x2_to_f16x2_hi(b23));
-        }
-      } else {
-#pragma unroll
-        for (int n = 0; n < kNT; n += 2) {
-          // matrices: keys 0-7 and 8-15 of column chunk n, then of chunk n + 1
-          const uint4 x = ldsm_t(vs + value_at<C::kRowV, false>(lane & 15, n + (lane >> 4)));
-          mma16816<false>(acc[n], pa[0], pa[1], pa[2], pa[3], x.x, x.y);
-          mma16816<false>(acc[n + 1], pa[0], pa[1], pa[2], pa[3], x.z, x.w);
-          if constexpr (kHi) {
-            mma16816<false>(acc[n], pr[0], pr[1], pr[2], pr[3], x.x, x.y);
-            mma16816<false>(acc[n + 1], pr[0], pr[1], pr[2], pr[3], x.z, x.w);
-          }
-        }
-      }
-      __syncwarp();  // every lane has read the values
-      if (next < steps) copy_rows<C::kRowV, false, E4M3>(vs, vbase, voff, rows_next);
+      if (i < steps) copy_values(i, i, now);
       cp_commit();
-      stage = stage + 1 == C::kStages ? 0 : stage + 1;
     }
+  };
 
-    // ---- the warps join ----
-    l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 1);
-    l_lo += __shfl_xor_sync(0xffffffffu, l_lo, 2);
-    if constexpr (kHi) {
-      l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 1);
-      l_hi += __shfl_xor_sync(0xffffffffu, l_hi, 2);
-    }
-    cp_wait<0>();
-    __syncwarp();
-    if (t4 == 0) {
-      s_ml[warp][g] = make_float2(m_lo, l_lo);
-      if constexpr (kHi) s_ml[warp][g + 8] = make_float2(m_hi, l_hi);
-    }
-    {
-      float* part = reinterpret_cast<float*>(smem + warp * C::kWarpBytes);
+  begin_item(&s_items[0]);
+  fill_ring();
+  for (int cur = 0; s_items[cur].more; cur ^= 1) {
+      // Queries, as the second operand's registers, a tile of eight rows at a
+      // time: row g, the columns that a thread reads of a key row in one 16-byte
+      // load.  c[q][e]: the factor of the scores of row 8q + 2t + e.
+      uint32_t qr[kQT][kQ];
+      float c[kQT][2];
+      {
+        float unit = P.scale_log2;
+        if (E4M3 && P.cache.k.scale) unit *= __ldg(P.cache.k.scale + it->kvh);
+        const int rows = it->rows;
+        const uint16_t* qp = P.q + it->b * P.q_row + (int64_t)it->head * DQK;
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        const float a0 = kHi || E4M3 ? acc[n][0] : acc[n][0] + acc[n][2];
-        const float a1 = kHi || E4M3 ? acc[n][1] : acc[n][1] + acc[n][3];
+        for (int q = 0; q < kQT; ++q) {
+          const int row = 8 * q + g;
+#pragma unroll
+          for (int j = 0; j < DQK / 32; ++j) {
+            const int col = E4M3 ? 16 * key_chunk<C::kRowK>(j / 2, t4) + 8 * (j % 2)
+                                 : 8 * key_chunk<C::kRowK>(j, t4);
+            const uint4 w = row < rows ? __ldg(reinterpret_cast<const uint4*>(qp + row * DQK + col))
+                                       : make_uint4(0, 0, 0, 0);
+            qr[q][4 * j] = w.x, qr[q][4 * j + 1] = w.y;
+            qr[q][4 * j + 2] = w.z, qr[q][4 * j + 3] = w.w;
+          }
+          c[q][0] = c[q][1] = unit;
+          if constexpr (E4M3) {  // to fp16, by a power of two
+            float big = 0.f;
+#pragma unroll
+            for (int i = 0; i < kQ; ++i) big = max3(big, fabsf(bf_lo(qr[q][i])), fabsf(bf_hi(qr[q][i])));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+            big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+            // 2^e <= big < 2^(e+1); an infinite query makes its row's scores NaN
+            const int e = max((int)(__float_as_uint(big) >> 23) - 127, -100);
+            const float down = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23);
+            const float up = e > 127 ? __uint_as_float(0x7FC00000u)
+                                     : __uint_as_float((uint32_t)(127 + min(e, 126)) << 23);
+#pragma unroll
+            for (int i = 0; i < kQ; ++i)
+              qr[q][i] = pack_f16(bf_lo(qr[q][i]) * down, bf_hi(qr[q][i]) * down);
+            c[q][0] *= __shfl_sync(0xffffffffu, up, 8 * t4);  // of row 2t, and 2t + 1
+            c[q][1] *= __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
+          }
+        }
+      }
+
+      float acc[kQT][kVT][4];
+      float m[kQT][2], l[kQT][2];  // of rows 8q + 2t + e
+#pragma unroll
+      for (int q = 0; q < kQT; ++q) {
+#pragma unroll
+        for (int i = 0; i < kVT; ++i) acc[q][i][0] = acc[q][i][1] = acc[q][i][2] = acc[q][i][3] = 0.f;
+        m[q][0] = m[q][1] = -INFINITY;
+        l[q][0] = l[q][1] = 0.f;
+      }
+
+      int stage = 0, i = 0;
+      // the last steps are left for when the next item is known (found by one thread
+      // late enough that a piece claimed for it waits for little)
+#pragma unroll 1
+      for (int leg = 0; leg < 2; ++leg) {
+      const int leg_end = leg == 0 ? max(steps - 4, 0) : steps;
+#pragma unroll 1
+      for (; i < leg_end; ++i) {
+        const uint32_t ks = ring + stage * C::kBytes, vs = ks + C::kBytesK;
+        cp_wait<2 * C::kStages - 1>();
+        __syncwarp();
+        const uint32_t seen = s_rows[warp][stage];
+        // scores, [keys 16n + g, + 8][rows 8q + 2t, + 1]; the chunks of a key row that
+        // this thread reads are in two places, by the parity of j
+        constexpr bool kLines = C::kRowK % 128 == 0;  // else: chunks 64 bytes apart
+        const uint32_t k0 = ks + g * C::kRowK + ((key_chunk<C::kRowK>(0, t4) ^ swizzle<C::kRowK>(g)) << 4);
+        const uint32_t k_at[2] = {k0, kLines ? k0 ^ 16 : k0 + 64};
+        float s[kQT][kKT][4];
+#pragma unroll
+        for (int q = 0; q < kQT; ++q)
+#pragma unroll
+          for (int n = 0; n < kKT; ++n) s[q][n][0] = s[q][n][1] = s[q][n][2] = s[q][n][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < C::kRowK / 64; ++j) {
+#pragma unroll
+          for (int n = 0; n < kKT; ++n) {
+            const uint4 a = lds128(k_at[j & 1] + 16 * n * C::kRowK + 128 * (j >> 1));
+            const uint4 b = lds128(k_at[j & 1] + (16 * n + 8) * C::kRowK + 128 * (j >> 1));
+            if constexpr (E4M3) {
+              const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                const uint32_t a0 = f16x2_lo(aw[h]), a2 = f16x2_hi(aw[h]);
+                const uint32_t a1 = f16x2_lo(bw[h]), a3 = f16x2_hi(bw[h]);
+#pragma unroll
+                for (int q = 0; q < kQT; ++q)
+                  mma16816<true>(s[q][n], a0, a1, a2, a3, qr[q][8 * j + 2 * h], qr[q][8 * j + 2 * h + 1]);
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < kQT; ++q) {
+                mma16816<false>(s[q][n], a.x, b.x, a.y, b.y, qr[q][4 * j], qr[q][4 * j + 1]);
+                mma16816<false>(s[q][n], a.z, b.z, a.w, b.w, qr[q][4 * j + 2], qr[q][4 * j + 3]);
+              }
+            }
+          }
+        }
+        __syncwarp();  // every lane has read the keys
+        const int next = i + C::kStages;
+        const int now = page;
+        if (next < steps) {
+          page = page_of(next + 1);
+          copy_keys(next, stage, now);
+        }
+        cp_commit();
+
+        // running maximum and sum; keys that take no part are -inf.  (The factors c
+        // are positive: the largest score has the largest product.)
+        if (seen != kAllRows) {
+#pragma unroll
+          for (int n = 0; n < kKT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!((seen >> (16 * n + g + (e >> 1) * 8)) & 1))
+#pragma unroll
+                for (int q = 0; q < kQT; ++q) s[q][n][e] = -INFINITY;
+        }
+        float x[kQT][2];
+        bool rises = false;
+#pragma unroll
+        for (int q = 0; q < kQT; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            x[q][e] = fmaxf(s[q][0][e], s[q][0][2 + e]);
+#pragma unroll
+            for (int n = 1; n < kKT; ++n) x[q][e] = max3(x[q][e], s[q][n][e], s[q][n][2 + e]);
+            x[q][e] *= c[q][e];
+            rises |= x[q][e] > m[q][e];  // (of this thread's keys: enough to know)
+          }
+        if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+          for (int q = 0; q < kQT; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float y = x[q][e];
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 4));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
+              y = fmaxf(y, m[q][e]);
+              const float f = m[q][e] == -INFINITY ? 0.f : ex2(m[q][e] - y);
+              m[q][e] = y;
+              l[q][e] *= f;
+#pragma unroll
+              for (int v = 0; v < kVT; ++v) {
+                acc[q][v][e] *= f;
+                acc[q][v][2 + e] *= f;
+              }
+            }
+        }
+        // probabilities, as the second operand: transposed in pairs of bits
+        uint32_t p[kQT][kKT][2], rest[kQT][kKT][2];
+#pragma unroll
+        for (int q = 0; q < kQT; ++q) {
+          const float z0 = m[q][0] == -INFINITY ? 0.f : -m[q][0];
+          const float z1 = m[q][1] == -INFINITY ? 0.f : -m[q][1];
+#pragma unroll
+          for (int n = 0; n < kKT; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float p0 = ex2(fmaf(s[q][n][2 * h], c[q][0], z0));
+              const float p1 = ex2(fmaf(s[q][n][2 * h + 1], c[q][1], z1));
+              l[q][0] += p0;
+              l[q][1] += p1;
+              if constexpr (E4M3) {
+                p[q][n][h] = transpose8x8(pack_f16(p0, p1));
+              } else {
+                const uint32_t w = pack_bf16(p0, p1);
+                p[q][n][h] = transpose8x8(w);
+                rest[q][n][h] = transpose8x8(pack_bf16(p0 - bf_lo(w), p1 - bf_hi(w)));
+              }
+            }
+        }
+
+        cp_wait<2 * C::kStages - 1>();
+        __syncwarp();
         if constexpr (E4M3) {
-          part[g * DV + (2 * t4) * kNT + n] = a0;
-          part[g * DV + (2 * t4 + 1) * kNT + n] = a1;
-          if constexpr (kHi) {
-            part[(g + 8) * DV + (2 * t4) * kNT + n] = acc[n][2];
-            part[(g + 8) * DV + (2 * t4 + 1) * kNT + n] = acc[n][3];
+          // a thread reads DV / 8 columns (DV/8 g ..) of the keys 2t, 2t + 1, 2t + 8
+          // and 2t + 9; column tile v holds columns DV/8 g + 2v (row g) and
+          // + 2v + 1 (row g + 8).
+          const uint32_t v0 = vs + 2 * t4 * C::kRowV +
+                              (DV == 128 ? (g ^ swizzle<C::kRowV>(2 * t4)) << 4
+                                         : (((g >> 1) ^ swizzle<C::kRowV>(2 * t4)) << 4) + (g & 1) * 8);
+          // of rows 2t and 2t + 1 (and their likes, eight rows further)
+          const uint32_t v_at[2] = {v0, (DV == 128 ? v0 ^ 16 : v0) + C::kRowV};
+#pragma unroll
+          for (int n = 0; n < kKT; ++n) {
+            uint32_t w[4][DV / 32];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t at = v_at[r & 1] + (16 * n + 8 * (r >> 1)) * C::kRowV;
+              if constexpr (DV == 128) {
+                const uint4 y = lds128(at);
+                w[r][0] = y.x, w[r][1] = y.y, w[r][DV / 32 - 2] = y.z, w[r][DV / 32 - 1] = y.w;
+              } else {
+                const uint2 y = lds64(at);
+                w[r][0] = y.x, w[r][1] = y.y;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < DV / 32; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t lo = __byte_perm(w[0][j], w[1][j], h ? 0x7362 : 0x5140);
+                const uint32_t hi = __byte_perm(w[2][j], w[3][j], h ? 0x7362 : 0x5140);
+                const uint32_t a0 = f16x2_lo(lo), a1 = f16x2_hi(lo), a2 = f16x2_lo(hi), a3 = f16x2_hi(hi);
+#pragma unroll
+                for (int q = 0; q < kQT; ++q)
+                  mma16816<true>(acc[q][2 * j + h], a0, a1, a2, a3, p[q][n][0], p[q][n][1]);
+              }
           }
         } else {
-          *reinterpret_cast<float2*>(part + g * DV + 8 * n + 2 * t4) = make_float2(a0, a1);
-          if constexpr (kHi)
-            *reinterpret_cast<float2*>(part + (g + 8) * DV + 8 * n + 2 * t4) =
-                make_float2(acc[n][2], acc[n][3]);
-        }
-      }
-    }
-    __syncthreads();
-
-    const ItemParts parts = item_parts(item_at, rg.tiles, total, n_cta);
-    const int my_part = (int)blockIdx.x - parts.cta0;
-    const int my_slot = parts.slot(my_part);
-    const float v_scale = E4M3 && P.cache.v.scale ? __ldg(P.cache.v.scale + kvh) : 1.f;
-    for (int e = tid; e < rows * DV / 4; e += kThreads) {
-      const int row = e / (DV / 4), c = (e - row * (DV / 4)) * 4;
-      float m = s_ml[0][row].x;
+          // matrices: column chunks 2v and 2v + 1 of keys 0 - 7, then of keys 8 - 15
+          const int row = (lane & 7) + ((lane >> 4) << 3);
+          const uint32_t v_row = vs + row * C::kRowV, v_swz = (((lane >> 3) & 1) ^ (lane & 7)) << 4;
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, s_ml[w][row].x);
-      const float z = m == -INFINITY ? 0.f : m;
-      float l = 0.f;
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int v = 0; v < kVT; ++v) {
+            const uint4 a = ldsm_t(v_row + (v_swz ^ ((2 * v & 6) << 4)) + (v >> 2) * 128);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = s_ml[w][row];
-        const float f = ex2(ml.x - z);
-        const float4 x = *reinterpret_cast<const float4*>(smem + w * C::kWarpBytes +
-                                                          (row * DV + c) * 4);
-        l += ml.y * f;
-        s.x += x.x * f;
-        s.y += x.y * f;
-        s.z += x.z * f;
-        s.w += x.w * f;
-      }
-      if (parts.count == 1) {
-        const float inv = l == 0.f ? 0.f : v_scale / l;
-        store_row4<DV>(P, b, head, row, c, s, inv);
-        if (c == 0 && P.lse) P.lse[(int64_t)b * P.Hq + head + row] = lse_of(m, l);
-      } else {
-        __stcg(reinterpret_cast<float4*>(
-                   P.acc + ((int64_t)my_slot * kMaxTileRows + row) * DV + c),
-               s);
-        if (c == 0)
-          __stcg(reinterpret_cast<float2*>(P.ml) + my_slot * kMaxTileRows + row,
-                 make_float2(m, l));
-      }
-    }
-    __syncthreads();  // the rings are free again; the part is written
-
-    if (parts.count > 1) {
-      // last of the group's parts joins the group; last of the groups the item
-      const int grp = my_part / kJoinParts;
-      const int n_grp = (parts.count + kJoinParts - 1) / kJoinParts;
-      const Joined group{parts, grp * kJoinParts, min((grp + 1) * kJoinParts, parts.count), 1};
-      auto arrive_last = [&](int* counter, int expect) {
-        if (tid == 0) {
-          __threadfence();
-          const int last = atomicAdd(counter, 1) == expect - 1;
-          if (last) *counter = 0;  // ready for the next call
-          __threadfence();
-          s_last = last;
+            for (int q = 0; q < kQT; ++q) {
+              mma16816<false>(acc[q][v], a.x, a.y, a.z, a.w, p[q][0][0], p[q][0][1]);
+              mma16816<false>(acc[q][v], a.x, a.y, a.z, a.w, rest[q][0][0], rest[q][0][1]);
+            }
+          }
         }
-        __syncthreads();
-        const bool last = s_last != 0;
-        __syncthreads();
-        return last;
+        __syncwarp();  // every lane has read the values
+        if (next < steps) copy_values(next, stage, now);
+        cp_commit();
+        stage = stage + 1 == C::kStages ? 0 : stage + 1;
+      }
+
+      if (leg == 0 && tid == 0)
+        next_item<kStep, kKeys>(P, s_line, s_before, kThreads, chunk, s_walk, &s_items[cur ^ 1]);
+      }
+
+      // ---- the warps join: the upper half's O to shared memory, the lower half
+      // adds its own, then all threads the halves' ----
+#pragma unroll
+      for (int q = 0; q < kQT; ++q)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 4);
+          l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 8);
+          l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 16);
+          if (g == 0) s_ml[warp][8 * q + 2 * t4 + e] = make_float2(m[q][e], l[q][e]);
+        }
+      float* const part = joined + warp % C::kHalf * (C::kJoin / 4);
+      auto place = [&](int q, int v, int e) {
+        const int col = E4M3 ? DV / 8 * g + 2 * v + (e >> 1) : 16 * v + g + (e >> 1) * 8;
+        return part + (8 * q + 2 * t4 + (e & 1)) * C::kPitch + col;
       };
-      if (arrive_last(P.counters + group.slot(0), group.count())) {
-        join_parts<DV, R>(P, group, rows, n_grp == 1 ? -1 : group.slot(0), b, head, v_scale,
-                          s_wgt, s_tot);
-        __syncthreads();
-        if (n_grp > 1 && arrive_last(P.counters + kDecodeSlots + parts.slot0, n_grp)) {
-          const Joined groups{parts, 0, parts.count, kJoinParts};
-          join_parts<DV, R>(P, groups, rows, -1, b, head, v_scale, s_wgt, s_tot);
-          __syncthreads();
+      if (warp >= C::kHalf) {
+#pragma unroll
+        for (int q = 0; q < kQT; ++q)
+#pragma unroll
+          for (int v = 0; v < kVT; ++v)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) *place(q, v, e) = acc[q][v][e];
+      }
+      __syncthreads();  // (the next item is known, too)
+      const Item* const done = it;
+      begin_item(&s_items[cur ^ 1]);
+      if (warp < C::kHalf) {
+#pragma unroll
+        for (int q = 0; q < kQT; ++q) {
+          float f[2], h[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = 8 * q + 2 * t4 + e;
+            const float2 y = s_ml[warp + C::kHalf][row];
+            const float top = fmaxf(m[q][e], y.x);
+            const float z = top == -INFINITY ? 0.f : top;
+            f[e] = ex2(m[q][e] - z);
+            h[e] = ex2(y.x - z);
+            if (g == 0) s_ml2[warp][row] = make_float2(top, l[q][e] * f[e] + y.y * h[e]);
+          }
+#pragma unroll
+          for (int v = 0; v < kVT; ++v)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float* at = place(q, v, e);
+              *at = acc[q][v][e] * f[e & 1] + *at * h[e & 1];
+            }
         }
       }
+      fill_ring();  // of the next item
+      __syncthreads();
+
+      const int b = done->b, head = done->head, rows = done->rows;
+      const ItemParts parts = done->parts;
+      const int my_part = done->my_part;
+      const int my_slot = parts.slot(my_part);
+      const float v_scale = E4M3 && P.cache.v.scale ? __ldg(P.cache.v.scale + done->kvh) : 1.f;
+      for (int e = tid; e < rows * DV / 4; e += kThreads) {
+        const int row = e / (DV / 4), col = (e - row * (DV / 4)) * 4;
+        float top = s_ml2[0][row].x;
+#pragma unroll
+        for (int w = 1; w < C::kHalf; ++w) top = fmaxf(top, s_ml2[w][row].x);
+        const float z = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::kHalf; ++w) {
+          const float2 ml = s_ml2[w][row];
+          const float f = ex2(ml.x - z);
+          const float4 y = *reinterpret_cast<const float4*>(joined + w * (C::kJoin / 4) +
+                                                            row * C::kPitch + col);
+          sum += ml.y * f;
+          o.x += y.x * f;
+          o.y += y.y * f;
+          o.z += y.z * f;
+          o.w += y.w * f;
+        }
+        if (parts.count == 1) {
+          store_row4<DV>(P, b, head, row, col, o, sum == 0.f ? 0.f : v_scale / sum);
+          if (col == 0 && P.lse) P.lse[(int64_t)b * P.Hq + head + row] = lse_of(top, sum);
+        } else {
+          __stcg(reinterpret_cast<float4*>(
+                     P.acc + ((int64_t)my_slot * kMaxTileRows + row) * DV + col), o);
+          if (col == 0)
+            __stcg(reinterpret_cast<float2*>(P.ml) + my_slot * kMaxTileRows + row,
+                   make_float2(top, sum));
+        }
+      }
+      __syncthreads();  // the parts are read, and this one is written
+
+      // The last of kJoinParts parts joins them, the last of as many of such groups
+      // joins those, and so on to the whole item.
+      int stride = 1;  // parts of a group that is joined already
+#pragma unroll 1
+      for (int level = 0; stride < parts.count; ++level, stride *= kJoinParts) {
+        const int begin = my_part / (stride * kJoinParts) * (stride * kJoinParts);
+        const Joined j{parts, begin, min(begin + stride * kJoinParts, parts.count), stride};
+        if (tid == 0) {
+          int* counter = P.counters + level * kDecodeSlots + j.slot(0);
+          s_last = arrive(counter) == j.count() - 1;
+          if (s_last) *counter = 0;  // ready for the next call
+        }
+        __syncthreads();
+        if (!s_last) break;
+        join_parts<DV, R, kThreads>(P, j, rows, j.begin == 0 && j.end == parts.count ? -1 : j.slot(0),
+                                    b, head, v_scale, reinterpret_cast<float2*>(joined));
+        __syncthreads();
+      }
+    }
+  // the last CTA leaves the claims at zero
+  if (tid == 0 && s_line.pieces > s_line.n) {
+    __threadfence();
+    if (atomicAdd(&P.header->done, 1) == s_line.n - 1) {
+      P.header->claimed = 0;
+      P.header->done = 0;
     }
   }
 }
 
-template <int DQK, int DV, bool E4M3, int R>
-cudaError_t launch_typed(const DecodeLaunch& L, const DecodeParams& P, long long most) {
-  auto* kernel = decode_kernel<DQK, DV, E4M3, R>;
+template <int DQK, int DV, bool E4M3, int R, bool IN_PAGE>
+cudaError_t launch_typed(const DecodeLaunch& L, const DecodeParams& P) {
+  auto* kernel = decode_kernel<DQK, DV, E4M3, R, IN_PAGE>;
   using C = Cfg<DQK, DV, E4M3, R>;
-  constexpr int kSmem = C::kSmem;
-  const int grid = (int)std::min<long long>(
-      std::min(kMaxDecodeCtas, C::kCtasPerSm * L.num_sms), most);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  // as many CTAs as fit on the SMs, but not more than there can be tiles
+  constexpr long long kKeys = C::kTile;
+  const long long keys = std::min<long long>(
+      (long long)L.cache.max_pages * L.cache.page_size,
+      L.window >= 0 ? (long long)L.window + 1 + C::kStep : INT32_MAX);
+  const long long most = (long long)L.B * P.items_per_seq * ((keys + kKeys - 1) / kKeys);
+  const int grid =
+      (int)std::min<long long>(std::min(kMaxDecodeCtas, 2 * L.num_sms), most);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, kThreads, kSmem, L.stream>>>(P);
+  kernel<<<grid, C::kThreads, C::kSmem, L.stream>>>(P);
   return cudaGetLastError();
 }
 
+template <int DQK, int DV, bool E4M3, int R>
+cudaError_t launch_rows(const DecodeLaunch& L, const DecodeParams& P) {
+  return L.cache.page_size % Cfg<DQK, DV, E4M3, R>::kStep == 0
+             ? launch_typed<DQK, DV, E4M3, R, true>(L, P)
+             : launch_typed<DQK, DV, E4M3, R, false>(L, P);
+}
+
 template <int DQK, int DV>
-cudaError_t launch_dims(const DecodeLaunch& L, const DecodeParams& P, long long most) {
+cudaError_t launch_dims(const DecodeLaunch& L, const DecodeParams& P) {
   const bool wide = L.tile_rows > 8;
   if (L.cache.e4m3)
-    return wide ? launch_typed<DQK, DV, true, 16>(L, P, most) : launch_typed<DQK, DV, true, 8>(L, P, most);
-  return wide ? launch_typed<DQK, DV, false, 16>(L, P, most) : launch_typed<DQK, DV, false, 8>(L, P, most);
+    return wide ? launch_rows<DQK, DV, true, 16>(L, P) : launch_rows<DQK, DV, true, 8>(L, P);
+  return wide ? launch_rows<DQK, DV, false, 16>(L, P) : launch_rows<DQK, DV, false, 8>(L, P);
 }
 
 }  // namespace
@@ -782,13 +951,9 @@ cudaError_t launch_decode(const DecodeLaunch& L) {
   P.ml = L.ml;
   P.acc = L.acc;
   P.status = L.status;
-  // as many CTAs as fit on the SMs, but not more than there can be tiles
-  const long long keys = std::min<long long>((long long)L.cache.max_pages * L.cache.page_size,
-                                             L.window >= 0 ? (long long)L.window + 1 + kSub : INT32_MAX);
-  const long long most = (long long)L.B * P.items_per_seq * ((keys + kKeys - 1) / kKeys + 1);
-  if (L.dqk == 64) return launch_dims<64, 64>(L, P, most);
-  if (L.dqk == 128) return launch_dims<128, 128>(L, P, most);
-  if (L.dqk == 192) return launch_dims<192, 128>(L, P, most);
+  if (L.dqk == 64) return launch_dims<64, 64>(L, P);
+  if (L.dqk == 128) return launch_dims<128, 128>(L, P);
+  if (L.dqk == 192) return launch_dims<192, 128>(L, P);
   return cudaErrorInvalidValue;
 }
 

@@ -3,6 +3,7 @@
 // decode workspace and the launches.  Host code; the arithmetic is in
 // attn_rope.cu and attn_decode.cu.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -58,10 +59,11 @@ bool cache_side(const void* base, const float* scale, long long page, long long 
   const long long unit = 16 / elt;
   if (base == nullptr || !aligned(base, 16) || !aligned(scale, 4)) return false;
   if (page < 0 || token < 0 || head < 0 || page % unit || token % unit || head % unit) return false;
+  if (page / unit > UINT32_MAX || token / unit > UINT32_MAX) return false;
   out->base = static_cast<char*>(const_cast<void*>(base));
   out->scale = scale;
-  out->page = page * elt;
-  out->token = token * elt;
+  out->page = (uint32_t)(page / unit);
+  out->token = (uint32_t)(token / unit);
   out->head = head * elt;
   return true;
 }
@@ -97,11 +99,14 @@ int check_cache(const attn_paged_cache* c, const int* table, int max_pages, long
   return ATTN_OK;
 }
 
+// SMs of the current device (asked once for each).
 int sm_count() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  if (dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -184,6 +189,8 @@ int attn_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int
   L.nseq = B;
   L.pos0 = pos0;
   L.d = d;
+  L.num_sms = sm_count();
+  if (L.num_sms <= 0) return ATTN_ERR_CUDA;
   L.stream = static_cast<cudaStream_t>(stream);
   return cuda_err(launch_rope(L));
 }
@@ -232,6 +239,8 @@ int attn_cache_append(const attn_paged_cache* cache, const int* block_table, int
   L.per_seq = T / B;
   L.dqk = cache->dqk;
   L.dv = cache->dv;
+  L.num_sms = sm_count();
+  if (L.num_sms <= 0) return ATTN_ERR_CUDA;
   L.status = cache_status_ptr();
   if (!L.status) return ATTN_ERR_CUDA;
   L.stream = static_cast<cudaStream_t>(stream);
@@ -281,7 +290,7 @@ int attn_decode(const attn_paged_cache* cache, const int* block_table, int max_p
   L.window = window_left;
   L.scale_log2 = scale * kLog2e;
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  L.header = reinterpret_cast<const uint32_t*>(base);
+  L.header = reinterpret_cast<DecodeHeader*>(base);
   L.counters = reinterpret_cast<int*>(base + 256);
   base += 256 + ((kDecodeCounterBytes + 255) & ~size_t(255));
   L.ml = reinterpret_cast<float*>(base);

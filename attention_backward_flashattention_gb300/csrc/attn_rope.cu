@@ -12,10 +12,14 @@
 // output's type once.
 //
 // Bound: memory.  Each element is read once and written once (2 + 2 bytes; 2 + 1
-// into an e4m3 cache), against three flops.  So a block takes a few whole token rows,
-// computes each (position, pair) angle once for all heads into shared memory,
-// and every thread moves units of 16 columns — two 16-byte loads and stores — two
-// units at a time, the first loads issued before the angles are computed.
+// into an e4m3 cache), against three flops.  What is left to do is to keep the
+// index work and the angles off the path:
+//   * a thread moves units of 16 columns, two 16-byte loads and stores each, and
+//     keeps its unit (head, columns, destination) from token to token of its
+//     block, so the divisions that find it are paid once;
+//   * a block takes several token rows where there are many, computes each
+//     (position, pair) angle once for all heads into shared memory, and has its
+//     first loads, two units a thread, on their way meanwhile.
 #include <algorithm>
 #include <cstring>
 
@@ -34,16 +38,26 @@ int* cache_status_ptr() {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnitsInFlight = 2;     // units a thread loads before it uses the first
+constexpr int kMostThreads = 512;
 constexpr int kMaxTokens = 32;        // token rows of one block at most
 constexpr int kMaxAngles = 2048;      // (token, pair) angles of one block at most
+constexpr int kRounds = 8;            // tokens a thread walks over, where there are many
 
-// Token rows of a block: enough units that each thread has kUnitsInFlight.
-int tokens_per_block(int units_per_token, int dim) {
-  int n = kThreads * kUnitsInFlight / std::max(units_per_token, 1);
-  if (dim > 0) n = std::min(n, kMaxAngles / (dim / 2));
-  return std::max(1, std::min(n, kMaxTokens));
+// Shape of the blocks over `rows` token rows of `units` units each: `side`
+// token rows side by side (about 256 threads, or one row of up to 512 units), and
+// up to kRounds of them one after the other as long as every SM has some blocks.
+struct BlockShape {
+  int threads, side, tokens, blocks;
+};
+BlockShape block_shape(int rows, int units, int dim, int sms) {
+  BlockShape s;
+  const int most = dim > 0 ? std::min(kMaxTokens, kMaxAngles / (dim / 2)) : kMaxTokens;
+  s.side = std::min(std::max(1, 256 / units), most);
+  s.threads = std::min(kMostThreads, cdiv(s.side * units, 32) * 32);
+  const int rounds = std::max(1, std::min(kRounds, rows / (s.side * sms * 8)));
+  s.tokens = std::min(s.side * rounds, most);
+  s.blocks = cdiv(rows, s.tokens);
+  return s;
 }
 
 // Sixteen columns of a head, in two chunks of eight: columns ca .. ca + 7 and
@@ -88,7 +102,7 @@ __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
 __device__ __forceinline__ void fill_angles(float2* sc, const int* pos, int tokens,
                                             const Rotation& rot, bool inverse) {
   const int pairs = rot.dim >> 1, units = rot.dim >> 4;
-  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+  for (int i = threadIdx.x; i < tokens * pairs; i += blockDim.x) {
     const int t = i / pairs, pair = i - t * pairs;
     const long long p = inverse ? -(long long)pos[t] : (long long)pos[t];
     const unsigned long long turn = (unsigned long long)p * __ldg(rot.rates + pair);
@@ -147,23 +161,21 @@ struct RopeParams {
 
 // ----------------------------------------------------------------------------
 // attn_rope: blocks 0 .. t[0].blocks - 1 take the queries, the others the keys.
-//
-// Measured (GB300): see the rates at the launch below.
 // ----------------------------------------------------------------------------
 template <int D, typename Offsets>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kMostThreads, 2)
 rope_kernel(const __grid_constant__ RopeParams P, const __grid_constant__ Offsets off) {
   __shared__ int pos[kMaxTokens];
   __shared__ __align__(16) float2 sc[kMaxAngles];
   constexpr int kUnits = D / 16;
   const int which = blockIdx.x < P.t[0].blocks ? 0 : 1;
   const RopeTensor& X = P.t[which];
-  const int row0 = (blockIdx.x - (which ? P.t[0].blocks : 0)) * X.tokens_per_block;
-  const int tokens = min(X.tokens_per_block, X.rows - row0);
-  const int per_token = X.H * kUnits;
-  const int n = tokens * per_token;
-  const uint16_t* x = static_cast<const uint16_t*>(X.x);
-  uint16_t* y = static_cast<uint16_t*>(X.y);
+  const int row0 = (blockIdx.x - (which ? P.t[0].blocks : 0)) * X.tokens;
+  const int tokens = min(X.tokens, X.rows - row0);
+  const int units = X.H * kUnits;  // of a token row
+  const int side = X.side;
+  const uint16_t* x = static_cast<const uint16_t*>(X.x) + row0 * X.x_row;
+  uint16_t* y = static_cast<uint16_t*>(X.y) + row0 * X.y_row;
 
   if (threadIdx.x < tokens) {
     const int r = row0 + threadIdx.x;
@@ -177,50 +189,62 @@ rope_kernel(const __grid_constant__ RopeParams P, const __grid_constant__ Offset
       pos[threadIdx.x] = P.pos0 + X.shift + r % X.T;
     }
   }
-  bool ready = false;
-  for (int base = threadIdx.x; base - (int)threadIdx.x < n; base += kThreads * kUnitsInFlight) {
-    Unit w[kUnitsInFlight];
-    int64_t ya[kUnitsInFlight], yb[kUnitsInFlight];
-    int tok[kUnitsInFlight], unit[kUnitsInFlight];
+
+  // this thread's unit, and the token rows t0, t0 + side, ... of it
+  const int t0 = threadIdx.x / units;
+  int at = threadIdx.x - t0 * units;
+  int unit = 0, ca = 0, cb = 0;  // columns within a row
+  auto take = [&]() {
+    const int head = at / kUnits;
+    unit = at - head * kUnits;
+    unit_columns(P.rot, unit, ca, cb);
+    ca += head * D;
+    cb += head * D;
+  };
+  Unit w[2];
+  auto load = [&](int t) {
 #pragma unroll
-    for (int j = 0; j < kUnitsInFlight; ++j) {
-      const int item = base + j * kThreads;
-      tok[j] = -1;
-      if (item < n) {
-        tok[j] = item / per_token;
-        const int rem = item - tok[j] * per_token;
-        const int head = rem / kUnits;
-        unit[j] = rem - head * kUnits;
-        int ca, cb;
-        unit_columns(P.rot, unit[j], ca, cb);
-        const int64_t xr = (int64_t)(row0 + tok[j]) * X.x_row + head * D;
-        const int64_t yr = (int64_t)(row0 + tok[j]) * X.y_row + head * D;
-        ya[j] = yr + ca;
-        yb[j] = yr + cb;
-        w[j].a = *reinterpret_cast<const uint4*>(x + xr + ca);
-        w[j].b = *reinterpret_cast<const uint4*>(x + xr + cb);
-      }
+    for (int j = 0; j < 2; ++j) {
+      if (t + j * side >= tokens) break;
+      const uint16_t* row = x + (t + j * side) * X.x_row;
+      w[j].a = *reinterpret_cast<const uint4*>(row + ca);
+      w[j].b = *reinterpret_cast<const uint4*>(row + cb);
     }
-    if (!ready) {  // the same in every thread: the first loads are on their way
-      __syncthreads();
-      fill_angles(sc, pos, tokens, P.rot, P.inverse != 0);
-      __syncthreads();
-      ready = true;
-    }
+  };
+  bool busy = t0 < min(side, tokens) && at < units;
+  int t = t0;
+  if (busy) {
+    take();
+    load(t);
+  }
+  __syncthreads();
+  fill_angles(sc, pos, tokens, P.rot, P.inverse != 0);
+  __syncthreads();
+  while (busy) {
 #pragma unroll
-    for (int j = 0; j < kUnitsInFlight; ++j) {
-      if (tok[j] < 0) continue;
-      if (unit[j] < (P.rot.dim >> 4)) {
+    for (int j = 0; j < 2; ++j) {
+      const int tj = t + j * side;
+      if (tj >= tokens) break;
+      if (unit < (P.rot.dim >> 4)) {
         float a[8], b[8];
         unpack8(w[j].a, a);
         unpack8(w[j].b, b);
-        turn_unit(sc, tok[j], unit[j], P.rot, a, b);
+        turn_unit(sc, tj, unit, P.rot, a, b);
         w[j].a = pack8(a);
         w[j].b = pack8(b);
       }
-      *reinterpret_cast<uint4*>(y + ya[j]) = w[j].a;
-      *reinterpret_cast<uint4*>(y + yb[j]) = w[j].b;
+      uint16_t* row = y + tj * X.y_row;
+      *reinterpret_cast<uint4*>(row + ca) = w[j].a;
+      *reinterpret_cast<uint4*>(row + cb) = w[j].b;
     }
+    t += 2 * side;
+    if (t >= tokens) {  // the next unit, in rows of more units than threads
+      at += blockDim.x;
+      busy = at < units && units > (int)blockDim.x;
+      t = t0;
+      if (busy) take();
+    }
+    if (busy) load(t);
   }
 }
 
@@ -232,7 +256,7 @@ struct AppendParams {
   const uint16_t *k, *v, *q;
   uint16_t* q_out;
   int64_t k_row, v_row, q_row, q_out_row;
-  int B, T, Hq, per_seq, tokens_per_block;
+  int B, T, Hq, per_seq, tokens, side;
   Rotation rot;
   int* status;
 };
@@ -254,18 +278,17 @@ __device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
 }
 
 template <int DQK, int DV, bool E4M3, typename Offsets>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kMostThreads, 2)
 append_kernel(const __grid_constant__ AppendParams P, const __grid_constant__ Offsets off) {
   __shared__ int pos[kMaxTokens];
   __shared__ int64_t koff[kMaxTokens], voff[kMaxTokens];  // byte offset of the slot; -1: none
   __shared__ __align__(16) float2 sc[kMaxAngles];
   constexpr int kUnits = DQK / 16, kUnitsV = DV / 16;
-  constexpr int kBytes = E4M3 ? 1 : 2;
-  const int row0 = blockIdx.x * P.tokens_per_block;
-  const int tokens = min(P.tokens_per_block, P.T - row0);
+  const int row0 = blockIdx.x * P.tokens;
+  const int tokens = min(P.tokens, P.T - row0);
   const int n_q = P.Hq * kUnits, n_k = P.cache.heads * kUnits, n_v = P.cache.heads * kUnitsV;
-  const int per_token = n_q + n_k + n_v;
-  const int n = tokens * per_token;
+  const int units = n_q + n_k + n_v;  // of a token
+  const int side = P.side;
 
   if (threadIdx.x < tokens) {
     const int r = row0 + threadIdx.x;
@@ -284,8 +307,9 @@ append_kernel(const __grid_constant__ AppendParams P, const __grid_constant__ Of
       int page = -1;
       if (slot < P.cache.max_pages) page = P.cache.table[s * P.cache.table_stride + slot];
       if (page_in(P.cache, page)) {
-        ko = token_at(P.cache, P.cache.k, page, p);
-        vo = token_at(P.cache, P.cache.v, page, p);
+        const int in = p - slot * P.cache.page_size;
+        ko = token_at(P.cache.k, page, in);
+        vo = token_at(P.cache.v, page, in);
       } else {
         atomicCAS(P.status, 0, kStatusBadPage);
       }
@@ -294,105 +318,132 @@ append_kernel(const __grid_constant__ AppendParams P, const __grid_constant__ Of
     koff[threadIdx.x] = ko;
     voff[threadIdx.x] = vo;
   }
-  bool ready = false;
-  for (int base = threadIdx.x; base - (int)threadIdx.x < n; base += kThreads * kUnitsInFlight) {
-    Unit w[kUnitsInFlight];
-    int tok[kUnitsInFlight], head[kUnitsInFlight], unit[kUnitsInFlight], what[kUnitsInFlight];
-    int ca[kUnitsInFlight], cb[kUnitsInFlight];
-#pragma unroll
-    for (int j = 0; j < kUnitsInFlight; ++j) {
-      const int item = base + j * kThreads;
-      tok[j] = -1;
-      if (item < n) {
-        tok[j] = item / per_token;
-        int rem = item - tok[j] * per_token;
-        const uint16_t* x;
-        if (rem < n_q + n_k) {
-          what[j] = rem < n_q ? 0 : 1;
-          if (what[j]) rem -= n_q;
-          head[j] = rem / kUnits;
-          unit[j] = rem - head[j] * kUnits;
-          unit_columns(P.rot, unit[j], ca[j], cb[j]);
-          x = (what[j] ? P.k + (row0 + tok[j]) * P.k_row : P.q + (row0 + tok[j]) * P.q_row) +
-              head[j] * DQK;
-        } else {
-          what[j] = 2;
-          rem -= n_q + n_k;
-          head[j] = rem / kUnitsV;
-          unit[j] = rem - head[j] * kUnitsV;
-          ca[j] = unit[j] * 16;
-          cb[j] = ca[j] + 8;
-          x = P.v + (row0 + tok[j]) * P.v_row + head[j] * DV;
-        }
-        w[j].a = *reinterpret_cast<const uint4*>(x + ca[j]);
-        w[j].b = *reinterpret_cast<const uint4*>(x + cb[j]);
+  // this thread's unit: where it is read, where it goes, whether it turns
+  const int t0 = threadIdx.x / units;
+  int at = threadIdx.x - t0 * units;
+  int unit = 0, ca = 0, cb = 0;
+  bool turns = false;
+  const uint16_t* x = nullptr;
+  int64_t x_row = 0;
+  char* y = nullptr;                    // q_out (rows y_row bytes apart) or one side of the cache
+  const int64_t* slots = nullptr;       // null: q_out
+  float scale = 1.f;
+  auto take = [&]() {
+    int rem = at;
+    if (rem < n_q + n_k) {
+      const bool key = rem >= n_q;
+      if (key) rem -= n_q;
+      const int head = rem / kUnits;
+      unit = rem - head * kUnits;
+      turns = unit < (P.rot.dim >> 4);
+      unit_columns(P.rot, unit, ca, cb);
+      x_row = key ? P.k_row : P.q_row;
+      x = (key ? P.k : P.q) + row0 * x_row + head * DQK;
+      if (key) {
+        y = P.cache.k.base + head * P.cache.k.head;
+        slots = koff;
+        if (E4M3 && P.cache.k.scale) scale = __ldg(P.cache.k.scale + head);
+      } else {
+        y = reinterpret_cast<char*>(P.q_out + row0 * P.q_out_row + head * DQK);
+        slots = nullptr;
       }
+    } else {
+      rem -= n_q + n_k;
+      const int head = rem / kUnitsV;
+      unit = rem - head * kUnitsV;
+      turns = false;
+      ca = unit * 16;
+      cb = ca + 8;
+      x_row = P.v_row;
+      x = P.v + row0 * x_row + head * DV;
+      y = P.cache.v.base + head * P.cache.v.head;
+      slots = voff;
+      scale = E4M3 && P.cache.v.scale ? __ldg(P.cache.v.scale + head) : 1.f;
     }
-    if (!ready) {  // the same in every thread: the first loads are on their way
-      __syncthreads();
-      fill_angles(sc, pos, tokens, P.rot, false);
-      __syncthreads();
-      ready = true;
-    }
+  };
+  Unit w[2];
+  auto load = [&](int t) {
 #pragma unroll
-    for (int j = 0; j < kUnitsInFlight; ++j) {
-      if (tok[j] < 0 || pos[tok[j]] < 0) continue;
-      const bool turns = what[j] < 2 && unit[j] < (P.rot.dim >> 4);
+    for (int j = 0; j < 2; ++j) {
+      if (t + j * side >= tokens) break;
+      const uint16_t* row = x + (t + j * side) * x_row;
+      w[j].a = *reinterpret_cast<const uint4*>(row + ca);
+      w[j].b = *reinterpret_cast<const uint4*>(row + cb);
+    }
+  };
+  bool busy = t0 < min(side, tokens) && at < units;
+  int t = t0;
+  if (busy) {
+    take();
+    load(t);
+  }
+  __syncthreads();
+  fill_angles(sc, pos, tokens, P.rot, false);
+  __syncthreads();
+  while (busy) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int tj = t + j * side;
+      if (tj >= tokens) break;
+      if (pos[tj] < 0) continue;
+      const bool eight = E4M3 && slots != nullptr;
       float a[8], b[8];
-      if (turns || (E4M3 && what[j] > 0)) {
+      if (turns || eight) {
         unpack8(w[j].a, a);
         unpack8(w[j].b, b);
       }
-      if (turns) turn_unit(sc, tok[j], unit[j], P.rot, a, b);
-      if (what[j] == 0) {
-        uint16_t* y = P.q_out + (row0 + tok[j]) * P.q_out_row + head[j] * DQK;
-        if (turns) {
+      if (turns) {
+        turn_unit(sc, tj, unit, P.rot, a, b);
+        if (!eight) {
           w[j].a = pack8(a);
           w[j].b = pack8(b);
         }
-        *reinterpret_cast<uint4*>(y + ca[j]) = w[j].a;
-        *reinterpret_cast<uint4*>(y + cb[j]) = w[j].b;
+      }
+      char* row;
+      if (slots != nullptr) {
+        if (slots[tj] < 0) continue;
+        row = y + slots[tj];
       } else {
-        const CacheSide& side = what[j] == 1 ? P.cache.k : P.cache.v;
-        const int64_t at = what[j] == 1 ? koff[tok[j]] : voff[tok[j]];
-        if (at < 0) continue;
-        char* y = side.base + at + head[j] * side.head;
-        if constexpr (E4M3) {
-          const float scale = side.scale ? __ldg(side.scale + head[j]) : 1.f;
-          *reinterpret_cast<uint2*>(y + ca[j] * kBytes) = quantise8(a, scale);
-          *reinterpret_cast<uint2*>(y + cb[j] * kBytes) = quantise8(b, scale);
-        } else {
-          if (turns) {
-            w[j].a = pack8(a);
-            w[j].b = pack8(b);
-          }
-          *reinterpret_cast<uint4*>(y + ca[j] * kBytes) = w[j].a;
-          *reinterpret_cast<uint4*>(y + cb[j] * kBytes) = w[j].b;
-        }
+        row = y + tj * P.q_out_row * 2;
+      }
+      if (eight) {
+        *reinterpret_cast<uint2*>(row + ca) = quantise8(a, scale);
+        *reinterpret_cast<uint2*>(row + cb) = quantise8(b, scale);
+      } else {
+        *reinterpret_cast<uint4*>(row + ca * 2) = w[j].a;
+        *reinterpret_cast<uint4*>(row + cb * 2) = w[j].b;
       }
     }
+    t += 2 * side;
+    if (t >= tokens) {  // the next unit, where a token has more units than there are threads
+      at += blockDim.x;
+      busy = at < units && units > (int)blockDim.x;
+      t = t0;
+      if (busy) take();
+    }
+    if (busy) load(t);
   }
 }
 
 template <int D>
-cudaError_t rope_typed(const RopeLaunch& L, const RopeParams& P, int blocks) {
+cudaError_t rope_typed(const RopeLaunch& L, const RopeParams& P, int blocks, int threads) {
   if (L.cu[0] != nullptr) {
     PairOffsets off;
     std::memcpy(&off.q, L.cu[0], sizeof(RowOffsets));
     std::memcpy(&off.k, L.cu[1], sizeof(RowOffsets));
-    rope_kernel<D><<<blocks, kThreads, 0, L.stream>>>(P, off);
+    rope_kernel<D><<<blocks, threads, 0, L.stream>>>(P, off);
   } else {
-    rope_kernel<D><<<blocks, kThreads, 0, L.stream>>>(P, NoOffsets{});
+    rope_kernel<D><<<blocks, threads, 0, L.stream>>>(P, NoOffsets{});
   }
   return cudaGetLastError();
 }
 
 template <int DQK, int DV, bool E4M3>
-cudaError_t append_typed(const AppendLaunch& L, const AppendParams& P, int blocks) {
+cudaError_t append_typed(const AppendLaunch& L, const AppendParams& P, int blocks, int threads) {
   if (L.offsets != nullptr)
-    append_kernel<DQK, DV, E4M3><<<blocks, kThreads, 0, L.stream>>>(P, *L.offsets);
+    append_kernel<DQK, DV, E4M3><<<blocks, threads, 0, L.stream>>>(P, *L.offsets);
   else
-    append_kernel<DQK, DV, E4M3><<<blocks, kThreads, 0, L.stream>>>(P, NoOffsets{});
+    append_kernel<DQK, DV, E4M3><<<blocks, threads, 0, L.stream>>>(P, NoOffsets{});
   return cudaGetLastError();
 }
 
@@ -401,13 +452,16 @@ cudaError_t append_typed(const AppendLaunch& L, const AppendParams& P, int block
 cudaError_t launch_rope(const RopeLaunch& L) {
   RopeParams P;
   std::memset(&P, 0, sizeof(P));
-  int blocks = 0;
+  int blocks = 0, threads = 0;
   for (int i = 0; i < 2; ++i) {
     P.t[i] = L.t[i];
     if (P.t[i].rows == 0) continue;
-    P.t[i].tokens_per_block = tokens_per_block(P.t[i].H * (L.d / 16), L.rot.dim);
-    P.t[i].blocks = cdiv(P.t[i].rows, P.t[i].tokens_per_block);
-    blocks += P.t[i].blocks;
+    const BlockShape s = block_shape(P.t[i].rows, P.t[i].H * (L.d / 16), L.rot.dim, L.num_sms);
+    P.t[i].tokens = s.tokens;
+    P.t[i].side = s.side;
+    P.t[i].blocks = s.blocks;
+    blocks += s.blocks;
+    threads = std::max(threads, s.threads);  // (a wider block serves the narrower tensor too)
   }
   if (blocks == 0) return cudaSuccess;
   P.rot = L.rot;
@@ -415,9 +469,9 @@ cudaError_t launch_rope(const RopeLaunch& L) {
   P.nseq = L.nseq;
   P.pos0 = L.pos0;
   switch (L.d) {
-    case 64: return rope_typed<64>(L, P, blocks);
-    case 128: return rope_typed<128>(L, P, blocks);
-    case 192: return rope_typed<192>(L, P, blocks);
+    case 64: return rope_typed<64>(L, P, blocks, threads);
+    case 128: return rope_typed<128>(L, P, blocks, threads);
+    case 192: return rope_typed<192>(L, P, blocks, threads);
   }
   return cudaErrorInvalidValue;
 }
@@ -441,12 +495,14 @@ cudaError_t launch_append(const AppendLaunch& L) {
   P.rot = L.rot;
   P.status = L.status;
   const int units = (L.Hq + L.cache.heads) * (L.dqk / 16) + L.cache.heads * (L.dv / 16);
-  P.tokens_per_block = tokens_per_block(units, L.rot.dim);
-  const int blocks = cdiv(L.T, P.tokens_per_block);
+  const BlockShape shape = block_shape(L.T, units, L.rot.dim, L.num_sms);
+  P.tokens = shape.tokens;
+  P.side = shape.side;
+  const int blocks = shape.blocks, threads = shape.threads;
   const bool e = L.cache.e4m3 != 0;
-  if (L.dqk == 64) return e ? append_typed<64, 64, true>(L, P, blocks) : append_typed<64, 64, false>(L, P, blocks);
-  if (L.dqk == 128) return e ? append_typed<128, 128, true>(L, P, blocks) : append_typed<128, 128, false>(L, P, blocks);
-  if (L.dqk == 192) return e ? append_typed<192, 128, true>(L, P, blocks) : append_typed<192, 128, false>(L, P, blocks);
+  if (L.dqk == 64) return e ? append_typed<64, 64, true>(L, P, blocks, threads) : append_typed<64, 64, false>(L, P, blocks, threads);
+  if (L.dqk == 128) return e ? append_typed<128, 128, true>(L, P, blocks, threads) : append_typed<128, 128, false>(L, P, blocks, threads);
+  if (L.dqk == 192) return e ? append_typed<192, 128, true>(L, P, blocks, threads) : append_typed<192, 128, false>(L, P, blocks, threads);
   return cudaErrorInvalidValue;
 }
 
