@@ -10,7 +10,7 @@ kernels: there is no CPU path, and a missing library raises at first use.
 """
 from __future__ import annotations
 
-import contextlib
+import array
 import ctypes
 import math
 import os
@@ -75,6 +75,8 @@ class _CacheStruct(ctypes.Structure):
 def load():
     """Load the CUDA library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -152,10 +154,10 @@ def load():
 
 
 def _ptr(x):
-    if x is None:
-        return None
     if isinstance(x, torch.Tensor):
         return x.data_ptr()
+    if x is None:
+        return None
     return int(x)
 
 
@@ -176,16 +178,22 @@ def _stream(s):
 class _HostInts:
     """Keeps a host int32 array alive for the duration of a call."""
 
+    __slots__ = ("arr",)
+
     def __init__(self, values):
         if values is None:
             self.arr = None
-        else:
-            vals = [int(v) for v in (values.tolist() if hasattr(values, "tolist") else values)]
-            self.arr = (ctypes.c_int * len(vals))(*vals)
+            return
+        if hasattr(values, "tolist"):
+            values = values.tolist()
+        try:
+            self.arr = array.array("i", values)
+        except TypeError:
+            self.arr = array.array("i", [int(v) for v in values])
 
     @property
     def ptr(self):
-        return None if self.arr is None else ctypes.cast(self.arr, ctypes.c_void_p)
+        return None if self.arr is None else self.arr.buffer_info()[0]
 
 
 # ----------------------------------------------------------------------------
@@ -388,7 +396,9 @@ def _struct(x):
     """Address of a ctypes structure (or of a Rotation's or PagedCache's), or None."""
     if x is None:
         return None
-    return ctypes.addressof(getattr(x, "struct", x))
+    if isinstance(x, ctypes.Structure):
+        return ctypes.addressof(x)
+    return x.address
 
 
 def attn_rope(q, k, q_out, k_out, B, Hq, Hk, Tq, Tk, d, q_row, k_row, q_out_row, k_out_row,
@@ -565,6 +575,7 @@ class Rotation:
         self.begin, self.dim, self.interleaved = int(begin), 2 * len(words), bool(interleaved)
         self.struct = _RotationStruct(self.rates.data_ptr(), self.begin, self.dim,
                                       ROPE_PAIRS if interleaved else ROPE_HALVES)
+        self.address = ctypes.addressof(self.struct)
 
 
 class PagedCache:
@@ -599,6 +610,7 @@ class PagedCache:
             k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
             *k_cache.stride()[:3], *v_cache.stride()[:3], kinds[k_cache.dtype], pages, page_size,
             heads, dqk, self.dv)
+        self.address = ctypes.addressof(self.struct)
 
 
 class _On:
@@ -623,40 +635,32 @@ class _On:
             c.__exit__(*exc)
 
 
-_HERE_NOW = contextlib.nullcontext()
+def _here(index, stream):
+    """Whether a call for device `index` and `stream` runs where the caller is."""
+    return stream is None and index == torch.cuda.current_device()
 
 
-def _on(index, stream):
-    """_On(index, stream), or nothing to enter where that is where the caller is."""
-    if stream is None and index == torch.cuda.current_device():
-        return _HERE_NOW
-    return _On(index, stream)
-
-
-def _rows(t, name, heads=None, d=None):
-    """Distance in elements between the token rows of a bf16 (..., H, d) tensor whose leading
-    dimensions are evenly spaced rows of dense heads."""
+def _rows(t, shape, name):
+    """Distance in elements between the token rows of a bf16 tensor t of this shape, (T, H, d) or
+    (B, T, H, d), whose rows are evenly spaced, each of adjacent heads and with its own memory."""
     if t.dtype is not torch.bfloat16:
         raise ValueError(f"{name} must be bfloat16")
-    shape = t.shape
-    if len(shape) < 3 or (heads is not None and shape[-2] != heads) or (d is not None
-                                                                      and shape[-1] != d):
-        raise ValueError(f"{name} must be (rows, heads, d)")
+    H, d = shape[-2], shape[-1]
     if t.is_contiguous():
-        return shape[-2] * shape[-1]
+        return H * d
     stride = t.stride()
-    if (shape[-1] > 1 and stride[-1] != 1) or (shape[-2] > 1 and stride[-2] != shape[-1]):
+    if (d > 1 and stride[-1] != 1) or (H > 1 and stride[-2] != d):
         raise ValueError(f"the heads of a row of {name} must be adjacent")
-    row, span = 0, 1  # span: rows below the dimension at hand
-    for n, s in zip(reversed(shape[:-2]), reversed(stride[:-2])):
-        if n == 1:
-            continue
-        if row == 0:
-            row = s
-        elif s != row * span:
+    T = shape[-3]
+    row = stride[-3] if T > 1 else H * d
+    if len(shape) == 4 and shape[0] > 1:
+        if T > 1 and stride[0] != row * T:
             raise ValueError(f"the rows of {name} must be evenly spaced")
-        span *= n
-    return row if row else shape[-2] * shape[-1]
+        if T == 1:
+            row = stride[0]
+    if row < H * d:  # (a broadcast dimension has a stride of 0)
+        raise ValueError(f"the rows of {name} must have their own memory")
+    return row
 
 
 def _device_of(t, *others):
@@ -683,37 +687,42 @@ def rope(q, k, rotation, inverse=False, pos0=0, cu_seqlens=None, cu_seqlens_k=No
     x = q if q is not None else k
     if x is None:
         raise ValueError("q and k are both None")
+    shape = x.shape
     varlen = cu_seqlens is not None
-    for name, t in (("q", q), ("k", k)):
-        if t is not None and t.dim() != (3 if varlen else 4):
-            raise ValueError(f"{name} must have {3 if varlen else 4} dimensions")
-        if t is not None and (t.shape[-1] != x.shape[-1]
-                              or (not varlen and t.shape[0] != x.shape[0])):
-            raise ValueError("q and k must agree in batch and head size")
-    B = len(cu_seqlens) - 1 if varlen else x.shape[0]
-    at = 0 if varlen else 1
-    Tq = x.shape[at] if q is None else q.shape[at]
-    Tk = x.shape[at] if k is None else k.shape[at]
+    if len(shape) != (3 if varlen else 4):
+        raise ValueError(f"q and k must have {3 if varlen else 4} dimensions")
+    other = k.shape if q is not None and k is not None else shape
+    if len(other) != len(shape) or other[-1] != shape[-1] or (not varlen and other[0] != shape[0]):
+        raise ValueError("q and k must agree in batch and head size")
+    if varlen:
+        B, Tq, Tk = len(cu_seqlens) - 1, shape[0], other[0]
+    else:
+        B, Tq, Tk = shape[0], shape[1], other[1]
+    q_row = 0 if q is None else _rows(q, shape, "q")
+    k_row = 0 if k is None else _rows(k, other, "k")
     q_out, k_out = out if out is not None else (None, None)
+    q_out_row = k_out_row = 0  # dense
     if out is not None:
         for name, t, o in (("q", q, q_out), ("k", k, k_out)):
             if (t is None) != (o is None) or (o is not None and o.shape != t.shape):
                 raise ValueError(f"out must hold a tensor like {name}")
-    rows = [0 if t is None else _rows(t, n) for t, n in
-            ((q, "q"), (k, "k"), (q_out, "out[0]"), (k_out, "out[1]"))]
+        q_out_row = 0 if q is None else _rows(q_out, shape, "out[0]")
+        k_out_row = 0 if k is None else _rows(k_out, other, "out[1]")
     index = _device_of(x, k, q_out, k_out, rotation.rates)
-    with _on(index, stream):
-        if out is None:
-            q_out = None if q is None else torch.empty(q.shape, dtype=torch.bfloat16,
-                                                       device=q.device)
-            k_out = None if k is None else torch.empty(k.shape, dtype=torch.bfloat16,
-                                                       device=k.device)
-            rows[2:] = 0, 0  # dense
-        if x.numel() == 0:
-            return q_out, k_out
-        rc = attn_rope(q, k, q_out, k_out, B, 0 if q is None else q.shape[-2],
-                       0 if k is None else k.shape[-2], Tq, Tk, x.shape[-1], *rows, rotation,
-                       inverse, pos0, cu_seqlens, cu_seqlens_k)
+    if not _here(index, stream):
+        with _On(index, stream):
+            return rope(q, k, rotation, inverse, pos0, cu_seqlens, cu_seqlens_k, out)
+    if out is None:
+        device = x.device
+        q_out = None if q is None else torch.empty(shape, dtype=torch.bfloat16, device=device)
+        k_out = None if k is None else torch.empty(other, dtype=torch.bfloat16, device=device)
+    if x.numel() == 0:
+        return q_out, k_out
+    cu, cuk = _HostInts(cu_seqlens), _HostInts(cu_seqlens_k)
+    rc = load().attn_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B,
+                          0 if q is None else shape[-2], 0 if k is None else other[-2], Tq, Tk,
+                          shape[-1], q_row, k_row, q_out_row, k_out_row, rotation.address,
+                          int(inverse), int(pos0), cu.ptr, cuk.ptr, _stream(None))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_rope")
     return q_out, k_out
@@ -726,9 +735,11 @@ def _check_tables(cache, block_table, lens):
     B, width = block_table.shape
     stride = width
     if not block_table.is_contiguous():
-        if width > 1 and block_table.stride(1) != 1:
-            raise ValueError("block_table must be int32 (sequences, pages) with adjacent entries")
-        stride = max(block_table.stride(0), width)
+        if B > 1:
+            stride = block_table.stride(0)
+        if (width > 1 and block_table.stride(1) != 1) or stride < width:
+            raise ValueError("block_table must be int32 (sequences, pages) with adjacent entries, "
+                             "each row with its own memory")
     if lens.dtype is not torch.int32 or lens.shape != (B,) or not lens.is_contiguous():
         raise ValueError("lens must be contiguous int32, one per row of block_table")
     return B, width, stride
@@ -743,29 +754,35 @@ def cache_append(cache, k, v, block_table, lens, q=None, rotation=None, cu_seqle
     sequence brings T / sequences tokens.  k is rotated to its position if a rotation is
     given, and so is q (T,Hq,dqk), which is returned (in q_out, which may be q)."""
     B, width, stride = _check_tables(cache, block_table, lens)
-    T = k.shape[0]
-    k_row = _rows(k, "k", cache.heads, cache.dqk)
-    v_row = _rows(v, "v", cache.heads, cache.dv)
-    if k.dim() != 3 or v.dim() != 3 or v.shape[0] != T:
-        raise ValueError("k and v must be (T, heads, d) with the same T")
+    k_shape, v_shape, heads = k.shape, v.shape, cache.heads
+    T = k_shape[0]
+    if k_shape != (T, heads, cache.dqk) or v_shape != (T, heads, cache.dv):
+        raise ValueError("k and v must be (T, heads, d) with the cache's heads and the same T")
     if cu_seqlens is not None and len(cu_seqlens) != B + 1:
         raise ValueError("cu_seqlens must have one entry more than there are sequences")
+    k_row, v_row = _rows(k, k_shape, "k"), _rows(v, v_shape, "v")
     q_row = out_row = Hq = 0
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T:
+        q_shape = q.shape
+        if len(q_shape) != 3 or q_shape[0] != T or q_shape[2] != cache.dqk:
             raise ValueError("q must be (T, heads, dqk)")
-        q_row, Hq = _rows(q, "q", None, cache.dqk), q.shape[1]
+        Hq, q_row = q_shape[1], _rows(q, q_shape, "q")
     if q_out is not None:
-        if q is None or q_out.shape != q.shape:
+        if q is None or q_out.shape != q_shape:
             raise ValueError("q_out must have q's shape")
-        out_row = _rows(q_out, "q_out")
+        out_row = _rows(q_out, q_shape, "q_out")
     index = _device_of(cache.k_cache, k, v, q, q_out, block_table, lens,
                        None if rotation is None else rotation.rates)
-    with _on(index, stream):
-        if q is not None and q_out is None:
-            q_out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-        rc = attn_cache_append(cache, block_table, width, stride, lens, B, T, cu_seqlens, k,
-                               k_row, v, v_row, q, q_row, q_out, out_row, Hq, rotation)
+    if not _here(index, stream):
+        with _On(index, stream):
+            return cache_append(cache, k, v, block_table, lens, q, rotation, cu_seqlens, q_out)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+    cu = _HostInts(cu_seqlens)
+    rc = load().attn_cache_append(cache.address, block_table.data_ptr(), width, stride,
+                                  lens.data_ptr(), B, T, cu.ptr, k.data_ptr(), k_row,
+                                  v.data_ptr(), v_row, _ptr(q), q_row, _ptr(q_out), out_row, Hq,
+                                  None if rotation is None else rotation.address, _stream(None))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_append")
     return q_out
@@ -778,7 +795,7 @@ def decode_workspace(device=None, stream=None):
     if device.type != "cuda":
         raise ValueError("a decode workspace must be on a CUDA device")
     index = torch.cuda.current_device() if device.index is None else device.index
-    with _on(index, stream):
+    with _On(index, stream):
         ws = torch.empty(attn_decode_workspace_size(), dtype=torch.uint8, device=device)
         rc = attn_decode_workspace_init(ws, ws.numel())
     if rc != ATTN_OK:
@@ -796,11 +813,10 @@ def decode(cache, q, block_table, lens, scale=None, window_left=-1, with_lse=Tru
     workspace: from decode_workspace() (None: one is made and initialised for this call).
     out: (o, lse) to write to (lse may be None)."""
     B, width, stride = _check_tables(cache, block_table, lens)
-    q_row = _rows(q, "q", None, cache.dqk)
     shape = q.shape
-    if len(shape) != 3 or shape[0] != B:
+    if len(shape) != 3 or shape[0] != B or shape[2] != cache.dqk:
         raise ValueError("q must be (sequences, heads, dqk)")
-    Hq = shape[1]
+    Hq, q_row = shape[1], _rows(q, shape, "q")
     o, lse = out if out is not None else (None, None)
     if out is not None and (o.dtype is not torch.bfloat16 or o.shape != (B, Hq, cache.dv)
                             or not o.is_contiguous()):
@@ -811,15 +827,20 @@ def decode(cache, q, block_table, lens, scale=None, window_left=-1, with_lse=Tru
     index = _device_of(cache.k_cache, q, block_table, lens, workspace, o, lse)
     if scale is None:
         scale = 1.0 / math.sqrt(cache.dqk)
-    with _on(index, stream):
-        if out is None:
-            o = torch.empty((B, Hq, cache.dv), dtype=torch.bfloat16, device=q.device)
-            lse = torch.empty((B, Hq), dtype=torch.float32, device=q.device) if with_lse else None
-        if workspace is None:
-            workspace = decode_workspace(index)
-        rc = attn_decode(cache, block_table, width, stride, lens, B, q, q_row, o, lse, Hq,
-                         window_left, scale, workspace,
-                         workspace.numel() * workspace.element_size())
+    if not _here(index, stream):
+        with _On(index, stream):
+            return decode(cache, q, block_table, lens, scale, window_left, with_lse, workspace,
+                          out)
+    if out is None:
+        device = q.device
+        o = torch.empty((B, Hq, cache.dv), dtype=torch.bfloat16, device=device)
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=device) if with_lse else None
+    if workspace is None:
+        workspace = decode_workspace(index)
+    rc = load().attn_decode(cache.address, block_table.data_ptr(), width, stride, lens.data_ptr(),
+                            B, q.data_ptr(), q_row, o.data_ptr(),
+                            None if lse is None else lse.data_ptr(), Hq, int(window_left),
+                            float(scale), workspace.data_ptr(), workspace.nbytes, _stream(None))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode")
     return o, lse

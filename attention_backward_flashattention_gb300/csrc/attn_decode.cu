@@ -329,8 +329,8 @@ struct Item {
   int b, kvh, head, rows;
   int tile0, tile1;
   KeyRange keys;
-  ItemParts parts;
-  int my_part;
+  long long at;                  // the item's first tile on the line
+  int piece;                     // the piece that these tiles are in
   int more;                      // 0: nothing is left, and the rest is not set
 };
 // Where it is on the line.
@@ -343,7 +343,7 @@ struct Walk {
 // The next item with tiles, of this piece or of one claimed now.  One thread calls
 // it.  before[i]: tiles in front of the sequences i * chunk ..
 template <int STEP, int TILE>
-__device__ __noinline__ void next_item(const DecodeParams& P, const Line& line,
+__device__ __forceinline__ void next_item(const DecodeParams& P, const Line& line,
                                        const long long* before, int threads, int chunk, Walk& k,
                                        Item* w) {
   auto range = [&](int b, int& len) {
@@ -379,8 +379,8 @@ __device__ __noinline__ void next_item(const DecodeParams& P, const Line& line,
       w->tile0 = tile0;
       w->tile1 = tile1;
       w->keys = keys;
-      w->parts = item_parts(line, item_at, keys.tiles);
-      w->my_part = k.piece - w->parts.first;
+      w->at = item_at;
+      w->piece = k.piece;
       w->more = 1;
       return;
     }
@@ -829,8 +829,8 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
       __syncthreads();
 
       const int b = done->b, head = done->head, rows = done->rows;
-      const ItemParts parts = done->parts;
-      const int my_part = done->my_part;
+      const ItemParts parts = item_parts(s_line, done->at, done->keys.tiles);
+      const int my_part = done->piece - parts.first;
       const int my_slot = parts.slot(my_part);
       const float v_scale = E4M3 && P.cache.v.scale ? __ldg(P.cache.v.scale + done->kvh) : 1.f;
       for (int e = tid; e < rows * DV / 4; e += kThreads) {
@@ -907,7 +907,8 @@ cudaError_t launch_typed(const DecodeLaunch& L, const DecodeParams& P) {
   const long long most = (long long)L.B * P.items_per_seq * ((keys + kKeys - 1) / kKeys);
   const int grid =
       (int)std::min<long long>(std::min(kMaxDecodeCtas, 2 * L.num_sms), most);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   kernel<<<grid, C::kThreads, C::kSmem, L.stream>>>(P);
   return cudaGetLastError();

@@ -38,22 +38,28 @@ int* cache_status_ptr() {
 
 namespace {
 
-constexpr int kMostThreads = 512;
+// Threads of a block at most, and blocks on an SM that the registers are to leave
+// room for: many loads on their way (bf16), or the registers that eight-bit
+// conversions need.
+template <bool E4M3>
+struct Bounds {
+  static constexpr int kThreads = E4M3 ? 384 : 256, kBlocks = E4M3 ? 2 : 5;
+};
 constexpr int kMaxTokens = 32;        // token rows of one block at most
 constexpr int kMaxAngles = 2048;      // (token, pair) angles of one block at most
-constexpr int kRounds = 8;            // tokens a thread walks over, where there are many
+constexpr int kRounds = 4;            // tokens a thread walks over, where there are many
 
 // Shape of the blocks over `rows` token rows of `units` units each: `side`
-// token rows side by side (about 256 threads, or one row of up to 512 units), and
+// token rows side by side (about 256 threads, or one row), and
 // up to kRounds of them one after the other as long as every SM has some blocks.
 struct BlockShape {
   int threads, side, tokens, blocks;
 };
-BlockShape block_shape(int rows, int units, int dim, int sms) {
+BlockShape block_shape(int rows, int units, int dim, int sms, int most_threads) {
   BlockShape s;
   const int most = dim > 0 ? std::min(kMaxTokens, kMaxAngles / (dim / 2)) : kMaxTokens;
-  s.side = std::min(std::max(1, 256 / units), most);
-  s.threads = std::min(kMostThreads, cdiv(s.side * units, 32) * 32);
+  s.side = std::min(std::max(1, std::min(256, most_threads) / units), most);
+  s.threads = std::min(most_threads, cdiv(s.side * units, 32) * 32);
   const int rounds = std::max(1, std::min(kRounds, rows / (s.side * sms * 8)));
   s.tokens = std::min(s.side * rounds, most);
   s.blocks = cdiv(rows, s.tokens);
@@ -163,7 +169,7 @@ struct RopeParams {
 // attn_rope: blocks 0 .. t[0].blocks - 1 take the queries, the others the keys.
 // ----------------------------------------------------------------------------
 template <int D, typename Offsets>
-__global__ void __launch_bounds__(kMostThreads, 2)
+__global__ void __launch_bounds__(Bounds<false>::kThreads, Bounds<false>::kBlocks)
 rope_kernel(const __grid_constant__ RopeParams P, const __grid_constant__ Offsets off) {
   __shared__ int pos[kMaxTokens];
   __shared__ __align__(16) float2 sc[kMaxAngles];
@@ -202,20 +208,18 @@ rope_kernel(const __grid_constant__ RopeParams P, const __grid_constant__ Offset
     cb += head * D;
   };
   Unit w[2];
-  auto load = [&](int t) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (t + j * side >= tokens) break;
-      const uint16_t* row = x + (t + j * side) * X.x_row;
-      w[j].a = *reinterpret_cast<const uint4*>(row + ca);
-      w[j].b = *reinterpret_cast<const uint4*>(row + cb);
-    }
+  auto load = [&](int t, Unit& w) {
+    if (t >= tokens) return;
+    const uint16_t* row = x + t * X.x_row;
+    w.a = *reinterpret_cast<const uint4*>(row + ca);
+    w.b = *reinterpret_cast<const uint4*>(row + cb);
   };
   bool busy = t0 < min(side, tokens) && at < units;
   int t = t0;
   if (busy) {
     take();
-    load(t);
+    load(t, w[0]);
+    load(t + side, w[1]);
   }
   __syncthreads();
   fill_angles(sc, pos, tokens, P.rot, P.inverse != 0);
@@ -236,15 +240,20 @@ rope_kernel(const __grid_constant__ RopeParams P, const __grid_constant__ Offset
       uint16_t* row = y + tj * X.y_row;
       *reinterpret_cast<uint4*>(row + ca) = w[j].a;
       *reinterpret_cast<uint4*>(row + cb) = w[j].b;
+      load(tj + 2 * side, w[j]);
     }
     t += 2 * side;
-    if (t >= tokens) {  // the next unit, in rows of more units than threads
+    const bool fresh = t >= tokens;
+    if (fresh) {  // the next unit, in rows of more units than threads
       at += blockDim.x;
       busy = at < units && units > (int)blockDim.x;
       t = t0;
       if (busy) take();
     }
-    if (busy) load(t);
+    if (fresh && busy) {
+      load(t, w[0]);
+      load(t + side, w[1]);
+    }
   }
 }
 
@@ -261,24 +270,39 @@ struct AppendParams {
   int* status;
 };
 
-// Eight values as e4m3 of x / scale, saturated (one rounding: the division is
-// correctly rounded to fp32 first, which moves a value across a border between two e4m3
-// neighbours only where it lies within 2^-24 of it).
-__device__ __forceinline__ uint2 quantise8(const float (&x)[8], float scale) {
+// Division by a scale s as a product with 1 / s in two terms.  With hi = 1 / s
+// rounded and lo = (1 - s hi) hi, x (hi + lo) is x / s to 2^-47; the error-free
+// product x hi = p + e (Dekker's, by fma) keeps that up to one rounding to fp32, as a
+// division has: a quotient on the border between two e4m3 neighbours stays there.
+struct Scale {
+  float hi = 1.f, lo = 0.f;
+  __device__ __forceinline__ void set(float s) {
+    hi = __fdiv_rn(1.f, s);
+    lo = fmaf(-s, hi, 1.f) * hi;
+  }
+  __device__ __forceinline__ float divide(float x) const {
+    const float p = x * hi;
+    const float q = p + fmaf(x, lo, fmaf(x, hi, -p));
+    return fabsf(p) <= 3.402823466e38f ? q : p;  // (infinite: no rest to add)
+  }
+};
+
+// Eight values as e4m3 of x / scale, saturated.
+__device__ __forceinline__ uint2 quantise8(const float (&x)[8], const Scale& scale) {
   uint32_t h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     uint16_t r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
         : "=h"(r)
-        : "f"(__fdiv_rn(x[2 * i + 1], scale)), "f"(__fdiv_rn(x[2 * i], scale)));
+        : "f"(scale.divide(x[2 * i + 1])), "f"(scale.divide(x[2 * i])));
     h[i] = r;
   }
   return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
 template <int DQK, int DV, bool E4M3, typename Offsets>
-__global__ void __launch_bounds__(kMostThreads, 2)
+__global__ void __launch_bounds__(Bounds<E4M3>::kThreads, Bounds<E4M3>::kBlocks)
 append_kernel(const __grid_constant__ AppendParams P, const __grid_constant__ Offsets off) {
   __shared__ int pos[kMaxTokens];
   __shared__ int64_t koff[kMaxTokens], voff[kMaxTokens];  // byte offset of the slot; -1: none
@@ -327,7 +351,7 @@ append_kernel(const __grid_constant__ AppendParams P, const __grid_constant__ Of
   int64_t x_row = 0;
   char* y = nullptr;                    // q_out (rows y_row bytes apart) or one side of the cache
   const int64_t* slots = nullptr;       // null: q_out
-  float scale = 1.f;
+  Scale scale;
   auto take = [&]() {
     int rem = at;
     if (rem < n_q + n_k) {
@@ -342,7 +366,7 @@ append_kernel(const __grid_constant__ AppendParams P, const __grid_constant__ Of
       if (key) {
         y = P.cache.k.base + head * P.cache.k.head;
         slots = koff;
-        if (E4M3 && P.cache.k.scale) scale = __ldg(P.cache.k.scale + head);
+        if (E4M3 && P.cache.k.scale) scale.set(__ldg(P.cache.k.scale + head));
       } else {
         y = reinterpret_cast<char*>(P.q_out + row0 * P.q_out_row + head * DQK);
         slots = nullptr;
@@ -358,24 +382,22 @@ append_kernel(const __grid_constant__ AppendParams P, const __grid_constant__ Of
       x = P.v + row0 * x_row + head * DV;
       y = P.cache.v.base + head * P.cache.v.head;
       slots = voff;
-      scale = E4M3 && P.cache.v.scale ? __ldg(P.cache.v.scale + head) : 1.f;
+      if constexpr (E4M3) scale.set(P.cache.v.scale ? __ldg(P.cache.v.scale + head) : 1.f);
     }
   };
   Unit w[2];
-  auto load = [&](int t) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (t + j * side >= tokens) break;
-      const uint16_t* row = x + (t + j * side) * x_row;
-      w[j].a = *reinterpret_cast<const uint4*>(row + ca);
-      w[j].b = *reinterpret_cast<const uint4*>(row + cb);
-    }
+  auto load = [&](int t, Unit& w) {
+    if (t >= tokens) return;
+    const uint16_t* row = x + t * x_row;
+    w.a = *reinterpret_cast<const uint4*>(row + ca);
+    w.b = *reinterpret_cast<const uint4*>(row + cb);
   };
   bool busy = t0 < min(side, tokens) && at < units;
   int t = t0;
   if (busy) {
     take();
-    load(t);
+    load(t, w[0]);
+    load(t + side, w[1]);
   }
   __syncthreads();
   fill_angles(sc, pos, tokens, P.rot, false);
@@ -385,43 +407,48 @@ append_kernel(const __grid_constant__ AppendParams P, const __grid_constant__ Of
     for (int j = 0; j < 2; ++j) {
       const int tj = t + j * side;
       if (tj >= tokens) break;
-      if (pos[tj] < 0) continue;
       const bool eight = E4M3 && slots != nullptr;
-      float a[8], b[8];
-      if (turns || eight) {
-        unpack8(w[j].a, a);
-        unpack8(w[j].b, b);
-      }
-      if (turns) {
-        turn_unit(sc, tj, unit, P.rot, a, b);
-        if (!eight) {
-          w[j].a = pack8(a);
-          w[j].b = pack8(b);
-        }
-      }
       char* row;
+      bool put = pos[tj] >= 0;
       if (slots != nullptr) {
-        if (slots[tj] < 0) continue;
+        put = put && slots[tj] >= 0;
         row = y + slots[tj];
       } else {
         row = y + tj * P.q_out_row * 2;
       }
-      if (eight) {
-        *reinterpret_cast<uint2*>(row + ca) = quantise8(a, scale);
-        *reinterpret_cast<uint2*>(row + cb) = quantise8(b, scale);
-      } else {
-        *reinterpret_cast<uint4*>(row + ca * 2) = w[j].a;
-        *reinterpret_cast<uint4*>(row + cb * 2) = w[j].b;
+      if (put) {
+        float a[8], b[8];
+        if (turns || eight) {
+          unpack8(w[j].a, a);
+          unpack8(w[j].b, b);
+        }
+        if (turns) turn_unit(sc, tj, unit, P.rot, a, b);
+        if (eight) {
+          *reinterpret_cast<uint2*>(row + ca) = quantise8(a, scale);
+          *reinterpret_cast<uint2*>(row + cb) = quantise8(b, scale);
+        } else {
+          if (turns) {
+            w[j].a = pack8(a);
+            w[j].b = pack8(b);
+          }
+          *reinterpret_cast<uint4*>(row + ca * 2) = w[j].a;
+          *reinterpret_cast<uint4*>(row + cb * 2) = w[j].b;
+        }
       }
+      load(tj + 2 * side, w[j]);
     }
     t += 2 * side;
-    if (t >= tokens) {  // the next unit, where a token has more units than there are threads
+    const bool fresh = t >= tokens;
+    if (fresh) {  // the next unit, where a token has more units than there are threads
       at += blockDim.x;
       busy = at < units && units > (int)blockDim.x;
       t = t0;
       if (busy) take();
     }
-    if (busy) load(t);
+    if (fresh && busy) {
+      load(t, w[0]);
+      load(t + side, w[1]);
+    }
   }
 }
 
@@ -439,11 +466,11 @@ cudaError_t rope_typed(const RopeLaunch& L, const RopeParams& P, int blocks, int
 }
 
 template <int DQK, int DV, bool E4M3>
-cudaError_t append_typed(const AppendLaunch& L, const AppendParams& P, int blocks, int threads) {
+cudaError_t append_typed(const AppendLaunch& L, const AppendParams& P, const BlockShape& s) {
   if (L.offsets != nullptr)
-    append_kernel<DQK, DV, E4M3><<<blocks, threads, 0, L.stream>>>(P, *L.offsets);
+    append_kernel<DQK, DV, E4M3><<<s.blocks, s.threads, 0, L.stream>>>(P, *L.offsets);
   else
-    append_kernel<DQK, DV, E4M3><<<blocks, threads, 0, L.stream>>>(P, NoOffsets{});
+    append_kernel<DQK, DV, E4M3><<<s.blocks, s.threads, 0, L.stream>>>(P, NoOffsets{});
   return cudaGetLastError();
 }
 
@@ -456,7 +483,8 @@ cudaError_t launch_rope(const RopeLaunch& L) {
   for (int i = 0; i < 2; ++i) {
     P.t[i] = L.t[i];
     if (P.t[i].rows == 0) continue;
-    const BlockShape s = block_shape(P.t[i].rows, P.t[i].H * (L.d / 16), L.rot.dim, L.num_sms);
+    const BlockShape s = block_shape(P.t[i].rows, P.t[i].H * (L.d / 16), L.rot.dim, L.num_sms,
+                                     Bounds<false>::kThreads);
     P.t[i].tokens = s.tokens;
     P.t[i].side = s.side;
     P.t[i].blocks = s.blocks;
@@ -494,15 +522,18 @@ cudaError_t launch_append(const AppendLaunch& L) {
   P.per_seq = L.per_seq;
   P.rot = L.rot;
   P.status = L.status;
-  const int units = (L.Hq + L.cache.heads) * (L.dqk / 16) + L.cache.heads * (L.dv / 16);
-  const BlockShape shape = block_shape(L.T, units, L.rot.dim, L.num_sms);
-  P.tokens = shape.tokens;
-  P.side = shape.side;
-  const int blocks = shape.blocks, threads = shape.threads;
   const bool e = L.cache.e4m3 != 0;
-  if (L.dqk == 64) return e ? append_typed<64, 64, true>(L, P, blocks, threads) : append_typed<64, 64, false>(L, P, blocks, threads);
-  if (L.dqk == 128) return e ? append_typed<128, 128, true>(L, P, blocks, threads) : append_typed<128, 128, false>(L, P, blocks, threads);
-  if (L.dqk == 192) return e ? append_typed<192, 128, true>(L, P, blocks, threads) : append_typed<192, 128, false>(L, P, blocks, threads);
+  const int units = (L.Hq + L.cache.heads) * (L.dqk / 16) + L.cache.heads * (L.dv / 16);
+  const BlockShape s = block_shape(L.T, units, L.rot.dim, L.num_sms,
+                                   e ? Bounds<true>::kThreads : Bounds<false>::kThreads);
+  P.tokens = s.tokens;
+  P.side = s.side;
+  if (L.dqk == 64)
+    return e ? append_typed<64, 64, true>(L, P, s) : append_typed<64, 64, false>(L, P, s);
+  if (L.dqk == 128)
+    return e ? append_typed<128, 128, true>(L, P, s) : append_typed<128, 128, false>(L, P, s);
+  if (L.dqk == 192)
+    return e ? append_typed<192, 128, true>(L, P, s) : append_typed<192, 128, false>(L, P, s);
   return cudaErrorInvalidValue;
 }
 

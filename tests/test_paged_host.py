@@ -203,16 +203,35 @@ def test_paged_cache_rejects():
 
 
 def test_rows_of_views():
+    rows = lambda t: binding._rows(t, t.shape, "x")
     x = torch.zeros(2, 5, 3, 4, 64, dtype=torch.bfloat16)
-    assert binding._rows(x.select(2, 1), "x") == 3 * 4 * 64   # a slot of a packed buffer
-    assert binding._rows(torch.zeros(7, 4, 64, dtype=torch.bfloat16), "x") == 256
-    assert binding._rows(x[:, :1, 0], "x") == 5 * 3 * 4 * 64   # one row per batch
+    assert rows(x.select(2, 1)) == 3 * 4 * 64                 # a slot of a packed buffer
+    assert rows(torch.zeros(7, 4, 64, dtype=torch.bfloat16)) == 256
+    assert rows(x[:, :1, 0]) == 5 * 3 * 4 * 64                # one row per batch
     with pytest.raises(ValueError, match="evenly"):
-        binding._rows(x[:, :4, 0], "x")
+        rows(x[:, :4, 0])
     with pytest.raises(ValueError, match="adjacent"):
-        binding._rows(x[:, :, 0].transpose(1, 2), "x")
+        rows(x[:, :, 0].transpose(1, 2))
     with pytest.raises(ValueError, match="bfloat16"):
-        binding._rows(x[:, :, 0].float(), "x")
+        rows(x[:, :, 0].float())
+    one = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    assert rows(one[:, :2]) == 128                            # a single row: any distance does
+    for broadcast in (one.expand(5, 4, 64), one[None].expand(3, 1, 4, 64),
+                      x[:1, :, 0].expand(2, 5, 4, 64), x[:, :1, 0].expand(2, 5, 4, 64)):
+        with pytest.raises(ValueError, match="evenly|own memory"):
+            rows(broadcast)
+
+
+def test_tables_of_views():
+    cache = binding.PagedCache(*_tensors())
+    lens = torch.zeros(3, dtype=torch.int32)
+    big = torch.zeros(3, 10, dtype=torch.int32)
+    assert binding._check_tables(cache, big, lens) == (3, 10, 10)
+    assert binding._check_tables(cache, big[:, 2:6], lens) == (3, 4, 10)
+    assert binding._check_tables(cache, big[:1, 2:6], lens[:1]) == (1, 4, 4)
+    for bad in (big[:1].expand(3, 10), big[:, :1].expand(3, 10), big[:, ::2], big.t()[:3]):
+        with pytest.raises(ValueError):
+            binding._check_tables(cache, bad, lens)
 
 
 def _refused(call, *args, **kw):
