@@ -283,8 +283,8 @@ int attn_decode(const attn_paged_cache* cache, const int* block_table, int max_p
   L.B = B;
   L.Hq = Hq;
   L.group = Hq / cache->heads;
-  // groups of more than 16 heads are cut into tiles of equal size
-  L.row_tiles = cdiv(L.group, kMaxTileRows);
+  // large groups are cut into tiles of equal size
+  L.row_tiles = cdiv(L.group, most_tile_rows(cache->dqk, L.cache.e4m3 != 0));
   L.tile_rows = cdiv(L.group, L.row_tiles);
   L.row_tiles = cdiv(L.group, L.tile_rows);
   L.window = window_left;

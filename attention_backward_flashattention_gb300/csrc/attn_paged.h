@@ -138,14 +138,15 @@ __host__ __device__ inline uint32_t seen_bits(const KeyRange& g, int key, int st
 // How the line of `total` tiles is cut into pieces for up to `grid` CTAs.
 // n CTAs take a first piece each and claim smaller ones as they get done (an SM's
 // share of the memory rate differs by up to a third, so equal shares end far
-// apart): n pieces of 26/32 of an equal share, then k n of `small`/32, as small as
-// leaves a piece two tiles.  A line too short for that has n equal pieces of at
-// least kMinTiles, or one per item if that is more.  Where the cuts are depends on
+// apart): n pieces of 26/32 of an equal share, then 2 n of 3/32.  A line whose
+// shares are short (below kMinClaims tiles, where the work around a piece costs more
+// than the unevenness) has n equal pieces of at least kMinTiles, or one per item if
+// that is more.  Where the cuts are depends on
 // the lengths alone.
 // A cut within `tol` tiles of an item's end is moved to it: short items are not
 // split, and long ones leave no crumbs.
 constexpr int kMinTiles = 2;
-constexpr int kMostSmall = 6;  // small pieces per CTA at most
+constexpr int kMinClaims = 64;
 struct Line {
   long long total, unit;  // unit: the line's length in units of cut weight
   long long tol;
@@ -163,9 +164,9 @@ __host__ __device__ inline Line make_line(long long total, long long items, int 
   if (n < items) n = items;  // (items <= total)
   l.n = n < grid ? (int)n : grid;
   const long long tiles = div_line(total, l.n);  // of an equal share
-  l.small = tiles >= 64 ? 3 : 0;
+  l.small = tiles >= kMinClaims ? 3 : 0;
   l.big = l.small ? 26 : 1;
-  l.pieces = l.small ? l.n * (1 + 6 / l.small) : l.n;
+  l.pieces = l.small ? 3 * l.n : l.n;
   l.unit = l.small ? 32ll * l.n : l.n;
   l.tol = l.small ? tiles / 32 : tiles >= 16 ? tiles / 6 : tiles / 2;
   return l;
@@ -231,9 +232,9 @@ cudaError_t launch_append(const AppendLaunch& L);
 
 // Decode workspace, carved in this order (sizes fixed: any call fits).
 constexpr int kMaxDecodeCtas = 304;               // CTAs of one decode call at most
-constexpr int kMaxPieces = 7 * kMaxDecodeCtas;    // pieces of its line of tiles (make_line)
+constexpr int kMaxPieces = 3 * kMaxDecodeCtas;    // pieces of its line of tiles (make_line)
 constexpr int kDecodeSlots = 2 * kMaxPieces;      // partial results: two per piece
-constexpr int kMaxTileRows = 16;                  // query rows of one work item at most
+constexpr int kMaxTileRows = 32;                  // query rows of one work item at most
 constexpr int kMaxDv = 128;
 constexpr uint32_t kDecodeReady = 0x5A5A5A5Au;    // header word of an initialised workspace
 struct DecodeHeader {
@@ -246,6 +247,11 @@ constexpr size_t kDecodeMlBytes = (size_t)kDecodeSlots * kMaxTileRows * 2 * size
 constexpr size_t kDecodeAccBytes = (size_t)kDecodeSlots * kMaxTileRows * kMaxDv * sizeof(float);
 constexpr size_t kDecodeWorkspaceBytes =
     256 + ((kDecodeCounterBytes + 255) & ~size_t(255)) + kDecodeMlBytes + kDecodeAccBytes;
+
+// Query rows of one work item at most: what the registers hold.
+inline int most_tile_rows(int dqk, bool e4m3) {
+  return dqk == 64 ? kMaxTileRows : dqk == 192 ? 16 : e4m3 ? 24 : kMaxTileRows;
+}
 
 struct DecodeLaunch {
   CacheView cache;
@@ -267,6 +273,7 @@ struct DecodeLaunch {
   cudaStream_t stream;
 };
 cudaError_t launch_decode(const DecodeLaunch& L);
+cudaError_t launch_decode_e4m3(const DecodeLaunch& L);
 
 // Device address of the cache kernels' sticky status word on the current device.
 int* cache_status_ptr();

@@ -123,7 +123,7 @@ int main() {
     for (int& t : tiles) total += t = 1 + rnd(longest);
     const Line l = make_line(total, n_items, 1 + rnd(kMaxDecodeCtas));
     need(l.n >= 1 && l.n <= kMaxDecodeCtas && l.n <= total && l.pieces <= kMaxPieces &&
-             (l.pieces == l.n || l.pieces == l.n * (1 + 6 / l.small)), "line");
+             (l.pieces == l.n || l.pieces == 3 * l.n), "line");
     need(cut(l, 0) == 0 && cut(l, l.pieces) == total, "ends");
     for (int p = 0; p < l.pieces; ++p) need(cut(l, p) < cut(l, p + 1), "pieces hold tiles");
     std::vector<long long> begin;  // first tile of each item

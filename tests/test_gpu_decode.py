@@ -68,7 +68,7 @@ RAGGED = [0, 1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 129, 300]
 @pytest.mark.parametrize("d", [(64, 64), (128, 128), (192, 128)])
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("heads,group", [(1, 1), (3, 2), (2, 8), (2, 9), (1, 16), (2, 17),
-                                         (1, 40)])
+                                         (1, 24), (1, 32), (1, 40), (1, 71)])
 def test_heads_and_lengths(ws, d, kind, heads, group):
     Case(d, kind, RAGGED, heads, group).check(ws)
 
@@ -90,7 +90,7 @@ def test_windows(ws, kind, window):
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("heads,group,n", [(1, 1, 20011), (1, 8, 70001), (2, 12, 40000),
-                                           (16, 1, 5000)])
+                                           (1, 32, 9000), (16, 1, 5000)])
 def test_long_sequences_are_joined(ws, kind, heads, group, n):
     """One sequence shared by up to all CTAs: one level of joining and two."""
     Case((128, 128), kind, [n], heads, group, page=64, peak=2.0).check(ws)

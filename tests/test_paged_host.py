@@ -132,9 +132,9 @@ def test_decode_rejects(kw, code):
 def test_workspace():
     n = binding.attn_decode_workspace_size()
     assert n % 256 == 0
-    # header, counters, and two partial results of 16 rows for each of 7 * 304 pieces
-    slots = 2 * 7 * 304
-    assert n == 256 + -(-4 * slots * 4 // 256) * 256 + slots * 16 * (2 + 128) * 4
+    # header, counters, and two partial results of 32 rows for each of 3 * 304 pieces
+    slots = 2 * 3 * 304
+    assert n == 256 + -(-4 * slots * 4 // 256) * 256 + slots * 32 * (2 + 128) * 4
     assert binding.attn_decode_workspace_init(None, n, 0) == INV
     assert binding.attn_decode_workspace_init(A + 16, n, 0) == INV
     assert binding.attn_decode_workspace_init(A, n - 1, 0) == binding.ATTN_ERR_WORKSPACE_TOO_SMALL
