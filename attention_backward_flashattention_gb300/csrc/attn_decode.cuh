@@ -389,12 +389,8 @@ __device__ __forceinline__ void next_item(const DecodeParams& P, const Line& lin
       w->more = 1;
       return;
     }
-    if (k.piece >= 0) {  // (-1: the first piece is still to come)
-      if (line.pieces == line.n) break;  // a piece for each: nothing is claimed
-      k.piece = line.n + atomicAdd(&P.header->claimed, 1);
-    } else {
-      k.piece = blockIdx.x;
-    }
+    if (line.pieces == line.n) break;  // a piece for each: nothing is claimed
+    k.piece = line.n + atomicAdd(&P.header->claimed, 1);
     if (k.piece >= line.pieces) break;
     k.at = cut(line, k.piece);
     k.stop = cut(line, k.piece + 1);
@@ -462,20 +458,24 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
     if (tid == 0) atomicCAS(P.status, 0, kStatusNotReady);
     return;
   }
+  const long long items = P.items_per_seq;
+  const Line line = make_line(all * items, P.B * items, gridDim.x);
+  if ((int)blockIdx.x >= line.n) return;
   // (threads without sequences: in front of nothing, behind every tile)
-  s_before[tid] = before * P.items_per_seq;
+  s_before[tid] = before * items;
+  if (tid == 0) s_line = line;
+  const long long start = cut(line, blockIdx.x);
   __syncthreads();
-  if (tid == 0) {
-    s_line = make_line(all * P.items_per_seq, (long long)P.B * P.items_per_seq, gridDim.x);
-    s_items[0].more = 0;
-    if ((int)blockIdx.x < s_line.n) {
-      s_walk.piece = -1;
-      s_walk.at = s_walk.stop = 0;
-      next_item<kStep, kKeys>(P, s_line, s_before, kThreads, chunk, s_walk, &s_items[0]);
-    }
+  if (start >= before * items && start < (before + mine) * items) {
+    // this thread's sequences hold the first tile of the CTA's first piece
+    s_walk.piece = blockIdx.x;
+    s_walk.at = start;
+    s_walk.stop = cut(line, blockIdx.x + 1);
+    s_walk.b = b_lo;
+    s_walk.seq_at = before * items;
+    next_item<kStep, kKeys>(P, line, s_before, kThreads, chunk, s_walk, &s_items[0]);
   }
   __syncthreads();
-  if ((int)blockIdx.x >= s_line.n) return;
   const uint32_t ring = smem_u32(smem) + warp * C::kRing;
 
   // Where a step of an item lies.  (What is the same for all steps of an item is
