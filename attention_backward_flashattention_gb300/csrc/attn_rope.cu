@@ -20,6 +20,12 @@
 //   * a block takes several token rows where there are many, computes each
 //     (position, pair) angle once for all heads into shared memory, and has its
 //     first loads, two units a thread, on their way meanwhile.
+// Measured on a GB300 (a plain copy there: 6.78 TB/s): rotation of 537 MB (B 1, T
+// 32768, 16 + 16 heads of 128) 81.6 us, 6.58 TB/s; of 458 MB of ragged (192, 64 of it
+// turned) heads 70.2 us, 6.52 TB/s; append of 16.8 K prompt tokens, 32 query and 8 key
+// heads of 128, into e4m3: 378 MB in 77.9 us, 4.86 TB/s (the conversions' registers
+// leave a third of the warps: 85 registers, 21 warps of 64 on an SM; with 64 registers
+// they spill, 82 us); (192, 128) heads, 336 MB in 59.3 us, 5.66 TB/s.
 #include <algorithm>
 #include <cstring>
 
@@ -39,8 +45,9 @@ int* cache_status_ptr() {
 namespace {
 
 // Threads of a block at most, and blocks on an SM that the registers are to leave
-// room for: many loads on their way (bf16), or the registers that eight-bit
-// conversions need.
+// room for: many loads on their way (bf16: 59.5 us where 512 threads and two
+// blocks take 63.7), or the registers that eight-bit conversions need (76.5 us, and
+// 82 to 104 us with others; the (192, 128) append and the e4m3 append above).
 template <bool E4M3>
 struct Bounds {
   static constexpr int kThreads = E4M3 ? 384 : 256, kBlocks = E4M3 ? 2 : 5;
@@ -50,8 +57,9 @@ constexpr int kMaxAngles = 2048;      // (token, pair) angles of one block at mo
 constexpr int kRounds = 4;            // tokens a thread walks over, where there are many
 
 // Shape of the blocks over `rows` token rows of `units` units each: `side`
-// token rows side by side (about 256 threads, or one row), and
-// up to kRounds of them one after the other as long as every SM has some blocks.
+// token rows side by side (about 256 threads, or one row), and up to kRounds of
+// them one after the other as long as every SM has some blocks (4 and 8 measure
+// alike, 16 loses 4 to 10 %: a block's angles come before its first store).
 struct BlockShape {
   int threads, side, tokens, blocks;
 };

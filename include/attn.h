@@ -345,7 +345,8 @@ int attn_step_host_status(const void* scratch, int B, int H, int T, int dqk, int
 /*
  * Position rotation and the paged key / value cache: what a model needs around
  * the attention above to see positions (training and serving) and to generate
- * token by token (serving).  No counterpart on the pages.
+ * token by token (serving).  No counterpart on the pages.  As with the calls
+ * above, make the first call on a device before any stream capture.
  */
 
 /*
@@ -369,8 +370,8 @@ typedef struct attn_rotation {
  * position, finite, of any size) to the fixed-point form that the kernels
  * read: the fraction of a turn per position, times 2^64.  A position times
  * that word, modulo 2^64, is the angle modulo one turn, so an angle is as exact
- * at position two billion as at position one.  Copy the words to the device
- * once.  Returns ATTN_ERR_INVALID_ARG for NULL, n <= 0 or a rate that is not
+ * at position two billion as at position one (the word is off by at most two
+ * units and 2^-105 of the rate).  Copy the words to the device once.  Returns ATTN_ERR_INVALID_ARG for NULL, n <= 0 or a rate that is not
  * finite.
  */
 int attn_rope_rates(const double* rates_rad, int n, unsigned long long* out);

@@ -100,6 +100,22 @@ def test_long_and_short_together(ws):
     Case((64, 64), "bf16", [30000] + [5] * 40 + [0] * 3 + [4000], 2, 4, page=32).check(ws)
 
 
+@pytest.mark.parametrize("kind,lens", [("bf16", [70001, 64000, 60007, 66000]),
+                                       ("e4m3", [140001, 128000, 120007, 132000])])
+def test_claimed_pieces(ws, kind, lens):
+    """A line long enough that its CTAs claim pieces of it: right, the same bits every time
+    (whichever CTA works on a piece), and the claims are back at zero for the next call."""
+    c = Case((64, 64), kind, lens, 8, 2, page=64)
+    small = Case((64, 64), kind, [100, 0, 3000], 8, 2, page=64)
+    other = small.run(ws)
+    first = c.check(ws)
+    for _ in range(5):
+        got = c.run(ws)
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+        got = small.run(ws)
+        assert torch.equal(got[0], other[0]) and torch.equal(got[1], other[1])
+
+
 def test_many_sequences(ws):
     """More sequences than a block has threads, and than CTAs."""
     lens = [(i * 37) % 90 for i in range(700)]
