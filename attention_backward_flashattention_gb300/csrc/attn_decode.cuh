@@ -20,7 +20,8 @@
 //     memory that only it uses (no block barrier until an item ends).  The
 //     products are m16n8k16 with the keys (then the value columns) as the 16 rows
 //     and the query heads as the 8 columns, so a group of eight heads fills
-//     them (up to four such tiles share a step's registers); m, l and O of the warp's keys stay in registers.
+//     them (up to four such tiles share a step's registers); m, l and O of the
+//     warp's keys stay in registers.
 //   * The warps join in shared memory when the item or the piece ends.  The next
 //     item is known by then, and its first steps are on their way before the
 //     join is done.  An item that lies in one piece is then finished; else the
@@ -155,7 +156,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // later, and what was written before earlier additions is seen here.
 __device__ __forceinline__ int arrive(int* counter) {
   int old;
-  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"
+               : "=r"(old)
+               : "l"(counter)
+               : "memory");
   return old;
 }
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
@@ -355,8 +359,8 @@ struct Walk {
 // it.  before[i]: tiles in front of the sequences i * chunk ..
 template <int STEP, int TILE>
 __device__ __forceinline__ void next_item(const DecodeParams& P, const Line& line,
-                                       const long long* before, int threads, int chunk, Walk& k,
-                                       Item* w) {
+                                          const long long* before, int threads, int chunk,
+                                          Walk& k, Item* w) {
   auto range = [&](int b, int& len) {
     len = __ldg(P.cache.lens + b);
     return key_range(P.cache, P.window, len, STEP, TILE);
@@ -550,89 +554,89 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
   begin_item(&s_items[0]);
   fill_ring();
   for (int cur = 0; s_items[cur].more; cur ^= 1) {
-      // Queries, as the second operand's registers, a tile of eight rows at a
-      // time: row g, the columns that a thread reads of a key row in one 16-byte
-      // load.  c[q][e]: the factor of the scores of row 8q + 2t + e.
-      uint32_t qr[C::kQueriesShared ? 1 : kQT][kQ];
-      float c[kQT][2];
-      {
-        float unit = P.scale_log2;
-        if (E4M3 && P.cache.k.scale) unit *= __ldg(P.cache.k.scale + it->kvh);
-        const int rows = it->rows;
-        const uint16_t* qp = P.q + it->b * P.q_row + (int64_t)it->head * DQK;
-        auto load_tile = [&](int q, uint32_t (&w)[kQ]) {  // what row g was scaled down by
-          const int row = 8 * q + g;
+    // Queries, as the second operand's registers, a tile of eight rows at a
+    // time: row g, the columns that a thread reads of a key row in one 16-byte
+    // load.  c[q][e]: the factor of the scores of row 8q + 2t + e.
+    uint32_t qr[C::kQueriesShared ? 1 : kQT][kQ];
+    float c[kQT][2];
+    {
+      float unit = P.scale_log2;
+      if (E4M3 && P.cache.k.scale) unit *= __ldg(P.cache.k.scale + it->kvh);
+      const int rows = it->rows;
+      const uint16_t* qp = P.q + it->b * P.q_row + (int64_t)it->head * DQK;
+      auto load_tile = [&](int q, uint32_t (&w)[kQ]) {  // what row g was scaled down by
+        const int row = 8 * q + g;
 #pragma unroll
-          for (int j = 0; j < DQK / 32; ++j) {
-            const int col = E4M3 ? 16 * key_chunk<C::kRowK>(j / 2, t4) + 8 * (j % 2)
-                                 : 8 * key_chunk<C::kRowK>(j, t4);
-            const uint4 x = row < rows ? __ldg(reinterpret_cast<const uint4*>(qp + row * DQK + col))
-                                       : make_uint4(0, 0, 0, 0);
-            w[4 * j] = x.x, w[4 * j + 1] = x.y;
-            w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
-          }
-          if constexpr (!E4M3) return 1.f;
-          // to fp16, by a power of two
-          float big = 0.f;
+        for (int j = 0; j < DQK / 32; ++j) {
+          const int col = E4M3 ? 16 * key_chunk<C::kRowK>(j / 2, t4) + 8 * (j % 2)
+                               : 8 * key_chunk<C::kRowK>(j, t4);
+          const uint4 x = row < rows ? __ldg(reinterpret_cast<const uint4*>(qp + row * DQK + col))
+                                     : make_uint4(0, 0, 0, 0);
+          w[4 * j] = x.x, w[4 * j + 1] = x.y;
+          w[4 * j + 2] = x.z, w[4 * j + 3] = x.w;
+        }
+        if constexpr (!E4M3) return 1.f;
+        // to fp16, by a power of two
+        float big = 0.f;
 #pragma unroll
-          for (int i = 0; i < kQ; ++i) big = max3(big, fabsf(bf_lo(w[i])), fabsf(bf_hi(w[i])));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          // 2^e <= big < 2^(e+1); an infinite query makes its row's scores NaN
-          const int e = max((int)(__float_as_uint(big) >> 23) - 127, -100);
-          const float down = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23);
+        for (int i = 0; i < kQ; ++i) big = max3(big, fabsf(bf_lo(w[i])), fabsf(bf_hi(w[i])));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // 2^e <= big < 2^(e+1); an infinite query makes its row's scores NaN
+        const int e = max((int)(__float_as_uint(big) >> 23) - 127, -100);
+        const float down = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23);
 #pragma unroll
-          for (int i = 0; i < kQ; ++i) w[i] = pack_f16(bf_lo(w[i]) * down, bf_hi(w[i]) * down);
-          return e > 127 ? __uint_as_float(0x7FC00000u)
-                         : __uint_as_float((uint32_t)(127 + min(e, 126)) << 23);
-        };
-        if constexpr (C::kQueriesShared) {  // each warp a tile, as every warp reads it
-          for (int q = warp; q < kQT; q += kWarps) {
-            load_tile(q, qr[0]);
+        for (int i = 0; i < kQ; ++i) w[i] = pack_f16(bf_lo(w[i]) * down, bf_hi(w[i]) * down);
+        return e > 127 ? __uint_as_float(0x7FC00000u)
+                       : __uint_as_float((uint32_t)(127 + min(e, 126)) << 23);
+      };
+      if constexpr (C::kQueriesShared) {  // each warp a tile, as every warp reads it
+        for (int q = warp; q < kQT; q += kWarps) {
+          load_tile(q, qr[0]);
 #pragma unroll
-            for (int j = 0; j < kQ / 4; ++j)
-              queries[(q * (kQ / 4) + j) * 32 + lane] =
-                  make_uint4(qr[0][4 * j], qr[0][4 * j + 1], qr[0][4 * j + 2], qr[0][4 * j + 3]);
-          }
-          __syncthreads();
+          for (int j = 0; j < kQ / 4; ++j)
+            queries[(q * (kQ / 4) + j) * 32 + lane] =
+                make_uint4(qr[0][4 * j], qr[0][4 * j + 1], qr[0][4 * j + 2], qr[0][4 * j + 3]);
+        }
+        __syncthreads();
 #pragma unroll
-          for (int q = 0; q < kQT; ++q)
-            for (int e = 0; e < 2; ++e) c[q][e] = unit;
-        } else {
+        for (int q = 0; q < kQT; ++q)
+          for (int e = 0; e < 2; ++e) c[q][e] = unit;
+      } else {
 #pragma unroll
-          for (int q = 0; q < kQT; ++q) {
-            const float up = load_tile(q, qr[q]);
-            c[q][0] = c[q][1] = unit;
-            if constexpr (E4M3) {
-              c[q][0] *= __shfl_sync(0xffffffffu, up, 8 * t4);  // of row 2t, and 2t + 1
-              c[q][1] *= __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
-            }
+        for (int q = 0; q < kQT; ++q) {
+          const float up = load_tile(q, qr[q]);
+          c[q][0] = c[q][1] = unit;
+          if constexpr (E4M3) {
+            c[q][0] *= __shfl_sync(0xffffffffu, up, 8 * t4);  // of row 2t, and 2t + 1
+            c[q][1] *= __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
           }
         }
       }
-      // four registers of tile q's queries
-      auto query = [&](int q, int i) {
-        if constexpr (C::kQueriesShared) return queries[(q * (kQ / 4) + i) * 32 + lane];
-        constexpr int kLast = C::kQueriesShared ? 0 : kQT - 1;
-        const uint32_t* w = qr[q < kLast ? q : kLast] + 4 * i;
-        return make_uint4(w[0], w[1], w[2], w[3]);
-      };
+    }
+    // four registers of tile q's queries
+    auto query = [&](int q, int i) {
+      if constexpr (C::kQueriesShared) return queries[(q * (kQ / 4) + i) * 32 + lane];
+      constexpr int kLast = C::kQueriesShared ? 0 : kQT - 1;
+      const uint32_t* w = qr[q < kLast ? q : kLast] + 4 * i;
+      return make_uint4(w[0], w[1], w[2], w[3]);
+    };
 
-      float acc[kQT][kVT][4];
-      float m[kQT][2], l[kQT][2];  // of rows 8q + 2t + e
+    float acc[kQT][kVT][4];
+    float m[kQT][2], l[kQT][2];  // of rows 8q + 2t + e
 #pragma unroll
-      for (int q = 0; q < kQT; ++q) {
+    for (int q = 0; q < kQT; ++q) {
 #pragma unroll
-        for (int i = 0; i < kVT; ++i) acc[q][i][0] = acc[q][i][1] = acc[q][i][2] = acc[q][i][3] = 0.f;
-        m[q][0] = m[q][1] = -INFINITY;
-        l[q][0] = l[q][1] = 0.f;
-      }
+      for (int i = 0; i < kVT; ++i) acc[q][i][0] = acc[q][i][1] = acc[q][i][2] = acc[q][i][3] = 0.f;
+      m[q][0] = m[q][1] = -INFINITY;
+      l[q][0] = l[q][1] = 0.f;
+    }
 
-      int stage = 0, i = 0;
-      // the last steps are left for when the next item is known (found by one thread
-      // late enough that a piece claimed for it waits for little)
+    int stage = 0, i = 0;
+    // the last steps are left for when the next item is known (found by one thread
+    // late enough that a piece claimed for it waits for little)
 #pragma unroll 1
-      for (int leg = 0; leg < 2; ++leg) {
+    for (int leg = 0; leg < 2; ++leg) {
       const int leg_end = leg == 0 ? max(steps - 4, 0) : steps;
 #pragma unroll 1
       for (; i < leg_end; ++i) {
@@ -643,7 +647,8 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
         // scores, [keys 16n + g, + 8][rows 8q + 2t, + 1]; the chunks of a key row that
         // this thread reads are in two places, by the parity of j
         constexpr bool kLines = C::kRowK % 128 == 0;  // else: chunks 64 bytes apart
-        const uint32_t k0 = ks + g * C::kRowK + ((key_chunk<C::kRowK>(0, t4) ^ swizzle<C::kRowK>(g)) << 4);
+        const uint32_t k0 =
+            ks + g * C::kRowK + ((key_chunk<C::kRowK>(0, t4) ^ swizzle<C::kRowK>(g)) << 4);
         const uint32_t k_at[2] = {k0, kLines ? k0 ^ 16 : k0 + 64};
         float s[kQT][kKT][4];
 #pragma unroll
@@ -767,7 +772,8 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
           // + 2v + 1 (row g + 8).
           const uint32_t v0 = vs + 2 * t4 * C::kRowV +
                               (DV == 128 ? (g ^ swizzle<C::kRowV>(2 * t4)) << 4
-                                         : (((g >> 1) ^ swizzle<C::kRowV>(2 * t4)) << 4) + (g & 1) * 8);
+                                         : (((g >> 1) ^ swizzle<C::kRowV>(2 * t4)) << 4) +
+                                              (g & 1) * 8);
           // of rows 2t and 2t + 1 (and their likes, eight rows further)
           const uint32_t v_at[2] = {v0, (DV == 128 ? v0 ^ 16 : v0) + C::kRowV};
 #pragma unroll
@@ -790,7 +796,8 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
               for (int h = 0; h < 2; ++h) {
                 const uint32_t lo = __byte_perm(w[0][j], w[1][j], h ? 0x7362 : 0x5140);
                 const uint32_t hi = __byte_perm(w[2][j], w[3][j], h ? 0x7362 : 0x5140);
-                const uint32_t a0 = f16x2_lo(lo), a1 = f16x2_hi(lo), a2 = f16x2_lo(hi), a3 = f16x2_hi(hi);
+                const uint32_t a0 = f16x2_lo(lo), a1 = f16x2_hi(lo);
+                const uint32_t a2 = f16x2_lo(hi), a3 = f16x2_hi(hi);
 #pragma unroll
                 for (int q = 0; q < kQT; ++q)
                   mma16816<true>(acc[q][2 * j + h], a0, a1, a2, a3, p[q][n][0], p[q][n][1]);
@@ -818,118 +825,118 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
 
       if (leg == 0 && tid == 0)
         next_item<kStep, kKeys>(P, s_line, s_before, kThreads, chunk, s_walk, &s_items[cur ^ 1]);
-      }
+    }
 
-      // ---- the warps join: the upper half's O to shared memory, the lower half
-      // adds its own, then all threads the halves' ----
+    // ---- the warps join: the upper half's O to shared memory, the lower half
+    // adds its own, then all threads the halves' ----
+#pragma unroll
+    for (int q = 0; q < kQT; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 4);
+        l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 8);
+        l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 16);
+        if (g == 0) s_ml[warp][8 * q + 2 * t4 + e] = make_float2(m[q][e], l[q][e]);
+      }
+    float* const part = joined + warp % C::kHalf * (C::kJoin / 4);
+    auto place = [&](int q, int v, int e) {
+      const int col = E4M3 ? DV / 8 * g + 2 * v + (e >> 1) : 16 * v + g + (e >> 1) * 8;
+      return part + (8 * q + 2 * t4 + (e & 1)) * C::kPitch + col;
+    };
+    if (warp >= C::kHalf) {
 #pragma unroll
       for (int q = 0; q < kQT; ++q)
 #pragma unroll
+        for (int v = 0; v < kVT; ++v)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) *place(q, v, e) = acc[q][v][e];
+    }
+    __syncthreads();  // (the next item is known, too)
+    const Item* const done = it;
+    begin_item(&s_items[cur ^ 1]);
+    if (warp < C::kHalf) {
+#pragma unroll
+      for (int q = 0; q < kQT; ++q) {
+        float f[2], h[2];
+#pragma unroll
         for (int e = 0; e < 2; ++e) {
-          l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 4);
-          l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 8);
-          l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 16);
-          if (g == 0) s_ml[warp][8 * q + 2 * t4 + e] = make_float2(m[q][e], l[q][e]);
+          const int row = 8 * q + 2 * t4 + e;
+          const float2 y = s_ml[warp + C::kHalf][row];
+          const float top = fmaxf(m[q][e], y.x);
+          const float z = top == -INFINITY ? 0.f : top;
+          f[e] = ex2(m[q][e] - z);
+          h[e] = ex2(y.x - z);
+          if (g == 0) s_ml2[warp][row] = make_float2(top, l[q][e] * f[e] + y.y * h[e]);
         }
-      float* const part = joined + warp % C::kHalf * (C::kJoin / 4);
-      auto place = [&](int q, int v, int e) {
-        const int col = E4M3 ? DV / 8 * g + 2 * v + (e >> 1) : 16 * v + g + (e >> 1) * 8;
-        return part + (8 * q + 2 * t4 + (e & 1)) * C::kPitch + col;
-      };
-      if (warp >= C::kHalf) {
 #pragma unroll
-        for (int q = 0; q < kQT; ++q)
+        for (int v = 0; v < kVT; ++v)
 #pragma unroll
-          for (int v = 0; v < kVT; ++v)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) *place(q, v, e) = acc[q][v][e];
-      }
-      __syncthreads();  // (the next item is known, too)
-      const Item* const done = it;
-      begin_item(&s_items[cur ^ 1]);
-      if (warp < C::kHalf) {
-#pragma unroll
-        for (int q = 0; q < kQT; ++q) {
-          float f[2], h[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = 8 * q + 2 * t4 + e;
-            const float2 y = s_ml[warp + C::kHalf][row];
-            const float top = fmaxf(m[q][e], y.x);
-            const float z = top == -INFINITY ? 0.f : top;
-            f[e] = ex2(m[q][e] - z);
-            h[e] = ex2(y.x - z);
-            if (g == 0) s_ml2[warp][row] = make_float2(top, l[q][e] * f[e] + y.y * h[e]);
+          for (int e = 0; e < 4; ++e) {
+            float* at = place(q, v, e);
+            *at = acc[q][v][e] * f[e & 1] + *at * h[e & 1];
           }
-#pragma unroll
-          for (int v = 0; v < kVT; ++v)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float* at = place(q, v, e);
-              *at = acc[q][v][e] * f[e & 1] + *at * h[e & 1];
-            }
-        }
-      }
-      fill_ring();  // of the next item
-      __syncthreads();
-
-      const int b = done->b, head = done->head, rows = done->rows;
-      const ItemParts parts = item_parts(s_line, done->at, done->keys.tiles);
-      const int my_part = done->piece - parts.first;
-      const int my_slot = parts.slot(my_part);
-      const float v_scale = E4M3 && P.cache.v.scale ? __ldg(P.cache.v.scale + done->kvh) : 1.f;
-      for (int e = tid; e < rows * DV / 4; e += kThreads) {
-        const int row = e / (DV / 4), col = (e - row * (DV / 4)) * 4;
-        float top = s_ml2[0][row].x;
-#pragma unroll
-        for (int w = 1; w < C::kHalf; ++w) top = fmaxf(top, s_ml2[w][row].x);
-        const float z = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < C::kHalf; ++w) {
-          const float2 ml = s_ml2[w][row];
-          const float f = ex2(ml.x - z);
-          const float4 y = *reinterpret_cast<const float4*>(joined + w * (C::kJoin / 4) +
-                                                            row * C::kPitch + col);
-          sum += ml.y * f;
-          o.x += y.x * f;
-          o.y += y.y * f;
-          o.z += y.z * f;
-          o.w += y.w * f;
-        }
-        if (parts.count == 1) {
-          store_row4<DV>(P, b, head, row, col, o, sum == 0.f ? 0.f : v_scale / sum);
-          if (col == 0 && P.lse) P.lse[(int64_t)b * P.Hq + head + row] = lse_of(top, sum);
-        } else {
-          __stcg(reinterpret_cast<float4*>(
-                     P.acc + ((int64_t)my_slot * kMaxTileRows + row) * DV + col), o);
-          if (col == 0)
-            __stcg(reinterpret_cast<float2*>(P.ml) + my_slot * kMaxTileRows + row,
-                   make_float2(top, sum));
-        }
-      }
-      __syncthreads();  // the parts are read, and this one is written
-
-      // The last of kJoinParts parts joins them, the last of as many of such groups
-      // joins those, and so on to the whole item.
-      int stride = 1;  // parts of a group that is joined already
-#pragma unroll 1
-      for (int level = 0; stride < parts.count; ++level, stride *= kJoinParts) {
-        const int begin = my_part / (stride * kJoinParts) * (stride * kJoinParts);
-        const Joined j{parts, begin, min(begin + stride * kJoinParts, parts.count), stride};
-        if (tid == 0) {
-          int* counter = P.counters + level * kDecodeSlots + j.slot(0);
-          s_last = arrive(counter) == j.count() - 1;
-          if (s_last) *counter = 0;  // ready for the next call
-        }
-        __syncthreads();
-        if (!s_last) break;
-        join_parts<DV, R, kThreads>(P, j, rows, j.begin == 0 && j.end == parts.count ? -1 : j.slot(0),
-                                    b, head, v_scale, reinterpret_cast<float2*>(joined));
-        __syncthreads();
       }
     }
+    fill_ring();  // of the next item
+    __syncthreads();
+
+    const int b = done->b, head = done->head, rows = done->rows;
+    const ItemParts parts = item_parts(s_line, done->at, done->keys.tiles);
+    const int my_part = done->piece - parts.first;
+    const int my_slot = parts.slot(my_part);
+    const float v_scale = E4M3 && P.cache.v.scale ? __ldg(P.cache.v.scale + done->kvh) : 1.f;
+    for (int e = tid; e < rows * DV / 4; e += kThreads) {
+      const int row = e / (DV / 4), col = (e - row * (DV / 4)) * 4;
+      float top = s_ml2[0][row].x;
+#pragma unroll
+      for (int w = 1; w < C::kHalf; ++w) top = fmaxf(top, s_ml2[w][row].x);
+      const float z = top == -INFINITY ? 0.f : top;
+      float sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < C::kHalf; ++w) {
+        const float2 ml = s_ml2[w][row];
+        const float f = ex2(ml.x - z);
+        const float4 y = *reinterpret_cast<const float4*>(joined + w * (C::kJoin / 4) +
+                                                          row * C::kPitch + col);
+        sum += ml.y * f;
+        o.x += y.x * f;
+        o.y += y.y * f;
+        o.z += y.z * f;
+        o.w += y.w * f;
+      }
+      if (parts.count == 1) {
+        store_row4<DV>(P, b, head, row, col, o, sum == 0.f ? 0.f : v_scale / sum);
+        if (col == 0 && P.lse) P.lse[(int64_t)b * P.Hq + head + row] = lse_of(top, sum);
+      } else {
+        __stcg(reinterpret_cast<float4*>(
+                   P.acc + ((int64_t)my_slot * kMaxTileRows + row) * DV + col), o);
+        if (col == 0)
+          __stcg(reinterpret_cast<float2*>(P.ml) + my_slot * kMaxTileRows + row,
+                 make_float2(top, sum));
+      }
+    }
+    __syncthreads();  // the parts are read, and this one is written
+
+    // The last of kJoinParts parts joins them, the last of as many of such groups
+    // joins those, and so on to the whole item.
+    int stride = 1;  // parts of a group that is joined already
+#pragma unroll 1
+    for (int level = 0; stride < parts.count; ++level, stride *= kJoinParts) {
+      const int begin = my_part / (stride * kJoinParts) * (stride * kJoinParts);
+      const Joined j{parts, begin, min(begin + stride * kJoinParts, parts.count), stride};
+      if (tid == 0) {
+        int* counter = P.counters + level * kDecodeSlots + j.slot(0);
+        s_last = arrive(counter) == j.count() - 1;
+        if (s_last) *counter = 0;  // ready for the next call
+      }
+      __syncthreads();
+      if (!s_last) break;
+      join_parts<DV, R, kThreads>(P, j, rows, j.begin == 0 && j.end == parts.count ? -1 : j.slot(0),
+                                  b, head, v_scale, reinterpret_cast<float2*>(joined));
+      __syncthreads();
+    }
+  }
   // the last CTA leaves the claims at zero
   if (tid == 0 && s_line.pieces > s_line.n) {
     __threadfence();
@@ -972,7 +979,9 @@ cudaError_t launch_dims(const DecodeLaunch& L, const DecodeParams& P) {
     case 1: return launch_rows<DQK, DV, E4M3, 8>(L, P);
     case 2: return launch_rows<DQK, DV, E4M3, 16>(L, P);
     case 3: if constexpr (DQK != 192) return launch_rows<DQK, DV, E4M3, 24>(L, P); break;
-    case 4: if constexpr (DQK == 64 || (DQK == 128 && !E4M3)) return launch_rows<DQK, DV, E4M3, 32>(L, P); break;
+    case 4:
+      if constexpr (DQK == 64 || (DQK == 128 && !E4M3)) return launch_rows<DQK, DV, E4M3, 32>(L, P);
+      break;
   }
   return cudaErrorInvalidValue;
 }

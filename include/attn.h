@@ -371,8 +371,8 @@ typedef struct attn_rotation {
  * read: the fraction of a turn per position, times 2^64.  A position times
  * that word, modulo 2^64, is the angle modulo one turn, so an angle is as exact
  * at position two billion as at position one (the word is off by at most two
- * units and 2^-105 of the rate).  Copy the words to the device once.  Returns ATTN_ERR_INVALID_ARG for NULL, n <= 0 or a rate that is not
- * finite.
+ * units and 2^-105 of the rate).  Copy the words to the device once.  Returns
+ * ATTN_ERR_INVALID_ARG for NULL, n <= 0 or a rate that is not finite.
  */
 int attn_rope_rates(const double* rates_rad, int n, unsigned long long* out);
 
@@ -385,9 +385,9 @@ int attn_rope_rates(const double* rates_rad, int n, unsigned long long* out);
  * positions start at pos0).  Variable length: cu_seqlens_q / cu_seqlens_k as in
  * attn_fwd_ex (host; Tq and Tk are then totals, at most ATTN_MAX_VARLEN_SEQS
  * sequences), sequence by sequence.  A query in front of the first key
- * (Lq > Lk) has a negative position, which turns the other way.  *_row: elements between token rows
- * of each tensor, a multiple of 8 and at least H*d (0: H*d); a slot of a packed
- * (B,T,3,H,d) buffer has 3*H*d.  inverse = 1 turns the other way: the gradient
+ * (Lq > Lk) has a negative position, which turns the other way.  *_row: elements
+ * between token rows of each tensor, a multiple of 8 and at least H*d (0: H*d); a
+ * slot of a packed (B,T,3,H,d) buffer has 3*H*d.  inverse = 1 turns the other way: the gradient
  * with respect to the unrotated tensor from the gradient with respect to the
  * rotated one.  d is 64, 128 or 192; pos0 >= 0 and every position below 2^31.
  * Computed in fp32 and rounded to bf16 once.
@@ -406,8 +406,8 @@ int attn_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int
  * holds both k and v are all described by strides.  Bases and strides are
  * multiples of 16 bytes; distinct elements must not overlap.
  * type ATTN_CACHE_BF16: bf16.  ATTN_CACHE_E4M3: 8-bit floats, each standing
- * for its value times k_scale[head] / v_scale[head] (device fp32, one positive
- * value per key head; NULL: 1).
+ * for its value times k_scale[head] / v_scale[head] (device fp32, one value
+ * per key head, from 2^-100 to 2^100; NULL: 1).
  *
  * Which pages a sequence uses is in its row of a block table (device int32,
  * B rows of max_pages entries, table_stride entries apart): its token t is
