@@ -265,6 +265,14 @@ def test_helpers_reject_shapes():
     assert "CUDA" not in _refused(binding.rope, x, x, rot, out=(x, None))
 
 
+def test_offsets_of_another_length_are_not_read_past_their_end():
+    x = torch.zeros(16, 4, 64, dtype=torch.bfloat16)
+    rot = binding.Rotation([1.0] * 32, device="cpu")
+    for cu_k in ([0, 16], [0, 4, 8, 16], []):
+        assert "same length" in _refused(binding.rope, x, x, rot, cu_seqlens=[0, 8, 16],
+                                         cu_seqlens_k=cu_k)
+
+
 def test_helpers_reject_host_tensors():
     """A host pointer never reaches a kernel."""
     k, v = _tensors()
