@@ -826,6 +826,8 @@ def decode(cache, q, block_table, lens, scale=None, window_left=-1, with_lse=Tru
     if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (B, Hq)
                             or not lse.is_contiguous()):
         raise ValueError("out[1] must be contiguous float32 (sequences, heads)")
+    if workspace is not None and not workspace.is_contiguous():  # (nbytes counts its memory)
+        raise ValueError("workspace must be contiguous")
     index = _device_of(cache.k_cache, q, block_table, lens, workspace, o, lse)
     if scale is None:
         scale = 1.0 / math.sqrt(cache.dqk)

@@ -273,6 +273,14 @@ def test_offsets_of_another_length_are_not_read_past_their_end():
                                          cu_seqlens_k=cu_k)
 
 
+def test_a_broadcast_workspace_is_no_workspace():
+    cache = binding.PagedCache(*_tensors())
+    table, lens = torch.zeros(2, 4, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    ws = torch.zeros(1, dtype=torch.uint8).expand(binding.attn_decode_workspace_size())
+    q = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    assert "workspace" in _refused(binding.decode, cache, q, table, lens, workspace=ws)
+
+
 def test_helpers_reject_host_tensors():
     """A host pointer never reaches a kernel."""
     k, v = _tensors()
