@@ -719,6 +719,9 @@ def rope(q, k, rotation, inverse=False, pos0=0, cu_seqlens=None, cu_seqlens_k=No
         q_out = None if q is None else torch.empty(shape, dtype=torch.bfloat16, device=device)
         k_out = None if k is None else torch.empty(other, dtype=torch.bfloat16, device=device)
     if x.numel() == 0:
+        if q is not None and k is not None and k.numel() > 0:  # no queries: the keys alone
+            cu = cu_seqlens if cu_seqlens_k is None else cu_seqlens_k
+            rope(None, k, rotation, inverse, pos0, cu, None, (None, k_out))
         return q_out, k_out
     cu, cuk = _HostInts(cu_seqlens), _HostInts(cu_seqlens_k)
     rc = load().attn_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B,

@@ -65,6 +65,22 @@ def test_more_queries_than_keys_turn_backwards():
     _check(qo, q, torch.arange(9).cuda() - 5, freq, 0, False)
 
 
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("varlen", [False, True])
+def test_keys_beside_no_queries(varlen, given):
+    """A step without queries still turns its keys."""
+    q, k, freq = _rand(40, 1, 0, 2, 64), _rand(41, 1, 7, 2, 64), inv_freq(64)
+    kw = {}
+    if varlen:
+        q, k, kw = q[0], k[0], dict(cu_seqlens=[0, 0, 0], cu_seqlens_k=[0, 3, 7])
+    if given:
+        kw["out"] = (torch.empty_like(q), torch.full_like(k, 7.0))
+    qo, ko = binding.rope(q, k, binding.Rotation(freq), **kw)
+    assert qo.shape == q.shape
+    pos = [0, 1, 2, 0, 1, 2, 3] if varlen else range(7)
+    _check(ko, k, torch.tensor(list(pos)).cuda(), freq, 0, False)
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_variable_length(inter):
     lq, lk = [5, 0, 1, 130, 17], [9, 3, 1, 130, 40]
