@@ -783,6 +783,8 @@ def cache_append(cache, k, v, block_table, lens, q=None, rotation=None, cu_seqle
             return cache_append(cache, k, v, block_table, lens, q, rotation, cu_seqlens, q_out)
     if q is not None and q_out is None:
         q_out = torch.empty(q_shape, dtype=torch.bfloat16, device=q.device)
+    if T == 0:  # (tensors without elements have no address)
+        return q_out
     cu = _HostInts(cu_seqlens)
     rc = load().attn_cache_append(cache.address, block_table.data_ptr(), width, stride,
                                   lens.data_ptr(), B, T, cu.ptr, k.data_ptr(), k_row,

@@ -154,6 +154,17 @@ def test_unused_rows_are_left_alone(cu):
     c.check(q_out, written=used)
 
 
+@pytest.mark.parametrize("cu", [None, [0, 0, 0]])
+def test_a_step_without_new_tokens(cu):
+    c = Case((64, 64), "bf16", "token", 16, [3, 5], [1, 1], dim=64)
+    none = [x[:0].contiguous() for x in (c.k, c.v, c.q)]
+    got = binding.cache_append(c.cache, none[0], none[1], c.table, c.lens_t(), q=none[2],
+                               rotation=c.rot, cu_seqlens=cu)
+    assert got.shape == (0, 4, 64)
+    assert binding.cache_append(c.cache, none[0], none[1], c.table, c.lens_t()) is None
+    assert torch.equal(bits(c.kc), bits(c.before[0])) and torch.equal(bits(c.vc), bits(c.before[1]))
+
+
 def test_fewer_cached_than_new():
     """lens below the number of new tokens: the ones in front of position 0 are ignored."""
     c = Case((64, 64), "bf16", "token", 16, past=[0], new=[5], dim=64)
