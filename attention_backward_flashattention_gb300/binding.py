@@ -698,6 +698,10 @@ def rope(q, k, rotation, inverse=False, pos0=0, cu_seqlens=None, cu_seqlens_k=No
         B, Tq, Tk = len(cu_seqlens) - 1, shape[0], other[0]
         if cu_seqlens_k is not None and len(cu_seqlens_k) != B + 1:
             raise ValueError("cu_seqlens and cu_seqlens_k must have the same length")
+        if k is None and B >= 0 and cu_seqlens_k is not None:  # the keys that the queries end
+            Tk = int(cu_seqlens_k[-1])
+        if q is None and cu_seqlens_k is not None:
+            cu_seqlens = cu_seqlens_k
     else:
         B, Tq, Tk = shape[0], shape[1], other[1]
     q_row = 0 if q is None else _rows(q, shape, "q")

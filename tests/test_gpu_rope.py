@@ -81,6 +81,19 @@ def test_keys_beside_no_queries(varlen, given):
     _check(ko, k, torch.tensor(list(pos)).cuda(), freq, 0, False)
 
 
+def test_one_side_of_a_variable_length_pair():
+    """Queries without their keys, and keys without their queries, at the pair's positions."""
+    cu, cuk = [0, 2, 2, 7], [0, 6, 9, 14]
+    q, k, rot = _rand(42, 7, 3, 64), _rand(43, 14, 2, 64), binding.Rotation(inv_freq(64))
+    qo, ko = binding.rope(q, k, rot, cu_seqlens=cu, cu_seqlens_k=cuk)
+    pos = torch.tensor([4, 5, 0, 1, 2, 3, 4]).cuda()
+    _check(qo, q, pos, inv_freq(64), 0, False)
+    q1, none = binding.rope(q, None, rot, cu_seqlens=cu, cu_seqlens_k=cuk)
+    assert none is None and torch.equal(q1, qo)
+    none, k1 = binding.rope(None, k, rot, cu_seqlens=cu, cu_seqlens_k=cuk)
+    assert none is None and torch.equal(k1, ko)
+
+
 @pytest.mark.parametrize("inter", [False, True])
 def test_variable_length(inter):
     lq, lk = [5, 0, 1, 130, 17], [9, 3, 1, 130, 40]
