@@ -583,7 +583,7 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
         // 2^e <= big < 2^(e+1); an infinite query makes its row's scores NaN
-        const int e = max((int)(__float_as_uint(big) >> 23) - 127, -100);
+        const int e = max((int)(__float_as_uint(big) >> 23) - 127, -126);
         const float down = __uint_as_float((uint32_t)(127 - min(e, 126)) << 23);
 #pragma unroll
         for (int i = 0; i < kQ; ++i) w[i] = pack_f16(bf_lo(w[i]) * down, bf_hi(w[i]) * down);
@@ -610,6 +610,13 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
           if constexpr (E4M3) {
             c[q][0] *= __shfl_sync(0xffffffffu, up, 8 * t4);  // of row 2t, and 2t + 1
             c[q][1] *= __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
+            // (a factor of zero would make a hidden key's -inf NaN, one of inf a score of
+            // zero; from 2^-126 down all scores are zero for the softmax; NaN stays)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if (c[q][e] < 0x1p-126f) c[q][e] = 0x1p-126f;
+              if (c[q][e] > 0x1p127f) c[q][e] = 0x1p127f;
+            }
           }
         }
       }

@@ -218,6 +218,17 @@ def test_values_that_are_not_finite_stay_in_their_row(ws):
     assert torch.isnan(o[0, 2:]).all() and torch.isfinite(o[1]).all()
 
 
+@pytest.mark.parametrize("q_exp,k_exp,v_exp", [(None, -100, 100), (None, 0, 0), (-100, 100, -100),
+                                               (60, -60, 0), (-60, 60, 0), (-100, -100, 0)])
+def test_e4m3_scales_from_one_end_to_the_other(ws, q_exp, k_exp, v_exp):
+    """Queries of zero (None) and of extreme sizes; products of all factors from 2^-200 on."""
+    c = Case((128, 128), "e4m3", [20, 1, 700], 2, 4, page=16, scales=False)
+    c.q = c.q * 2.0 ** q_exp if q_exp is not None else torch.zeros_like(c.q)
+    c.ks, c.vs = torch.full((2,), 2.0 ** k_exp).cuda(), torch.full((2,), 2.0 ** v_exp).cuda()
+    c.cache = binding.PagedCache(c.kc, c.vc, c.ks, c.vs)
+    c.check(ws)
+
+
 def test_scores_of_minus_infinity_are_an_empty_row(ws):
     c = Case((64, 64), "bf16", [20, 20], 1, 2, page=16)
     c.kc[c.table[0].long()] = 0
@@ -260,6 +271,38 @@ def test_another_stream(ws):
     s.synchronize()
     for o, lse in got:
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_sequences_share_pages(ws, kind):
+    """A prompt in common: the same pages in several rows of the table, and twice in one."""
+    c = Case((128, 128), kind, [500, 500, 470, 512], 2, 4, page=32)
+    c.lens = [500, 490, 470, 512]  # (each sees slots that Case left readable)
+    c.lens_t = torch.tensor(c.lens, dtype=torch.int32).cuda()
+    c.table[1] = c.table[0]
+    c.table[2, :14] = c.table[0, :14]
+    c.table[3, 5] = c.table[3, 4]
+    c.check(ws)
+
+
+@pytest.mark.parametrize("window", [-1, 0, 100])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_no_sequence_has_a_key(ws, kind, window):
+    """A batch of unused rows alone: zeros, and nothing read through a table of -1."""
+    c = Case((128, 128), kind, [0] * 6, 2, 4, page=16, window=window)
+    c.lens_t = torch.tensor([0, -1, -2 ** 31, 0, -7, -2 ** 31 + 1], dtype=torch.int32).cuda()
+    o, lse = c.check(ws)
+    assert (o == 0).all() and (lse == -math.inf).all()
+
+
+def test_whole_parts_of_minus_infinity(ws):
+    """Scores of -inf over the first half of a sequence that many CTAs share."""
+    n, hidden = 20000, 10007
+    c = Case((128, 128), "bf16", [n], 1, 8, page=16)
+    c.q[:, :, 0] = 1.0
+    for j in range(hidden // 16 + 1):
+        c.kc[int(c.table[0, j]), :min(16, hidden - 16 * j), :, 0] = -float("inf")
+    check_decode(c.run(ws), c.ref(hidden={0: range(hidden)}))
 
 
 def test_two_calls_at_once(ws):
