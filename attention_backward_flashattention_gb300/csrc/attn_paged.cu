@@ -7,6 +7,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <limits>
 
 #include "../../include/attn.h"
 #include "attn_internal.h"
@@ -269,7 +270,9 @@ int attn_decode(const attn_paged_cache* cache, const int* block_table, int max_p
   if (rc) return rc;
   if (q == nullptr || o == nullptr || workspace == nullptr || Hq <= 0 || window_left < -1)
     return ATTN_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  // (a factor that is 0 or inf would make a hidden key's -inf, or a score of 0, NaN)
+  if (!(scale >= std::numeric_limits<float>::min()) || !std::isfinite(scale * kLog2e))
+    return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256))
     return ATTN_ERR_INVALID_ARG;
   if (!row_stride(&q_row, Hq, cache->dqk)) return ATTN_ERR_INVALID_ARG;

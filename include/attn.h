@@ -459,17 +459,18 @@ int attn_cache_append(const attn_paged_cache* cache, const int* block_table, int
  * Attention of one new token per sequence over the cache: q (B,Hq,dqk) bf16
  * (rows q_row elements apart; 0: dense), o (B,Hq,dv) bf16, lse (B,Hq) fp32 or
  * NULL.  Query head h uses key head h / (Hq / heads); Hq is a multiple of
- * `heads`.  The token sits at position lens[b] - 1 and sees the keys 0 ..
- * lens[b] - 1, or with window_left >= 0 only lens[b] - 1 - window_left ..
- * lens[b] - 1 (-1: no window).  A row that sees no key (lens[b] <= 0), or
- * whose scores are all -inf, gets O = 0 and LSE = -inf.  Keys and values that
- * a row does not see never touch it, whatever their bits; one that it sees
- * and that is not finite makes the row not finite.
+ * `heads`.  scale: positive, normal and below 2^127.  The token sits at position
+ * lens[b] - 1 and sees the keys 0 .. lens[b] - 1, or with window_left >= 0 only
+ * lens[b] - 1 - window_left .. lens[b] - 1 (-1: no window).  A row that sees no
+ * key (lens[b] <= 0), or whose scores are all -inf, gets O = 0 and LSE = -inf.
+ * Keys and values that a row does not see never touch it, whatever their bits;
+ * one that it sees and that is not finite makes the row not finite (a key whose
+ * score is -inf weighs nothing).
  *
- * The work is split over the keys of all sequences alike, in equal shares; the
- * parts of a row are joined by the last of its CTAs to finish, in a fixed
- * order: results do not depend on timing (they do on the shares, so on the
- * other lengths of the batch).
+ * The work is split over the keys of all sequences alike, in pieces that depend
+ * on the lengths alone; the parts of a row are joined by the last of its CTAs to
+ * finish, in a fixed order: results do not depend on timing (they do on the
+ * pieces, so on the other lengths of the batch).
  *
  * workspace: attn_decode_workspace_size() bytes, 256-byte aligned, initialised
  * ONCE with attn_decode_workspace_init() before its first use; each call

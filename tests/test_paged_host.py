@@ -117,6 +117,11 @@ def test_append_of_nothing_launches_nothing():
     assert _append(T=0, q=None, q_out=None) == binding.ATTN_OK
 
 
+@pytest.mark.parametrize("scale", [1e-45, 1e-39, 3e38])
+def test_decode_rejects_scales_whose_factor_is_no_normal_number(scale):
+    assert _decode(scale=scale) == INV
+
+
 @pytest.mark.parametrize("kw,code", BAD_TABLES + [
     (dict(q=None), INV), (dict(o=None), INV), (dict(q=A + 8), INV), (dict(o=A + 8), INV),
     (dict(lse=A + 2), INV), (dict(Hq=0), INV), (dict(Hq=6), INV), (dict(q_row=128), INV),
