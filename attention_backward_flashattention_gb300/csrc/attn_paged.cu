@@ -214,7 +214,7 @@ int attn_cache_append(const attn_paged_cache* cache, const int* block_table, int
       (q && (!row_stride(&q_row, Hq, cache->dqk) || !row_stride(&q_out_row, Hq, cache->dqk))))
     return ATTN_ERR_INVALID_ARG;
   if ((int64_t)std::max(q ? Hq : 0, cache->heads) * cache->dqk > (1 << 20) ||
-      T > INT32_MAX - 1024)
+      T > INT32_MAX - (1 << 20))
     return ATTN_ERR_UNSUPPORTED;
   rc = check_rotation(rotation, cache->dqk, &L.rot);
   if (rc) return rc;

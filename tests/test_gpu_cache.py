@@ -121,6 +121,23 @@ def test_far_positions_and_long_prompts():
     c.check(c.append())
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,hq,heads,dim,past,new", [
+    ((64, 64), 1, 1, 64, [5, 0, 7, 100], [40000, 3, 0, 31007]),   # many rows side by side
+    ((64, 64), 2, 1, 0, [5, 0], [30000, 3001]),                   # no rotation
+    ((128, 128), 130, 2, 128, [3, 0], [2000, 1501]),              # more units than a block has
+    ((128, 128), 100, 20, 96, [0], [2501]),                       # threads, and nearly so
+    ((192, 128), 16, 16, 64, [777, 0, 1], [3001, 2000, 1])])
+def test_long_walks_over_the_rows(kind, d, hq, heads, dim, past, new):
+    c = Case(d, kind, "token", 64, past, new, hq=hq, heads=heads, begin=d[0] - dim if dim else 0,
+             dim=dim, inter=d[0] == 192)
+    c.check(c.append())
+    q = c.q.clone()
+    got = c.append(q_out=c.q).clone()  # in place
+    c.q = q
+    c.check(got)
+
+
 def test_without_queries_and_in_place():
     c = Case((128, 128), "bf16", "token", 16, past=[3, 9], new=[1, 1], dim=128)
     assert binding.cache_append(c.cache, c.k, c.v, c.table, c.lens_t(), rotation=c.rot) is None
