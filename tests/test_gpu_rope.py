@@ -162,6 +162,19 @@ def test_gradient(inter):
         assert abs(left - right) <= slack
 
 
+@pytest.mark.parametrize("shape", [(3, 5), (7, 2, 64), (2, 3, 4, 64), (1, 1, 1), (0, 4, 64)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_new_outputs_are_like_torch_empty(shape, dtype):
+    want = torch.empty(shape, dtype=dtype, device="cuda")
+    for got in (binding._empty(shape, dtype, want.device),
+                binding._empty(torch.Size(shape), dtype, want.device)):
+        assert got.shape == want.shape and got.stride() == want.stride()
+        assert got.dtype == dtype and got.device == want.device and got.is_contiguous()
+        assert not got.requires_grad
+    with torch.inference_mode():
+        assert binding._empty(shape, dtype, want.device).is_inference()
+
+
 def test_pass_through_bits():
     """Columns that do not turn keep their bits, NaN payloads and infinities among them, and do
     not touch the others."""
