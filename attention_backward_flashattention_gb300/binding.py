@@ -653,9 +653,18 @@ def _empty(shape, dtype, device):
     return _empty_strided(shape, strides, dtype)
 
 
+# (the current device, once CUDA is up)
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
 def _here(index, stream):
-    """Whether a call for device `index` and `stream` runs where the caller is."""
-    return stream is None and index == torch.cuda.current_device()
+    """Whether a call for tensors on device `index` and for `stream` runs where the caller is."""
+    return stream is None and index == _get_device()
+
+
+def _current(index):
+    """Handle of the current stream of the current device, `index`."""
+    return _stream(None) if _raw_stream is None else _raw_stream(index)
 
 
 def _rows(t, shape, name):
@@ -749,7 +758,7 @@ def rope(q, k, rotation, inverse=False, pos0=0, cu_seqlens=None, cu_seqlens_k=No
     rc = load().attn_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B,
                           0 if q is None else shape[-2], 0 if k is None else other[-2], Tq, Tk,
                           shape[-1], q_row, k_row, q_out_row, k_out_row, rotation.address,
-                          int(inverse), int(pos0), cu.ptr, cuk.ptr, _stream(None))
+                          int(inverse), int(pos0), cu.ptr, cuk.ptr, _current(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_rope")
     return q_out, k_out
@@ -811,7 +820,7 @@ def cache_append(cache, k, v, block_table, lens, q=None, rotation=None, cu_seqle
     rc = load().attn_cache_append(cache.address, block_table.data_ptr(), width, stride,
                                   lens.data_ptr(), B, T, cu.ptr, k.data_ptr(), k_row,
                                   v.data_ptr(), v_row, _ptr(q), q_row, _ptr(q_out), out_row, Hq,
-                                  None if rotation is None else rotation.address, _stream(None))
+                                  None if rotation is None else rotation.address, _current(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_append")
     return q_out
@@ -871,7 +880,7 @@ def decode(cache, q, block_table, lens, scale=None, window_left=-1, with_lse=Tru
     rc = load().attn_decode(cache.address, block_table.data_ptr(), width, stride, lens.data_ptr(),
                             B, q.data_ptr(), q_row, o.data_ptr(),
                             None if lse is None else lse.data_ptr(), Hq, int(window_left),
-                            float(scale), workspace.data_ptr(), workspace.nbytes, _stream(None))
+                            float(scale), workspace.data_ptr(), workspace.nbytes, _current(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode")
     return o, lse

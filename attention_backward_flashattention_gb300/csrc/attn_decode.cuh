@@ -28,8 +28,8 @@
 //     part goes to the workspace, and the CTA that arrives last joins the parts
 //     in the order of their pieces.  Over kJoinParts parts are joined in levels.
 // Measured on a GB300 (a plain copy there: 6.78 TB/s): 64 sequences up to 8190 long,
-// 8 key heads, group 4, bf16: 1.03 GB in 163 - 166 us, 6.2 - 6.3 TB/s; 128 sequences up
-// to 16384, group 8, e4m3: 2.15 GB in 352 - 366 us, 5.9 - 6.1 TB/s; one of 250007
+// 8 key heads, group 4, bf16: 1.03 GB in 162 - 166 us, 6.2 - 6.4 TB/s; 128 sequences up
+// to 16384, group 8, e4m3: 2.15 GB in 333 - 370 us by card, 5.8 - 6.4 TB/s; one of 250007
 // tokens, two key heads: 256 MB in 55 us, 4.7 TB/s, of which 5 us pass before the
 // memory is busy and 10 us in the three levels of joins after it.
 // Legacy matrix instructions are enough here: at the measured 6.8 TB/s a bf16
