@@ -617,7 +617,7 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
     };
 
     float acc[kQT][kVT][4];
-    float m[kQT][2], l[kQT][2];  // of rows 8q + 2t + e
+    float m[kQT][2], l[kQT][2];  // of rows 8q + 2t + e (m: the largest score, without c)
 #pragma unroll
     for (int q = 0; q < kQT; ++q) {
 #pragma unroll
@@ -692,7 +692,10 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
         cp_commit();
 
         // running maximum and sum; keys that take no part are -inf.  (The factors c
-        // are positive: the largest score has the largest product.)
+        // are positive: the largest score has the largest product.)  The maximum is
+        // kept as a score, not as a product with c: c times a difference of scores is
+        // exact to 2^-23 of itself at any size, and 0 for the largest, where a rounded
+        // product of 2^29 is off by up to 16.
         if (seen != kAllRows) {
 #pragma unroll
           for (int n = 0; n < kKT; ++n)
@@ -711,7 +714,6 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
             x[q][e] = fmaxf(s[q][0][e], s[q][0][2 + e]);
 #pragma unroll
             for (int n = 1; n < kKT; ++n) x[q][e] = max3(x[q][e], s[q][n][e], s[q][n][2 + e]);
-            x[q][e] *= c[q][e];
             rises |= x[q][e] > m[q][e];  // (of this thread's keys: enough to know)
           }
         if (__any_sync(0xffffffffu, rises)) {
@@ -724,7 +726,7 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 8));
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 16));
               y = fmaxf(y, m[q][e]);
-              const float f = m[q][e] == -INFINITY ? 0.f : ex2(m[q][e] - y);
+              const float f = m[q][e] == -INFINITY ? 0.f : ex2((m[q][e] - y) * c[q][e]);
               m[q][e] = y;
               l[q][e] *= f;
 #pragma unroll
@@ -738,14 +740,14 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
         uint32_t p[kQT][kKT][2], rest[kQT][kKT][2];
 #pragma unroll
         for (int q = 0; q < kQT; ++q) {
-          const float z0 = m[q][0] == -INFINITY ? 0.f : -m[q][0];
-          const float z1 = m[q][1] == -INFINITY ? 0.f : -m[q][1];
+          const float z0 = m[q][0] == -INFINITY ? 0.f : m[q][0];
+          const float z1 = m[q][1] == -INFINITY ? 0.f : m[q][1];
 #pragma unroll
           for (int n = 0; n < kKT; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float p0 = ex2(fmaf(s[q][n][2 * h], c[q][0], z0));
-              const float p1 = ex2(fmaf(s[q][n][2 * h + 1], c[q][1], z1));
+              const float p0 = ex2((s[q][n][2 * h] - z0) * c[q][0]);
+              const float p1 = ex2((s[q][n][2 * h + 1] - z1) * c[q][1]);
               l[q][0] += p0;
               l[q][1] += p1;
               if constexpr (E4M3) {
@@ -823,10 +825,13 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
 
     // ---- the warps join: the upper half's O to shared memory, the lower half
     // adds its own, then all threads the halves' ----
+    // (From here on m is the product with c, rounded as a plain fp32 form rounds its
+    // scores.  One that overflows makes the row not finite.)
 #pragma unroll
     for (int q = 0; q < kQT; ++q)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
+        if (m[q][e] != -INFINITY) m[q][e] *= c[q][e];
         l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 4);
         l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 8);
         l[q][e] += __shfl_xor_sync(0xffffffffu, l[q][e], 16);

@@ -465,7 +465,7 @@ int attn_cache_append(const attn_paged_cache* cache, const int* block_table, int
  * key (lens[b] <= 0), or whose scores are all -inf, gets O = 0 and LSE = -inf.
  * Keys and values that a row does not see never touch it, whatever their bits;
  * one that it sees and that is not finite makes the row not finite (a key whose
- * score is -inf weighs nothing).
+ * score is -inf weighs nothing), and so does a largest score beyond fp32.
  *
  * The work is split over the keys of all sequences alike, in pieces that depend
  * on the lengths alone; the parts of a row are joined by the last of its CTAs to
