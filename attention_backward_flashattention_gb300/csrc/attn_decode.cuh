@@ -44,8 +44,9 @@
 // much error to O as its own rounding to bf16 does.  An e4m3 cache is widened to
 // fp16 (exact), and so are the queries, scaled per row by a power of two to a
 // largest value in [1, 2) (exact but for elements below 2^-14 of the row's
-// largest, which lose bits below 2^-24 of it); the probabilities are fp16 (11
-// bits against the cache's 4).
+// largest, which lose bits below 2^-24 of it); the probabilities are fp16, 11
+// bits against the cache's 4, for weights down to 2^-29 of the largest that the
+// warp has seen (kLift); the least, below 2^-40, are zero.
 #pragma once
 
 #include <algorithm>
@@ -172,6 +173,9 @@ struct Cfg {
   static constexpr int kThreads = kWarps * 32;
   static constexpr int kHalf = kWarps / 2;
   static constexpr int kTile = kWarps * kStep;
+  // fp16 probabilities are 2^15 times as large until the warps join: 11 bits from the
+  // largest down to 2^-29 of it, some down to 2^-40 (fp16 ends at 2^-14 and 2^-25).
+  static constexpr float kLift = E4M3 ? 15.f : 0.f, kDrop = E4M3 ? 0x1p-15f : 1.f;
   // 32 query rows of 128 columns leave no registers for the queries themselves.
   static constexpr bool kQueriesShared = R == 32 && DQK == 128;
   static_assert(!(kQueriesShared && E4M3), "(their scales would have to be shared too)");
@@ -746,8 +750,9 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
           for (int n = 0; n < kKT; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float p0 = ex2((s[q][n][2 * h] - z0) * c[q][0]);
-              const float p1 = ex2((s[q][n][2 * h + 1] - z1) * c[q][1]);
+              const float d0 = s[q][n][2 * h] - z0, d1 = s[q][n][2 * h + 1] - z1;
+              const float p0 = ex2(E4M3 ? fmaf(d0, c[q][0], C::kLift) : d0 * c[q][0]);
+              const float p1 = ex2(E4M3 ? fmaf(d1, c[q][1], C::kLift) : d1 * c[q][1]);
               l[q][0] += p0;
               l[q][1] += p1;
               if constexpr (E4M3) {
@@ -863,8 +868,8 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
           const float2 y = s_ml[warp + C::kHalf][row];
           const float top = fmaxf(m[q][e], y.x);
           const float z = top == -INFINITY ? 0.f : top;
-          f[e] = ex2(m[q][e] - z);
-          h[e] = ex2(y.x - z);
+          f[e] = ex2(m[q][e] - z) * C::kDrop;
+          h[e] = ex2(y.x - z) * C::kDrop;
           if (g == 0) s_ml2[warp][row] = make_float2(top, l[q][e] * f[e] + y.y * h[e]);
         }
 #pragma unroll

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from attention_backward_flashattention_gb300 import binding
-from tests.paged_common import BF16_HALF, bits, make_cache, make_table
+from tests.paged_common import BF16_HALF, bits, decode64, make_cache, make_table
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +120,33 @@ def test_an_infinite_query_of_an_empty_row(ws, kind):
                             torch.tensor([0, 20], dtype=torch.int32).cuda(), workspace=ws)
     assert (o[0] == 0).all() and (lse[0] == -math.inf).all()
     assert torch.isfinite(o[1]).all() and torch.isfinite(lse[1]).all()
+
+
+@pytest.mark.parametrize("d", [(64, 64), (128, 128), (192, 128)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("octaves", [4, 12.3, 18.4, 22.4, 27])
+@pytest.mark.parametrize("n,peak,heads", [(700, 0, 1), (700, 333, 2), (3000, 17, 1)])
+def test_a_long_flat_tail_behind_one_large_weight(ws, d, kind, octaves, n, peak, heads):
+    """One key weighs 2^octaves times each other and has a value of 0: what is left is the
+    tail, and none of it may be lost beside the peak."""
+    page, group = 16, 4
+    table, pages = make_table([n], page, 3)
+    g = torch.Generator(device="cpu").manual_seed(n + int(octaves))
+    kc = torch.zeros(pages, page, heads, d[0])
+    vc = torch.rand(pages, page, heads, d[1], generator=g) + 1
+    at = (int(table[0, peak // page]), peak % page)
+    kc[at[0], at[1], :, 0], vc[at[0], at[1]] = 256.0, 0.0
+    kc, vc = kc.to(DTYPE[kind]).cuda(), vc.to(DTYPE[kind]).cuda()
+    q = torch.zeros(1, heads * group, d[0], dtype=torch.bfloat16).cuda()
+    q[..., 0] = 1.0
+    scale = torch.tensor(octaves * math.log(2.0) / 256).item()
+    o, lse = binding.decode(binding.PagedCache(kc, vc), q, table,
+                            torch.tensor([n], dtype=torch.int32).cuda(), scale=scale, workspace=ws)
+    ro, rl, _, _ = decode64(q, kc, vc, table, [n], page, scale)
+    # a weight: rounded to 11 bits over an e4m3 cache, to 16 else; its exponent, up to 15 + octaves
+    # in size, is a sum and a product in fp32, and the exponential is good to 2^-22; the sums
+    # over n keys 2^-23 of the (positive) terms each at most
+    rel = (2.0 ** -11 if kind == "e4m3" else 2.0 ** -16) + (15 + octaves) * 2.0 ** -23 \
+        + 2.0 ** -22 + 2 * n * 2.0 ** -23
+    assert ((o.double() - ro).abs() <= (BF16_HALF + rel * (1 + BF16_HALF)) * ro.abs()).all()
+    assert ((lse.double() - rl).abs() <= rel + 2.0 ** -22 * rl.abs()).all()
