@@ -150,6 +150,14 @@ __device__ __forceinline__ int arrive(int* counter) {
                : "memory");
   return old;
 }
+// The product of three positive factors, the largest with the least first: no step leaves
+// the range unless the product does.  A NaN stays.
+__device__ __forceinline__ float product3(float a, float b, float c) {
+  const float lo = fminf(a, b), hi = fmaxf(a, b), mid = fmaxf(lo, fminf(hi, c));
+  const float p = fminf(lo, c) * fmaxf(hi, c) * mid;
+  const float bc = b * c;
+  return bc != bc ? bc : p;
+}
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
@@ -551,8 +559,8 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
     uint32_t qr[C::kQueriesShared ? 1 : kQT][kQ];
     float c[kQT][2];
     {
-      float unit = P.scale_log2;
-      if (E4M3 && P.cache.k.scale) unit *= __ldg(P.cache.k.scale + it->kvh);
+      const float unit = P.scale_log2;
+      const float k_scale = E4M3 && P.cache.k.scale ? __ldg(P.cache.k.scale + it->kvh) : 1.f;
       const int rows = it->rows;
       const uint16_t* qp = P.q + it->b * P.q_row + (int64_t)it->head * DQK;
       auto load_tile = [&](int q, uint32_t (&w)[kQ]) {  // what row g was scaled down by
@@ -599,8 +607,9 @@ decode_kernel(const __grid_constant__ DecodeParams P) {
           const float up = load_tile(q, qr[q]);
           c[q][0] = c[q][1] = unit;
           if constexpr (E4M3) {
-            c[q][0] *= __shfl_sync(0xffffffffu, up, 8 * t4);  // of row 2t, and 2t + 1
-            c[q][1] *= __shfl_sync(0xffffffffu, up, 8 * t4 + 4);
+            const float f = product3(unit, k_scale, up);
+            c[q][0] = __shfl_sync(0xffffffffu, f, 8 * t4);  // of row 2t, and 2t + 1
+            c[q][1] = __shfl_sync(0xffffffffu, f, 8 * t4 + 4);
             // (a factor of zero would make a hidden key's -inf NaN, one of inf a score of
             // zero; from 2^-126 down all scores are zero for the softmax; NaN stays)
 #pragma unroll

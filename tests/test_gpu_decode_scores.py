@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from attention_backward_flashattention_gb300 import binding
-from tests.paged_common import BF16_HALF, bits, decode64, make_cache, make_table
+from tests.paged_common import (BF16_HALF, bits, check_decode, decode64, make_cache, make_table)
 
 pytestmark = pytest.mark.gpu
 
@@ -150,3 +150,23 @@ def test_a_long_flat_tail_behind_one_large_weight(ws, d, kind, octaves, n, peak,
         + 2.0 ** -22 + 2 * n * 2.0 ** -23
     assert ((o.double() - ro).abs() <= (BF16_HALF + rel * (1 + BF16_HALF)) * ro.abs()).all()
     assert ((lse.double() - rl).abs() <= rel + 2.0 ** -22 * rl.abs()).all()
+
+
+@pytest.mark.parametrize("q_exp,k_exp,scale_exp,k_size", [(-122, 100, 28, -12), (124, -80, -64, 0),
+                                                          (-122, 100, 20, -6), (60, 60, -125, 0)])
+def test_e4m3_factors_of_which_two_alone_leave_the_range(ws, q_exp, k_exp, scale_exp, k_size):
+    """The softmax scale, the keys' scale and the queries' size: their product is an ordinary
+    factor, the product of two of them is not."""
+    lens, page, heads, group, d = [1, 2, 20, 300], 16, 2, 4, 128
+    table, pages = make_table(lens, page, 5)
+    kc = (make_cache(pages, page, heads, d, "e4m3", "token", 6).float() * 2.0 ** k_size).to(
+        torch.float8_e4m3fn)
+    vc = make_cache(pages, page, heads, d, "e4m3", "token", 7)
+    g = torch.Generator(device="cpu").manual_seed(8)
+    q = (torch.randn(len(lens), heads * group, d, generator=g).clamp(-3, 3)
+         * 2.0 ** q_exp).to(torch.bfloat16).cuda()
+    ks, vs = torch.full((heads,), 2.0 ** k_exp).cuda(), torch.full((heads,), 1 / 64).cuda()
+    scale = 2.0 ** scale_exp
+    got = binding.decode(binding.PagedCache(kc, vc, ks, vs), q, table,
+                         torch.tensor(lens, dtype=torch.int32).cuda(), scale=scale, workspace=ws)
+    check_decode(got, decode64(q, kc, vc, table, lens, page, scale, -1, ks, vs))
