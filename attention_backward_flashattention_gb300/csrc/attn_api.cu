@@ -44,6 +44,13 @@ int num_sms_current() {
   return cache[dev];
 }
 
+// The band's bounds.  No key is further than Tk from a query of its sequence: a longer
+// bound sees as much, and the kernels' sums with it would wrap.
+void set_window(SeqShape* sh, int causal, int window_left, int window_right) {
+  sh->wl = std::min(window_left, sh->Tk);
+  sh->wr = causal ? 0 : std::min(window_right, sh->Tk);
+}
+
 // Common shape checks of the forward and backward entry points.  cu / cuk:
 // query / key offsets of a variable-length batch (cuk == cu when the keys
 // share the queries' offsets).  Returns ATTN_OK or an error.
@@ -398,8 +405,7 @@ int attn_fwd_ex(const void* q, const void* k, const void* v, void* o, float* lse
   L.sh.nq_units = cdiv(Tq, kFwdRows);
   L.sh.causal = causal ? 1 : 0;
   L.sh.band_off = varlen ? 0 : Tk - Tq;
-  L.sh.wl = window_left;
-  L.sh.wr = causal ? 0 : window_right;
+  set_window(&L.sh, causal, window_left, window_right);
   L.sh.descending = 0;
   // Rank-major forward order when every head's K and V fit in L2 together
   // (measured: the GPT-2-shaped layer, 25 MB of K and V, 8 % faster than
@@ -505,8 +511,7 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
   L.sh.nk_tiles = cdiv(Tk, kTile);
   L.sh.causal = causal ? 1 : 0;
   L.sh.band_off = varlen ? 0 : Tk - Tq;
-  L.sh.wl = window_left;
-  L.sh.wr = causal ? 0 : window_right;
+  set_window(&L.sh, causal, window_left, window_right);
   L.sh.descending = deterministic ? 1 : 0;
   rc = set_block_mask(&L.sh, block_mask, mask_batches, mask_heads, B, H, Tq, Tk, cu_seqlens,
                       cuk);
