@@ -175,6 +175,13 @@ def _stream(s):
     return int(s)
 
 
+def _c_int(v):
+    """v as the nearest int that C's has room for (ctypes would cut off the upper bits): a window
+    longer than any sequence stays one, and a position out of range is refused by the library."""
+    v = int(v)
+    return v if -2 ** 31 <= v < 2 ** 31 else 2 ** 31 - 1 if v > 0 else -2 ** 31
+
+
 class _HostInts:
     """Keeps a host int32 array alive for the duration of a call."""
 
@@ -210,7 +217,7 @@ def attn_fwd_window(q, k, v, o, lse, B, H, Tq, Tk, dqk, dv, causal, window_left,
                     scale, cu_seqlens=None, layout=LAYOUT_BTHD, stream=None) -> int:
     cu = _HostInts(cu_seqlens)
     return load().attn_fwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Tq, Tk,
-                                  dqk, dv, int(causal), int(window_left), int(window_right),
+                                  dqk, dv, int(causal), _c_int(window_left), _c_int(window_right),
                                   float(scale), cu.ptr, layout, _stream(stream))
 
 
@@ -220,7 +227,7 @@ def attn_bwd_window(q, k, v, o, dO, lse, dq, dk, dv_out, B, H, Tq, Tk, dqk, dv, 
     cu = _HostInts(cu_seqlens)
     return load().attn_bwd_window(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse),
                                   _ptr(dq), _ptr(dk), _ptr(dv_out), B, H, Tq, Tk, dqk, dv,
-                                  int(causal), int(window_left), int(window_right),
+                                  int(causal), _c_int(window_left), _c_int(window_right),
                                   float(scale), cu.ptr, layout, int(deterministic),
                                   _ptr(workspace), int(workspace_bytes), _stream(stream))
 
@@ -230,7 +237,7 @@ def attn_fwd_ex(q, k, v, o, lse, B, H, Tq, Tk, dqk, dv, causal, window_left, win
                 cu_seqlens_k=None, layout=LAYOUT_BTHD, stream=None) -> int:
     cq, ck = _HostInts(cu_seqlens_q), _HostInts(cu_seqlens_k)
     return load().attn_fwd_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, H, Tq, Tk, dqk,
-                              dv, int(causal), int(window_left), int(window_right),
+                              dv, int(causal), _c_int(window_left), _c_int(window_right),
                               _ptr(block_mask), int(mask_batches), int(mask_heads), float(scale),
                               cq.ptr, ck.ptr, layout, _stream(stream))
 
@@ -242,7 +249,7 @@ def attn_bwd_ex(q, k, v, o, dO, lse, dq, dk, dv_out, B, H, Tq, Tk, dqk, dv, caus
     cq, ck = _HostInts(cu_seqlens_q), _HostInts(cu_seqlens_k)
     return load().attn_bwd_ex(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse), _ptr(dq),
                               _ptr(dk), _ptr(dv_out), B, H, Tq, Tk, dqk, dv, int(causal),
-                              int(window_left), int(window_right), _ptr(block_mask),
+                              _c_int(window_left), _c_int(window_right), _ptr(block_mask),
                               int(mask_batches), int(mask_heads), float(scale), cq.ptr, ck.ptr,
                               layout, int(deterministic), _ptr(workspace), int(workspace_bytes),
                               _stream(stream))
@@ -407,7 +414,7 @@ def attn_rope(q, k, q_out, k_out, B, Hq, Hk, Tq, Tk, d, q_row, k_row, q_out_row,
     cq, ck = _HostInts(cu_seqlens_q), _HostInts(cu_seqlens_k)
     return load().attn_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B, Hq, Hk, Tq, Tk, d,
                             q_row, k_row, q_out_row, k_out_row, _struct(rotation), int(inverse),
-                            int(pos0), cq.ptr, ck.ptr, _stream(stream))
+                            _c_int(pos0), cq.ptr, ck.ptr, _stream(stream))
 
 
 def attn_cache_append(cache, block_table, max_pages, table_stride, lens, B, T, cu_seqlens, k,
@@ -437,7 +444,7 @@ def attn_decode(cache, block_table, max_pages, table_stride, lens, B, q, q_row, 
                 window_left, scale, workspace, workspace_bytes, stream=None) -> int:
     return load().attn_decode(_struct(cache), _ptr(block_table), max_pages, table_stride,
                               _ptr(lens), B, _ptr(q), q_row, _ptr(o), _ptr(lse), Hq,
-                              int(window_left), float(scale), _ptr(workspace),
+                              _c_int(window_left), float(scale), _ptr(workspace),
                               int(workspace_bytes), _stream(stream))
 
 
@@ -573,7 +580,7 @@ class Rotation:
         signed = [w - (1 << 64) if w >> 63 else w for w in words]
         self.rates = torch.tensor(signed, dtype=torch.int64, device=device)
         self.begin, self.dim, self.interleaved = int(begin), 2 * len(words), bool(interleaved)
-        self.struct = _RotationStruct(self.rates.data_ptr(), self.begin, self.dim,
+        self.struct = _RotationStruct(self.rates.data_ptr(), _c_int(self.begin), self.dim,
                                       ROPE_PAIRS if interleaved else ROPE_HALVES)
         self.address = ctypes.addressof(self.struct)
 
@@ -594,6 +601,8 @@ class PagedCache:
         if k_cache.dtype not in kinds or v_cache.dtype != k_cache.dtype:
             raise ValueError("the caches must both be bfloat16 or both float8_e4m3fn")
         pages, page_size, heads, dqk = k_cache.shape
+        if max(k_cache.shape) > 2 ** 31 - 1:
+            raise ValueError("a cache's sizes must be below 2^31")
         for t in (k_cache, v_cache):
             if t.stride(3) != 1:
                 raise ValueError("the columns of a cache row must be adjacent")
@@ -758,7 +767,7 @@ def rope(q, k, rotation, inverse=False, pos0=0, cu_seqlens=None, cu_seqlens_k=No
     rc = load().attn_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B,
                           0 if q is None else shape[-2], 0 if k is None else other[-2], Tq, Tk,
                           shape[-1], q_row, k_row, q_out_row, k_out_row, rotation.address,
-                          int(inverse), int(pos0), cu.ptr, cuk.ptr, _current(index))
+                          int(inverse), _c_int(pos0), cu.ptr, cuk.ptr, _current(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_rope")
     return q_out, k_out
@@ -879,7 +888,7 @@ def decode(cache, q, block_table, lens, scale=None, window_left=-1, with_lse=Tru
         workspace = decode_workspace(index)
     rc = load().attn_decode(cache.address, block_table.data_ptr(), width, stride, lens.data_ptr(),
                             B, q.data_ptr(), q_row, o.data_ptr(),
-                            None if lse is None else lse.data_ptr(), Hq, int(window_left),
+                            None if lse is None else lse.data_ptr(), Hq, _c_int(window_left),
                             float(scale), workspace.data_ptr(), workspace.nbytes, _current(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode")

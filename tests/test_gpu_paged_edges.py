@@ -1,0 +1,68 @@
+"""The rotation's, the cache's and the decode's helpers at the edges of what they take: integers
+beyond 32 bits."""
+import pytest
+import torch
+
+from attention_backward_flashattention_gb300 import binding
+from tests.paged_common import inv_freq, make_cache, make_table
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from attention_backward_flashattention_gb300 import build
+    build.build()
+    binding.attn_cache_status()
+
+
+def _rand(seed, *shape):
+    g = torch.Generator(device="cpu").manual_seed(seed)
+    return torch.randn(shape, generator=g).to(torch.bfloat16).cuda()
+
+
+def _serving(lens=(100, 7, 300), page=16, heads=2, group=4, d=64):
+    table, pages = make_table(list(lens), page, 3)
+    cache = binding.PagedCache(make_cache(pages, page, heads, d, "bf16", "token", 4),
+                               make_cache(pages, page, heads, d, "bf16", "token", 5))
+    q = _rand(6, len(lens), heads * group, d)
+    return cache, q, table, torch.tensor(lens, dtype=torch.int32).cuda()
+
+
+# ---- integers beyond 32 bits --------------------------------------------------
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31, 2 ** 32, 2 ** 32 + 3, 2 ** 70])
+def test_windows_longer_than_any_sequence(window):
+    cache, q, table, lens = _serving()
+    want = binding.decode(cache, q, table, lens)
+    got = binding.decode(cache, q, table, lens, window_left=window)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    x = _rand(7, 1, 200, 2, 64)
+    a = binding.forward(x, x, x, window=(window, 0))
+    b = binding.forward(x, x, x, window=(200, 0))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ga = binding.backward(x, x, x, a[0], x, a[1], window=(window, 0), deterministic=True)
+    gb = binding.backward(x, x, x, b[0], x, b[1], window=(200, 0), deterministic=True)
+    assert all(torch.equal(s, t) for s, t in zip(ga, gb))
+
+
+@pytest.mark.parametrize("window", [-2, -2 ** 31 - 1, -2 ** 32, -2 ** 32 + 5])
+def test_negative_windows_are_refused(window):
+    cache, q, table, lens = _serving()
+    with pytest.raises(binding.AttnError):
+        binding.decode(cache, q, table, lens, window_left=window)
+
+
+@pytest.mark.parametrize("pos0", [2 ** 31, 2 ** 32, 2 ** 32 + 5, -1, -2 ** 32 + 5])
+def test_positions_beyond_32_bits_are_refused(pos0):
+    x = _rand(8, 1, 4, 2, 64)
+    with pytest.raises(binding.AttnError):
+        binding.rope(x, x, binding.Rotation(inv_freq(64)), pos0=pos0)
+
+
+@pytest.mark.parametrize("begin", [2 ** 32, 2 ** 32 + 16, -2 ** 32])
+def test_columns_beyond_32_bits_are_refused(begin):
+    x = _rand(8, 1, 4, 2, 64)
+    with pytest.raises(binding.AttnError):
+        binding.rope(x, x, binding.Rotation(inv_freq(32), begin=begin))
