@@ -626,15 +626,7 @@ int attn_bwd_status(const void* workspace, void* stream) {
 }
 
 int attn_fwd_status(void* stream) {
-  int* p = fwd_status_ptr();
-  if (!p) return ATTN_ERR_CUDA;
-  int st = 0;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemcpyAsync(&st, p, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess)
-    return ATTN_ERR_CUDA;
-  if (cudaMemsetAsync(p, 0, sizeof(int), s) != cudaSuccess) return ATTN_ERR_CUDA;
-  if (cudaStreamSynchronize(s) != cudaSuccess) return ATTN_ERR_CUDA;
-  return st;
+  return take_status(fwd_status_ptr(), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -76,6 +76,9 @@ int bwd_pair_smem_bytes();
 
 // Device address of the forward kernels' status word on the current device.
 int* fwd_status_ptr();
+// Reads a sticky device status word and clears it, in one step on `stream`, which it
+// synchronises.  Returns the word, or ATTN_ERR_CUDA.
+int take_status(int* status, cudaStream_t stream);
 // Device address of forward work-item counter `slot` on the current device.
 constexpr int kFwdClaimSlots = 256;
 int* fwd_claim_ptr(int slot);

@@ -309,15 +309,7 @@ int attn_decode(const attn_paged_cache* cache, const int* block_table, int max_p
 }
 
 int attn_cache_status(void* stream) {
-  int* p = cache_status_ptr();
-  if (!p) return ATTN_ERR_CUDA;
-  int st = 0;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaMemcpyAsync(&st, p, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess)
-    return ATTN_ERR_CUDA;
-  if (cudaMemsetAsync(p, 0, sizeof(int), s) != cudaSuccess) return ATTN_ERR_CUDA;
-  if (cudaStreamSynchronize(s) != cudaSuccess) return ATTN_ERR_CUDA;
-  return st;
+  return take_status(cache_status_ptr(), static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -489,7 +489,8 @@ int attn_decode(const attn_paged_cache* cache, const int* block_table, int max_p
 /*
  * Synchronises `stream`, returns the sticky device status of attn_cache_append
  * and attn_decode on the current device (ATTN_OK, ATTN_ERR_BAD_PAGE or
- * ATTN_ERR_WORKSPACE_NOT_READY; the first since the last read) and clears it.
+ * ATTN_ERR_WORKSPACE_NOT_READY; the first since the last read) and clears it, in
+ * one step: what a call on another stream reports meanwhile is kept for the next read.
  */
 int attn_cache_status(void* stream);
 

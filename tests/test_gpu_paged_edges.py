@@ -1,5 +1,7 @@
 """The rotation's, the cache's and the decode's helpers at the edges of what they take: integers
-beyond 32 bits."""
+beyond 32 bits, and the device status."""
+import threading
+
 import pytest
 import torch
 
@@ -66,3 +68,76 @@ def test_columns_beyond_32_bits_are_refused(begin):
     x = _rand(8, 1, 4, 2, 64)
     with pytest.raises(binding.AttnError):
         binding.rope(x, x, binding.Rotation(inv_freq(32), begin=begin))
+
+
+# ---- the device status ------------------------------------------------------------
+def test_no_error_is_lost_between_reading_and_clearing_the_status():
+    """A call on another stream reports a bad page while the status is read all the time:
+    every such report is read once the call is done."""
+    cache, q, table, lens = _serving(lens=(5,))
+    bad = table.clone()
+    bad[:] = -1
+    ws = binding.decode_workspace()
+    out = binding.decode(cache, q, bad, lens, workspace=ws)
+    torch.cuda.synchronize()
+    assert binding.attn_cache_status() == binding.ATTN_ERR_BAD_PAGE
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    rounds, index = 300, torch.cuda.current_device()
+    done, go = threading.Event(), threading.Event()
+    failed = []
+
+    def worker():
+        try:
+            torch.cuda.set_device(index)
+            for _ in range(rounds):
+                if not go.wait(60):
+                    raise RuntimeError("not started")
+                go.clear()
+                binding.decode(cache, q, bad, lens, workspace=ws, out=out, stream=a)
+                a.synchronize()
+                done.set()
+        except Exception as e:  # (for the reader to see)
+            failed.append(e)
+            done.set()
+
+    t = threading.Thread(target=worker)
+    t.start()
+    lost = 0
+    for _ in range(rounds):
+        done.clear()
+        go.set()
+        found = 0
+        while not done.is_set():
+            found += binding.attn_cache_status(b) == binding.ATTN_ERR_BAD_PAGE
+        found += binding.attn_cache_status(b) == binding.ATTN_ERR_BAD_PAGE
+        lost += found == 0
+        if failed:
+            break
+    t.join(60)
+    assert not failed, failed
+    assert lost == 0 and binding.attn_cache_status() == binding.ATTN_OK
+
+
+def test_status_read_on_many_threads():
+    """Each report is read by one of the readers, by one alone."""
+    cache, q, table, lens = _serving(lens=(5,))
+    bad = table.clone()
+    bad[:] = -1
+    ws = binding.decode_workspace()
+    index = torch.cuda.current_device()
+    for _ in range(20):
+        binding.decode(cache, q, bad, lens, workspace=ws)
+        torch.cuda.synchronize()
+        got = []
+
+        def read():
+            torch.cuda.set_device(index)
+            s = torch.cuda.Stream()
+            got.append(binding.attn_cache_status(s))
+
+        readers = [threading.Thread(target=read) for _ in range(8)]
+        for r in readers:
+            r.start()
+        for r in readers:
+            r.join(60)
+        assert sorted(got) == [binding.ATTN_ERR_BAD_PAGE] + [binding.ATTN_OK] * 7
