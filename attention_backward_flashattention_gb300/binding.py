@@ -763,9 +763,11 @@ def rope(q, k, rotation, inverse=False, pos0=0, cu_seqlens=None, cu_seqlens_k=No
             cu = cu_seqlens if cu_seqlens_k is None else cu_seqlens_k
             rope(None, k, rotation, inverse, pos0, cu, None, (None, k_out))
         return q_out, k_out
+    if k is not None and k.numel() == 0:  # no keys: the queries alone, in front of the first
+        k = None
     cu, cuk = _HostInts(cu_seqlens), _HostInts(cu_seqlens_k)
-    rc = load().attn_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B,
-                          0 if q is None else shape[-2], 0 if k is None else other[-2], Tq, Tk,
+    rc = load().attn_rope(_ptr(q), _ptr(k), _ptr(q_out), None if k is None else _ptr(k_out),
+                          B, 0 if q is None else shape[-2], 0 if k is None else other[-2], Tq, Tk,
                           shape[-1], q_row, k_row, q_out_row, k_out_row, rotation.address,
                           int(inverse), _c_int(pos0), cu.ptr, cuk.ptr, _current(index))
     if rc != ATTN_OK:
@@ -884,6 +886,8 @@ def decode(cache, q, block_table, lens, scale=None, window_left=-1, with_lse=Tru
         device = q.device
         o = _empty((B, Hq, cache.dv), torch.bfloat16, device)
         lse = _empty((B, Hq), torch.float32, device) if with_lse else None
+    if B == 0:  # (tensors without elements have no address)
+        return o, lse
     if workspace is None:
         workspace = decode_workspace(index)
     rc = load().attn_decode(cache.address, block_table.data_ptr(), width, stride, lens.data_ptr(),

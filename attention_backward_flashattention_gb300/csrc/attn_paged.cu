@@ -145,7 +145,8 @@ int attn_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16))
     return ATTN_ERR_INVALID_ARG;
-  if (B <= 0 || Tq <= 0 || Tk <= 0 || pos0 < 0 || (q && Hq <= 0) || (k && Hk <= 0))
+  if (B <= 0 || Tq < 0 || Tk < 0 || pos0 < 0 || (q && (Hq <= 0 || Tq == 0)) ||
+      (k && (Hk <= 0 || Tk == 0)))
     return ATTN_ERR_INVALID_ARG;
   if (!head_size(d)) return ATTN_ERR_UNSUPPORTED;
   if ((q && (!row_stride(&q_row, Hq, d) || !row_stride(&q_out_row, Hq, d))) ||

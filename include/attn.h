@@ -382,7 +382,7 @@ int attn_rope_rates(const double* rates_rad, int n, unsigned long long* out);
  * output may be its input (in place), and must not overlap it otherwise.
  * Positions are those of attn_fwd: key j of a sequence is at pos0 + j, query
  * i at pos0 + i + (Tk - Tq) (pass Tk = Tq when only q is given and its
- * positions start at pos0).  Variable length: cu_seqlens_q / cu_seqlens_k as in
+ * positions start at pos0; Tk = 0 is taken where k is NULL, Tq = 0 where q is).  Variable length: cu_seqlens_q / cu_seqlens_k as in
  * attn_fwd_ex (host; Tq and Tk are then totals, at most ATTN_MAX_VARLEN_SEQS
  * sequences), sequence by sequence.  A query in front of the first key
  * (Lq > Lk) has a negative position, which turns the other way.  *_row: elements

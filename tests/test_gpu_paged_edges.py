@@ -1,12 +1,12 @@
 """The rotation's, the cache's and the decode's helpers at the edges of what they take: integers
-beyond 32 bits, and the device status."""
+beyond 32 bits, sizes of zero, and the device status."""
 import threading
 
 import pytest
 import torch
 
 from attention_backward_flashattention_gb300 import binding
-from tests.paged_common import inv_freq, make_cache, make_table
+from tests.paged_common import inv_freq, make_cache, make_table, rotate64, rotation_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -68,6 +68,50 @@ def test_columns_beyond_32_bits_are_refused(begin):
     x = _rand(8, 1, 4, 2, 64)
     with pytest.raises(binding.AttnError):
         binding.rope(x, x, binding.Rotation(inv_freq(32), begin=begin))
+
+
+# ---- sizes of zero --------------------------------------------------------------
+@pytest.mark.parametrize("width", [0, 4])
+@pytest.mark.parametrize("given", [False, True])
+def test_decode_of_an_empty_batch(width, given):
+    cache, q, _, _ = _serving()
+    table = torch.zeros(0, width, dtype=torch.int32, device="cuda")
+    lens = torch.zeros(0, dtype=torch.int32, device="cuda")
+    out = (torch.empty(0, 8, 64, dtype=torch.bfloat16, device="cuda"),
+           torch.empty(0, 8, device="cuda")) if given else None
+    o, lse = binding.decode(cache, q[:0], table, lens, out=out)
+    assert o.shape == (0, 8, 64) and o.dtype == torch.bfloat16 and o.is_cuda
+    assert lse.shape == (0, 8) and lse.dtype == torch.float32
+    if given:
+        assert o is out[0] and lse is out[1]
+    else:
+        assert binding.decode(cache, q[:0], table, lens, with_lse=False)[1] is None
+    new = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    assert binding.cache_append(cache, new, new, table, lens, q=q[:0]).shape == (0, 8, 64)
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("varlen", [False, True])
+def test_queries_beside_no_keys(varlen, given):
+    """Keys of no rows: the queries still turn, all of them in front of the first key."""
+    q, k, freq = _rand(9, 1, 7, 2, 64), _rand(10, 1, 0, 3, 64), inv_freq(64)
+    pos, kw = torch.arange(7) - 7 + 20, dict(pos0=20)
+    if varlen:
+        q, k = q[0], k[0]
+        kw.update(cu_seqlens=[0, 3, 7], cu_seqlens_k=[0, 0, 0])
+        pos = torch.tensor([-3, -2, -1, -4, -3, -2, -1]) + 20
+    if given:
+        kw["out"] = (torch.full_like(q, 7.0), torch.empty_like(k))
+    rot = binding.Rotation(freq)
+    qo, ko = binding.rope(q, k, rot, **kw)
+    assert ko.shape == k.shape
+    want, mag = rotate64(q.reshape(7, 2, 64), pos.cuda(), freq, 0, False)
+    assert ((qo.reshape(7, 2, 64).double() - want).abs() <= rotation_bound(want, mag)).all()
+    if given:
+        assert qo is kw["out"][0]
+    empty = binding.rope(q[..., :0, :, :], k, rot, pos0=20) if not varlen else \
+        binding.rope(q[:0], k, rot, cu_seqlens=[0, 0], cu_seqlens_k=[0, 0])
+    assert empty[0].numel() == 0 and empty[1].numel() == 0
 
 
 # ---- the device status ------------------------------------------------------------

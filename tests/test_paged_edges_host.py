@@ -47,3 +47,18 @@ def test_sizes_of_a_cache_beyond_32_bits_are_refused():
     one = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="2\\^31"):
         binding.PagedCache(one.expand(2 ** 32 + 3, 1, 1, 64), one.expand(2 ** 32 + 3, 1, 1, 64))
+
+
+A = 0x10000  # an aligned, never-dereferenced stand-in address
+
+
+@pytest.mark.parametrize("q,k,tq,tk,code", [
+    (A, A, 0, 4, binding.ATTN_ERR_INVALID_ARG), (A, A, 4, 0, binding.ATTN_ERR_INVALID_ARG),
+    (A, None, 4, -1, binding.ATTN_ERR_INVALID_ARG), (None, A, -1, 4, binding.ATTN_ERR_INVALID_ARG),
+    (A, None, 0, 0, binding.ATTN_ERR_INVALID_ARG),
+    (A, None, 2 ** 31 - 1, 0, binding.ATTN_ERR_UNSUPPORTED)])
+def test_rotation_of_one_side_beside_none(q, k, tq, tk, code):
+    """Only the side that is not given may have no rows."""
+    rot = binding._RotationStruct(A, 0, 64, 0)
+    assert binding.attn_rope(q, k, q, k, 1, 2, 2, tq, tk, 64, 0, 0, 0, 0, rot, stream=0,
+                             pos0=1 if code == binding.ATTN_ERR_UNSUPPORTED else 0) == code
