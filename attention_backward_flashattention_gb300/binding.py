@@ -585,12 +585,25 @@ class Rotation:
         self.address = ctypes.addressof(self.struct)
 
 
+def _rows_apart(t):
+    """Whether the rows of a cache tensor (pages, page_size, heads, d) have their own memory each,
+    as those of any slice or permutation of a dense tensor have."""
+    extent = t.shape[3]
+    for stride, size in sorted(zip(t.stride()[:3], t.shape[:3])):
+        if size > 1:
+            if stride < extent:
+                return False
+            extent += stride * (size - 1)
+    return True
+
+
 class PagedCache:
     """A paged key / value cache over the caller's tensors.
 
     k_cache (pages, page_size, heads, dqk) and v_cache (pages, page_size, heads, dv),
     bf16 or float8_e4m3fn, with any strides whose columns are adjacent (a cache kept
-    as (pages, heads, page_size, d) is passed transposed).  k_scale, v_scale: fp32
+    as (pages, heads, page_size, d) is passed transposed; one with broadcast dimensions can be
+    read, but not appended to).  k_scale, v_scale: fp32
     per key head, the value of one stored unit of an e4m3 cache (None: 1)."""
 
     def __init__(self, k_cache, v_cache, k_scale=None, v_scale=None):
@@ -614,6 +627,7 @@ class PagedCache:
                 raise ValueError("k_scale and v_scale must be contiguous fp32, one per key head, "
                                  "on the cache's device")
         self.k_cache, self.v_cache, self.k_scale, self.v_scale = k_cache, v_cache, k_scale, v_scale
+        self.rows_apart = _rows_apart(k_cache) and _rows_apart(v_cache)
         self.page_size, self.heads, self.dqk, self.dv = page_size, heads, dqk, v_cache.shape[3]
         self.struct = _CacheStruct(
             k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale), _ptr(v_scale),
@@ -803,6 +817,9 @@ def cache_append(cache, k, v, block_table, lens, q=None, rotation=None, cu_seqle
     B, width, stride = _check_tables(cache, block_table, lens)
     k_shape, v_shape, heads = k.shape, v.shape, cache.heads
     T = k_shape[0]
+    if not cache.rows_apart:
+        raise ValueError("the rows of k_cache and v_cache must have their own memory each to be "
+                         "appended to")
     if k_shape != (T, heads, cache.dqk) or v_shape != (T, heads, cache.dv):
         raise ValueError("k and v must be (T, heads, d) with the cache's heads and the same T")
     if cu_seqlens is not None and len(cu_seqlens) != B + 1:

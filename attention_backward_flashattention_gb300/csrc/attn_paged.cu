@@ -100,6 +100,24 @@ int check_cache(const attn_paged_cache* c, const int* table, int max_pages, long
   return ATTN_OK;
 }
 
+// Whether no two rows of d columns of a cache side share memory: each dimension steps over
+// all that the narrower ones cover.  Tokens written to rows that do share it would race.
+bool rows_apart(const attn_paged_cache* c, long long page, long long token, long long head,
+                int d) {
+  struct {
+    long long stride;
+    int size;
+  } dims[3] = {{page, c->num_pages}, {token, c->page_size}, {head, c->heads}};
+  std::sort(dims, dims + 3, [](const auto& a, const auto& b) { return a.stride < b.stride; });
+  __int128 extent = d;
+  for (const auto& dim : dims) {
+    if (dim.size == 1) continue;
+    if (dim.stride < extent) return false;
+    extent += (__int128)dim.stride * (dim.size - 1);
+  }
+  return true;
+}
+
 // SMs of the current device (asked once for each).
 int sm_count() {
   static std::atomic<int> known[64];
@@ -208,6 +226,11 @@ int attn_cache_append(const attn_paged_cache* cache, const int* block_table, int
   if (rc) return rc;
   if (k == nullptr || v == nullptr || (q == nullptr) != (q_out == nullptr) || T < 0 ||
       (q && Hq <= 0))
+    return ATTN_ERR_INVALID_ARG;
+  if (!rows_apart(cache, cache->k_page_stride, cache->k_token_stride, cache->k_head_stride,
+                  cache->dqk) ||
+      !rows_apart(cache, cache->v_page_stride, cache->v_token_stride, cache->v_head_stride,
+                  cache->dv))
     return ATTN_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(q, 16) || !aligned(q_out, 16))
     return ATTN_ERR_INVALID_ARG;

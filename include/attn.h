@@ -404,7 +404,9 @@ int attn_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int
  * k_token_stride + head * k_head_stride + c, in elements (v likewise), so
  * (pages, tokens, heads, d), (pages, heads, tokens, d) and one buffer that
  * holds both k and v are all described by strides.  Bases and strides are
- * multiples of 16 bytes; distinct elements must not overlap.
+ * multiples of 16 bytes.  To be appended to, rows must have their own memory, and
+ * each stride be as long as all that the shorter ones cover (else
+ * ATTN_ERR_INVALID_ARG); the decode only reads, and takes any.
  * type ATTN_CACHE_BF16: bf16.  ATTN_CACHE_E4M3: 8-bit floats, each standing
  * for its value times k_scale[head] / v_scale[head] (device fp32, one value
  * per key head, from 2^-100 to 2^100; NULL: 1).

@@ -62,3 +62,49 @@ def test_rotation_of_one_side_beside_none(q, k, tq, tk, code):
     rot = binding._RotationStruct(A, 0, 64, 0)
     assert binding.attn_rope(q, k, q, k, 1, 2, 2, tq, tk, 64, 0, 0, 0, 0, rot, stream=0,
                              pos0=1 if code == binding.ATTN_ERR_UNSUPPORTED else 0) == code
+
+
+def _append(**kw):
+    a = dict(k=A, v=A, k_scale=None, v_scale=None, k_page_stride=16 * 4 * 64,
+             k_token_stride=4 * 64, k_head_stride=64, v_page_stride=16 * 4 * 64,
+             v_token_stride=4 * 64, v_head_stride=64, type=0, num_pages=10, page_size=16, heads=4,
+             dqk=64, dv=64)
+    a.update(kw)
+    # (no new tokens: nothing is launched)
+    return binding.attn_cache_append(binding._CacheStruct(**a), A, 4, 4, A, 2, 0, None, A, 0, A, 0,
+                                     None, 0, None, 0, 0, stream=0)
+
+
+@pytest.mark.parametrize("kw,ok", [
+    (dict(), True),
+    (dict(k_token_stride=64, k_head_stride=16 * 64), True),              # head-major pages
+    (dict(k_page_stride=64, k_token_stride=640, k_head_stride=10240), True),  # pages innermost
+    (dict(num_pages=1, k_page_stride=0, v_page_stride=0), True),
+    (dict(page_size=1, k_token_stride=0, v_token_stride=0), True),
+    (dict(heads=1, k_head_stride=0, v_head_stride=0), True),
+    (dict(v_page_stride=2 ** 34, num_pages=2 ** 31 - 1), True),
+    (dict(k_page_stride=0), False), (dict(v_page_stride=0), False),
+    (dict(k_token_stride=0), False), (dict(v_head_stride=0), False),
+    (dict(k_head_stride=56), False),                  # heads of 64 columns 56 apart
+    (dict(k_token_stride=3 * 64), False),             # tokens inside their neighbours' heads
+    (dict(v_page_stride=15 * 4 * 64), False),         # pages that share a token
+    (dict(k_token_stride=64, k_head_stride=64), False),
+    (dict(type=1, k_head_stride=48), False)])
+def test_append_wants_rows_with_their_own_memory(kw, ok):
+    assert _append(**kw) == (binding.ATTN_OK if ok else binding.ATTN_ERR_INVALID_ARG)
+
+
+def test_a_broadcast_cache_is_not_appended_to():
+    full = torch.zeros(6, 16, 2, 64, dtype=torch.bfloat16)
+    table, lens = torch.zeros(2, 4, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    new = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    for shared in (full[:1].expand(6, 16, 2, 64), full[:, :1].expand(6, 16, 2, 64),
+                   full[:, :, :1].expand(6, 16, 2, 64),
+                   full.flatten().as_strided((6, 16, 2, 64), (1024, 128, 64, 1))):
+        for cache in (binding.PagedCache(shared, full), binding.PagedCache(full, shared)):
+            with pytest.raises(ValueError, match="own memory"):
+                binding.cache_append(cache, new, new, table, lens)
+    big = torch.zeros(6, 3, 32, 4, 64, dtype=torch.bfloat16)
+    for own in (full, full[::2, ::3, 1:], big[:, 1], big[:, 0, ::2, :, :].transpose(1, 2),
+                big.permute(2, 0, 1, 3, 4)[:, :, 0], full[:1].expand(1, 16, 2, 64)):
+        assert binding.PagedCache(own, own).rows_apart
