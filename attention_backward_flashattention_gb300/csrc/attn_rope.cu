@@ -4,10 +4,11 @@
 // Mathematics.  Pair i of a head at position p turns by p * w_i.  The rate w_i
 // is stored as a fraction of a turn times 2^64, so p * rate modulo 2^64 is the
 // angle modulo one turn with no loss at far positions (in fp32 the product
-// p * w_i at p = 10^6 is off by 0.03 rad).  Its top 32 bits, as a signed
-// fraction, go to sincospif, whose argument is then in [-1, 1): the angle
-// handed over is off by at most pi * 2^-24, of the order of sincospif's own
-// rounding.  Negative positions (the inverse rotation negates p) work by two's
+// p * w_i at p = 10^6 is off by 0.03 rad).  The nearest quarter turn is taken off
+// in whole numbers, and what is left, to 2^-33 of a half turn, goes to sincospif
+// as an argument in [-1/4, 1/4), rounded to 2^-24 of itself: next to a zero of the
+// sine or the cosine the small one of the two has as many right bits as the large
+// one.  Negative positions (the inverse rotation negates p) work by two's
 // complement.  The rotation is two products and a sum in fp32, rounded to the
 // output's type once.
 //
@@ -117,9 +118,14 @@ __device__ __forceinline__ void fill_angles(float2* sc, const int* pos, int toke
     const int t = i / pairs, pair = i - t * pairs;
     const long long p = inverse ? -(long long)pos[t] : (long long)pos[t];
     const unsigned long long turn = (unsigned long long)p * __ldg(rot.rates + pair);
+    // turn = quarter * 2^62 + rest, -2^61 <= rest < 2^61: bits 30 .. 61 are rest / 2^30
+    const uint32_t quarter = ((uint32_t)(turn >> 61) + 1) >> 1;
+    const float rest = (float)(int)(uint32_t)(turn >> 30);
     float s, c;
-    sincospif((float)(int)(turn >> 32) * 4.656612873077393e-10f /* 2^-31 */, &s, &c);
-    sc[((t * 4 + ((pair & 7) >> 1)) * units + (pair >> 3)) * 2 + (pair & 1)] = make_float2(c, s);
+    sincospif(rest * 0x1p-33f, &s, &c);
+    const float x = quarter & 1 ? -s : c, y = quarter & 1 ? c : s;
+    sc[((t * 4 + ((pair & 7) >> 1)) * units + (pair >> 3)) * 2 + (pair & 1)] =
+        quarter & 2 ? make_float2(-x, -y) : make_float2(x, y);
   }
 }
 
