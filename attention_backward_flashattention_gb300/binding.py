@@ -659,15 +659,39 @@ class _On:
 
 
 # Uninitialised memory on the current device without torch.empty's way through its dispatcher,
-# which takes about 3 us after a launch (two outputs: 16 us a decode call, 11 this way)
+# which takes about 3 us after a launch (two outputs: 16 us a decode call, 11 this way).  Where
+# that way is looked at (modes, the filling of new memory in deterministic mode) it is taken.
 _empty_strided = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None),
                          "_empty_strided_cuda", None)
+_dispatch_modes = getattr(torch._C, "_len_torch_dispatch_stack", None)
+_function_modes = getattr(torch._C, "_len_torch_function_stack", None)
+if _dispatch_modes is None or _function_modes is None:
+    _empty_strided = None
+_empty_is_known = False
+
+
+def _know_empty(device):
+    """The private function is used only where it does what this file takes it to do."""
+    global _empty_strided, _empty_is_known
+    try:
+        got = _empty_strided((2, 3), (3, 1), torch.float32)
+        want = torch.empty((2, 3), dtype=torch.float32, device=device)
+        same = all(getattr(got, a) == getattr(want, a)
+                   for a in ("shape", "dtype", "device", "requires_grad", "layout"))
+        if not same or got.stride() != want.stride():
+            _empty_strided = None
+    except Exception:  # (whatever another version of it raises)
+        _empty_strided = None
+    _empty_is_known = True
 
 
 def _empty(shape, dtype, device):
     """torch.empty(shape, dtype=dtype, device=device) for the current CUDA device."""
     shape = tuple(shape)
-    if _empty_strided is None or 0 in shape:
+    if not _empty_is_known and _empty_strided is not None:
+        _know_empty(device)
+    if (_empty_strided is None or 0 in shape or _dispatch_modes() or _function_modes()
+            or torch.are_deterministic_algorithms_enabled()):
         return torch.empty(shape, dtype=dtype, device=device)
     strides, n = (1,), 1
     for d in shape[:0:-1]:

@@ -1,5 +1,5 @@
 """The rotation's, the cache's and the decode's helpers at the edges of what they take: integers
-beyond 32 bits, sizes of zero, and the device status."""
+beyond 32 bits, sizes of zero, torch's modes, and the device status."""
 import threading
 
 import pytest
@@ -112,6 +112,45 @@ def test_queries_beside_no_keys(varlen, given):
     empty = binding.rope(q[..., :0, :, :], k, rot, pos0=20) if not varlen else \
         binding.rope(q[:0], k, rot, cu_seqlens=[0, 0], cu_seqlens_k=[0, 0])
     assert empty[0].numel() == 0 and empty[1].numel() == 0
+
+
+# ---- torch's modes ----------------------------------------------------------------
+def test_outputs_are_seen_by_dispatch_modes_and_deterministic_filling():
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Seen(TorchDispatchMode):
+        def __init__(self):
+            super().__init__()
+            self.calls = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            self.calls.append(str(func))
+            return func(*args, **(kwargs or {}))
+
+    with Seen() as seen:
+        binding._empty((3, 5), torch.bfloat16, torch.device("cuda", 0))
+    assert any("empty" in c for c in seen.calls)
+    was = torch.are_deterministic_algorithms_enabled()
+    try:
+        torch.use_deterministic_algorithms(True)
+        x = binding._empty((3, 5), torch.bfloat16, torch.device("cuda", 0))
+        assert torch.isnan(x).all()  # as torch.empty fills new memory there
+    finally:
+        torch.use_deterministic_algorithms(was)
+    x = binding._empty((3, 5), torch.float32, torch.device("cuda", 0))
+    assert x.shape == (3, 5) and x.is_contiguous()
+
+
+def test_another_meaning_of_the_private_allocation_is_not_used(monkeypatch):
+    device = torch.device("cuda", torch.cuda.current_device())
+    for other in (lambda *a: torch.zeros(2, 3),
+                  lambda *a: torch.empty(3, 2, device=device).t(),
+                  lambda a, b: None):
+        monkeypatch.setattr(binding, "_empty_strided", other)
+        monkeypatch.setattr(binding, "_empty_is_known", False)
+        x = binding._empty((4, 6), torch.bfloat16, device)
+        assert x.shape == (4, 6) and x.is_contiguous() and x.is_cuda
+        assert x.dtype == torch.bfloat16 and binding._empty_strided is None
 
 
 # ---- the device status ------------------------------------------------------------
