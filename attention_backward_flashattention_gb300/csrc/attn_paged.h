@@ -102,8 +102,6 @@ __host__ __device__ inline int64_t token_at(const CacheSide& s, int page, int in
 
 // The decode's line of tiles.  A warp steps over `step` keys (16, or 32 of an
 // e4m3 cache); a tile is a step of each of its CTA's warps.
-constexpr int kMaxStepKeys = 32;
-constexpr int kMaxTileKeys = 6 * kMaxStepKeys;
 constexpr int kJoinParts = 8;   // parts of an item joined at a time
 
 struct KeyRange {
