@@ -9,8 +9,9 @@
 // Bound: memory.  Every cached key and value is read once, for 2 * group flops
 // per byte (bf16): the read of the cache is the floor.  What the layout does
 // about it:
-//   * A work item is a (sequence, key head, tile of up to 32 of the query heads
-//     that share it), so one read serves such a group.
+//   * A work item is a (sequence, key head, tile of the query heads that share it),
+//     so one read serves such a tile: up to 32 heads, 24 of 128 columns over an e4m3
+//     cache, 16 of (192, 128) (what the registers hold; larger groups are read again).
 //   * The keys of all items, in tiles, are one line that is cut into pieces
 //     whose places depend on the lengths alone: a first piece per CTA, then
 //     smaller ones that the CTAs claim as they get done (make_line).  The grid

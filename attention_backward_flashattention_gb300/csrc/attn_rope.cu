@@ -53,9 +53,15 @@ constexpr int kRounds = 4;            // tokens a thread walks over, where there
 
 // Append: as many threads as an SM has room for at 64 registers, in blocks of about
 // kBlockThreads or of one token's units.  Units of a thread on their way (kDepth), and
-// its rows of a chunk (kRounds): measured for the appends above, 2 and 2 take 56 us in
-// bf16 (2 and 4: 59, 3 and 4: 63: more in flight costs a memory that reads and writes at
-// once), 3 and 4 take 63 us into e4m3 (2 and 4: 64, 3 and 2: 66, 3 and 8: 67).
+// its rows of a chunk (kRounds), by the cache's type: prompts of 10 to 26 K tokens, in us,
+//                       2 and 2   2 and 4   3 and 4   4 and 4
+//   bf16, (192, 128)        57        59        62        62
+//   bf16, 128               68        68        72        76
+//   bf16, 64                43        43        44        44
+//   e4m3, (192, 128)        55        55        55        57
+//   e4m3, 128               68        65        63        64
+//   e4m3, 64                51        45        45        47
+// (2 and 1: 49 to 89.)  More in flight costs a memory that reads and writes at once.
 constexpr int kAppendThreads = 1024, kBlockThreads = 256;
 template <bool E4M3>
 struct Append {
