@@ -688,11 +688,12 @@ def _know_empty(device):
 def _empty(shape, dtype, device):
     """torch.empty(shape, dtype=dtype, device=device) for the current CUDA device."""
     shape = tuple(shape)
-    if not _empty_is_known and _empty_strided is not None:
-        _know_empty(device)
     if (_empty_strided is None or 0 in shape or _dispatch_modes() or _function_modes()
             or torch.are_deterministic_algorithms_enabled()):
         return torch.empty(shape, dtype=dtype, device=device)
+    if not _empty_is_known:
+        _know_empty(device)
+        return _empty(shape, dtype, device)
     strides, n = (1,), 1
     for d in shape[:0:-1]:
         n *= d
