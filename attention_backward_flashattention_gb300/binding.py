@@ -44,7 +44,8 @@ EXPORTED = ("attn_fwd", "attn_bwd_workspace_size", "attn_bwd", "attn_bwd_status"
             "attn_step_host_status", "attn_fwd_window", "attn_bwd_window", "attn_fwd_ex",
             "attn_bwd_ex", "attn_debug_cache_stats", "attn_debug_set_bwd_variant",
             "attn_rope_rates", "attn_rope", "attn_cache_append", "attn_cache_status",
-            "attn_decode", "attn_decode_workspace_size", "attn_decode_workspace_init")
+            "attn_decode", "attn_decode_workspace_size", "attn_decode_workspace_init",
+            "attn_fwd_grouped", "attn_bwd_grouped")
 BLOCK = 128  # rows per block of a block-sparse mask
 
 _lock = threading.Lock()
@@ -61,6 +62,11 @@ class _RotationStruct(ctypes.Structure):
     """attn_rotation of include/attn.h."""
     _fields_ = [("rates", ctypes.c_void_p), ("begin", ctypes.c_int), ("dim", ctypes.c_int),
                 ("style", ctypes.c_int)]
+
+
+class _RowsStruct(ctypes.Structure):
+    """attn_rows of include/attn.h."""
+    _fields_ = [(n, ctypes.c_longlong) for n in ("q", "k", "v", "o", "d_o", "dq", "dk", "dv")]
 
 
 class _CacheStruct(ctypes.Structure):
@@ -149,6 +155,12 @@ def load():
         lib.attn_decode_workspace_init.restype = I
         lib.attn_decode.argtypes = [P, P, I, L, P, I, P, L, P, P, I, I, F, P, SZ, P]
         lib.attn_decode.restype = I
+        lib.attn_fwd_grouped.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, P, I, I, I, F, P, P,
+                                         P]
+        lib.attn_fwd_grouped.restype = I
+        lib.attn_bwd_grouped.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, I, I,
+                                         I, F, P, P, I, P, SZ, P]
+        lib.attn_bwd_grouped.restype = I
         _lib = lib
         return lib
 
@@ -253,6 +265,29 @@ def attn_bwd_ex(q, k, v, o, dO, lse, dq, dk, dv_out, B, H, Tq, Tk, dqk, dv, caus
                               int(mask_batches), int(mask_heads), float(scale), cq.ptr, ck.ptr,
                               layout, int(deterministic), _ptr(workspace), int(workspace_bytes),
                               _stream(stream))
+
+
+def attn_fwd_grouped(q, k, v, o, lse, B, Hq, Hk, Tq, Tk, dqk, dv, rows, causal, window_left,
+                     window_right, scale, cu_seqlens_q=None, cu_seqlens_k=None,
+                     stream=None) -> int:
+    cq, ck = _HostInts(cu_seqlens_q), _HostInts(cu_seqlens_k)
+    return load().attn_fwd_grouped(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse), B, Hq, Hk, Tq,
+                                   Tk, dqk, dv, _struct(rows), int(causal), _c_int(window_left),
+                                   _c_int(window_right), float(scale), cq.ptr, ck.ptr,
+                                   _stream(stream))
+
+
+def attn_bwd_grouped(q, k, v, o, dO, lse, dq, dk, dv_out, B, Hq, Hk, Tq, Tk, dqk, dv, rows,
+                     causal, window_left, window_right, scale, cu_seqlens_q=None,
+                     cu_seqlens_k=None, deterministic=False, workspace=None, workspace_bytes=0,
+                     stream=None) -> int:
+    cq, ck = _HostInts(cu_seqlens_q), _HostInts(cu_seqlens_k)
+    return load().attn_bwd_grouped(_ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(dO), _ptr(lse),
+                                   _ptr(dq), _ptr(dk), _ptr(dv_out), B, Hq, Hk, Tq, Tk, dqk, dv,
+                                   _struct(rows), int(causal), _c_int(window_left),
+                                   _c_int(window_right), float(scale), cq.ptr, ck.ptr,
+                                   int(deterministic), _ptr(workspace), int(workspace_bytes),
+                                   _stream(stream))
 
 
 def _mask_dims(block_mask):
@@ -481,9 +516,15 @@ def forward(q, k, v, causal=False, scale=None, cu_seqlens=None, layout=LAYOUT_BT
     block_mask: device uint8 [NQ][NK] or [Bm][Hm][NQ][NK] (NQ, NK: blocks of
     BLOCK rows), non-zero = the block pair takes part, or None.
     cu_seqlens_k: key offsets of a variable-length batch when they differ
-    from cu_seqlens (the query offsets), or None."""
+    from cu_seqlens (the query offsets), or None.
+    k and v may have fewer heads than q (grouped heads: query head h uses key
+    head h * Hk // Hq), and q, k, v rows that lie apart (slices of one
+    projection); neither goes with a block mask."""
     B, H, Tq, Tk, dqk, dv = _dims(q, k, v, cu_seqlens, layout)
     scale = 1.0 / math.sqrt(dqk) if scale is None else scale
+    if layout == LAYOUT_BTHD and _is_grouped(q, k, v):
+        return _forward_grouped(q, k, v, causal, scale, cu_seqlens, with_lse, stream, window,
+                                block_mask, cu_seqlens_k)
     o = torch.empty(q.shape[:-2] + (H, dv), dtype=torch.bfloat16, device=q.device)
     lse = None
     if with_lse:
@@ -502,9 +543,13 @@ def backward(q, k, v, o, dO, lse, causal=False, scale=None, cu_seqlens=None,
              layout=LAYOUT_BTHD, deterministic=False, workspace=None, stream=None, out=None,
              window=None, block_mask=None, cu_seqlens_k=None):
     """(dq, dk, dv) as bf16 tensors shaped like q, k, v (a packed buffer for layout 1).
-    window, block_mask, cu_seqlens_k: as in forward()."""
+    window, block_mask, cu_seqlens_k, grouped heads and rows that lie apart: as in
+    forward(); dk and dv then have the key heads, summed over their query heads."""
     B, H, Tq, Tk, dqk, dv = _dims(q, k, v, cu_seqlens, layout)
     scale = 1.0 / math.sqrt(dqk) if scale is None else scale
+    if layout == LAYOUT_BTHD and _is_grouped(q, k, v, o, dO, *(out if out is not None else ())):
+        return _backward_grouped(q, k, v, o, dO, lse, causal, scale, cu_seqlens, deterministic,
+                                 workspace, stream, out, window, block_mask, cu_seqlens_k)
     if out is not None:
         dq, dk, dvt = out
     elif layout == LAYOUT_PACKED_QKV:
@@ -748,6 +793,101 @@ def _device_of(t, *others):
         if o is not None and o.get_device() != index:
             raise ValueError(f"tensors must be on one CUDA device (cuda:{index})")
     return index
+
+
+# ----------------------------------------------------------------------------
+# Grouped heads, rows apart
+# ----------------------------------------------------------------------------
+def _is_grouped(q, k, v, *others):
+    """Whether a call goes to the entry points for grouped heads and rows that lie apart."""
+    return (k.shape[-2] != q.shape[-2] or v.shape[-2] != q.shape[-2]
+            or not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous()
+                    and all(t.is_contiguous() for t in others)))
+
+
+def _grouped_dims(q, k, v, cu_seqlens, cu_seqlens_k, window, block_mask):
+    """(B, Hq, Hk, Tq, Tk, dqk, dv), (window_left, window_right) of a checked call."""
+    if block_mask is not None:
+        raise ValueError("a block mask needs as many key heads as query heads, and dense tensors")
+    B, Hq, Tq, Tk, dqk, dv = _dims(q, k, v, cu_seqlens, LAYOUT_BTHD)
+    Hk = k.shape[-2]
+    if k.shape[:-1] != v.shape[:-1] or k.shape[-1] != dqk:
+        raise ValueError("k and v must agree in rows and heads, and k with q in head size")
+    if Hk == 0 or Hq % Hk:
+        raise ValueError("the query heads must be a multiple of the key heads")
+    if cu_seqlens is None and k.shape[0] != B:
+        raise ValueError("q, k and v must agree in batch")
+    if cu_seqlens is not None and cu_seqlens_k is not None and len(cu_seqlens_k) != B + 1:
+        raise ValueError("cu_seqlens and cu_seqlens_k must have the same length")
+    if cu_seqlens is None and cu_seqlens_k is not None:
+        raise ValueError("cu_seqlens_k needs cu_seqlens")
+    return (B, Hq, Hk, Tq, Tk, dqk, dv), ((-1, -1) if window is None else window)
+
+
+def _forward_grouped(q, k, v, causal, scale, cu_seqlens, with_lse, stream, window, block_mask,
+                     cu_seqlens_k):
+    dims, (wl, wr) = _grouped_dims(q, k, v, cu_seqlens, cu_seqlens_k, window, block_mask)
+    B, Hq, Hk, Tq, Tk, dqk, dv = dims
+    rows = _RowsStruct(_rows(q, q.shape, "q"), _rows(k, k.shape, "k"), _rows(v, v.shape, "v"))
+    index = _device_of(q, k, v)
+    if not _here(index, stream):
+        with _On(index, stream):
+            return _forward_grouped(q, k, v, causal, scale, cu_seqlens, with_lse, None, window,
+                                    block_mask, cu_seqlens_k)
+    device = q.device
+    o = _empty(q.shape[:-1] + (dv,), torch.bfloat16, device)
+    lse = None
+    if with_lse:
+        lse = _empty((Hq, Tq) if cu_seqlens is not None else (B, Hq, Tq), torch.float32, device)
+    if q.numel() == 0:  # (tensors without elements have no address)
+        return o, lse
+    rc = attn_fwd_grouped(q, k, v, o, lse, *dims, rows, causal, wl, wr, scale, cu_seqlens,
+                          cu_seqlens_k, _current(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_fwd_grouped")
+    return o, lse
+
+
+def _backward_grouped(q, k, v, o, dO, lse, causal, scale, cu_seqlens, deterministic, workspace,
+                      stream, out, window, block_mask, cu_seqlens_k):
+    dims, (wl, wr) = _grouped_dims(q, k, v, cu_seqlens, cu_seqlens_k, window, block_mask)
+    B, Hq, Hk, Tq, Tk, dqk, dv = dims
+    shape = q.shape[:-1] + (dv,)
+    if o.shape != shape or dO.shape != shape:
+        raise ValueError("o and dO must have q's rows and heads, and v's head size")
+    if (lse.dtype is not torch.float32 or not lse.is_contiguous()
+            or lse.shape != ((Hq, Tq) if cu_seqlens is not None else (B, Hq, Tq))):
+        raise ValueError("lse must be the forward's contiguous fp32 statistic")
+    grads = out if out is not None else (None, None, None)
+    for g, t, name in zip(grads, (q, k, v), "qkv"):
+        if out is not None and g.shape != t.shape:
+            raise ValueError(f"out must hold a tensor like {name}")
+    if workspace is not None and not workspace.is_contiguous():  # (nbytes counts its memory)
+        raise ValueError("workspace must be contiguous")
+    rows = _RowsStruct(_rows(q, q.shape, "q"), _rows(k, k.shape, "k"), _rows(v, v.shape, "v"),
+                       _rows(o, shape, "o"), _rows(dO, shape, "dO"),
+                       *(0 if g is None else _rows(g, g.shape, "out") for g in grads))
+    index = _device_of(q, k, v, o, dO, lse, workspace, *grads)
+    if not _here(index, stream):
+        with _On(index, stream):
+            return _backward_grouped(q, k, v, o, dO, lse, causal, scale, cu_seqlens,
+                                     deterministic, workspace, None, out, window, block_mask,
+                                     cu_seqlens_k)
+    device = q.device
+    if out is None:
+        grads = [_empty(t.shape, torch.bfloat16, device) for t in (q, k, v)]
+    dq, dk, dvt = grads
+    if q.numel() == 0:  # (tensors without elements have no address; no query sees a key)
+        return dq, dk.zero_(), dvt.zero_()
+    need = attn_bwd_workspace_size(B, Hq, Tq, Tk, dqk, dv, cu_seqlens is not None, deterministic)
+    if workspace is None or workspace.nbytes < need:
+        workspace = _empty((max(need, 1),), torch.uint8, device)
+    rc = attn_bwd_grouped(q, k, v, o, dO, lse, dq, dk, dvt, *dims, rows, causal, wl, wr, scale,
+                          cu_seqlens, cu_seqlens_k, deterministic, workspace, workspace.nbytes,
+                          _current(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_bwd_grouped")
+    return dq, dk, dvt
 
 
 def rope(q, k, rotation, inverse=False, pos0=0, cu_seqlens=None, cu_seqlens_k=None, out=None,

@@ -51,7 +51,7 @@ void set_window(SeqShape* sh, int causal, int window_left, int window_right) {
   sh->wr = causal ? 0 : std::min(window_right, sh->Tk);
 }
 
-// Common shape checks of the forward and backward entry points.  cu / cuk:
+// Common shape checks of the forward and backward entry points (H: query heads).  cu / cuk:
 // query / key offsets of a variable-length batch (cuk == cu when the keys
 // share the queries' offsets).  Returns ATTN_OK or an error.
 int check_shape(int B, int H, int Tq, int Tk, int dqk, int dv, int causal, const int* cu,
@@ -108,7 +108,8 @@ int order_impl(const int* cu, const int* cuk, int nseq, int* order) {
 enum TableKind { kFwdTable = 0, kBwdTable = 1, kBwdPairTable = 2 };
 
 // Variable-length tables: sequences by work; items per sequence are (its
-// 256-row query units (forward), kv-tiles or kv-tile pairs (backward)) x H;
+// 256-row query units (forward), kv-tiles or kv-tile pairs (backward)) x H (query
+// heads in the forward, key heads in the backward);
 // q-tiles numbered sequence by sequence.
 void build_tables(const int* cu, const int* cuk, int nseq, int H, int kind, VarlenTables* t,
                   int* n_items, int* n_qtiles) {
@@ -240,6 +241,28 @@ struct Layout {
   int64_t g_q_row, g_k_row, g_v_row;  // ... of dq / dk / dv
 };
 
+// Distances between token rows of grouped heads: the caller's, 0 for dense.  False where
+// rows overlap or a distance is no multiple of 16 bytes (TMA) or too long for its maps.
+bool make_layout(const attn_rows* r, int Hq, int Hk, int dqk, int dv, Layout* L, int64_t* do_row) {
+  const attn_rows none = {};
+  if (r == nullptr) r = &none;
+  bool ok = true;
+  auto row = [&ok](long long given, int H, int d) -> int64_t {
+    const int64_t dense = (int64_t)H * d, n = given == 0 ? dense : given;
+    ok = ok && n >= dense && n % 8 == 0 && n < (1ll << 38);
+    return n;
+  };
+  L->q_row = row(r->q, Hq, dqk);
+  L->k_row = row(r->k, Hk, dqk);
+  L->v_row = row(r->v, Hk, dv);
+  L->o_row = row(r->o, Hq, dv);
+  *do_row = row(r->d_o, Hq, dv);
+  L->g_q_row = row(r->dq, Hq, dqk);
+  L->g_k_row = row(r->dk, Hk, dqk);
+  L->g_v_row = row(r->dv, Hk, dv);
+  return ok;
+}
+
 Layout make_layout(int layout, int H, int dqk, int dv) {
   Layout L;
   if (layout == ATTN_LAYOUT_PACKED_QKV) {
@@ -318,6 +341,215 @@ std::atomic<void*> g_prof_stop{nullptr};
 // ... and around the preprocess and the dQ conversion kernels
 std::atomic<void*> g_prof_aux[4] = {{nullptr}, {nullptr}, {nullptr}, {nullptr}};
 
+// The forward of H query heads over Hk key heads (H a multiple of Hk), with the rows' distances
+// in `lay`.  `layout` only says which shapes go with it.
+int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int Hk,
+             int Tq, int Tk, int dqk, int dv, int causal, int window_left, int window_right,
+             const unsigned char* block_mask, int mask_batches, int mask_heads, float scale,
+             const int* cu_seqlens_q, const int* cu_seqlens_k, int layout, const Layout& lay,
+             void* stream) {
+  const int* cu_seqlens = cu_seqlens_q;
+  const int* cuk = cu_seqlens_k != nullptr ? cu_seqlens_k : cu_seqlens_q;
+  if (!q || !k || !v || !o) return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;  // running max assumes s > 0
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
+      (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)))
+    return ATTN_ERR_INVALID_ARG;
+  int rc = check_shape(B, H, Tq, Tk, dqk, dv, causal, cu_seqlens, cuk, layout, window_left,
+                       window_right);
+  if (rc) return rc;
+  if (block_mask != nullptr && ((mask_batches != 1 && mask_batches != B) ||
+                                (mask_heads != 1 && mask_heads != H)))
+    return ATTN_ERR_INVALID_ARG;
+
+  FwdLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  static thread_local VarlenTables tables;
+  const bool varlen = cu_seqlens != nullptr;
+  const int64_t rows_q = varlen ? Tq : (int64_t)B * Tq;
+  const int64_t rows_k = varlen ? Tk : (int64_t)B * Tk;
+  HostCache& hc = host_cache();
+  if (!hc.map(&L.tm_q, q, dqk, H, rows_q, dqk, lay.q_row, kTile) ||
+      !hc.map(&L.tm_k, k, dqk, Hk, rows_k, dqk, lay.k_row, kTile) ||
+      !hc.map(&L.tm_v, v, dv, Hk, rows_k, dv, lay.v_row, kTile))
+    return ATTN_ERR_CUDA;
+  L.sh.nseq = B;
+  L.sh.H = H;
+  L.sh.Hk = Hk;
+  L.sh.group = H / Hk;
+  L.sh.varlen = varlen ? 1 : 0;
+  L.sh.Tq = Tq;
+  L.sh.Tk = Tk;
+  L.sh.nq_tiles = cdiv(Tq, kTile);
+  L.sh.nk_tiles = cdiv(Tk, kTile);
+  L.sh.nq_units = cdiv(Tq, kFwdRows);
+  L.sh.causal = causal ? 1 : 0;
+  L.sh.band_off = varlen ? 0 : Tk - Tq;
+  set_window(&L.sh, causal, window_left, window_right);
+  L.sh.descending = 0;
+  // Rank-major forward order when every head's K and V fit in L2 together
+  // (measured: the GPT-2-shaped layer, 25 MB of K and V, 8 % faster than
+  // head-major); head-major keeps a few heads' K and V in L2 otherwise.
+  constexpr int64_t kL2FitBytes = 48ll << 20;
+  L.sh.rank_major = !varlen && (int64_t)B * Tk * Hk * (dqk + dv) * 2 <= kL2FitBytes ? 1 : 0;
+  rc = set_block_mask(&L.sh, block_mask, mask_batches, mask_heads, B, H, Tq, Tk, cu_seqlens,
+                      cuk);
+  if (rc) return rc;
+  if (varlen) {
+    int n_items = 0, n_qt = 0;
+    hc.tables(cu_seqlens, cuk, B, H, kFwdTable, &tables, &n_items, &n_qt);
+    L.sh.n_items = n_items;
+    L.tables = &tables;
+    L.lse_head_stride = Tq;
+    L.lse_seq_stride = 0;
+  } else {
+    L.sh.n_items = B * H * L.sh.nq_units;
+    L.tables = nullptr;
+    L.lse_head_stride = Tq;
+    L.lse_seq_stride = (int64_t)H * Tq;
+  }
+  if (L.sh.n_items == 0) return ATTN_OK;
+  L.o = o;
+  L.lse = lse;
+  L.o_row_stride = lay.o_row;
+  L.scale_log2 = scale * kLog2e;
+  L.status = fwd_status_ptr();
+  if (!L.status) return ATTN_ERR_CUDA;
+  // work-item counters of its own (the previous kernel on them left them at zero)
+  static std::atomic<unsigned> next_claim{0};
+  L.claim = fwd_claim_ptr((int)(next_claim.fetch_add(1) % kFwdClaimSlots));
+  if (!L.claim) return ATTN_ERR_CUDA;
+  const int sms = num_sms_current();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  L.grid = std::min(L.sh.n_items, sms);
+  L.stream = static_cast<cudaStream_t>(stream);
+  return cuda_err(launch_fwd(L, dqk, dv));
+}
+
+// The backward of fwd_impl; do_row: elements between token rows of dO.
+int bwd_impl(const void* q, const void* k, const void* v, const void* o, const void* dO,
+             const float* lse, void* dq, void* dk, void* dv_out, int B, int H, int Hk, int Tq,
+             int Tk, int dqk, int dv, int causal, int window_left, int window_right,
+             const unsigned char* block_mask, int mask_batches, int mask_heads, float scale,
+             const int* cu_seqlens_q, const int* cu_seqlens_k, int layout, const Layout& lay,
+             int64_t do_row, int deterministic, void* workspace, size_t workspace_bytes,
+             void* stream) {
+  const int* cu_seqlens = cu_seqlens_q;
+  const int* cuk = cu_seqlens_k != nullptr ? cu_seqlens_k : cu_seqlens_q;
+  if (!q || !k || !v || !o || !dO || !lse || !dq || !dk || !dv_out || !workspace)
+    return ATTN_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dO) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv_out) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return ATTN_ERR_INVALID_ARG;
+  int rc = check_shape(B, H, Tq, Tk, dqk, dv, causal, cu_seqlens, cuk, layout, window_left,
+                       window_right);
+  if (rc) return rc;
+  if (block_mask != nullptr && ((mask_batches != 1 && mask_batches != B) ||
+                                (mask_heads != 1 && mask_heads != H)))
+    return ATTN_ERR_INVALID_ARG;
+  const bool varlen = cu_seqlens != nullptr;
+  if (workspace_bytes < attn_bwd_workspace_size(B, H, Tq, Tk, dqk, dv, varlen, deterministic))
+    return ATTN_ERR_WORKSPACE_TOO_SMALL;
+
+  BwdLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  static thread_local VarlenTables tables;
+  const int64_t rows_q = varlen ? Tq : (int64_t)B * Tq;
+  const int64_t rows_k = varlen ? Tk : (int64_t)B * Tk;
+  HostCache& hc = host_cache();
+  if (!hc.map(&L.tm_q, q, dqk, H, rows_q, dqk, lay.q_row, kTile) ||
+      !hc.map(&L.tm_k, k, dqk, Hk, rows_k, dqk, lay.k_row, kTile) ||
+      !hc.map(&L.tm_v, v, dv, Hk, rows_k, dv, lay.v_row, kTile) ||
+      !hc.map(&L.tm_do, dO, dv, H, rows_q, dv, do_row, kTile))
+    return ATTN_ERR_CUDA;
+  L.sh.nseq = B;
+  L.sh.H = H;
+  L.sh.Hk = Hk;
+  L.sh.group = H / Hk;
+  L.sh.varlen = varlen ? 1 : 0;
+  L.sh.Tq = Tq;
+  L.sh.Tk = Tk;
+  L.sh.nq_tiles = cdiv(Tq, kTile);
+  L.sh.nk_tiles = cdiv(Tk, kTile);
+  L.sh.causal = causal ? 1 : 0;
+  L.sh.band_off = varlen ? 0 : Tk - Tq;
+  set_window(&L.sh, causal, window_left, window_right);
+  L.sh.descending = deterministic ? 1 : 0;
+  // Grouped heads: few items, each as long as its group; longest first over all heads where
+  // Q, dO and the fp32 dQ of the call fit in L2 together, by head otherwise.
+  constexpr int64_t kBwdL2FitBytes = 64ll << 20;
+  L.sh.rank_major =
+      H != Hk && rows_q * H * (dqk + dv + 2ll * dqk) * 2 <= kBwdL2FitBytes ? 1 : 0;
+  rc = set_block_mask(&L.sh, block_mask, mask_batches, mask_heads, B, H, Tq, Tk, cu_seqlens,
+                      cuk);
+  if (rc) return rc;
+  const int sms = num_sms_current();
+  if (sms <= 0) return ATTN_ERR_CUDA;
+  // The CTA-pair main kernel covers d = 128 without a block mask or a left
+  // window edge or grouped heads (causal, non-causal, right-bounded bands; fixed or variable
+  // length), on at least two SMs.
+  const int variant = g_bwd_variant.load();
+  const bool pair_ok = dqk == 128 && dv == 128 && block_mask == nullptr && window_left < 0 &&
+                       H == Hk && sms >= 2;
+  L.pair = pair_ok && variant != 1 && (variant == 2 || kPairByDefault) ? 1 : 0;
+  if (L.pair && (!hc.map(&L.tm_q64, q, dqk, H, rows_q, dqk, lay.q_row, 64) ||
+                 !hc.map(&L.tm_do64, dO, dv, H, rows_q, dv, do_row, 64)))
+    return ATTN_ERR_CUDA;
+  int n_qtiles;
+  if (varlen) {
+    int n_items = 0;
+    hc.tables(cu_seqlens, cuk, B, Hk, L.pair ? kBwdPairTable : kBwdTable, &tables, &n_items,
+              &n_qtiles);
+    L.sh.n_items = n_items;
+    L.tables = &tables;
+    L.lse_head_stride = Tq;
+    L.lse_seq_stride = 0;
+  } else {
+    L.sh.n_items = B * Hk * (L.pair ? cdiv(L.sh.nk_tiles, 2) : L.sh.nk_tiles);
+    n_qtiles = B * L.sh.nq_tiles;
+    L.tables = nullptr;
+    L.lse_head_stride = Tq;
+    L.lse_seq_stride = (int64_t)H * Tq;
+  }
+  if (L.sh.n_items == 0) return ATTN_OK;
+  // carve the workspace (sizes from the bound, offsets fixed by the query)
+  const WsSizes w = ws_sizes(qtiles_bound(B, Tq, varlen), H, dqk);
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  L.ws.header = reinterpret_cast<int*>(base);
+  L.ws.sem = reinterpret_cast<int*>(base + w.header);
+  L.ws.nlse2 = reinterpret_cast<float*>(base + w.header + w.sem);
+  L.ws.ndsum = reinterpret_cast<float*>(base + w.header + w.sem + w.stat);
+  L.ws.dq_acc = reinterpret_cast<float*>(base + w.header + w.sem + 2 * w.stat);
+  L.o = o;
+  L.dout = dO;
+  L.lse = lse;
+  L.dq = dq;
+  L.dk = dk;
+  L.dv = dv_out;
+  L.q_row_stride = lay.q_row;
+  L.k_row_stride = lay.k_row;
+  L.v_row_stride = lay.v_row;
+  L.o_row_stride = lay.o_row;
+  L.do_row_stride = do_row;
+  L.dq_row_stride = lay.g_q_row;
+  L.dk_row_stride = lay.g_k_row;
+  L.dv_row_stride = lay.g_v_row;
+  L.scale = scale;
+  L.scale_log2 = scale * kLog2e;
+  L.n_qtiles = n_qtiles;
+  L.deterministic = deterministic ? 1 : 0;
+  L.sem_bias = g_sem_bias.load();
+  L.prof_start = static_cast<cudaEvent_t>(g_prof_start.load());
+  L.prof_stop = static_cast<cudaEvent_t>(g_prof_stop.load());
+  for (int e = 0; e < 4; ++e) L.prof_aux[e] = static_cast<cudaEvent_t>(g_prof_aux[e].load());
+  L.num_sms = sms;
+  L.grid = L.pair ? 2 * std::min(L.sh.n_items, sms / 2) : std::min(L.sh.n_items, sms);
+  L.stream = static_cast<cudaStream_t>(stream);
+  return cuda_err(launch_bwd(L, dqk, dv));
+}
+
 }  // namespace
 
 extern "C" {
@@ -369,81 +601,22 @@ int attn_fwd_ex(const void* q, const void* k, const void* v, void* o, float* lse
                 int Tq, int Tk, int dqk, int dv, int causal, int window_left, int window_right,
                 const unsigned char* block_mask, int mask_batches, int mask_heads, float scale,
                 const int* cu_seqlens_q, const int* cu_seqlens_k, int layout, void* stream) {
-  const int* cu_seqlens = cu_seqlens_q;
-  const int* cuk = cu_seqlens_k != nullptr ? cu_seqlens_k : cu_seqlens_q;
-  if (!q || !k || !v || !o) return ATTN_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;  // running max assumes s > 0
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) ||
-      (lse && (reinterpret_cast<uintptr_t>(lse) & 3u)))
-    return ATTN_ERR_INVALID_ARG;
-  int rc = check_shape(B, H, Tq, Tk, dqk, dv, causal, cu_seqlens, cuk, layout, window_left,
-                       window_right);
-  if (rc) return rc;
-  if (block_mask != nullptr && ((mask_batches != 1 && mask_batches != B) ||
-                                (mask_heads != 1 && mask_heads != H)))
-    return ATTN_ERR_INVALID_ARG;
+  return fwd_impl(q, k, v, o, lse, B, H, H, Tq, Tk, dqk, dv, causal, window_left, window_right,
+                  block_mask, mask_batches, mask_heads, scale, cu_seqlens_q, cu_seqlens_k, layout,
+                  make_layout(layout, H, dqk, dv), stream);
+}
 
-  FwdLaunch L;
-  std::memset(&L, 0, sizeof(L));
-  static thread_local VarlenTables tables;
-  const bool varlen = cu_seqlens != nullptr;
-  const Layout lay = make_layout(layout, H, dqk, dv);
-  const int64_t rows_q = varlen ? Tq : (int64_t)B * Tq;
-  const int64_t rows_k = varlen ? Tk : (int64_t)B * Tk;
-  HostCache& hc = host_cache();
-  if (!hc.map(&L.tm_q, q, dqk, H, rows_q, dqk, lay.q_row, kTile) ||
-      !hc.map(&L.tm_k, k, dqk, H, rows_k, dqk, lay.k_row, kTile) ||
-      !hc.map(&L.tm_v, v, dv, H, rows_k, dv, lay.v_row, kTile))
-    return ATTN_ERR_CUDA;
-  L.sh.nseq = B;
-  L.sh.H = H;
-  L.sh.varlen = varlen ? 1 : 0;
-  L.sh.Tq = Tq;
-  L.sh.Tk = Tk;
-  L.sh.nq_tiles = cdiv(Tq, kTile);
-  L.sh.nk_tiles = cdiv(Tk, kTile);
-  L.sh.nq_units = cdiv(Tq, kFwdRows);
-  L.sh.causal = causal ? 1 : 0;
-  L.sh.band_off = varlen ? 0 : Tk - Tq;
-  set_window(&L.sh, causal, window_left, window_right);
-  L.sh.descending = 0;
-  // Rank-major forward order when every head's K and V fit in L2 together
-  // (measured: the GPT-2-shaped layer, 25 MB of K and V, 8 % faster than
-  // head-major); head-major keeps a few heads' K and V in L2 otherwise.
-  constexpr int64_t kL2FitBytes = 48ll << 20;
-  L.sh.rank_major = !varlen && (int64_t)B * Tk * H * (dqk + dv) * 2 <= kL2FitBytes ? 1 : 0;
-  rc = set_block_mask(&L.sh, block_mask, mask_batches, mask_heads, B, H, Tq, Tk, cu_seqlens,
-                      cuk);
-  if (rc) return rc;
-  if (varlen) {
-    int n_items = 0, n_qt = 0;
-    hc.tables(cu_seqlens, cuk, B, H, kFwdTable, &tables, &n_items, &n_qt);
-    L.sh.n_items = n_items;
-    L.tables = &tables;
-    L.lse_head_stride = Tq;
-    L.lse_seq_stride = 0;
-  } else {
-    L.sh.n_items = B * H * L.sh.nq_units;
-    L.tables = nullptr;
-    L.lse_head_stride = Tq;
-    L.lse_seq_stride = (int64_t)H * Tq;
-  }
-  if (L.sh.n_items == 0) return ATTN_OK;
-  L.o = o;
-  L.lse = lse;
-  L.o_row_stride = lay.o_row;
-  L.scale_log2 = scale * kLog2e;
-  L.status = fwd_status_ptr();
-  if (!L.status) return ATTN_ERR_CUDA;
-  // work-item counters of its own (the previous kernel on them left them at zero)
-  static std::atomic<unsigned> next_claim{0};
-  L.claim = fwd_claim_ptr((int)(next_claim.fetch_add(1) % kFwdClaimSlots));
-  if (!L.claim) return ATTN_ERR_CUDA;
-  const int sms = num_sms_current();
-  if (sms <= 0) return ATTN_ERR_CUDA;
-  L.grid = std::min(L.sh.n_items, sms);
-  L.stream = static_cast<cudaStream_t>(stream);
-  return cuda_err(launch_fwd(L, dqk, dv));
+int attn_fwd_grouped(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                     int Hq, int Hk, int Tq, int Tk, int dqk, int dv, const attn_rows* rows,
+                     int causal, int window_left, int window_right, float scale,
+                     const int* cu_seqlens_q, const int* cu_seqlens_k, void* stream) {
+  Layout lay;
+  int64_t do_row;
+  if (Hq <= 0 || Hk <= 0 || Hq % Hk != 0) return ATTN_ERR_INVALID_ARG;
+  if (!supported_dims(dqk, dv)) return ATTN_ERR_UNSUPPORTED;
+  if (!make_layout(rows, Hq, Hk, dqk, dv, &lay, &do_row)) return ATTN_ERR_INVALID_ARG;
+  return fwd_impl(q, k, v, o, lse, B, Hq, Hk, Tq, Tk, dqk, dv, causal, window_left, window_right,
+                  nullptr, 1, 1, scale, cu_seqlens_q, cu_seqlens_k, ATTN_LAYOUT_BTHD, lay, stream);
 }
 
 int attn_bwd(const void* q, const void* k, const void* v, const void* o, const void* dO,
@@ -471,114 +644,28 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
                 const unsigned char* block_mask, int mask_batches, int mask_heads, float scale,
                 const int* cu_seqlens_q, const int* cu_seqlens_k, int layout, int deterministic,
                 void* workspace, size_t workspace_bytes, void* stream) {
-  const int* cu_seqlens = cu_seqlens_q;
-  const int* cuk = cu_seqlens_k != nullptr ? cu_seqlens_k : cu_seqlens_q;
-  if (!q || !k || !v || !o || !dO || !lse || !dq || !dk || !dv_out || !workspace)
-    return ATTN_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return ATTN_ERR_INVALID_ARG;
-  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(dO) ||
-      !aligned16(dq) || !aligned16(dk) || !aligned16(dv_out) ||
-      (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u))
-    return ATTN_ERR_INVALID_ARG;
-  int rc = check_shape(B, H, Tq, Tk, dqk, dv, causal, cu_seqlens, cuk, layout, window_left,
-                       window_right);
-  if (rc) return rc;
-  if (block_mask != nullptr && ((mask_batches != 1 && mask_batches != B) ||
-                                (mask_heads != 1 && mask_heads != H)))
-    return ATTN_ERR_INVALID_ARG;
-  const bool varlen = cu_seqlens != nullptr;
-  if (workspace_bytes < attn_bwd_workspace_size(B, H, Tq, Tk, dqk, dv, varlen, deterministic))
-    return ATTN_ERR_WORKSPACE_TOO_SMALL;
-
-  BwdLaunch L;
-  std::memset(&L, 0, sizeof(L));
-  static thread_local VarlenTables tables;
   const Layout lay = make_layout(layout, H, dqk, dv);
-  const int64_t rows_q = varlen ? Tq : (int64_t)B * Tq;
-  const int64_t rows_k = varlen ? Tk : (int64_t)B * Tk;
-  HostCache& hc = host_cache();
-  if (!hc.map(&L.tm_q, q, dqk, H, rows_q, dqk, lay.q_row, kTile) ||
-      !hc.map(&L.tm_k, k, dqk, H, rows_k, dqk, lay.k_row, kTile) ||
-      !hc.map(&L.tm_v, v, dv, H, rows_k, dv, lay.v_row, kTile) ||
-      !hc.map(&L.tm_do, dO, dv, H, rows_q, dv, lay.o_row, kTile))
-    return ATTN_ERR_CUDA;
-  L.sh.nseq = B;
-  L.sh.H = H;
-  L.sh.varlen = varlen ? 1 : 0;
-  L.sh.Tq = Tq;
-  L.sh.Tk = Tk;
-  L.sh.nq_tiles = cdiv(Tq, kTile);
-  L.sh.nk_tiles = cdiv(Tk, kTile);
-  L.sh.causal = causal ? 1 : 0;
-  L.sh.band_off = varlen ? 0 : Tk - Tq;
-  set_window(&L.sh, causal, window_left, window_right);
-  L.sh.descending = deterministic ? 1 : 0;
-  rc = set_block_mask(&L.sh, block_mask, mask_batches, mask_heads, B, H, Tq, Tk, cu_seqlens,
-                      cuk);
-  if (rc) return rc;
-  const int sms = num_sms_current();
-  if (sms <= 0) return ATTN_ERR_CUDA;
-  // The CTA-pair main kernel covers d = 128 without a block mask or a left
-  // window edge (causal, non-causal, right-bounded bands; fixed or variable
-  // length), on at least two SMs.
-  const int variant = g_bwd_variant.load();
-  const bool pair_ok = dqk == 128 && dv == 128 && block_mask == nullptr && window_left < 0 &&
-                       sms >= 2;
-  L.pair = pair_ok && variant != 1 && (variant == 2 || kPairByDefault) ? 1 : 0;
-  if (L.pair && (!hc.map(&L.tm_q64, q, dqk, H, rows_q, dqk, lay.q_row, 64) ||
-                 !hc.map(&L.tm_do64, dO, dv, H, rows_q, dv, lay.o_row, 64)))
-    return ATTN_ERR_CUDA;
-  int n_qtiles;
-  if (varlen) {
-    int n_items = 0;
-    hc.tables(cu_seqlens, cuk, B, H, L.pair ? kBwdPairTable : kBwdTable, &tables, &n_items,
-              &n_qtiles);
-    L.sh.n_items = n_items;
-    L.tables = &tables;
-    L.lse_head_stride = Tq;
-    L.lse_seq_stride = 0;
-  } else {
-    L.sh.n_items = B * H * (L.pair ? cdiv(L.sh.nk_tiles, 2) : L.sh.nk_tiles);
-    n_qtiles = B * L.sh.nq_tiles;
-    L.tables = nullptr;
-    L.lse_head_stride = Tq;
-    L.lse_seq_stride = (int64_t)H * Tq;
-  }
-  if (L.sh.n_items == 0) return ATTN_OK;
-  // carve the workspace (sizes from the bound, offsets fixed by the query)
-  const WsSizes w = ws_sizes(qtiles_bound(B, Tq, varlen), H, dqk);
-  uint8_t* base = static_cast<uint8_t*>(workspace);
-  L.ws.header = reinterpret_cast<int*>(base);
-  L.ws.sem = reinterpret_cast<int*>(base + w.header);
-  L.ws.nlse2 = reinterpret_cast<float*>(base + w.header + w.sem);
-  L.ws.ndsum = reinterpret_cast<float*>(base + w.header + w.sem + w.stat);
-  L.ws.dq_acc = reinterpret_cast<float*>(base + w.header + w.sem + 2 * w.stat);
-  L.o = o;
-  L.dout = dO;
-  L.lse = lse;
-  L.dq = dq;
-  L.dk = dk;
-  L.dv = dv_out;
-  L.q_row_stride = lay.q_row;
-  L.k_row_stride = lay.k_row;
-  L.v_row_stride = lay.v_row;
-  L.o_row_stride = lay.o_row;
-  L.do_row_stride = lay.o_row;
-  L.dq_row_stride = lay.g_q_row;
-  L.dk_row_stride = lay.g_k_row;
-  L.dv_row_stride = lay.g_v_row;
-  L.scale = scale;
-  L.scale_log2 = scale * kLog2e;
-  L.n_qtiles = n_qtiles;
-  L.deterministic = deterministic ? 1 : 0;
-  L.sem_bias = g_sem_bias.load();
-  L.prof_start = static_cast<cudaEvent_t>(g_prof_start.load());
-  L.prof_stop = static_cast<cudaEvent_t>(g_prof_stop.load());
-  for (int e = 0; e < 4; ++e) L.prof_aux[e] = static_cast<cudaEvent_t>(g_prof_aux[e].load());
-  L.num_sms = sms;
-  L.grid = L.pair ? 2 * std::min(L.sh.n_items, sms / 2) : std::min(L.sh.n_items, sms);
-  L.stream = static_cast<cudaStream_t>(stream);
-  return cuda_err(launch_bwd(L, dqk, dv));
+  return bwd_impl(q, k, v, o, dO, lse, dq, dk, dv_out, B, H, H, Tq, Tk, dqk, dv, causal,
+                  window_left, window_right, block_mask, mask_batches, mask_heads, scale,
+                  cu_seqlens_q, cu_seqlens_k, layout, lay, lay.o_row, deterministic, workspace,
+                  workspace_bytes, stream);
+}
+
+int attn_bwd_grouped(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                     const float* lse, void* dq, void* dk, void* dv_out, int B, int Hq, int Hk,
+                     int Tq, int Tk, int dqk, int dv, const attn_rows* rows, int causal,
+                     int window_left, int window_right, float scale, const int* cu_seqlens_q,
+                     const int* cu_seqlens_k, int deterministic, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  Layout lay;
+  int64_t do_row;
+  if (Hq <= 0 || Hk <= 0 || Hq % Hk != 0) return ATTN_ERR_INVALID_ARG;
+  if (!supported_dims(dqk, dv)) return ATTN_ERR_UNSUPPORTED;
+  if (!make_layout(rows, Hq, Hk, dqk, dv, &lay, &do_row)) return ATTN_ERR_INVALID_ARG;
+  return bwd_impl(q, k, v, o, dO, lse, dq, dk, dv_out, B, Hq, Hk, Tq, Tk, dqk, dv, causal,
+                  window_left, window_right, nullptr, 1, 1, scale, cu_seqlens_q, cu_seqlens_k,
+                  ATTN_LAYOUT_BTHD, lay, do_row, deterministic, workspace, workspace_bytes,
+                  stream);
 }
 
 int attn_profile_main_kernel(void* event_start, void* event_stop) {

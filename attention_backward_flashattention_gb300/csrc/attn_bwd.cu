@@ -424,8 +424,11 @@ struct MainArgs {
 };
 
 // kMask: built with block-mask support (sh.blk non-null); the kernels without
-// it carry none of the mask's walks.
-template <int DQK, int DV, typename Tables, bool kMask>
+// it carry none of the mask's walks.  kGroup: several query heads share a key head
+// (sh.group > 1, never with a block mask): an item's walk takes the q-tiles of its
+// key head's first query head, then those of the next, as one sequence of steps, so
+// dK and dV are summed over the group in tensor memory and stored once.
+template <int DQK, int DV, typename Tables, bool kMask, bool kGroup>
 __global__ void __launch_bounds__(kMainThreads, 1)
     attn_bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q,
                          const __grid_constant__ CUtensorMap tm_k,
@@ -449,6 +452,8 @@ __global__ void __launch_bounds__(kMainThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const SeqShape& sh = a.sh;
+  static_assert(!(kMask && kGroup), "block masks and grouped heads");
+  const int group = kGroup ? sh.group : 1;
   Abort ab{&bars->abort_flag, a.ws.header};
   ATTN_TRACE_DECL;
   auto sQ_of = [&](uint32_t st) { return sStage + st * (C::kQBytes + C::kdOBytes); };
@@ -530,12 +535,13 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         const int nq = cdiv(it.Lq, kTile);
         const int i0 = first_qtile(sh, it, it.tile), i1 = last_qtile(sh, it, it.tile, nq) + 1;
         const uint8_t* col = mask_col<kMask>(sh, it);
+        for (int qh = it.head * group; ok && qh < (it.head + 1) * group; ++qh)
         for (int i = next_qtile(sh, col, i0, i1), inext; i < i1; i = inext, ++q_it) {
           inext = next_qtile(sh, col, i + 1, i1);
           const uint32_t st = q_it % C::kStages;
           const uint32_t par = ((q_it / C::kStages) & 1) ^ 1;
           const int qrow = it.row0 + i * kTile;
-          const int64_t g = (int64_t)(it.tile_base + i) * sh.H + it.head;
+          const int64_t g = (int64_t)(it.tile_base + i) * sh.H + qh;
           // Q (with the row statistics) and dO of the q-tile.  dO's stage is
           // released by dV, early in a step, and Q's by dK, late in it: at
           // d <= 128 dO goes first, so that it lands a step ahead of dP; at
@@ -550,7 +556,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
             const uint32_t qb = smem_u32(&bars->q_full[st]);
             mbar_arrive_expect_tx(qb, C::kQBytes + C::kStatBytes);
             for (int p = 0; p < C::kQPanels; ++p)
-              tma_load_3d(sQ_of(st) + p * kPanelBytes, &tm_q, qb, p * 64, it.head, qrow);
+              tma_load_3d(sQ_of(st) + p * kPanelBytes, &tm_q, qb, p * 64, qh, qrow);
             bulk_load(sStat + st * C::kStatBytes, a.ws.nlse2 + g * kTile, kTile * 4, qb);
             bulk_load(sStat + st * C::kStatBytes + kTile * 4, a.ws.ndsum + g * kTile, kTile * 4, qb);
             q_issued = q_it + 1;
@@ -563,7 +569,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
             const uint32_t db = smem_u32(&bars->do_full[st]);
             mbar_arrive_expect_tx(db, C::kdOBytes);
             for (int p = 0; p < C::kVPanels; ++p)
-              tma_load_3d(sdO_of(st) + p * kPanelBytes, &tm_do, db, p * 64, it.head, qrow);
+              tma_load_3d(sdO_of(st) + p * kPanelBytes, &tm_do, db, p * 64, qh, qrow);
             do_issued = q_it + 1;
             ATTN_TRACE_EV(42, q_it);
             return true;
@@ -654,7 +660,9 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         if (item >= sh.n_items) break;
         const Item it = decode_item(sh, tb, item, false);
         const int nq = cdiv(it.Lq, kTile);
-        const int i0 = first_qtile(sh, it, it.tile), i1 = last_qtile(sh, it, it.tile, nq) + 1;
+        const int i0 = first_qtile(sh, it, it.tile);
+        int i1 = last_qtile(sh, it, it.tile, nq) + 1;
+        if constexpr (kGroup) i1 = i0 + max(0, i1 - i0) * group;  // (only the count matters here)
         // Without a block mask the q-tiles are i0 .. i1-1.  With one, the
         // producer's per-stage flag says whether a stage's q-tile is the
         // item's last (read right after the stage's q_full wait, one step
@@ -791,6 +799,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       const int kidx0 = it.tile * kTile + r;  // this thread's key
       const bool key_ok = kidx0 < it.Lk;
       const uint8_t* col = mask_col<kMask>(sh, it);
+      for (int qh = 0; ok && qh < group; ++qh)
       for (int i = next_qtile(sh, col, i0, i1); i < i1;
            i = next_qtile(sh, col, i + 1, i1), ++q_it, ++gi) {
         const uint32_t st = q_it % C::kStages;
@@ -931,6 +940,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       const int i1 = last_qtile(sh, it, it.tile, nq) + 1;
       const uint8_t* col = mask_col<kMask>(sh, it);
       const int ifirst = next_qtile(sh, col, first_qtile(sh, it, it.tile), i1);
+      for (int qh = it.head * group; ok && qh < (it.head + 1) * group; ++qh)
       for (int i = ifirst; i < i1; i = next_qtile(sh, col, i + 1, i1), ++gi) {
         // deterministic order: contributions to q-tile i are added in
         // descending kv-tile order.  The tile's word holds 1 + the kv tile
@@ -978,7 +988,7 @@ __global__ void __launch_bounds__(kMainThreads, 1)
           st_release_gpu(a.ws.sem + rel_word, rel_val);
           rel_word = -1;
         }
-        const int64_t g = (int64_t)(it.tile_base + i) * sh.H + it.head;
+        const int64_t g = (int64_t)(it.tile_base + i) * sh.H + qh;
         float* acc = a.ws.dq_acc + g * (kTile * DQK);
         if (a.deterministic) {
           int* sem = a.ws.sem + 2 * g;
@@ -1193,8 +1203,9 @@ cudaError_t launch_all(const BwdLaunch& L, const Tables& tb) {
     if (L.pair) {
       e = launch_bwd_pair_main(L);
     } else {
-      auto* k = L.sh.blk != nullptr ? attn_bwd_main_kernel<DQK, DV, Tables, true>
-                                    : attn_bwd_main_kernel<DQK, DV, Tables, false>;
+      auto* k = L.sh.blk != nullptr ? attn_bwd_main_kernel<DQK, DV, Tables, true, false>
+                : L.sh.group > 1    ? attn_bwd_main_kernel<DQK, DV, Tables, false, true>
+                                    : attn_bwd_main_kernel<DQK, DV, Tables, false, false>;
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                C::kSmemBytes + kTraceSmem);
       if (e != cudaSuccess) return e;

@@ -30,6 +30,8 @@
 //             first); deterministic mode runs n descending, which is also the
 //             order in which each dQ tile receives its contributions, so a CTA
 //             only ever waits on work that was claimed before its own.
+//             Grouped heads: h is the key head, whose tiles take the q-tiles of all of its
+//             query heads; rank-major where a call's operands fit in L2 together.
 //   Variable-length batches run sequence by sequence, most work (Lq * Lk) first.
 #pragma once
 
@@ -60,7 +62,9 @@ struct NoTables {};
 
 struct SeqShape {
   int nseq;        // B (number of sequences)
-  int H;           // heads
+  int H;           // query heads
+  int Hk;          // key heads (H unless heads are grouped)
+  int group;       // query heads that share a key head: H / Hk
   int varlen;      // 1: lengths come from VarlenTables
   int Tq, Tk;      // fixed-length sequence lengths (varlen: total token counts)
   int nq_tiles;    // fixed-length: ceil(Tq/128)
@@ -76,7 +80,8 @@ struct SeqShape {
   int band_off;
   int wl, wr;
   int descending;  // backward only: 1 = kv-tiles n descending (deterministic mode)
-  int rank_major;  // forward, fixed length: 1 = units rank-major ((b, h) fastest)
+  int rank_major;  // 1 = units or kv-tiles rank-major ((b, h) fastest; within each sequence of
+                   // a variable-length batch, h fastest).  Backward: grouped heads only
   // Block mask (null: every tile pair in the band takes part).  Byte
   // [b][h][qt][kt] of a (mask batches, mask heads, q-tiles, kv-tiles) array;
   // a zero byte drops the pair (query tile qt, key tile kt) of sequence b,
@@ -87,7 +92,7 @@ struct SeqShape {
 };
 
 struct Item {
-  int seq, head, tile;  // tile = q-tile (forward) or kv-tile (backward)
+  int seq, head, tile;  // forward: query head, q-tile; backward: key head, kv-tile
   int row0;             // first token row of the sequence's queries
   int krow0;            // first token row of its keys
   int Lq, Lk;           // sequence lengths (queries, keys)
@@ -119,12 +124,19 @@ __device__ __forceinline__ Item decode_item<NoTables>(const SeqShape& sh, const 
     }
     it.tile = sh.nq_units - 1 - rank;
   } else {        // (b, h) major, tile rank fastest
-    bh = item / sh.nk_tiles;
-    rank = item - bh * sh.nk_tiles;
+    if (sh.rank_major) {
+      const int nbh = sh.nseq * sh.Hk;
+      rank = item / nbh;
+      bh = item - rank * nbh;
+    } else {
+      bh = item / sh.nk_tiles;
+      rank = item - bh * sh.nk_tiles;
+    }
     it.tile = sh.descending ? sh.nk_tiles - 1 - rank : rank;
   }
-  it.seq = bh / sh.H;
-  it.head = bh - it.seq * sh.H;
+  const int heads = forward ? sh.H : sh.Hk;
+  it.seq = bh / heads;
+  it.head = bh - it.seq * heads;
   it.Lq = sh.Tq;
   it.Lk = sh.Tk;
   it.row0 = it.seq * sh.Tq;
@@ -155,8 +167,14 @@ __device__ __forceinline__ Item decode_item<VarlenTables>(const SeqShape& sh,
   // forward items: 256-row query units; backward items: kv-tiles
   const int nt = forward ? cdiv(it.Lq, kFwdRows) : cdiv(it.Lk, kTile);
   // head, then tile rank
-  it.head = local / nt;
-  const int rank = local - it.head * nt;
+  int rank;
+  if (!forward && sh.rank_major) {
+    rank = local / sh.Hk;
+    it.head = local - rank * sh.Hk;
+  } else {
+    it.head = local / nt;
+    rank = local - it.head * nt;
+  }
   if (forward) it.tile = nt - 1 - rank;
   else it.tile = sh.descending ? nt - 1 - rank : rank;
   it.tile_base = tb.tile_start[it.seq];

@@ -318,6 +318,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             tma_load_3d(sQ + w * C::kQTileBytes + pnl * kPanelBytes, &tm_q, qf, pnl * 64, it.head,
                         it.row0 + it.tile * kFwdRows + w * kTile);
         const int krow0 = key_row0(sh, it);
+        const int kvhead = it.head / sh.group;
         // every kv tile either Q tile uses: lo0 .. hi1, or MaskOrder's tiles
         MaskOrder ord{0, lo0, lo0, 0};
         int who = 3, k0 = 0, k1 = 0, r = 0;
@@ -346,7 +347,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const uint32_t kf = smem_u32(&bars->k_full[sk]);
           mbar_arrive_expect_tx(kf, C::kKBytes);
           for (int pnl = 0; pnl < C::kQPanels; ++pnl)
-            tma_load_3d(sK + sk * C::kKBytes + pnl * kPanelBytes, &tm_k, kf, pnl * 64, it.head,
+            tma_load_3d(sK + sk * C::kKBytes + pnl * kPanelBytes, &tm_k, kf, pnl * 64, kvhead,
                         krow0 + j * kTile);
           k_issued = kv_it + 1;
           if (!(ok = mbar_wait(smem_u32(&bars->v_empty[sv]), ((kv_it / C::kVStages) & 1) ^ 1, ab)))
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const uint32_t vf = smem_u32(&bars->v_full[sv]);
           mbar_arrive_expect_tx(vf, C::kVBytes);
           for (int pnl = 0; pnl < C::kVPanels; ++pnl)
-            tma_load_3d(sV + sv * C::kVBytes + pnl * kPanelBytes, &tm_v, vf, pnl * 64, it.head,
+            tma_load_3d(sV + sv * C::kVBytes + pnl * kPanelBytes, &tm_v, vf, pnl * 64, kvhead,
                         krow0 + j * kTile);
           ++kv_it;
         }

@@ -208,6 +208,35 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
                 void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Grouped heads: Hq query heads over Hk key heads, Hq a multiple of Hk; query
+ * head h uses key head h / (Hq / Hk).  As attn_fwd_ex / attn_bwd_ex without a
+ * block mask (causal, windows, variable length and what they refuse; Hq == Hk
+ * is allowed), with the distances between token rows given tensor by tensor:
+ * q, o, dO, dq (.., Hq, d), k, v, dk, dv (.., Hk, d), the heads of a row
+ * adjacent, rows evenly spaced over the whole batch.  dk and dv are sums over
+ * the group's query heads, accumulated in fp32 and rounded once.  LSE has Hq
+ * heads.  Workspace: attn_bwd_workspace_size() with H = Hq.
+ * No counterpart on the pages.
+ *
+ * attn_rows: elements between token rows, a multiple of 8 and at least H*d (0:
+ * dense, H*d); the slices of one projection (T, (Hq + 2 Hk) * d) have its
+ * width.  NULL: all dense.  The forward reads q, k, v and o.
+ */
+typedef struct attn_rows {
+  long long q, k, v, o, d_o, dq, dk, dv;
+} attn_rows;
+int attn_fwd_grouped(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                     int Hq, int Hk, int Tq, int Tk, int dqk, int dv, const attn_rows* rows,
+                     int causal, int window_left, int window_right, float scale,
+                     const int* cu_seqlens_q, const int* cu_seqlens_k, void* stream);
+int attn_bwd_grouped(const void* q, const void* k, const void* v, const void* o, const void* dO,
+                     const float* lse, void* dq, void* dk, void* dv_out, int B, int Hq, int Hk,
+                     int Tq, int Tk, int dqk, int dv, const attn_rows* rows, int causal,
+                     int window_left, int window_right, float scale, const int* cu_seqlens_q,
+                     const int* cu_seqlens_k, int deterministic, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
  * Backward for callers that cannot allocate device memory (a plugin whose host
  * framework owns all device memory, or a loop where a device-synchronising
  * cudaMalloc is not allowed).  Same arguments and results as attn_bwd, minus
