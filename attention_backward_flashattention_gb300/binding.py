@@ -45,7 +45,8 @@ EXPORTED = ("attn_fwd", "attn_bwd_workspace_size", "attn_bwd", "attn_bwd_status"
             "attn_bwd_ex", "attn_debug_cache_stats", "attn_debug_set_bwd_variant",
             "attn_rope_rates", "attn_rope", "attn_cache_append", "attn_cache_status",
             "attn_decode", "attn_decode_workspace_size", "attn_decode_workspace_init",
-            "attn_fwd_grouped", "attn_bwd_grouped")
+            "attn_fwd_grouped", "attn_bwd_grouped", "attn_prefill",
+            "attn_prefill_workspace_size")
 BLOCK = 128  # rows per block of a block-sparse mask
 
 _lock = threading.Lock()
@@ -161,6 +162,10 @@ def load():
         lib.attn_bwd_grouped.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, I, I,
                                          I, F, P, P, I, P, SZ, P]
         lib.attn_bwd_grouped.restype = I
+        lib.attn_prefill_workspace_size.argtypes = []
+        lib.attn_prefill_workspace_size.restype = SZ
+        lib.attn_prefill.argtypes = [P, P, I, L, P, I, I, P, P, L, P, P, I, I, F, P, SZ, P]
+        lib.attn_prefill.restype = I
         _lib = lib
         return lib
 
@@ -481,6 +486,19 @@ def attn_decode(cache, block_table, max_pages, table_stride, lens, B, q, q_row, 
                               _ptr(lens), B, _ptr(q), q_row, _ptr(o), _ptr(lse), Hq,
                               _c_int(window_left), float(scale), _ptr(workspace),
                               int(workspace_bytes), _stream(stream))
+
+
+def attn_prefill_workspace_size() -> int:
+    return int(load().attn_prefill_workspace_size())
+
+
+def attn_prefill(cache, block_table, max_pages, table_stride, lens, B, T, cu_seqlens, q, q_row, o,
+                 lse, Hq, window_left, scale, workspace, workspace_bytes, stream=None) -> int:
+    cu = _HostInts(cu_seqlens)
+    return load().attn_prefill(_struct(cache), _ptr(block_table), max_pages, table_stride,
+                               _ptr(lens), B, T, cu.ptr, _ptr(q), q_row, _ptr(o), _ptr(lse), Hq,
+                               _c_int(window_left), float(scale), _ptr(workspace),
+                               int(workspace_bytes), _stream(stream))
 
 
 # ----------------------------------------------------------------------------
@@ -1078,4 +1096,65 @@ def decode(cache, q, block_table, lens, scale=None, window_left=-1, with_lse=Tru
                             float(scale), workspace.data_ptr(), workspace.nbytes, _current(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_decode")
+    return o, lse
+
+
+def prefill_workspace(device=None):
+    """A workspace for prefill(); calls that share one must be ordered on the GPU."""
+    device = torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError("a prefill workspace must be on a CUDA device")
+    return torch.empty(attn_prefill_workspace_size(), dtype=torch.uint8, device=device)
+
+
+def prefill(cache, q, block_table, lens, scale=None, window_left=-1, with_lse=True,
+            cu_seqlens=None, workspace=None, out=None, stream=None):
+    """Attention of a chunk of new tokens per sequence over a PagedCache that holds them already:
+    o (T,Hq,dv) bf16 and the log-sum-exp (T,Hq) fp32 (None unless with_lse).
+
+    q (T,Hq,dqk) bf16, Hq a multiple of the cache's heads; lens: device int32, each sequence's
+    length with the new tokens counted.  Without cu_seqlens (host offsets of the new rows) every
+    sequence brings T / sequences tokens.  A token sees the keys up to its own, with
+    window_left >= 0 only the last window_left + 1 of them.  workspace: from
+    prefill_workspace() (None: one is made for this call).  out: (o, lse) to write to (lse may
+    be None)."""
+    B, width, stride = _check_tables(cache, block_table, lens)
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != cache.dqk:
+        raise ValueError("q must be (T, heads, dqk)")
+    T, Hq, q_row = shape[0], shape[1], _rows(q, shape, "q")
+    if cu_seqlens is not None and len(cu_seqlens) != B + 1:
+        raise ValueError("cu_seqlens must have one entry more than there are sequences")
+    o, lse = out if out is not None else (None, None)
+    if out is not None and (o.dtype is not torch.bfloat16 or o.shape != (T, Hq, cache.dv)
+                            or not o.is_contiguous()):
+        raise ValueError("out[0] must be contiguous bfloat16 (T, heads, dv)")
+    if lse is not None and (lse.dtype is not torch.float32 or lse.shape != (T, Hq)
+                            or not lse.is_contiguous()):
+        raise ValueError("out[1] must be contiguous float32 (T, heads)")
+    if workspace is not None and not workspace.is_contiguous():  # (nbytes counts its memory)
+        raise ValueError("workspace must be contiguous")
+    index = _device_of(cache.k_cache, q, block_table, lens, workspace, o, lse)
+    if scale is None:
+        scale = 1.0 / math.sqrt(cache.dqk)
+    if not _here(index, stream):
+        with _On(index, stream):
+            return prefill(cache, q, block_table, lens, scale, window_left, with_lse, cu_seqlens,
+                           workspace, out)
+    if out is None:
+        device = q.device
+        o = _empty((T, Hq, cache.dv), torch.bfloat16, device)
+        lse = _empty((T, Hq), torch.float32, device) if with_lse else None
+    if T == 0 or B == 0:  # (tensors without elements have no address)
+        return o, lse
+    if workspace is None:
+        workspace = _empty((attn_prefill_workspace_size(),), torch.uint8, q.device)
+    cu = _HostInts(cu_seqlens)
+    rc = load().attn_prefill(cache.address, block_table.data_ptr(), width, stride,
+                             lens.data_ptr(), B, T, cu.ptr, q.data_ptr(), q_row, o.data_ptr(),
+                             None if lse is None else lse.data_ptr(), Hq, _c_int(window_left),
+                             float(scale), workspace.data_ptr(), workspace.nbytes,
+                             _current(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_prefill")
     return o, lse

@@ -12,6 +12,8 @@
 #include "../../include/attn.h"
 #include "attn_internal.h"
 #include "attn_paged.h"
+#include "attn_prefill.h"
+#include "tmap.h"
 
 using namespace attn;
 
@@ -330,6 +332,90 @@ int attn_decode(const attn_paged_cache* cache, const int* block_table, int max_p
   if (!L.status) return ATTN_ERR_CUDA;
   L.stream = static_cast<cudaStream_t>(stream);
   return cuda_err(launch_decode(L));
+}
+
+size_t attn_prefill_workspace_size(void) { return kPrefillWorkspaceBytes; }
+
+int attn_prefill(const attn_paged_cache* cache, const int* block_table, int max_pages,
+                 long long table_stride, const int* lens, int B, int T, const int* cu_seqlens,
+                 const void* q, long long q_row, void* o, float* lse, int Hq, int window_left,
+                 float scale, void* workspace, size_t workspace_bytes, void* stream) {
+  PrefillLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  int rc = check_cache(cache, block_table, max_pages, table_stride, lens, B, &L.cache);
+  if (rc) return rc;
+  if (q == nullptr || o == nullptr || workspace == nullptr || Hq <= 0 || T < 0 ||
+      window_left < -1)
+    return ATTN_ERR_INVALID_ARG;
+  // (a factor that is 0 or inf would make a hidden key's -inf, or a score of 0, NaN)
+  if (!(scale >= std::numeric_limits<float>::min()) || !std::isfinite(scale * kLog2e))
+    return ATTN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 4) || !aligned(workspace, 256))
+    return ATTN_ERR_INVALID_ARG;
+  if (!row_stride(&q_row, Hq, cache->dqk) || q_row >= (1ll << 38)) return ATTN_ERR_INVALID_ARG;
+  if (Hq % cache->heads != 0) return ATTN_ERR_INVALID_ARG;
+  const int group = Hq / cache->heads;
+  if (group > kTile || (int64_t)Hq * cache->dqk > (1 << 20) || T > INT32_MAX - (1 << 20) ||
+      B > (1 << 20))
+    return ATTN_ERR_UNSUPPORTED;
+  if (workspace_bytes < kPrefillWorkspaceBytes) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+  PrefillShape& sh = L.sh;
+  sh.B = B;
+  sh.group = group;
+  sh.per_tile = kTile / group;
+  // (a window as long as the table's room is none; shorter ones leave sums with it in range)
+  sh.window = window_left >= std::min<int64_t>((int64_t)max_pages * cache->page_size,
+                                               INT32_MAX - (1 << 20))
+                  ? -1
+                  : window_left;
+  static thread_local PrefillOffsets offsets;
+  int64_t units = 0;
+  if (cu_seqlens != nullptr) {
+    if (B > ATTN_MAX_VARLEN_SEQS) return ATTN_ERR_UNSUPPORTED;
+    if (cu_seqlens[0] != 0 || cu_seqlens[B] != T) return ATTN_ERR_INVALID_ARG;
+    for (int b = 0; b < B; ++b) {
+      if (cu_seqlens[b + 1] < cu_seqlens[b]) return ATTN_ERR_INVALID_ARG;
+      offsets.cu[b] = cu_seqlens[b];
+      offsets.unit0[b] = (int)units;
+      units += prefill_units(cu_seqlens[b + 1] - cu_seqlens[b], sh.per_tile);
+    }
+    offsets.cu[B] = T;
+    offsets.unit0[B] = (int)units;
+    L.offsets = &offsets;
+  } else {
+    if (T % B != 0) return ATTN_ERR_INVALID_ARG;
+    sh.per_seq = T / B;
+    sh.units_per_seq = prefill_units(sh.per_seq, sh.per_tile);
+    units = (int64_t)B * sh.units_per_seq;
+  }
+  if (T == 0) return ATTN_OK;
+  sh.units = (int)units;  // (at most T)
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return ATTN_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)cache->dqk, (cuuint64_t)Hq, (cuuint64_t)T};
+  const cuuint64_t strides[2] = {(cuuint64_t)cache->dqk * 2, (cuuint64_t)q_row * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)group, (cuuint32_t)sh.per_tile}, one[3] = {1, 1, 1};
+  if (enc(&L.tm_q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+          one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return ATTN_ERR_CUDA;
+  L.T = T;
+  L.Hq = Hq;
+  L.o = o;
+  L.lse = lse;
+  L.scale_log2 = scale * kLog2e;
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  L.desc = reinterpret_cast<PrefillDesc*>(base);
+  L.ml = reinterpret_cast<float2*>(base + kPrefillDescBytes);
+  L.acc = reinterpret_cast<float*>(base + kPrefillDescBytes + kPrefillMlBytes);
+  L.dqk = cache->dqk;
+  L.dv = cache->dv;
+  L.num_sms = sm_count();
+  if (L.num_sms <= 0) return ATTN_ERR_CUDA;
+  L.status = cache_status_ptr();
+  if (!L.status) return ATTN_ERR_CUDA;
+  L.stream = static_cast<cudaStream_t>(stream);
+  return cuda_err(launch_prefill(L));
 }
 
 int attn_cache_status(void* stream) {

@@ -1,0 +1,901 @@
+// attn_prefill.cuh — attention of a chunk of new tokens per sequence over the paged cache.
+//
+// Mathematics.  New token i of n of a sequence of `len` tokens sits at position p = len - n + i
+// and sees the keys max(0, p - window) .. p:  O = sum_j w_j v_j / sum_j w_j with w_j =
+// 2^(c (s_j - m)), s_j = q . k_j, c = scale log2(e) (times the key head's scale of an e4m3 cache),
+// m a running maximum of the scores.  LSE = ln 2 (c m + log2 sum w).
+//
+// One CTA (512 threads) per SM, each with an equal share of the line of key tiles
+// (attn_prefill.h):
+//   warps 0-3, 4-7  softmax warpgroup w: thread = query row (TMEM lane) of query tile w
+//   warps 8-11      key and value rows from their pages to shared memory, 32 rows of a tile
+//                   each: copies of 16 bytes that the thread waits for in groups (any page
+//                   size and stride, and rows that nothing sees become zeros on the way)
+//   warp 12         MMA issuer: S_w = Q_w K^T, O_w += P_w V (tcgen05, accumulators in TMEM, P
+//                   in TMEM as the A operand)
+//   warp 13         walks over the share's units, loads their queries by TMA
+// A unit has two query tiles, or one whose key tiles the warpgroups take in turn (each with
+// its own O, joined in tensor memory at the end): with few rows the chain S -> softmax -> PV of
+// one tile runs beside the other's.  Parts of a unit that is cut leave unnormalised sums in the
+// workspace, and a second launch joins them in a fixed order.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <climits>
+
+#include "attn_internal.h"
+#include "attn_prefill.h"
+#include "ptx.cuh"
+
+namespace attn {
+namespace {
+
+constexpr int kPrefillThreads = 512;
+constexpr int kCopyWarp = 8, kPrefillMmaWarp = 12, kWalkWarp = 13;
+constexpr int kPrefillPanel = kTile * 128;  // [128 rows][64] bf16
+constexpr int kPrefillMaxSmem = 232448;
+constexpr int kKeyRing = 8;  // key tiles whose bits are kept (more than are under way)
+
+template <int DQK, int DV, bool E4M3>
+struct PrefillCfg {
+  static constexpr int kQTile = DQK / 64 * kPrefillPanel;
+  static constexpr int kKBytes = DQK / 64 * kPrefillPanel;
+  static constexpr int kVBytes = DV / 64 * kPrefillPanel;
+  static constexpr int kKStages = DQK == 64 ? 5 : DQK == 128 ? 3 : 2;
+  static constexpr int kVStages = DQK == 64 ? 5 : DQK == 128 ? 2 : 1;
+  static constexpr int kOffK = 2 * kQTile;
+  static constexpr int kOffV = kOffK + kKStages * kKBytes;
+  static constexpr int kOffBar = kOffV + kVStages * kVBytes;
+  static constexpr int kSmemBytes = kOffBar + 3072;
+  static_assert(kSmemBytes <= kPrefillMaxSmem, "shared memory budget");
+  static constexpr uint32_t kTmemO = 256;
+  // Registers a thread after the split of 512 x 128: softmax, copies, MMA and walk.
+  static constexpr uint32_t kRegsSoftmax = E4M3 ? 176 : 184;
+  static constexpr uint32_t kRegsCopy = E4M3 ? 88 : 72;
+  static constexpr uint32_t kRegsCtl = 72;
+  static_assert(2 * kRegsSoftmax + kRegsCopy + kRegsCtl <= 512, "register split");
+};
+
+struct PrefillBars {
+  uint64_t item_full[2], item_empty[2];
+  uint64_t q_full, q_empty;
+  uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t twin_full, twin_done;
+  uint64_t drain;
+  PrefillItem item[2];
+  uint32_t there[kKeyRing][4];  // of a key tile's 128 keys, which are in the cache
+  uint32_t bad[kKeyRing][4];    // of an edge tile's, whose values are not finite
+  float2 twin[2][kTile];         // (m, l) of a single tile's rows, by warpgroup
+  uint32_t tmem_base;
+  int abort_flag;
+};
+static_assert(sizeof(PrefillBars) <= 3072, "barrier block size");
+
+struct PrefillParams {
+  CacheView cache;
+  PrefillShape sh;
+  int64_t room;       // tokens that a row of the block table has pages for
+  int Hq;
+  __nv_bfloat16* o;
+  float* lse;
+  float scale_log2;
+  PrefillDesc* desc;
+  float2* ml;
+  float* acc;
+  int* status;
+};
+
+template <typename Offsets>
+__device__ __forceinline__ PrefillUnit unit_at(const PrefillParams& P, const Offsets& off, int i) {
+  int b, u, row0, n;
+  if constexpr (sizeof(Offsets) >= sizeof(PrefillOffsets)) {
+    int lo = 0, hi = P.sh.B - 1;  // the last sequence with unit0 <= i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (off.unit0[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+    u = i - off.unit0[b];
+    row0 = off.cu[b];
+    n = off.cu[b + 1] - row0;
+  } else {
+    b = i / P.sh.units_per_seq;
+    u = i - b * P.sh.units_per_seq;
+    n = P.sh.per_seq;
+    row0 = b * n;
+  }
+  const int len = __ldg(P.cache.lens + b);
+  if (len > P.room) atomicCAS(P.status, 0, kStatusBadPage);
+  return make_prefill_unit(P.sh, P.room, b, row0, n, len, u);
+}
+
+// P = 2^(c (S - m)) of a row's 128 scores as bf16 pairs, and its sum.  kFar: the scores are so
+// large that c m, rounded, is off by more than 2^-8: differences first, and c in two factors.
+template <bool kFar>
+__device__ __forceinline__ float prefill_exp(const uint32_t (&sr)[4][32], float f1, float f2_,
+                                             float m, uint32_t (&pk0)[32], uint32_t (&pk1)[32]) {
+  const float c = f1 * f2_;
+  const uint64_t c2 = f2(c, c), nm2 = kFar ? f2(-m, -m) : f2(-m * c, -m * c);
+  uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const uint64_t s2 = f2(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]));
+      float x0, x1;
+      if constexpr (kFar) {
+        const uint64_t d2 = add2(s2, nm2);
+        x0 = f2_lo(d2) * f1 * f2_;
+        x1 = f2_hi(d2) * f1 * f2_;
+      } else {
+        const uint64_t x2 = fma2(s2, c2, nm2);
+        x0 = f2_lo(x2);
+        x1 = f2_hi(x2);
+      }
+      const float p0 = ex2(x0), p1 = ex2(x1);
+      rs2[(e >> 1) & 3] = add2(rs2[(e >> 1) & 3], f2(p0, p1));
+      if (q < 2) pk0[q * 16 + e / 2] = pack_bf16(p0, p1);
+      else pk1[(q - 2) * 16 + e / 2] = pack_bf16(p0, p1);
+    }
+  }
+  const uint64_t s4 = add2(add2(rs2[0], rs2[1]), add2(rs2[2], rs2[3]));
+  return f2_lo(s4) + f2_hi(s4);
+}
+
+// 16 bytes from global memory to shared, or zeros.
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+
+// Four e4m3 values as two words of bf16 pairs (exact: a bf16 has every e4m3 value).
+__device__ __forceinline__ void e4m3_to_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  uint32_t h0, h1;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(h0), "=r"(h1)
+      : "r"(x));
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+  lo = pack_bf16(a.x, a.y);
+  hi = pack_bf16(b.x, b.y);
+}
+
+// Whether a word of two bf16 or four e4m3 values holds one that is not finite (all exponent bits
+// set; all seven bits of an e4m3 value, whose NaN that is).
+template <bool E4M3>
+__device__ __forceinline__ bool not_finite(uint32_t x) {
+  if constexpr (E4M3) return (((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+  return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+}
+
+template <int DQK, int DV, bool E4M3, typename Offsets>
+__global__ void __launch_bounds__(kPrefillThreads, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ PrefillParams P, const __grid_constant__ Offsets off) {
+  using C = PrefillCfg<DQK, DV, E4M3>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  PrefillBars* bars = reinterpret_cast<PrefillBars*>(smem + C::kOffBar);
+  const uint32_t sQ = smem_u32(smem), sK = sQ + C::kOffK, sV = sQ + C::kOffV;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const PrefillShape& sh = P.sh;
+  if (threadIdx.x == 0) P.desc[blockIdx.x].parts = 0;
+  if (sQ & 1023u) {  // the swizzled panels need a 1024-byte aligned window
+    if (threadIdx.x == 0) atomicCAS(P.status, 0, kStatusInternal);
+    return;
+  }
+
+  // ---- the line: every thread counts the tiles of some consecutive units
+  long long* before = reinterpret_cast<long long*>(smem);  // [512] tiles in front of a thread's
+  long long* warp_sum = before + kPrefillThreads;
+  const int per = (sh.units + kPrefillThreads - 1) / kPrefillThreads;
+  const int u0 = min(sh.units, (int)threadIdx.x * per), u1 = min(sh.units, u0 + per);
+  long long mine = 0;
+  for (int i = u0; i < u1; ++i) mine += unit_at(P, off, i).tiles;
+  long long upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += x;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  long long in_front = 0, per_head = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (i < warp) in_front += warp_sum[i];
+    per_head += warp_sum[i];
+  }
+  before[threadIdx.x] = in_front + upto - mine;
+  const PrefillLine line = make_prefill_line(per_head, sh.units, P.cache.heads, gridDim.x);
+  if ((int)blockIdx.x >= line.n) return;  // (before anything is set up)
+
+  Abort ab{&bars->abort_flag, P.status};
+  if (threadIdx.x == 0) {
+    bars->abort_flag = 0;
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(smem_u32(&bars->item_full[k]), 1);
+      mbar_init(smem_u32(&bars->item_empty[k]), 1 + 8 + 4);  // MMA, softmax warps, copy warps
+      mbar_init(smem_u32(&bars->s_full[k]), 1);
+      mbar_init(smem_u32(&bars->p_full[k]), 4);
+      mbar_init(smem_u32(&bars->o_done[k]), 1);
+    }
+    mbar_init(smem_u32(&bars->q_full), 1);
+    mbar_init(smem_u32(&bars->q_empty), 1);
+    for (int s = 0; s < C::kKStages; ++s) {
+      mbar_init(smem_u32(&bars->k_full[s]), 4);
+      mbar_init(smem_u32(&bars->k_empty[s]), 1);
+    }
+    for (int s = 0; s < C::kVStages; ++s) {
+      mbar_init(smem_u32(&bars->v_full[s]), 4);
+      mbar_init(smem_u32(&bars->v_empty[s]), 1);
+    }
+    mbar_init(smem_u32(&bars->twin_full), 8);
+    mbar_init(smem_u32(&bars->twin_done), 8);
+    mbar_init(smem_u32(&bars->drain), 1);
+    fence_barrier_init();
+  }
+  if (warp == kPrefillMmaWarp) {
+    tmem_alloc(smem_u32(&bars->tmem_base), 512);
+    tmem_relinquish();
+  }
+  if (warp == kWalkWarp && lane == 0) prefetch_tmap(&tm_q);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  // the walk's place on the line, found before the queries take `before`'s memory
+  PrefillWalk walk;
+  if (warp == kWalkWarp && lane == 0) {
+    const long long x0 = prefill_cut(line, blockIdx.x);
+    walk.line = line;
+    walk.c = blockIdx.x;
+    walk.units = sh.units;
+    walk.heads = P.cache.heads;
+    walk.head = (int)div_line(x0, per_head);
+    const long long x = x0 - walk.head * per_head;
+    int lo = 0, hi = kPrefillThreads - 1;  // the last thread with before <= x
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (before[mid] <= x) lo = mid; else hi = mid - 1;
+    }
+    walk.index = lo * per;
+    walk.at = walk.head * per_head + before[lo];
+    fence_proxy_async_smem();
+  }
+  __syncthreads();
+
+  if (warp >= kPrefillMmaWarp) {
+    regs_dec<C::kRegsCtl>();
+    if (warp == kWalkWarp && lane == 0) {
+      // ------------------------------------------------------------ walk, queries
+      uint32_t n = 0;  // items handed out
+      bool ok = true;
+      auto give = [&](const PrefillItem& it) -> bool {
+        const uint32_t slot = n & 1;
+        if (!mbar_wait(smem_u32(&bars->item_empty[slot]), ((n >> 1) & 1) ^ 1, ab)) return false;
+        bars->item[slot] = it;
+        mbar_arrive(smem_u32(&bars->item_full[slot]));
+        return true;
+      };
+      auto unit = [&](int i) { return unit_at(P, off, i); };
+      uint32_t q_loads = 0;
+      PrefillItem it;
+      walk.begin(unit);
+      while (walk.next(unit, &it)) {
+        if (it.parts > 0) P.desc[blockIdx.x] = PrefillDesc{it.parts, it.tok0, it.tokens, it.head};
+        if (!(ok = give(it))) break;
+        if (!(ok = mbar_wait(smem_u32(&bars->q_empty), (n & 1) ^ 1, ab))) break;
+        // rows past the sequence's tokens hold the next one's queries (or zeros): never stored
+        const int tiles = it.tokens <= sh.per_tile ? 1 : 2;
+        const uint32_t qf = smem_u32(&bars->q_full);
+        mbar_arrive_expect_tx(qf, (uint32_t)(tiles * (DQK / 64) * sh.per_tile * sh.group * 128));
+        q_loads = n + 1;
+        for (int w = 0; w < tiles; ++w)
+          for (int p = 0; p < DQK / 64; ++p)
+            tma_load_3d(sQ + w * C::kQTile + p * kPrefillPanel, &tm_q, qf, p * 64,
+                        it.head * sh.group, it.tok0 + w * sh.per_tile);
+        ++n;
+      }
+      if (ok) {
+        it.head = -1;
+        ok = give(it);
+      }
+      if (!ok && q_loads > 0) mbar_wait_drain(smem_u32(&bars->q_full), (q_loads - 1) & 1);
+    } else if (warp == kPrefillMmaWarp && lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
+      constexpr uint32_t idO = idesc_bf16(128, DV, false, true);
+      const uint64_t bQ = kmajor_base(sQ), bK = kmajor_base(sK), bV = mnmajor_base(sV, 128);
+      uint32_t n = 0, step = 0, cnt[2] = {0, 0};
+      bool ok = true;
+      auto W = [&](uint64_t& bar, uint32_t parity) -> bool {
+        if (!mbar_wait(smem_u32(&bar), parity, ab)) return false;
+        tc_fence_after();
+        return true;
+      };
+      for (;; ++n) {
+        if (!(ok = mbar_wait(smem_u32(&bars->item_full[n & 1]), (n >> 1) & 1, ab))) break;
+        const PrefillItem& item = bars->item[n & 1];
+        if (item.head < 0) break;
+        const int tiles = item.tiles;
+        const TileUse use = tile_use(sh, item);
+        mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
+        auto mma_S = [&](int w, uint32_t t) {
+          const uint64_t q = bQ + (uint64_t)((use.twin ? 0 : w) * (C::kQTile >> 4));
+          const uint64_t k = bK + (uint64_t)((t % C::kKStages) * (C::kKBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < DQK / 16; ++kk)
+            mma_bf16(tmem + w * 128, q + kmajor_step(kk, 128), k + kmajor_step(kk, 128), idS,
+                     kk > 0 ? 1u : 0u);
+          mma_commit(smem_u32(&bars->s_full[w]));
+        };
+        auto mma_PV = [&](int w, uint32_t t, bool first) {
+          const uint64_t v = bV + (uint64_t)((t % C::kVStages) * (C::kVBytes >> 4));
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_bf16_ts(tmem + C::kTmemO + w * DV, tmem + w * 128 + kk * 8, v + mnmajor_step(kk),
+                        idO, kk > 0 || !first ? 1u : 0u);
+        };
+        if (!(ok = W(bars->q_full, n & 1))) break;
+        if (!(ok = W(bars->k_full[step % C::kKStages], (step / C::kKStages) & 1))) break;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if (tile_used(use, w, 0)) mma_S(w, step);
+        mma_commit(smem_u32(&bars->k_empty[step % C::kKStages]));
+        if (tiles == 1) mma_commit(smem_u32(&bars->q_empty));
+        for (int t = 0; t < tiles; ++t, ++step) {
+          const bool next = t + 1 < tiles;
+          if (next) {
+            const uint32_t s1 = step + 1;
+            if (!(ok = W(bars->k_full[s1 % C::kKStages], (s1 / C::kKStages) & 1))) break;
+            // a warpgroup that has no part in this step starts on the next
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+              if (!tile_used(use, w, t) && tile_used(use, w, t + 1)) mma_S(w, s1);
+          }
+          if (!(ok = W(bars->v_full[step % C::kVStages], (step / C::kVStages) & 1))) break;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!tile_used(use, w, t)) continue;
+            if (!(ok = W(bars->p_full[w], cnt[w] & 1))) break;
+            ++cnt[w];
+            mma_PV(w, step, t == use.lo[w]);
+            if (t == use.hi[w]) mma_commit(smem_u32(&bars->o_done[w]));
+            if (next && tile_used(use, w, t + 1)) mma_S(w, step + 1);
+          }
+          if (!ok) break;
+          mma_commit(smem_u32(&bars->v_empty[step % C::kVStages]));
+          if (next) {
+            mma_commit(smem_u32(&bars->k_empty[(step + 1) % C::kKStages]));
+            if (t + 2 == tiles) mma_commit(smem_u32(&bars->q_empty));  // after the last S
+          }
+        }
+        if (!ok) break;
+      }
+      if (!ok) {
+        mma_commit(smem_u32(&bars->drain));
+        mbar_wait_drain(smem_u32(&bars->drain), 0);
+      }
+    }
+  } else if (warp >= kCopyWarp) {
+    if constexpr (C::kRegsCopy < 128) regs_dec<C::kRegsCopy>();
+    // -------------------------------------------------------------- keys and values
+    const int mw = warp - kCopyWarp;  // rows 32 mw .. 32 mw + 31 of every tile
+    uint32_t step = 0;
+    bool ok = true;
+    // copies on their way that have not been announced yet, oldest first: step numbers alternate
+    // key tile, value tile
+    constexpr int kAhead = C::kKStages + C::kVStages - 1;
+    uint32_t issued = 0, told = 0;  // key tile of step s: 2 s; its value tile: 2 s + 1
+    auto tell = [&]() {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const uint32_t s = told >> 1;
+        mbar_arrive(told & 1 ? smem_u32(&bars->v_full[s % C::kVStages])
+                             : smem_u32(&bars->k_full[s % C::kKStages]));
+      }
+      ++told;
+    };
+    // Waits; where that takes time, what is under way is announced first: it may be what the
+    // others wait for.
+    auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
+      if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&bar), parity))) return true;
+      cp_wait<0>();
+      while (told != issued) tell();
+      return mbar_wait_warp(smem_u32(&bar), parity, ab);
+    };
+    for (uint32_t n = 0;; ++n) {
+      if (!(ok = wait(bars->item_full[n & 1], (n >> 1) & 1))) break;
+      const PrefillItem it = bars->item[n & 1];
+      __syncwarp();
+      if (it.head < 0) break;
+      if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
+      const int* table = P.cache.table + it.seq * P.cache.table_stride;
+      const char* kbase = P.cache.k.base + it.head * P.cache.k.head;
+      const char* vbase = P.cache.v.base + it.head * P.cache.v.head;
+      // this lane's row of a key tile: the page is looked up a tile ahead
+      auto look_up = [&](int tile) -> int {
+        const int key = tile * kTile + mw * 32 + lane;
+        return key >= it.first && key < it.end ? __ldg(table + div_page(P.cache, key)) : -1;
+      };
+      int page = look_up(it.tile);
+      for (int t = 0; t < it.tiles && ok; ++t, ++step) {
+        const int key = (it.tile + t) * kTile + mw * 32 + lane;
+        const bool seen = key >= it.first && key < it.end;
+        const bool there = seen && page_in(P.cache, page);
+        if (seen && !there) atomicCAS(P.status, 0, kStatusBadPage);
+        const int in = key - div_page(P.cache, key) * P.cache.page_size;
+        // (-1: zeros)
+        const long long ko = there ? token_at(P.cache.k, page, in) : -1;
+        const long long vo = there ? token_at(P.cache.v, page, in) : -1;
+        const uint32_t bits = __ballot_sync(0xffffffffu, there);
+        if (t + 1 < it.tiles) page = look_up(it.tile + t + 1);
+        // Where some row does not see some key, values that are not finite may not reach the
+        // product (0 times them is NaN): they are looked for before the tile is handed on, zeros
+        // take their place, and the rows that see them become NaN by their sum.
+        uint32_t bad = 0;
+        const int key0 = (it.tile + t) * kTile;
+        if (key0 + kTile - 1 > it.pos0 ||
+            (sh.window >= 0 && key0 < it.pos0 + it.tokens - 1 - sh.window)) {
+          constexpr int kChunks = DV / (E4M3 ? 16 : 8), kRows = 32 / kChunks;
+#pragma unroll 1
+          for (int i0 = 0; i0 < kChunks; i0 += 4) {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int at = (i0 + i) * 32 + lane, row = at / kChunks, c = at - row * kChunks;
+              const long long from = __shfl_sync(0xffffffffu, vo, row);
+              v[i] = make_uint4(0, 0, 0, 0);
+              if (from >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(vbase + from + c * 16));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t found = __ballot_sync(
+                  0xffffffffu, not_finite<E4M3>(v[i].x) || not_finite<E4M3>(v[i].y) ||
+                                   not_finite<E4M3>(v[i].z) || not_finite<E4M3>(v[i].w));
+#pragma unroll
+              for (int k = 0; k < kRows; ++k)
+                if (found >> (k * kChunks) & ((1u << kChunks) - 1u))
+                  bad |= 1u << ((i0 + i) * kRows + k);
+            }
+          }
+        }
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          const uint32_t st = step % (side ? C::kVStages : C::kKStages);
+          const uint32_t parity = ((step / (side ? C::kVStages : C::kKStages)) & 1) ^ 1;
+          if (!(ok = wait(side ? bars->v_empty[st] : bars->k_empty[st], parity))) break;
+          if (side == 0 && lane == 0) {
+            bars->there[step % kKeyRing][mw] = bits;
+            bars->bad[step % kKeyRing][mw] = bad;
+          }
+          const uint32_t dst = (side ? sV + st * C::kVBytes : sK + st * C::kKBytes);
+          const char* base = side ? vbase : kbase;
+          const long long o = side ? (bad >> lane & 1u ? -1 : vo) : ko;
+          if constexpr (!E4M3) {
+            constexpr int kMost = DQK > DV ? DQK : DV;
+            const int chunks = (side ? DV : DQK) / 8;  // of 16 bytes, of a row
+#pragma unroll
+            for (int i = 0; i < kMost / 8; ++i) {
+              if (i >= chunks) break;
+              const int at = i * 32 + lane, row = at / chunks, c = at - row * chunks;
+              const long long from = __shfl_sync(0xffffffffu, o, row);
+              const int r = mw * 32 + row;
+              cp_async16_or_zero(dst + (c >> 3) * kPrefillPanel + sw128_offset(r, c & 7),
+                                 base + (from < 0 ? 0 : from + c * 16), from >= 0);
+            }
+          } else {
+            constexpr int kMost = DQK > DV ? DQK : DV;
+            const int chunks = (side ? DV : DQK) / 16;  // of 16 bytes, of a row
+            uint4 w[kMost / 16];
+#pragma unroll
+            for (int i = 0; i < kMost / 16; ++i) {
+              if (i >= chunks) break;
+              const int at = i * 32 + lane, row = at / chunks, c = at - row * chunks;
+              const long long from = __shfl_sync(0xffffffffu, o, row);
+              w[i] = make_uint4(0, 0, 0, 0);
+              if (from >= 0) w[i] = __ldg(reinterpret_cast<const uint4*>(base + from + c * 16));
+            }
+#pragma unroll
+            for (int i = 0; i < kMost / 16; ++i) {
+              if (i >= chunks) break;
+              const int at = i * 32 + lane, row = at / chunks, c = at - row * chunks;
+              const int r = mw * 32 + row;
+              const uint32_t panel = dst + (c >> 2) * kPrefillPanel;
+              uint32_t a[4], b[4];
+              e4m3_to_bf16(w[i].x, a[0], a[1]);
+              e4m3_to_bf16(w[i].y, a[2], a[3]);
+              e4m3_to_bf16(w[i].z, b[0], b[1]);
+              e4m3_to_bf16(w[i].w, b[2], b[3]);
+              st_shared_v4(panel + sw128_offset(r, (2 * c) & 7), a[0], a[1], a[2], a[3]);
+              st_shared_v4(panel + sw128_offset(r, (2 * c + 1) & 7), b[0], b[1], b[2], b[3]);
+            }
+          }
+          cp_commit();
+          ++issued;
+          if (E4M3) {
+            tell();
+          } else if (issued - told > kAhead) {
+            cp_wait<kAhead>();
+            tell();
+          }
+        }
+      }
+      if (!ok) break;
+    }
+    cp_wait<0>();
+    while (ok && told != issued) tell();
+  } else {
+    regs_inc<C::kRegsSoftmax>();
+    // -------------------------------------------------------------- softmax
+    const int w = warp >> 2;               // query tile, or every other key tile of a single one
+    const int r = (warp & 3) * 32 + lane;  // row of the tile == TMEM lane
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t tS = lanes + w * 128, tO = lanes + C::kTmemO + w * DV;
+    uint32_t step0 = 0, cnt = 0, twins = 0;
+    uint32_t done[2] = {0, 0};  // accumulators finished: this warpgroup's, the other's
+    bool ok = true;
+    const int rt = r / sh.group, rh = r - rt * sh.group;  // this row's token and head
+    for (uint32_t n = 0;; ++n) {
+      if (!(ok = mbar_wait_warp(smem_u32(&bars->item_full[n & 1]), (n >> 1) & 1, ab))) break;
+      const PrefillItem it = bars->item[n & 1];
+      __syncwarp();
+      if (it.head < 0) break;
+      if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
+      const TileUse use = tile_use(sh, it);
+      const int t0 = use.twin ? 0 : w * sh.per_tile;  // first token of this tile
+      const int tokens = min(it.tokens - t0, sh.per_tile);
+      const bool row_ok = rt < tokens;
+      const bool live = __any_sync(0xffffffffu, row_ok);  // (a warp without rows has no work)
+      const int pos = it.pos0 + t0 + rt;
+      // c in two factors, so that neither leaves fp32's range with the scale of an e4m3 cache
+      float f1 = P.scale_log2, f2_ = 1.f, v_scale = 1.f;
+      bool odd_c = false;
+      if constexpr (E4M3) {
+        if (P.cache.k.scale != nullptr) {
+          int e1, e2;
+          const float a = frexpf(P.scale_log2, &e1);
+          const float b = frexpf(__ldg(P.cache.k.scale + it.head), &e2);
+          const int e = e1 + e2, h = e >> 1;
+          f1 = ldexpf(a * b, h);
+          f2_ = ldexpf(1.f, e - h);
+          odd_c = e < -120 || e > 120;
+        }
+        if (P.cache.v.scale != nullptr) v_scale = __ldg(P.cache.v.scale + it.head);
+      }
+      const float c = f1 * f2_;
+      float m = -INFINITY, l = 0.f;
+      const int lo = use.lo[w], hi = use.hi[w];
+      for (int t = lo; t <= hi; t += use.twin ? 2 : 1) {
+        if (!(ok = mbar_wait_warp(smem_u32(&bars->s_full[w]), cnt & 1, ab))) break;
+        ++cnt;
+        tc_fence_after();
+        if (live) {
+          uint32_t sr[4][32];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, sr[q]);
+          const uint4 there =
+              *reinterpret_cast<const uint4*>(bars->there[(step0 + t) % kKeyRing]);
+          const int kbase = (it.tile + t) * kTile;
+          tmem_ld_wait();
+          // some row does not see some key of the tile: one that is not there, one after the
+          // first row's position, one in front of the last row's window
+          const bool edge = (there.x & there.y & there.z & there.w) != ~0u ||
+                            kbase + kTile - 1 > it.pos0 + t0 ||
+                            (sh.window >= 0 && kbase < it.pos0 + t0 + tokens - 1 - sh.window);
+          float mx[8];
+          bool sees_bad = false;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+          if (edge) {
+            const uint4 bad = *reinterpret_cast<const uint4*>(bars->bad[(step0 + t) % kKeyRing]);
+            // the row's keys, relative to the tile: klo .. khi - 1
+            const int khi = pos + 1 - kbase;
+            const int klo = sh.window >= 0 ? max(pos, 0) - sh.window - kbase : 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int a = min(32, max(0, klo - 32 * q)), b = min(32, max(0, khi - 32 * q));
+              uint32_t bits = q == 0 ? there.x : q == 1 ? there.y : q == 2 ? there.z : there.w;
+              bits &= b >= 32 ? ~0u : (1u << b) - 1u;
+              bits &= a >= 32 ? 0u : ~0u << a;
+              sees_bad |= (bits & (q == 0 ? bad.x : q == 1 ? bad.y : q == 2 ? bad.z : bad.w)) != 0;
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                const float x = (bits >> e) & 1u ? __uint_as_float(sr[q][e]) : -INFINITY;
+                sr[q][e] = __float_as_uint(x);
+                mx[e & 7] = fmaxf(mx[e & 7], x);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                mx[(e >> 1) & 7] = max3(mx[(e >> 1) & 7], __uint_as_float(sr[q][e]),
+                                        __uint_as_float(sr[q][e + 1]));
+            }
+          }
+          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
+          // the maximum moves (and O is rescaled) only when it grows by more than 2^8
+          const float m_new = fmaxf(m, top);
+          const bool none = m_new == -INFINITY;  // no key seen yet, or scores of -inf alone
+          const bool resc = !none && (m_new - m) * f1 * f2_ > 8.0f;
+          const float m_use = none ? 0.f : (resc ? m_new : m);
+          const float alpha = resc ? ex2((m - m_use) * f1 * f2_) : 1.0f;
+          uint32_t pk0[32], pk1[32];
+          const bool far = row_ok && (odd_c || !(fabsf(m_use * c) <= 65536.f));
+          float sum;
+          if (__any_sync(0xffffffffu, far)) sum = prefill_exp<true>(sr, f1, f2_, m_use, pk0, pk1);
+          else sum = prefill_exp<false>(sr, f1, f2_, m_use, pk0, pk1);
+          if (t > lo && __any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+            for (int q = 0; q < DV / 32; ++q) {
+              uint32_t ov[32];
+              tmem_ld32(tO + q * 32, ov);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+              tmem_st32(tO + q * 32, ov);
+            }
+          }
+          l = sees_bad ? NAN : l * alpha + sum;
+          m = none ? -INFINITY : m_use;
+          tmem_st32(tS, pk0);
+          tmem_st32(tS + 32, pk1);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[w]));
+      }
+      if (!ok) break;
+      step0 += it.tiles;
+      // -------- end of the part: O, or its sums
+      const int mine = hi >= lo ? 1 : 0, theirs = use.hi[w ^ 1] >= use.lo[w ^ 1] ? 1 : 0;
+      if (mine && !(ok = mbar_wait_warp(smem_u32(&bars->o_done[w]), done[0] & 1, ab))) break;
+      done[0] += mine;
+      float a_mine = 1.f, a_theirs = 0.f;
+      float top = m * f1 * f2_;  // in base 2
+      int q0 = 0, q1 = DV / 32;  // this warpgroup's columns, in 32s
+      if (use.twin) {
+        if (theirs && !(ok = mbar_wait_warp(smem_u32(&bars->o_done[w ^ 1]), done[1] & 1, ab)))
+          break;
+        // the halves: (m, l) through shared memory, O from both accumulators
+        bars->twin[w][r] = make_float2(top, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->twin_full));
+        if (!(ok = mbar_wait_warp(smem_u32(&bars->twin_full), twins & 1, ab))) break;
+        const float2 first = bars->twin[0][r], second = bars->twin[1][r];
+        const float t2 = fmaxf(first.x, second.x);
+        const float a0 = first.x == t2 ? (t2 == -INFINITY ? 0.f : 1.f) : ex2(first.x - t2);
+        const float a1 = second.x == t2 ? (t2 == -INFINITY ? 0.f : 1.f) : ex2(second.x - t2);
+        l = first.y * a0 + second.y * a1;
+        top = t2;
+        a_mine = w == 0 ? a0 : a1;
+        a_theirs = w == 0 ? a1 : a0;
+        if (w == 0) q1 = DV / 64; else q0 = DV / 64;
+      }
+      done[1] += theirs;
+      tc_fence_after();
+      const bool whole = it.slot < 0;
+      const int64_t token = (int64_t)it.tok0 + t0 + rt;
+      const int head = it.head * sh.group + rh;
+      const bool no_key = l == 0.f;
+      const float factor = (no_key ? 0.f : whole ? 1.0f / l : 1.0f) * v_scale;
+      const int64_t srow = (int64_t)it.slot * kPrefillRows + (use.twin ? 0 : w * kTile) + r;
+      if (live) {
+#pragma unroll 1
+        for (int q = q0; q < q1; ++q) {
+          uint32_t ov[32];
+          float x[32];
+          if (use.twin) {
+            // (an accumulator that nothing was added to holds anything: its factor is 0)
+            uint32_t ow[32];
+            tmem_ld32(lanes + C::kTmemO + w * DV + q * 32, ov);
+            tmem_ld32(lanes + C::kTmemO + (w ^ 1) * DV + q * 32, ow);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              x[e] = (a_mine == 0.f ? 0.f : __uint_as_float(ov[e]) * a_mine) +
+                     (a_theirs == 0.f ? 0.f : __uint_as_float(ow[e]) * a_theirs);
+          } else {
+            tmem_ld32(tO + q * 32, ov);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = __uint_as_float(ov[e]);
+          }
+          if (!row_ok) continue;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) x[e] = no_key ? 0.f : x[e] * factor;
+          if (whole) {
+            __nv_bfloat16* dst = P.o + (token * P.Hq + head) * DV + q * 32;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              *reinterpret_cast<uint4*>(dst + k) =
+                  make_uint4(pack_bf16(x[k], x[k + 1]), pack_bf16(x[k + 2], x[k + 3]),
+                             pack_bf16(x[k + 4], x[k + 5]), pack_bf16(x[k + 6], x[k + 7]));
+          } else {
+            float* dst = P.acc + srow * DV + q * 32;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8)
+              st_global_v8(dst + k, __float_as_uint(x[k]), __float_as_uint(x[k + 1]),
+                           __float_as_uint(x[k + 2]), __float_as_uint(x[k + 3]),
+                           __float_as_uint(x[k + 4]), __float_as_uint(x[k + 5]),
+                           __float_as_uint(x[k + 6]), __float_as_uint(x[k + 7]));
+          }
+        }
+        if (row_ok && (!use.twin || w == 0)) {
+          if (!whole) P.ml[srow] = make_float2(top, l);
+          else if (P.lse != nullptr)
+            P.lse[token * P.Hq + head] =
+                no_key ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
+        }
+      }
+      tc_fence_before();
+      if (use.twin) {
+        // both accumulators are read before either warpgroup lets the next unit's products in
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->twin_done));
+        if (!(ok = mbar_wait_warp(smem_u32(&bars->twin_done), twins & 1, ab))) break;
+        ++twins;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kPrefillMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ----------------------------------------------------------------------------
+// Join of the units that were cut: a warp per row, the parts in order.
+// ----------------------------------------------------------------------------
+constexpr int kJoinThreads = 256;
+struct PrefillJoin {
+  const PrefillDesc* desc;
+  const float2* ml;
+  const float* acc;
+  __nv_bfloat16* o;
+  float* lse;
+  int shares, group, per_tile, Hq;
+};
+
+template <int DV>
+__global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const PrefillJoin P) {
+  __shared__ int upto[kMaxPrefillCtas + 1];  // rows in front of each share's unit
+  __shared__ int sums[kJoinThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int rows = 0;
+  if (tid < P.shares) {
+    const PrefillDesc d = P.desc[tid];
+    rows = d.parts > 0 ? d.tokens * P.group : 0;
+  }
+  int x = rows;
+#pragma unroll
+  for (int k = 1; k < 32; k <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, k);
+    if (lane >= k) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
+  __syncthreads();
+  int front = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < kJoinThreads / 32; ++i) {
+    if (i < warp) front += sums[i];
+    total += sums[i];
+  }
+  if (tid <= P.shares) upto[tid] = front + x - rows;
+  __syncthreads();
+  constexpr int kV = DV / 32;  // columns of a lane
+  for (int i = blockIdx.x * (kJoinThreads / 32) + warp; i < total;
+       i += gridDim.x * (kJoinThreads / 32)) {
+    int lo = 0, hi = P.shares - 1;  // the last share with upto <= i (those without rows passed over)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (upto[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    const PrefillDesc d = P.desc[lo];
+    const int row = i - upto[lo];
+    const int tok = row / P.group, h = row - tok * P.group;
+    // the row's place among the slot's: two tiles of per_tile tokens
+    const int w = tok / P.per_tile;
+    const int place = w * kTile + (tok - w * P.per_tile) * P.group + h;
+    auto at = [&](int p) { return (int64_t)prefill_slot(lo, p) * kPrefillRows + place; };
+    float top = -INFINITY;
+    for (int p = lane; p < d.parts; p += 32) top = fmaxf(top, P.ml[at(p)].x);
+#pragma unroll
+    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    float sum = 0.f, acc[kV];
+#pragma unroll
+    for (int k = 0; k < kV; ++k) acc[k] = 0.f;
+    for (int p0 = 0; p0 < d.parts; p0 += 8) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        if (p0 + q >= d.parts) break;
+        const int64_t s = at(p0 + q);
+        const float2 ml = P.ml[s];
+        // (NaN stays: a part whose sums are not finite makes the row not finite)
+        const float weight = ml.x == top ? (top == -INFINITY ? 0.f : 1.f) : ex2(ml.x - top);
+        const float* src = P.acc + s * DV + lane * kV;
+        float v[kV];
+        if constexpr (kV == 4) {
+          const float4 f = *reinterpret_cast<const float4*>(src);
+          v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
+        } else {
+          const float2 f = *reinterpret_cast<const float2*>(src);
+          v[0] = f.x, v[1] = f.y;
+        }
+        sum += ml.y * weight;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) acc[k] += v[k] * weight;
+      }
+    }
+    const bool no_key = sum == 0.f;
+    const float inv = no_key ? 0.f : 1.0f / sum;
+    const int64_t out = (int64_t)(d.tok0 + tok) * P.Hq + d.head * P.group + h;
+    uint32_t pk[kV / 2];
+#pragma unroll
+    for (int k = 0; k < kV / 2; ++k) pk[k] = pack_bf16(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+    __nv_bfloat16* dst = P.o + out * DV + lane * kV;
+    if constexpr (kV == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = pk[0];
+    if (lane == 0 && P.lse != nullptr)
+      P.lse[out] = no_key ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+  }
+}
+
+template <int DQK, int DV, bool E4M3, typename Offsets>
+cudaError_t launch_prefill_typed(const PrefillLaunch& L, const Offsets& off) {
+  using C = PrefillCfg<DQK, DV, E4M3>;
+  PrefillParams P;
+  P.cache = L.cache;
+  P.sh = L.sh;
+  P.room = (int64_t)L.cache.max_pages * L.cache.page_size;
+  P.Hq = L.Hq;
+  P.o = static_cast<__nv_bfloat16*>(L.o);
+  P.lse = L.lse;
+  P.scale_log2 = L.scale_log2;
+  P.desc = L.desc;
+  P.ml = L.ml;
+  P.acc = L.acc;
+  P.status = L.status;
+  const int grid = L.num_sms < kMaxPrefillCtas ? L.num_sms : kMaxPrefillCtas;
+  auto* k = prefill_kernel<DQK, DV, E4M3, Offsets>;
+  cudaError_t e =
+      cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  k<<<grid, kPrefillThreads, C::kSmemBytes, L.stream>>>(L.tm_q, P, off);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  PrefillJoin J;
+  J.desc = L.desc;
+  J.ml = L.ml;
+  J.acc = L.acc;
+  J.o = P.o;
+  J.lse = L.lse;
+  J.shares = grid;
+  J.group = L.sh.group;
+  J.per_tile = L.sh.per_tile;
+  J.Hq = L.Hq;
+  prefill_join_kernel<DV><<<grid * 4, kJoinThreads, 0, L.stream>>>(J);
+  return cudaGetLastError();
+}
+
+template <int DQK, int DV, bool E4M3>
+cudaError_t launch_prefill_sized(const PrefillLaunch& L) {
+  if (L.offsets != nullptr) return launch_prefill_typed<DQK, DV, E4M3>(L, *L.offsets);
+  return launch_prefill_typed<DQK, DV, E4M3>(L, NoPrefillOffsets{});
+}
+
+}  // namespace
+}  // namespace attn

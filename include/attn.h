@@ -518,9 +518,44 @@ int attn_decode(const attn_paged_cache* cache, const int* block_table, int max_p
                 size_t workspace_bytes, void* stream);
 
 /*
- * Synchronises `stream`, returns the sticky device status of attn_cache_append
- * and attn_decode on the current device (ATTN_OK, ATTN_ERR_BAD_PAGE or
- * ATTN_ERR_WORKSPACE_NOT_READY; the first since the last read) and clears it, in
+ * Attention of a chunk of new tokens per sequence over the cache, which holds
+ * them already: a prompt's next piece, a few drafted tokens, single tokens, in
+ * one batch.  q (T,Hq,dqk) bf16, rows q_row elements apart; without cu_seqlens
+ * every sequence brings T / B tokens (T a multiple of B), with it (host, B + 1
+ * offsets, B at most ATTN_MAX_VARLEN_SEQS) sequence b brings rows cu_seqlens[b]
+ * .. cu_seqlens[b+1] - 1, as in attn_cache_append.  o (T,Hq,dv) bf16, lse
+ * (T,Hq) fp32 or NULL, dense.  Query head h uses key head h / (Hq / heads); Hq
+ * is a multiple of `heads`, at most 128 times it.  The i-th of n new tokens sits
+ * at position p = lens[b] - n + i and sees the keys 0 .. p, or with window_left
+ * >= 0 only p - window_left .. p.  scale: as in attn_decode.
+ * A row that sees no key (p < 0), or whose scores are all -inf, gets O = 0 and
+ * LSE = -inf.  As in attn_decode, keys and values that a row does not see never
+ * touch it, whatever their bits, one that it sees and that is not finite makes the
+ * row not finite (a key whose score is -inf weighs nothing, but its value has to
+ * be finite), and so does a largest score beyond fp32.
+ * Weights enter the second product rounded to bf16 (their sum is of unrounded
+ * ones): O is off by at most 2^-8 of the sum of |w_j v_j| besides its own
+ * rounding.
+ *
+ * The work is cut into equal shares of key tiles, at places that depend on the
+ * lengths alone, and parts of a row are joined in a fixed order by a second
+ * launch: results do not depend on timing (they do on the other lengths of the
+ * batch).
+ *
+ * workspace: attn_prefill_workspace_size() bytes, 256-byte aligned; needs no
+ * initialisation and keeps nothing between calls.  Calls that share a workspace,
+ * captured graphs included, must be ordered on the GPU.
+ */
+size_t attn_prefill_workspace_size(void);
+int attn_prefill(const attn_paged_cache* cache, const int* block_table, int max_pages,
+                 long long table_stride, const int* lens, int B, int T, const int* cu_seqlens,
+                 const void* q, long long q_row, void* o, float* lse, int Hq, int window_left,
+                 float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Synchronises `stream`, returns the sticky device status of attn_cache_append,
+ * attn_decode and attn_prefill on the current device (ATTN_OK, ATTN_ERR_BAD_PAGE,
+ * ATTN_ERR_WORKSPACE_NOT_READY or ATTN_ERR_TIMEOUT, a bounded wait that gave up; the first since the last read) and clears it, in
  * one step: what a call on another stream reports meanwhile is kept for the next read.
  */
 int attn_cache_status(void* stream);
