@@ -46,7 +46,8 @@ EXPORTED = ("attn_fwd", "attn_bwd_workspace_size", "attn_bwd", "attn_bwd_status"
             "attn_rope_rates", "attn_rope", "attn_cache_append", "attn_cache_status",
             "attn_decode", "attn_decode_workspace_size", "attn_decode_workspace_init",
             "attn_fwd_grouped", "attn_bwd_grouped", "attn_prefill",
-            "attn_prefill_workspace_size")
+            "attn_prefill_workspace_size", "attn_norm_rope", "attn_norm_rope_bwd",
+            "attn_norm_rope_bwd_workspace_size", "attn_cache_append_norm")
 BLOCK = 128  # rows per block of a block-sparse mask
 
 _lock = threading.Lock()
@@ -63,6 +64,17 @@ class _RotationStruct(ctypes.Structure):
     """attn_rotation of include/attn.h."""
     _fields_ = [("rates", ctypes.c_void_p), ("begin", ctypes.c_int), ("dim", ctypes.c_int),
                 ("style", ctypes.c_int)]
+
+
+class _NormStruct(ctypes.Structure):
+    """attn_head_norm of include/attn.h."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+class _NormRowsStruct(ctypes.Structure):
+    """attn_norm_rows of include/attn.h."""
+    _fields_ = [(n, ctypes.c_longlong) for n in ("q", "k", "dq_out", "dk_out", "dq", "dk")]
 
 
 class _RowsStruct(ctypes.Structure):
@@ -166,6 +178,16 @@ def load():
         lib.attn_prefill_workspace_size.restype = SZ
         lib.attn_prefill.argtypes = [P, P, I, L, P, I, I, P, P, L, P, P, I, I, F, P, SZ, P]
         lib.attn_prefill.restype = I
+        lib.attn_norm_rope.argtypes = [P, P, P, P, I, I, I, I, I, I, L, L, L, L, P, P, I, P, P, P]
+        lib.attn_norm_rope.restype = I
+        lib.attn_norm_rope_bwd_workspace_size.argtypes = [I]
+        lib.attn_norm_rope_bwd_workspace_size.restype = SZ
+        lib.attn_norm_rope_bwd.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, P, P, P, I, P,
+                                           P, P, SZ, P]
+        lib.attn_norm_rope_bwd.restype = I
+        lib.attn_cache_append_norm.argtypes = [P, P, I, L, P, I, I, P, P, L, P, L, P, L, P, L, I,
+                                               P, P, P]
+        lib.attn_cache_append_norm.restype = I
         _lib = lib
         return lib
 
@@ -465,6 +487,40 @@ def attn_cache_append(cache, block_table, max_pages, table_stride, lens, B, T, c
                                     _ptr(lens), B, T, cu.ptr, _ptr(k), k_row, _ptr(v), v_row,
                                     _ptr(q), q_row, _ptr(q_out), q_out_row, Hq,
                                     _struct(rotation), _stream(stream))
+
+
+def attn_cache_append_norm(cache, block_table, max_pages, table_stride, lens, B, T, cu_seqlens, k,
+                           k_row, v, v_row, q, q_row, q_out, q_out_row, Hq, norm=None,
+                           rotation=None, stream=None) -> int:
+    cu = _HostInts(cu_seqlens)
+    return load().attn_cache_append_norm(_struct(cache), _ptr(block_table), max_pages,
+                                         table_stride, _ptr(lens), B, T, cu.ptr, _ptr(k), k_row,
+                                         _ptr(v), v_row, _ptr(q), q_row, _ptr(q_out), q_out_row,
+                                         Hq, _struct(norm), _struct(rotation), _stream(stream))
+
+
+def attn_norm_rope(q, k, q_out, k_out, B, Hq, Hk, Tq, Tk, d, q_row, k_row, q_out_row, k_out_row,
+                   norm, rotation=None, pos0=0, cu_seqlens_q=None, cu_seqlens_k=None,
+                   stream=None) -> int:
+    cq, ck = _HostInts(cu_seqlens_q), _HostInts(cu_seqlens_k)
+    return load().attn_norm_rope(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), B, Hq, Hk, Tq, Tk, d,
+                                 q_row, k_row, q_out_row, k_out_row, _struct(norm),
+                                 _struct(rotation), _c_int(pos0), cq.ptr, ck.ptr, _stream(stream))
+
+
+def attn_norm_rope_bwd_workspace_size(d) -> int:
+    return int(load().attn_norm_rope_bwd_workspace_size(int(d)))
+
+
+def attn_norm_rope_bwd(q, k, dq_out, dk_out, dq, dk, dq_weight, dk_weight, B, Hq, Hk, Tq, Tk, d,
+                       rows, norm, rotation=None, pos0=0, cu_seqlens_q=None, cu_seqlens_k=None,
+                       workspace=None, workspace_bytes=0, stream=None) -> int:
+    cq, ck = _HostInts(cu_seqlens_q), _HostInts(cu_seqlens_k)
+    return load().attn_norm_rope_bwd(_ptr(q), _ptr(k), _ptr(dq_out), _ptr(dk_out), _ptr(dq),
+                                     _ptr(dk), _ptr(dq_weight), _ptr(dk_weight), B, Hq, Hk, Tq, Tk,
+                                     d, _struct(rows), _struct(norm), _struct(rotation),
+                                     _c_int(pos0), cq.ptr, ck.ptr, _ptr(workspace),
+                                     int(workspace_bytes), _stream(stream))
 
 
 def attn_cache_status(stream=None) -> int:
@@ -989,14 +1045,167 @@ def _check_tables(cache, block_table, lens):
     return B, width, stride
 
 
+class HeadNorm:
+    """The norm of each query and key head: x / sqrt(mean(x^2) + eps) times a weight per column
+    (q_weight, k_weight: contiguous fp32, one value per column of a head; None: ones)."""
+
+    def __init__(self, q_weight=None, k_weight=None, eps=1e-6):
+        for w in (q_weight, k_weight):
+            if w is not None and (w.dtype is not torch.float32 or w.dim() != 1
+                                  or not w.is_contiguous()):
+                raise ValueError("q_weight and k_weight must be contiguous fp32, one per column")
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, float(eps)
+        self.struct = _NormStruct(_ptr(q_weight), _ptr(k_weight), self.eps)
+        self.address = ctypes.addressof(self.struct)
+
+    def check(self, d):
+        for w in (self.q_weight, self.k_weight):
+            if w is not None and w.shape[0] != d:
+                raise ValueError("the norm's weights must have one value per column of a head")
+
+
+def _norm_dims(q, k, cu_seqlens, cu_seqlens_k):
+    """(B, Hq, Hk, Tq, Tk, d) and the offsets of queries and keys, of which one may be None."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k are both None")
+    varlen = cu_seqlens is not None
+    rank = 3 if varlen else 4
+    if any(t is not None and t.dim() != rank for t in (q, k)):
+        raise ValueError(f"q and k must have {rank} dimensions")
+    if q is not None and k is not None and (q.shape[-1] != k.shape[-1] or
+                                            (not varlen and q.shape[0] != k.shape[0])):
+        raise ValueError("q and k must agree in batch and head size")
+    if cu_seqlens_k is not None:
+        if not varlen:
+            raise ValueError("cu_seqlens_k needs cu_seqlens")
+        if len(cu_seqlens_k) != len(cu_seqlens):
+            raise ValueError("cu_seqlens and cu_seqlens_k must have the same length")
+    if varlen:
+        B = len(cu_seqlens) - 1
+        if q is None and cu_seqlens_k is not None:
+            cu_seqlens = cu_seqlens_k
+        Tq = q.shape[0] if q is not None else k.shape[0]
+        if k is not None:
+            Tk = k.shape[0]
+        else:  # the keys that the queries end
+            Tk = int(cu_seqlens_k[-1]) if cu_seqlens_k is not None else Tq
+    else:
+        B = x.shape[0]
+        Tq, Tk = (t.shape[1] if t is not None else x.shape[1] for t in (q, k))
+    heads = lambda t: 0 if t is None else t.shape[-2]
+    return (B, heads(q), heads(k), Tq, Tk, x.shape[-1]), cu_seqlens, cu_seqlens_k
+
+
+def _like(name, t, o):
+    if (t is None) != (o is None) or (o is not None and o.shape != t.shape):
+        raise ValueError(f"there must be a tensor like {name}")
+
+
+def _or_rows(t, name):
+    return 0 if t is None else _rows(t, t.shape, name)
+
+
+def norm_rope(q, k, norm, rotation=None, pos0=0, cu_seqlens=None, cu_seqlens_k=None, out=None,
+              stream=None):
+    """(q, k) with each head normed by a HeadNorm and then rotated to its position, as bf16
+    tensors (either may be None; rotation None: normed alone).
+
+    Tensors, positions, offsets and out: as in rope()."""
+    dims, cu, cuk = _norm_dims(q, k, cu_seqlens, cu_seqlens_k)
+    norm.check(dims[-1])
+    q_out, k_out = out if out is not None else (None, None)
+    if out is not None:
+        _like("q", q, q_out)
+        _like("k", k, k_out)
+    rows = [_or_rows(t, n) for t, n in ((q, "q"), (k, "k"), (q_out, "out[0]"), (k_out, "out[1]"))]
+    x = q if q is not None else k
+    index = _device_of(x, k, q_out, k_out, norm.q_weight, norm.k_weight,
+                       None if rotation is None else rotation.rates)
+    if not _here(index, stream):
+        with _On(index, stream):
+            return norm_rope(q, k, norm, rotation, pos0, cu_seqlens, cu_seqlens_k, out)
+    if out is None:
+        q_out, k_out = (None if t is None else _empty(t.shape, torch.bfloat16, t.device)
+                        for t in (q, k))
+    # (tensors without elements have no address)
+    full = lambda t: None if t is None or t.numel() == 0 else t
+    if full(q) is None and full(k) is None:
+        return q_out, k_out
+    if full(q) is None and q is not None and cuk is not None:
+        cu = cuk
+    B, Hq, Hk, Tq, Tk, d = dims
+    if full(q) is None:
+        Tq = Tk if cu_seqlens is not None else 0
+    rc = attn_norm_rope(full(q), full(k), full(q_out), full(k_out), B, Hq, Hk, Tq, Tk, d, *rows,
+                        norm, rotation, pos0, cu, cuk, _current(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_norm_rope")
+    return q_out, k_out
+
+
+def norm_rope_backward(q, k, dq_out, dk_out, norm, rotation=None, pos0=0, cu_seqlens=None,
+                       cu_seqlens_k=None, workspace=None, out=None, stream=None):
+    """(dq, dk, dq_weight, dk_weight): the gradients of norm_rope(q, k, norm, ...) from those of
+    its outputs, dq_out and dk_out.  dq, dk: bf16 like q, k; those of the weights: fp32, one per
+    column (None where norm has no weight, or q or k is None).  out: (dq, dk) to write to, which
+    may be dq_out, dk_out or q, k themselves."""
+    dims, cu, cuk = _norm_dims(q, k, cu_seqlens, cu_seqlens_k)
+    d = dims[-1]
+    norm.check(d)
+    _like("q", q, dq_out)
+    _like("k", k, dk_out)
+    dq, dk = out if out is not None else (None, None)
+    if out is not None:
+        _like("q", q, dq)
+        _like("k", k, dk)
+    if workspace is not None and not workspace.is_contiguous():  # (nbytes counts its memory)
+        raise ValueError("workspace must be contiguous")
+    rows = _NormRowsStruct(*(_or_rows(t, n) for t, n in (
+        (q, "q"), (k, "k"), (dq_out, "dq_out"), (dk_out, "dk_out"), (dq, "out[0]"),
+        (dk, "out[1]"))))
+    x = q if q is not None else k
+    index = _device_of(x, k, dq_out, dk_out, dq, dk, workspace, norm.q_weight, norm.k_weight,
+                       None if rotation is None else rotation.rates)
+    if not _here(index, stream):
+        with _On(index, stream):
+            return norm_rope_backward(q, k, dq_out, dk_out, norm, rotation, pos0, cu_seqlens,
+                                      cu_seqlens_k, workspace, out)
+    device = x.device
+    if out is None:
+        dq, dk = (None if t is None else _empty(t.shape, torch.bfloat16, device) for t in (q, k))
+    full = lambda t: None if t is None or t.numel() == 0 else t
+    dqw, dkw = (None if t is None or w is None else
+                _empty((d,), torch.float32, device) if full(t) is not None else
+                torch.zeros(d, device=device)
+                for t, w in ((q, norm.q_weight), (k, norm.k_weight)))
+    if full(q) is None and full(k) is None:
+        return dq, dk, dqw, dkw
+    if full(q) is None and q is not None and cuk is not None:
+        cu = cuk
+    B, Hq, Hk, Tq, Tk, _ = dims
+    if full(q) is None:
+        Tq = Tk if cu_seqlens is not None else 0
+    if workspace is None:
+        workspace = _empty((max(1, attn_norm_rope_bwd_workspace_size(d)),), torch.uint8, device)
+    of = lambda t, o: None if full(t) is None else o
+    rc = attn_norm_rope_bwd(full(q), full(k), of(q, dq_out), of(k, dk_out), of(q, dq), of(k, dk),
+                            of(q, dqw), of(k, dkw), B, Hq, Hk, Tq, Tk, d, rows, norm, rotation,
+                            pos0, cu, cuk, workspace, workspace.nbytes, _current(index))
+    if rc != ATTN_OK:
+        raise AttnError(rc, "attn_norm_rope_bwd")
+    return dq, dk, dqw, dkw
+
+
 def cache_append(cache, k, v, block_table, lens, q=None, rotation=None, cu_seqlens=None,
-                 q_out=None, stream=None):
+                 q_out=None, stream=None, norm=None):
     """Appends new tokens' keys (T,heads,dqk) and values (T,heads,dv) to a PagedCache.
 
     lens: device int32, each sequence's length with the new tokens counted; block_table:
     device int32 (sequences, pages).  Without cu_seqlens (host offsets of the new rows) every
-    sequence brings T / sequences tokens.  k is rotated to its position if a rotation is
-    given, and so is q (T,Hq,dqk), which is returned (in q_out, which may be q)."""
+    sequence brings T / sequences tokens.  k is normed by a HeadNorm if one is given, then
+    rotated to its position if a rotation is given, and so is q (T,Hq,dqk), which is returned
+    (in q_out, which may be q)."""
     B, width, stride = _check_tables(cache, block_table, lens)
     k_shape, v_shape, heads = k.shape, v.shape, cache.heads
     T = k_shape[0]
@@ -1020,18 +1229,24 @@ def cache_append(cache, k, v, block_table, lens, q=None, rotation=None, cu_seqle
         out_row = _rows(q_out, q_shape, "q_out")
     index = _device_of(cache.k_cache, k, v, q, q_out, block_table, lens,
                        None if rotation is None else rotation.rates)
+    if norm is not None:
+        norm.check(cache.dqk)
+        _device_of(cache.k_cache, norm.q_weight, norm.k_weight)
     if not _here(index, stream):
         with _On(index, stream):
-            return cache_append(cache, k, v, block_table, lens, q, rotation, cu_seqlens, q_out)
+            return cache_append(cache, k, v, block_table, lens, q, rotation, cu_seqlens, q_out,
+                                norm=norm)
     if q is not None and q_out is None:
         q_out = _empty(q_shape, torch.bfloat16, q.device)
     if T == 0:  # (tensors without elements have no address)
         return q_out
     cu = _HostInts(cu_seqlens)
-    rc = load().attn_cache_append(cache.address, block_table.data_ptr(), width, stride,
-                                  lens.data_ptr(), B, T, cu.ptr, k.data_ptr(), k_row,
-                                  v.data_ptr(), v_row, _ptr(q), q_row, _ptr(q_out), out_row, Hq,
-                                  None if rotation is None else rotation.address, _current(index))
+    rc = load().attn_cache_append_norm(cache.address, block_table.data_ptr(), width, stride,
+                                       lens.data_ptr(), B, T, cu.ptr, k.data_ptr(), k_row,
+                                       v.data_ptr(), v_row, _ptr(q), q_row, _ptr(q_out), out_row,
+                                       Hq, None if norm is None else norm.address,
+                                       None if rotation is None else rotation.address,
+                                       _current(index))
     if rc != ATTN_OK:
         raise AttnError(rc, "attn_cache_append")
     return q_out

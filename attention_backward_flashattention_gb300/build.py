@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(OUT_DIR, "libattn_gb300.so")
 SOURCES = ["attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_bwd_pair.cu", "attn_noalloc.cu",
-           "attn_host.cu", "attn_paged.cu", "attn_rope.cu", "attn_decode.cu",
+           "attn_host.cu", "attn_paged.cu", "attn_rope.cu", "attn_norm.cu", "attn_decode.cu",
            "attn_decode_e4m3.cu", "attn_prefill.cu", "attn_prefill_e4m3.cu", "attn_status.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

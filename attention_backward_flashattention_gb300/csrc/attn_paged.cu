@@ -47,6 +47,15 @@ int check_rotation(const attn_rotation* r, int d, Rotation* out) {
   return ATTN_OK;
 }
 
+int check_norm(const attn_head_norm* n, HeadNorm* out) {
+  if (n == nullptr || !aligned(n->q_weight, 4) || !aligned(n->k_weight, 4)) return ATTN_ERR_INVALID_ARG;
+  // (eps keeps the root of a row of zeros finite)
+  if (!(n->eps >= std::numeric_limits<float>::min()) || !std::isfinite(n->eps))
+    return ATTN_ERR_INVALID_ARG;
+  *out = HeadNorm{n->q_weight, n->k_weight, n->eps};
+  return ATTN_OK;
+}
+
 // Host offsets of nseq sequences over `total` rows, into a by-value table.
 int check_offsets(const int* cu, int nseq, int total, RowOffsets* out) {
   if (nseq > ATTN_MAX_VARLEN_SEQS) return ATTN_ERR_UNSUPPORTED;
@@ -129,6 +138,73 @@ int sm_count() {
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
   if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
+}
+
+// The norm with the rotation (dy == null), and its backward: queries and keys, each x, dy, y
+// and their rows' distances.
+int norm_impl(const void* const* x, const void* const* dy, void* const* y, float* const* dw, int B,
+              int Hq, int Hk, int Tq, int Tk, int d, const long long (*given)[3],
+              const attn_head_norm* norm, const attn_rotation* rotation, int pos0,
+              const int* cu_seqlens_q, const int* cu_seqlens_k, void* workspace,
+              size_t workspace_bytes, void* stream) {
+  (void)workspace_bytes;
+  const int H[2] = {Hq, Hk}, T[2] = {Tq, Tk};
+  if (x[0] == nullptr && x[1] == nullptr) return ATTN_ERR_INVALID_ARG;
+  if (B <= 0 || Tq < 0 || Tk < 0 || pos0 < 0) return ATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i) {
+    if ((x[i] == nullptr) != (y[i] == nullptr)) return ATTN_ERR_INVALID_ARG;
+    if (x[i] != nullptr && (H[i] <= 0 || T[i] == 0)) return ATTN_ERR_INVALID_ARG;
+    if (!aligned(x[i], 16) || !aligned(y[i], 16) || (dy && !aligned(dy[i], 16)))
+      return ATTN_ERR_INVALID_ARG;
+  }
+  if (!head_size(d)) return ATTN_ERR_UNSUPPORTED;
+  NormLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  HeadNorm n;
+  int rc = check_norm(norm, &n);
+  if (rc) return rc;
+  if ((rc = check_rotation(rotation, d, &L.rot)) != 0) return rc;
+  static thread_local RowOffsets cu[2];
+  const bool varlen = cu_seqlens_q != nullptr;
+  if (!varlen && cu_seqlens_k != nullptr) return ATTN_ERR_INVALID_ARG;
+  const int* cuk = cu_seqlens_k != nullptr ? cu_seqlens_k : cu_seqlens_q;
+  if (varlen) {
+    if ((rc = check_offsets(cu_seqlens_q, B, Tq, &cu[0])) != 0) return rc;
+    if ((rc = check_offsets(cuk, B, Tk, &cu[1])) != 0) return rc;
+    L.cu[0] = &cu[0];
+    L.cu[1] = &cu[1];
+  }
+  if ((int64_t)pos0 + std::max(Tq, Tk) > INT32_MAX) return ATTN_ERR_UNSUPPORTED;
+  for (int i = 0; i < 2; ++i) {
+    if (x[i] == nullptr) continue;
+    long long row[3] = {given[i][0], given[i][1], given[i][2]};
+    for (long long& r : row)
+      if (!row_stride(&r, H[i], d)) return ATTN_ERR_INVALID_ARG;
+    const int64_t rows = varlen ? T[i] : (int64_t)B * T[i];
+    if (rows > INT32_MAX - 1024 || (int64_t)H[i] * d > (1 << 20)) return ATTN_ERR_UNSUPPORTED;
+    NormTensor& t = L.t[i];
+    t.x = x[i];
+    t.dy = dy ? dy[i] : nullptr;
+    t.y = y[i];
+    t.x_row = row[0];
+    t.dy_row = row[1];
+    t.y_row = row[2];
+    t.rows = (int)rows;
+    t.H = H[i];
+    t.T = T[i];
+    t.shift = !varlen && i == 0 ? Tk - Tq : 0;
+    t.weight = i ? n.k_weight : n.q_weight;
+    t.dw = dw ? dw[i] : nullptr;
+  }
+  L.eps = n.eps;
+  L.nseq = B;
+  L.pos0 = pos0;
+  L.d = d;
+  L.workspace = static_cast<float*>(workspace);
+  L.num_sms = sm_count();
+  if (L.num_sms <= 0) return ATTN_ERR_CUDA;
+  L.stream = static_cast<cudaStream_t>(stream);
+  return cuda_err(dy ? launch_norm_bwd(L) : launch_norm(L));
 }
 
 }  // namespace
@@ -217,11 +293,57 @@ int attn_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int
   return cuda_err(launch_rope(L));
 }
 
+int attn_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int Hq, int Hk,
+                   int Tq, int Tk, int d, long long q_row, long long k_row, long long q_out_row,
+                   long long k_out_row, const attn_head_norm* norm, const attn_rotation* rotation,
+                   int pos0, const int* cu_seqlens_q, const int* cu_seqlens_k, void* stream) {
+  const void* x[2] = {q, k};
+  void* y[2] = {q_out, k_out};
+  const long long rows[2][3] = {{q_row, 0, q_out_row}, {k_row, 0, k_out_row}};
+  return norm_impl(x, nullptr, y, nullptr, B, Hq, Hk, Tq, Tk, d, rows, norm, rotation, pos0,
+                   cu_seqlens_q, cu_seqlens_k, nullptr, 0, stream);
+}
+
+size_t attn_norm_rope_bwd_workspace_size(int d) { return head_size(d) ? norm_workspace_bytes(d) : 0; }
+
+int attn_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                       void* dq, void* dk, float* dq_weight, float* dk_weight, int B, int Hq,
+                       int Hk, int Tq, int Tk, int d, const attn_norm_rows* rows,
+                       const attn_head_norm* norm, const attn_rotation* rotation, int pos0,
+                       const int* cu_seqlens_q, const int* cu_seqlens_k, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  const void* x[2] = {q, k};
+  const void* dy[2] = {dq_out, dk_out};
+  void* y[2] = {dq, dk};
+  float* dw[2] = {dq_weight, dk_weight};
+  const attn_norm_rows none = {}, &r = rows != nullptr ? *rows : none;
+  const long long given[2][3] = {{r.q, r.dq_out, r.dq}, {r.k, r.dk_out, r.dk}};
+  if (workspace == nullptr || !aligned(workspace, 256)) return ATTN_ERR_INVALID_ARG;
+  for (int i = 0; i < 2; ++i)
+    if ((x[i] == nullptr) != (dy[i] == nullptr) || (x[i] == nullptr && dw[i] != nullptr) ||
+        !aligned(dw[i], 4))
+      return ATTN_ERR_INVALID_ARG;
+  if (head_size(d) && workspace_bytes < norm_workspace_bytes(d)) return ATTN_ERR_WORKSPACE_TOO_SMALL;
+  return norm_impl(x, dy, y, dw, B, Hq, Hk, Tq, Tk, d, given, norm, rotation, pos0, cu_seqlens_q,
+                   cu_seqlens_k, workspace, workspace_bytes, stream);
+}
+
 int attn_cache_append(const attn_paged_cache* cache, const int* block_table, int max_pages,
                       long long table_stride, const int* lens, int B, int T,
                       const int* cu_seqlens, const void* k, long long k_row, const void* v,
                       long long v_row, const void* q, long long q_row, void* q_out,
                       long long q_out_row, int Hq, const attn_rotation* rotation, void* stream) {
+  return attn_cache_append_norm(cache, block_table, max_pages, table_stride, lens, B, T, cu_seqlens,
+                                k, k_row, v, v_row, q, q_row, q_out, q_out_row, Hq, nullptr,
+                                rotation, stream);
+}
+
+int attn_cache_append_norm(const attn_paged_cache* cache, const int* block_table, int max_pages,
+                           long long table_stride, const int* lens, int B, int T,
+                           const int* cu_seqlens, const void* k, long long k_row, const void* v,
+                           long long v_row, const void* q, long long q_row, void* q_out,
+                           long long q_out_row, int Hq, const attn_head_norm* norm,
+                           const attn_rotation* rotation, void* stream) {
   AppendLaunch L;
   std::memset(&L, 0, sizeof(L));
   int rc = check_cache(cache, block_table, max_pages, table_stride, lens, B, &L.cache);
@@ -244,6 +366,11 @@ int attn_cache_append(const attn_paged_cache* cache, const int* block_table, int
     return ATTN_ERR_UNSUPPORTED;
   rc = check_rotation(rotation, cache->dqk, &L.rot);
   if (rc) return rc;
+  HeadNorm head_norm;
+  if (norm != nullptr) {
+    if ((rc = check_norm(norm, &head_norm)) != 0) return rc;
+    L.norm = &head_norm;
+  }
   static thread_local RowOffsets offsets;
   if (cu_seqlens != nullptr) {
     if ((rc = check_offsets(cu_seqlens, B, T, &offsets)) != 0) return rc;
@@ -271,7 +398,7 @@ int attn_cache_append(const attn_paged_cache* cache, const int* block_table, int
   L.status = cache_status_ptr();
   if (!L.status) return ATTN_ERR_CUDA;
   L.stream = static_cast<cudaStream_t>(stream);
-  return cuda_err(launch_append(L));
+  return cuda_err(norm != nullptr ? launch_append_norm(L) : launch_append(L));
 }
 
 size_t attn_decode_workspace_size(void) { return kDecodeWorkspaceBytes; }

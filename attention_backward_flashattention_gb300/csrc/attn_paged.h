@@ -214,6 +214,41 @@ __host__ __device__ inline ItemParts item_parts(const Line& l, long long at, int
   return p;
 }
 
+// Norm of queries and keys, head by head: x / sqrt(mean x^2 + eps) times a weight per column.
+struct HeadNorm {
+  const float *q_weight, *k_weight;  // null: ones
+  float eps;
+};
+
+// One tensor of the norm's kernels: x, and in the backward the gradient dy of what the
+// forward gives; y: what comes out.
+struct NormTensor {
+  const void *x, *dy;
+  void* y;
+  int64_t x_row, dy_row, y_row;  // elements between rows
+  int rows, H, T;                // T: rows per sequence (fixed length)
+  int shift;                     // fixed length: position of row 0 of a sequence
+  const float* weight;
+  float* dw;                     // gradient of the weight, or null
+};
+struct NormLaunch {
+  NormTensor t[2];          // queries, keys (rows == 0: absent)
+  Rotation rot;             // dim == 0: none
+  float eps;
+  int nseq;
+  const RowOffsets* cu[2];  // null: fixed length.  cu[0] / cu[1]: queries / keys
+  int pos0;
+  int d;
+  float* workspace;         // backward: sums of the weights' gradients, by block
+  int num_sms;
+  cudaStream_t stream;
+};
+cudaError_t launch_norm(const NormLaunch& L);
+cudaError_t launch_norm_bwd(const NormLaunch& L);
+// Blocks of the backward at most, by tensor (each leaves one row of sums).
+constexpr int kMaxNormBlocks = 1024;
+inline size_t norm_workspace_bytes(int d) { return 2ull * kMaxNormBlocks * d * sizeof(float); }
+
 struct AppendLaunch {
   CacheView cache;
   const void *k, *v, *q;
@@ -225,10 +260,12 @@ struct AppendLaunch {
   Rotation rot;
   int dqk, dv;
   int num_sms;
+  const HeadNorm* norm;  // null: none
   int* status;
   cudaStream_t stream;
 };
 cudaError_t launch_append(const AppendLaunch& L);
+cudaError_t launch_append_norm(const AppendLaunch& L);
 
 // Decode workspace, carved in this order (sizes fixed: any call fits).
 constexpr int kMaxDecodeCtas = 304;               // CTAs of one decode call at most

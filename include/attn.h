@@ -427,6 +427,45 @@ int attn_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int
               const int* cu_seqlens_q, const int* cu_seqlens_k, void* stream);
 
 /*
+ * Norm of each query and key head, with the position rotation in the same pass:
+ *     y = R(p) (x / sqrt(mean x^2 + eps) * w)
+ * over the d columns of a head; w: device fp32 per column, shared by the heads (q_weight,
+ * k_weight; 4-byte aligned; NULL: ones), R(p) the rotation at the row's position.
+ * eps: positive, normal and finite.  rotation may be NULL (the norm alone).  Tensors,
+ * rows, positions, offsets and limits are those of attn_rope; an output may be its
+ * input.  Computed in fp32 and rounded to bf16 once.
+ *
+ * attn_norm_rope_bwd: from x (q, k as the forward had them) and the gradients dq_out,
+ * dk_out of the forward's outputs, the gradients dq, dk of q and k (which may be
+ * dq_out / dk_out or q / k themselves, and must not overlap them otherwise) and,
+ * where not NULL, those of the weights (fp32, d values each, written, not added to):
+ * sums over all rows and heads in fp32, in a fixed order, so that they have the same
+ * bits every run.  Either of q and k may be NULL with all that goes with it.
+ * attn_norm_rows: elements between token rows of each (0: dense); NULL: all dense.
+ * workspace: attn_norm_rope_bwd_workspace_size(d) bytes (0 for another d), 256-byte
+ * aligned; needs no initialisation.  Calls that share it must be ordered on the GPU.
+ */
+typedef struct attn_head_norm {
+  const float* q_weight;
+  const float* k_weight;
+  float eps;
+} attn_head_norm;
+typedef struct attn_norm_rows {
+  long long q, k, dq_out, dk_out, dq, dk;
+} attn_norm_rows;
+int attn_norm_rope(const void* q, const void* k, void* q_out, void* k_out, int B, int Hq, int Hk,
+                   int Tq, int Tk, int d, long long q_row, long long k_row, long long q_out_row,
+                   long long k_out_row, const attn_head_norm* norm, const attn_rotation* rotation,
+                   int pos0, const int* cu_seqlens_q, const int* cu_seqlens_k, void* stream);
+size_t attn_norm_rope_bwd_workspace_size(int d);
+int attn_norm_rope_bwd(const void* q, const void* k, const void* dq_out, const void* dk_out,
+                       void* dq, void* dk, float* dq_weight, float* dk_weight, int B, int Hq,
+                       int Hk, int Tq, int Tk, int d, const attn_norm_rows* rows,
+                       const attn_head_norm* norm, const attn_rotation* rotation, int pos0,
+                       const int* cu_seqlens_q, const int* cu_seqlens_k, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
  * A paged cache of keys and values.  k and v (device) hold num_pages pages of
  * page_size tokens for each of `heads` key heads, dqk and dv columns wide;
  * element (page, token, head, c) of k is at page * k_page_stride + token *
@@ -485,6 +524,17 @@ int attn_cache_append(const attn_paged_cache* cache, const int* block_table, int
                       const int* cu_seqlens, const void* k, long long k_row, const void* v,
                       long long v_row, const void* q, long long q_row, void* q_out,
                       long long q_out_row, int Hq, const attn_rotation* rotation, void* stream);
+
+/*
+ * attn_cache_append with the norm of attn_norm_rope on the way: k and q are normed (each with
+ * its weight) and then turned; v is not.  norm NULL: attn_cache_append.
+ */
+int attn_cache_append_norm(const attn_paged_cache* cache, const int* block_table, int max_pages,
+                           long long table_stride, const int* lens, int B, int T,
+                           const int* cu_seqlens, const void* k, long long k_row, const void* v,
+                           long long v_row, const void* q, long long q_row, void* q_out,
+                           long long q_out_row, int Hq, const attn_head_norm* norm,
+                           const attn_rotation* rotation, void* stream);
 
 /*
  * Attention of one new token per sequence over the cache: q (B,Hq,dqk) bf16
