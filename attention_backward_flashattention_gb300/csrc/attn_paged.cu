@@ -129,6 +129,34 @@ bool rows_apart(const attn_paged_cache* c, long long page, long long token, long
   return true;
 }
 
+// Map of one side of a cache over (columns, heads and tokens, pages), boxes of `box` tokens of one
+// page and head: 64 columns swizzled as the products read them, or all bytes of an e4m3 row.  False
+// where it cannot be described so (broadcast dimensions, strides beyond a map's).
+bool page_map(CUtensorMap* map, const attn_paged_cache* c, bool values, int box, bool heads_inner) {
+  const bool e4m3 = c->type == ATTN_CACHE_E4M3;
+  const int d = values ? c->dv : c->dqk, elt = e4m3 ? 1 : 2;
+  const long long page = (values ? c->v_page_stride : c->k_page_stride) * elt;
+  const long long token = (values ? c->v_token_stride : c->k_token_stride) * elt;
+  const long long head = (values ? c->v_head_stride : c->k_head_stride) * elt;
+  for (long long s : {page, token, head})
+    if (s <= 0 || s >= (1ll << 40)) return false;
+  EncodeTiledFn enc = get_encode_tiled();
+  if (!enc) return false;
+  const cuuint64_t tokens = (cuuint64_t)c->page_size, heads = (cuuint64_t)c->heads;
+  const cuuint64_t dims[4] = {(cuuint64_t)d, heads_inner ? heads : tokens,
+                              heads_inner ? tokens : heads, (cuuint64_t)c->num_pages};
+  const cuuint64_t strides[3] = {(cuuint64_t)(heads_inner ? head : token),
+                                 (cuuint64_t)(heads_inner ? token : head), (cuuint64_t)page};
+  const cuuint32_t boxes[4] = {(cuuint32_t)(e4m3 ? d : 64), heads_inner ? 1u : (cuuint32_t)box,
+                               heads_inner ? (cuuint32_t)box : 1u, 1u};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return enc(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+             values ? c->v : c->k, dims, strides, boxes, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // SMs of the current device (asked once for each).
 int sm_count() {
   static std::atomic<int> known[64];
@@ -526,6 +554,14 @@ int attn_prefill(const attn_paged_cache* cache, const int* block_table, int max_
           one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return ATTN_ERR_CUDA;
+  // Boxes of rows of one page for whole tiles, where pages are multiples of 8 tokens (the
+  // swizzle's period) and the strides are what a map takes; else those tiles come by rows too.
+  L.box = cache->page_size % 32 == 0 ? 32 : cache->page_size % 16 == 0 ? 16
+                                        : cache->page_size % 8 == 0 ? 8 : 0;
+  L.heads_inner = cache->k_head_stride < cache->k_token_stride;
+  if (L.box > 0 && (!page_map(&L.tm_k, cache, false, L.box, L.heads_inner) ||
+                    !page_map(&L.tm_v, cache, true, L.box, L.heads_inner)))
+    L.box = 0;
   L.T = T;
   L.Hq = Hq;
   L.o = o;

@@ -9,8 +9,10 @@
 // (attn_prefill.h):
 //   warps 0-3, 4-7  softmax warpgroup w: thread = query row (TMEM lane) of query tile w
 //   warps 8-11      key and value rows from their pages to shared memory, 32 rows of a tile
-//                   each: copies of 16 bytes that the thread waits for in groups (any page
-//                   size and stride, and rows that nothing sees become zeros on the way)
+//                   each.  Tiles whose keys every row sees come by TMA, in boxes of rows that lie
+//                   in one page; the others, and pages that no box divides, row by row, where rows
+//                   that nothing sees, and values that are not finite, become zeros on the way.
+//                   e4m3 boxes land in a ring of their own, and the warp widens them
 //   warp 12         MMA issuer: S_w = Q_w K^T, O_w += P_w V (tcgen05, accumulators in TMEM, P
 //                   in TMEM as the A operand)
 //   warp 13         walks over the share's units, loads their queries by TMA
@@ -43,11 +45,16 @@ struct PrefillCfg {
   static constexpr int kQTile = DQK / 64 * kPrefillPanel;
   static constexpr int kKBytes = DQK / 64 * kPrefillPanel;
   static constexpr int kVBytes = DV / 64 * kPrefillPanel;
-  static constexpr int kKStages = DQK == 64 ? 5 : DQK == 128 ? 3 : 2;
-  static constexpr int kVStages = DQK == 64 ? 5 : DQK == 128 ? 2 : 1;
+  // stages of key and of value tiles (bf16), and of an e4m3 cache's bytes in front of them
+  static constexpr int kKStages = E4M3 ? (DQK == 64 ? 3 : 1) : DQK == 64 ? 5 : DQK == 128 ? 3 : 2;
+  static constexpr int kVStages = E4M3 ? (DQK == 64 ? 3 : DQK == 128 ? 2 : 1)
+                                       : DQK == 64 ? 5 : DQK == 128 ? 2 : 1;
+  static constexpr int kRaw = !E4M3 ? 0 : DQK == 64 ? 4 : DQK == 128 ? 2 : 1;
   static constexpr int kOffK = 2 * kQTile;
   static constexpr int kOffV = kOffK + kKStages * kKBytes;
-  static constexpr int kOffBar = kOffV + kVStages * kVBytes;
+  static constexpr int kOffRawK = kOffV + kVStages * kVBytes;
+  static constexpr int kOffRawV = kOffRawK + kRaw * kTile * DQK;
+  static constexpr int kOffBar = kOffRawV + kRaw * kTile * DV;
   static constexpr int kSmemBytes = kOffBar + 3072;
   static_assert(kSmemBytes <= kPrefillMaxSmem, "shared memory budget");
   static constexpr uint32_t kTmemO = 256;
@@ -64,6 +71,7 @@ struct PrefillBars {
   uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t twin_full, twin_done;
+  uint64_t raw_full[2][4][4];    // [keys, values][slot][copy warp]
   uint64_t drain;
   PrefillItem item[2];
   uint32_t there[kKeyRing][4];  // of a key tile's 128 keys, which are in the cache
@@ -76,6 +84,7 @@ static_assert(sizeof(PrefillBars) <= 3072, "barrier block size");
 
 struct PrefillParams {
   CacheView cache;
+  int box, heads_inner;
   PrefillShape sh;
   int64_t room;       // tokens that a row of the block table has pages for
   int Hq;
@@ -152,6 +161,18 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src
                : "memory");
 }
 
+// One box of a cache's map: token `in` and on of a page, one head, columns from `column` on.
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* m, uint32_t bar,
+                                              int column, int head, int in, int page,
+                                              bool heads_inner) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(column), "r"(heads_inner ? head : in),
+      "r"(heads_inner ? in : head), "r"(page)
+      : "memory");
+}
+
 // Four e4m3 values as two words of bf16 pairs (exact: a bf16 has every e4m3 value).
 __device__ __forceinline__ void e4m3_to_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
   uint32_t h0, h1;
@@ -176,6 +197,8 @@ __device__ __forceinline__ bool not_finite(uint32_t x) {
 template <int DQK, int DV, bool E4M3, typename Offsets>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ PrefillParams P, const __grid_constant__ Offsets off) {
   using C = PrefillCfg<DQK, DV, E4M3>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -236,6 +259,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     }
     mbar_init(smem_u32(&bars->twin_full), 8);
     mbar_init(smem_u32(&bars->twin_done), 8);
+    for (int i = 0; i < 2 * 4 * 4; ++i) mbar_init(smem_u32(&bars->raw_full[0][0][0] + i), 1);
     mbar_init(smem_u32(&bars->drain), 1);
     fence_barrier_init();
   }
@@ -311,10 +335,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
       constexpr uint32_t idO = idesc_bf16(128, DV, false, true);
       const uint64_t bQ = kmajor_base(sQ), bK = kmajor_base(sK), bV = mnmajor_base(sV, 128);
-      uint32_t n = 0, step = 0, cnt[2] = {0, 0};
+      uint32_t n = 0, step = 0, parity = 0;  // parity: of the next P of each warpgroup, by bit
       bool ok = true;
-      auto W = [&](uint64_t& bar, uint32_t parity) -> bool {
-        if (!mbar_wait(smem_u32(&bar), parity, ab)) return false;
+      auto W = [&](uint64_t& bar, uint32_t p) -> bool {
+        if (!mbar_wait(smem_u32(&bar), p, ab)) return false;
         tc_fence_after();
         return true;
       };
@@ -325,57 +349,54 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         const int tiles = item.tiles;
         const TileUse use = tile_use(sh, item);
         mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
-        auto mma_S = [&](int w, uint32_t t) {
-          const uint64_t q = bQ + (uint64_t)((use.twin ? 0 : w) * (C::kQTile >> 4));
-          const uint64_t k = bK + (uint64_t)((t % C::kKStages) * (C::kKBytes >> 4));
-#pragma unroll
-          for (int kk = 0; kk < DQK / 16; ++kk)
-            mma_bf16(tmem + w * 128, q + kmajor_step(kk, 128), k + kmajor_step(kk, 128), idS,
-                     kk > 0 ? 1u : 0u);
-          mma_commit(smem_u32(&bars->s_full[w]));
-        };
-        auto mma_PV = [&](int w, uint32_t t, bool first) {
-          const uint64_t v = bV + (uint64_t)((t % C::kVStages) * (C::kVBytes >> 4));
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_bf16_ts(tmem + C::kTmemO + w * DV, tmem + w * 128 + kk * 8, v + mnmajor_step(kk),
-                        idO, kk > 0 || !first ? 1u : 0u);
-        };
         if (!(ok = W(bars->q_full, n & 1))) break;
-        if (!(ok = W(bars->k_full[step % C::kKStages], (step / C::kKStages) & 1))) break;
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-          if (tile_used(use, w, 0)) mma_S(w, step);
-        mma_commit(smem_u32(&bars->k_empty[step % C::kKStages]));
-        if (tiles == 1) mma_commit(smem_u32(&bars->q_empty));
-        for (int t = 0; t < tiles; ++t, ++step) {
+        // After step t's P of a warpgroup: O += P V of step t, then S of step t + 1 (t = -1: the
+        // first S).  A warpgroup that has no part in step t starts on the next at once.  One
+        // place in the code for each product: unrolled over the warpgroups it spilled.
+        for (int t = -1; t < tiles; ++t, ++step) {
+          // (`step` is that of t + 1)
           const bool next = t + 1 < tiles;
-          if (next) {
-            const uint32_t s1 = step + 1;
-            if (!(ok = W(bars->k_full[s1 % C::kKStages], (s1 / C::kKStages) & 1))) break;
-            // a warpgroup that has no part in this step starts on the next
+          if (next && !(ok = W(bars->k_full[step % C::kKStages], (step / C::kKStages) & 1))) break;
+          const uint32_t sv = (step - 1) % C::kVStages;
+          if (t >= 0 && !(ok = W(bars->v_full[sv], ((step - 1) / C::kVStages) & 1))) break;
+          int w = tile_used(use, 0, t) && !tile_used(use, 1, t) ? 1 : 0;
+#pragma unroll 1
+          for (int turn = 0; turn < 2; ++turn, w ^= 1) {
+            const int lo = w ? use.lo[1] : use.lo[0], hi = w ? use.hi[1] : use.hi[0];
+            auto used = [&](int at) {
+              return at >= lo && at <= hi && (!use.twin || ((at ^ w) & 1) == 0);
+            };
+            const uint32_t tS = tmem + w * 128;
+            if (used(t)) {
+              if (!(ok = W(bars->p_full[w], (parity >> w) & 1))) break;
+              parity ^= 1u << w;
+              const uint32_t tO = tmem + C::kTmemO + w * DV;
+              const uint64_t v = bV + (uint64_t)(sv * (C::kVBytes >> 4));
+              mma_bf16_ts(tO, tS, v, idO, t == lo ? 0u : 1u);
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
-              if (!tile_used(use, w, t) && tile_used(use, w, t + 1)) mma_S(w, s1);
-          }
-          if (!(ok = W(bars->v_full[step % C::kVStages], (step / C::kVStages) & 1))) break;
+              for (int kk = 1; kk < kTile / 16; ++kk)
+                mma_bf16_ts(tO, tS + kk * 8, v + mnmajor_step(kk), idO, 1u);
+              if (t == hi) mma_commit(smem_u32(&bars->o_done[w]));
+            }
+            if (used(t + 1)) {
+              const uint64_t q = bQ + (uint64_t)((use.twin ? 0 : w) * (C::kQTile >> 4));
+              const uint64_t k = bK + (uint64_t)((step % C::kKStages) * (C::kKBytes >> 4));
 #pragma unroll
-          for (int w = 0; w < 2; ++w) {
-            if (!tile_used(use, w, t)) continue;
-            if (!(ok = W(bars->p_full[w], cnt[w] & 1))) break;
-            ++cnt[w];
-            mma_PV(w, step, t == use.lo[w]);
-            if (t == use.hi[w]) mma_commit(smem_u32(&bars->o_done[w]));
-            if (next && tile_used(use, w, t + 1)) mma_S(w, step + 1);
+              for (int kk = 0; kk < DQK / 16; ++kk)
+                mma_bf16(tS, q + kmajor_step(kk, 128), k + kmajor_step(kk, 128), idS,
+                         kk > 0 ? 1u : 0u);
+              mma_commit(smem_u32(&bars->s_full[w]));
+            }
           }
           if (!ok) break;
-          mma_commit(smem_u32(&bars->v_empty[step % C::kVStages]));
+          if (t >= 0) mma_commit(smem_u32(&bars->v_empty[sv]));
           if (next) {
-            mma_commit(smem_u32(&bars->k_empty[(step + 1) % C::kKStages]));
+            mma_commit(smem_u32(&bars->k_empty[step % C::kKStages]));
             if (t + 2 == tiles) mma_commit(smem_u32(&bars->q_empty));  // after the last S
           }
         }
         if (!ok) break;
+        --step;  // (the last pass was for no further tile)
       }
       if (!ok) {
         mma_commit(smem_u32(&bars->drain));
@@ -386,19 +407,25 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if constexpr (C::kRegsCopy < 128) regs_dec<C::kRegsCopy>();
     // -------------------------------------------------------------- keys and values
     const int mw = warp - kCopyWarp;  // rows 32 mw .. 32 mw + 31 of every tile
+    const bool leader = P.box > 0 && lane % max(P.box, 1) == 0;  // of a box, at its first row
     uint32_t step = 0;
     bool ok = true;
-    // copies on their way that have not been announced yet, oldest first: step numbers alternate
-    // key tile, value tile
+    // Copies by rows on their way that have not been announced yet.  `issued` counts the key and
+    // value tiles in turn (key tile of step s: 2 s), `told` those of them up to which all are
+    // announced; by_rows has a bit for each that has to be.
     constexpr int kAhead = C::kKStages + C::kVStages - 1;
-    uint32_t issued = 0, told = 0;  // key tile of step s: 2 s; its value tile: 2 s + 1
+    static_assert(kAhead < 32, "a bit each");
+    uint32_t issued = 0, told = 0, by_rows = 0;
     auto tell = [&]() {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        const uint32_t s = told >> 1;
-        mbar_arrive(told & 1 ? smem_u32(&bars->v_full[s % C::kVStages])
-                             : smem_u32(&bars->k_full[s % C::kKStages]));
+      if (by_rows >> (told & 31) & 1u) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          const uint32_t s = told >> 1;
+          mbar_arrive(told & 1 ? smem_u32(&bars->v_full[s % C::kVStages])
+                               : smem_u32(&bars->k_full[s % C::kKStages]));
+        }
+        by_rows &= ~(1u << (told & 31));
       }
       ++told;
     };
@@ -412,22 +439,46 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     };
     for (uint32_t n = 0;; ++n) {
       if (!(ok = wait(bars->item_full[n & 1], (n >> 1) & 1))) break;
-      const PrefillItem it = bars->item[n & 1];
+      const PrefillItem& item = bars->item[n & 1];
+      const int khead = item.head;
+      if (khead < 0) break;
+      const int* table = P.cache.table + item.seq * P.cache.table_stride;
+      const char* kbase = P.cache.k.base + khead * P.cache.k.head;
+      const char* vbase = P.cache.v.base + khead * P.cache.v.head;
+      const int first = item.first, end = item.end, tile0 = item.tile, tiles = item.tiles;
+      // a tile whose last key is past `right`, or whose first is in front of `left`, has keys that
+      // some row does not see
+      const int right = min(item.pos0, end - 1);
+      const int left = sh.window >= 0 ? item.pos0 + item.tokens - 1 - sh.window : 0;
       __syncwarp();
-      if (it.head < 0) break;
       if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
-      const int* table = P.cache.table + it.seq * P.cache.table_stride;
-      const char* kbase = P.cache.k.base + it.head * P.cache.k.head;
-      const char* vbase = P.cache.v.base + it.head * P.cache.v.head;
-      // this lane's row of a key tile: the page is looked up a tile ahead
-      auto look_up = [&](int tile) -> int {
-        const int key = tile * kTile + mw * 32 + lane;
-        return key >= it.first && key < it.end ? __ldg(table + div_page(P.cache, key)) : -1;
+      auto edge = [&](int t) {
+        const int key0 = (tile0 + t) * kTile;
+        return key0 + kTile - 1 > right || key0 < left;
       };
-      int page = look_up(it.tile);
-      for (int t = 0; t < it.tiles && ok; ++t, ++step) {
-        const int key = (it.tile + t) * kTile + mw * 32 + lane;
-        const bool seen = key >= it.first && key < it.end;
+      // this lane's row of a key tile: the page is looked up a tile ahead
+      auto look_up = [&](int t) -> int {
+        const int key = (tile0 + t) * kTile + mw * 32 + lane;
+        return t < tiles && key >= first && key < end ? __ldg(table + div_page(P.cache, key)) : -1;
+      };
+      // this lane's box of a tile, if the lane leads one, in the page that it has found
+      auto load_box = [&](int side, int t, int page, uint32_t dst, uint32_t bar) {
+        const int key = (tile0 + t) * kTile + mw * 32 + lane;
+        const int in = key - div_page(P.cache, key) * P.cache.page_size;
+        const CUtensorMap* map = side ? &tm_v : &tm_k;
+        if constexpr (E4M3) {
+          tma_load_page(dst + lane * (side ? DV : DQK), map, bar, 0, khead, in, page,
+                        P.heads_inner);
+        } else {
+          for (int p = 0; p < (side ? DV : DQK) / 64; ++p)
+            tma_load_page(dst + p * kPrefillPanel + (mw * 32 + lane) * 128, map, bar, p * 64, khead,
+                          in, page, P.heads_inner);
+        }
+      };
+      int page = look_up(0);
+      for (int t = 0; t < tiles && ok; ++t, ++step) {
+        const int key = (tile0 + t) * kTile + mw * 32 + lane;
+        const bool seen = key >= first && key < end;
         const bool there = seen && page_in(P.cache, page);
         if (seen && !there) atomicCAS(P.status, 0, kStatusBadPage);
         const int in = key - div_page(P.cache, key) * P.cache.page_size;
@@ -435,14 +486,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         const long long ko = there ? token_at(P.cache.k, page, in) : -1;
         const long long vo = there ? token_at(P.cache.v, page, in) : -1;
         const uint32_t bits = __ballot_sync(0xffffffffu, there);
-        if (t + 1 < it.tiles) page = look_up(it.tile + t + 1);
+        const int here = page;
+        page = look_up(t + 1);
         // Where some row does not see some key, values that are not finite may not reach the
         // product (0 times them is NaN): they are looked for before the tile is handed on, zeros
         // take their place, and the rows that see them become NaN by their sum.
         uint32_t bad = 0;
-        const int key0 = (it.tile + t) * kTile;
-        if (key0 + kTile - 1 > it.pos0 ||
-            (sh.window >= 0 && key0 < it.pos0 + it.tokens - 1 - sh.window)) {
+        const bool is_edge = edge(t);
+        if (is_edge) {
           constexpr int kChunks = DV / (E4M3 ? 16 : 8), kRows = 32 / kChunks;
 #pragma unroll 1
           for (int i0 = 0; i0 < kChunks; i0 += 4) {
@@ -466,6 +517,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             }
           }
         }
+        // all 32 rows by TMA (a page that is not in the cache: by rows, as zeros)
+        const bool boxes = P.box > 0 && !is_edge && bits == ~0u;
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
           const uint32_t st = step % (side ? C::kVStages : C::kKStages);
@@ -479,6 +532,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           const char* base = side ? vbase : kbase;
           const long long o = side ? (bad >> lane & 1u ? -1 : vo) : ko;
           if constexpr (!E4M3) {
+            if (boxes) {
+              const uint32_t bar = smem_u32(side ? &bars->v_full[st] : &bars->k_full[st]);
+              if (lane == 0) mbar_arrive_expect_tx(bar, 32 * (side ? DV : DQK) * 2);
+              __syncwarp();
+              if (leader) load_box(side, t, here, dst, bar);
+              ++issued;
+              if (told + 1 == issued) ++told;
+              continue;
+            }
             constexpr int kMost = DQK > DV ? DQK : DV;
             const int chunks = (side ? DV : DQK) / 8;  // of 16 bytes, of a row
 #pragma unroll
@@ -518,12 +580,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             }
           }
           cp_commit();
+          by_rows |= 1u << (issued & 31);
           ++issued;
           if (E4M3) {
-            tell();
+            while (told != issued) tell();
           } else if (issued - told > kAhead) {
             cp_wait<kAhead>();
-            tell();
+            while (issued - told > kAhead) tell();
           }
         }
       }
@@ -544,35 +607,45 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     const int rt = r / sh.group, rh = r - rt * sh.group;  // this row's token and head
     for (uint32_t n = 0;; ++n) {
       if (!(ok = mbar_wait_warp(smem_u32(&bars->item_full[n & 1]), (n >> 1) & 1, ab))) break;
-      const PrefillItem it = bars->item[n & 1];
-      __syncwarp();
-      if (it.head < 0) break;
-      if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
-      const TileUse use = tile_use(sh, it);
-      const int t0 = use.twin ? 0 : w * sh.per_tile;  // first token of this tile
-      const int tokens = min(it.tokens - t0, sh.per_tile);
+      const PrefillItem& item = bars->item[n & 1];  // (until this warp lets go of it)
+      if (item.head < 0) break;
+      int lo, hi, theirs;
+      bool twin;
+      {
+        const TileUse use = tile_use(sh, item);
+        twin = use.twin;
+        lo = use.lo[w];
+        hi = use.hi[w];
+        theirs = use.hi[w ^ 1] >= use.lo[w ^ 1] ? 1 : 0;
+      }
+      const int t0 = twin ? 0 : w * sh.per_tile;  // first token of this tile
+      const int tokens = min(item.tokens - t0, sh.per_tile);
+      const int first_pos = item.pos0 + t0;
       const bool row_ok = rt < tokens;
       const bool live = __any_sync(0xffffffffu, row_ok);  // (a warp without rows has no work)
-      const int pos = it.pos0 + t0 + rt;
+      // a tile whose last key is past `right`, or whose first is in front of `left`, has keys that
+      // some row does not see; this row sees keys from `see0` to its own
+      const int right = first_pos;
+      const int left = sh.window >= 0 ? first_pos + tokens - 1 - sh.window : INT_MIN;
+      const int see0 = sh.window >= 0 ? max(first_pos + rt, 0) - sh.window : 0;
+      const int key0 = item.tile * kTile;
       // c in two factors, so that neither leaves fp32's range with the scale of an e4m3 cache
-      float f1 = P.scale_log2, f2_ = 1.f, v_scale = 1.f;
+      float f1 = P.scale_log2, f2_ = 1.f;
       bool odd_c = false;
       if constexpr (E4M3) {
         if (P.cache.k.scale != nullptr) {
           int e1, e2;
           const float a = frexpf(P.scale_log2, &e1);
-          const float b = frexpf(__ldg(P.cache.k.scale + it.head), &e2);
+          const float b = frexpf(__ldg(P.cache.k.scale + item.head), &e2);
           const int e = e1 + e2, h = e >> 1;
           f1 = ldexpf(a * b, h);
           f2_ = ldexpf(1.f, e - h);
           odd_c = e < -120 || e > 120;
         }
-        if (P.cache.v.scale != nullptr) v_scale = __ldg(P.cache.v.scale + it.head);
       }
       const float c = f1 * f2_;
       float m = -INFINITY, l = 0.f;
-      const int lo = use.lo[w], hi = use.hi[w];
-      for (int t = lo; t <= hi; t += use.twin ? 2 : 1) {
+      for (int t = lo; t <= hi; t += twin ? 2 : 1) {
         if (!(ok = mbar_wait_warp(smem_u32(&bars->s_full[w]), cnt & 1, ab))) break;
         ++cnt;
         tc_fence_after();
@@ -582,13 +655,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, sr[q]);
           const uint4 there =
               *reinterpret_cast<const uint4*>(bars->there[(step0 + t) % kKeyRing]);
-          const int kbase = (it.tile + t) * kTile;
+          const int kbase = key0 + t * kTile;
           tmem_ld_wait();
           // some row does not see some key of the tile: one that is not there, one after the
           // first row's position, one in front of the last row's window
           const bool edge = (there.x & there.y & there.z & there.w) != ~0u ||
-                            kbase + kTile - 1 > it.pos0 + t0 ||
-                            (sh.window >= 0 && kbase < it.pos0 + t0 + tokens - 1 - sh.window);
+                            kbase + kTile - 1 > right || kbase < left;
           float mx[8];
           bool sees_bad = false;
 #pragma unroll
@@ -596,8 +668,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           if (edge) {
             const uint4 bad = *reinterpret_cast<const uint4*>(bars->bad[(step0 + t) % kKeyRing]);
             // the row's keys, relative to the tile: klo .. khi - 1
-            const int khi = pos + 1 - kbase;
-            const int klo = sh.window >= 0 ? max(pos, 0) - sh.window - kbase : 0;
+            const int khi = right + rt + 1 - kbase, klo = see0 - kbase;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int a = min(32, max(0, klo - 32 * q)), b = min(32, max(0, khi - 32 * q));
@@ -657,15 +728,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&bars->p_full[w]));
       }
       if (!ok) break;
-      step0 += it.tiles;
+      step0 += item.tiles;
       // -------- end of the part: O, or its sums
-      const int mine = hi >= lo ? 1 : 0, theirs = use.hi[w ^ 1] >= use.lo[w ^ 1] ? 1 : 0;
+      const int mine = hi >= lo ? 1 : 0;
       if (mine && !(ok = mbar_wait_warp(smem_u32(&bars->o_done[w]), done[0] & 1, ab))) break;
       done[0] += mine;
       float a_mine = 1.f, a_theirs = 0.f;
       float top = m * f1 * f2_;  // in base 2
       int q0 = 0, q1 = DV / 32;  // this warpgroup's columns, in 32s
-      if (use.twin) {
+      if (twin) {
         if (theirs && !(ok = mbar_wait_warp(smem_u32(&bars->o_done[w ^ 1]), done[1] & 1, ab)))
           break;
         // the halves: (m, l) through shared memory, O from both accumulators
@@ -685,18 +756,24 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       }
       done[1] += theirs;
       tc_fence_after();
-      const bool whole = it.slot < 0;
-      const int64_t token = (int64_t)it.tok0 + t0 + rt;
-      const int head = it.head * sh.group + rh;
+      const int slot = item.slot;
+      const bool whole = slot < 0;
+      const int64_t token = (int64_t)item.tok0 + t0 + rt;
+      const int head = item.head * sh.group + rh;
+      float v_scale = 1.f;
+      if constexpr (E4M3)
+        if (P.cache.v.scale != nullptr) v_scale = __ldg(P.cache.v.scale + item.head);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
       const bool no_key = l == 0.f;
       const float factor = (no_key ? 0.f : whole ? 1.0f / l : 1.0f) * v_scale;
-      const int64_t srow = (int64_t)it.slot * kPrefillRows + (use.twin ? 0 : w * kTile) + r;
+      const int64_t srow = (int64_t)slot * kPrefillRows + (twin ? 0 : w * kTile) + r;
       if (live) {
 #pragma unroll 1
         for (int q = q0; q < q1; ++q) {
           uint32_t ov[32];
           float x[32];
-          if (use.twin) {
+          if (twin) {
             // (an accumulator that nothing was added to holds anything: its factor is 0)
             uint32_t ow[32];
             tmem_ld32(lanes + C::kTmemO + w * DV + q * 32, ov);
@@ -732,7 +809,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                            __float_as_uint(x[k + 6]), __float_as_uint(x[k + 7]));
           }
         }
-        if (row_ok && (!use.twin || w == 0)) {
+        if (row_ok && (!twin || w == 0)) {
           if (!whole) P.ml[srow] = make_float2(top, l);
           else if (P.lse != nullptr)
             P.lse[token * P.Hq + head] =
@@ -740,7 +817,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         }
       }
       tc_fence_before();
-      if (use.twin) {
+      if (twin) {
         // both accumulators are read before either warpgroup lets the next unit's products in
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->twin_done));
@@ -860,6 +937,8 @@ cudaError_t launch_prefill_typed(const PrefillLaunch& L, const Offsets& off) {
   using C = PrefillCfg<DQK, DV, E4M3>;
   PrefillParams P;
   P.cache = L.cache;
+  P.box = L.box;
+  P.heads_inner = L.heads_inner;
   P.sh = L.sh;
   P.room = (int64_t)L.cache.max_pages * L.cache.page_size;
   P.Hq = L.Hq;
@@ -875,7 +954,7 @@ cudaError_t launch_prefill_typed(const PrefillLaunch& L, const Offsets& off) {
   cudaError_t e =
       cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  k<<<grid, kPrefillThreads, C::kSmemBytes, L.stream>>>(L.tm_q, P, off);
+  k<<<grid, kPrefillThreads, C::kSmemBytes, L.stream>>>(L.tm_q, L.tm_k, L.tm_v, P, off);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   PrefillJoin J;
   J.desc = L.desc;

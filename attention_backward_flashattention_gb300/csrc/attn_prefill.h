@@ -239,7 +239,10 @@ constexpr size_t kPrefillAccBytes =
 constexpr size_t kPrefillWorkspaceBytes = kPrefillDescBytes + kPrefillMlBytes + kPrefillAccBytes;
 
 struct PrefillLaunch {
-  CUtensorMap tm_q;  // panels of per_tile tokens times a group of heads
+  CUtensorMap tm_q;        // panels of per_tile tokens times a group of heads
+  CUtensorMap tm_k, tm_v;  // boxes of `box` tokens of one page and head
+  int box;                 // 8, 16 or 32 tokens, which a page is a multiple of; 0: no maps
+  int heads_inner;         // the maps' second dimension is the head, and the third the token
   CacheView cache;
   PrefillShape sh;
   const PrefillOffsets* offsets;  // null: per_seq tokens each
