@@ -46,10 +46,12 @@ struct PrefillCfg {
   static constexpr int kKBytes = DQK / 64 * kPrefillPanel;
   static constexpr int kVBytes = DV / 64 * kPrefillPanel;
   // stages of key and of value tiles (bf16), and of an e4m3 cache's bytes in front of them
-  static constexpr int kKStages = E4M3 ? (DQK == 64 ? 3 : 1) : DQK == 64 ? 5 : DQK == 128 ? 3 : 2;
+  static constexpr int kKStages = E4M3 ? (DQK == 64 ? 3 : DQK == 128 ? 2 : 1) : DQK == 64 ? 5 : DQK == 128 ? 3 : 2;
   static constexpr int kVStages = E4M3 ? (DQK == 64 ? 3 : DQK == 128 ? 2 : 1)
                                        : DQK == 64 ? 5 : DQK == 128 ? 2 : 1;
-  static constexpr int kRaw = !E4M3 ? 0 : DQK == 64 ? 4 : DQK == 128 ? 2 : 1;
+  static constexpr int kRaw = !E4M3 ? 0 : DQK == 64 ? 4 : 1;
+  static constexpr bool kSpareQ = E4M3 && DQK > 64;  // (see the copy warps)
+  static_assert(!kSpareQ || kTile * (DQK + DV) <= kQTile, "a key and a value tile's bytes");
   static constexpr int kOffK = 2 * kQTile;
   static constexpr int kOffV = kOffK + kKStages * kKBytes;
   static constexpr int kOffRawK = kOffV + kVStages * kVBytes;
@@ -60,8 +62,8 @@ struct PrefillCfg {
   static constexpr uint32_t kTmemO = 256;
   // Registers a thread after the split of 512 x 128: softmax, copies, MMA and walk.
   static constexpr uint32_t kRegsSoftmax = E4M3 ? 176 : 184;
-  static constexpr uint32_t kRegsCopy = E4M3 ? 88 : 72;
-  static constexpr uint32_t kRegsCtl = 72;
+  static constexpr uint32_t kRegsCopy = E4M3 ? 96 : 80;
+  static constexpr uint32_t kRegsCtl = 64;
   static_assert(2 * kRegsSoftmax + kRegsCopy + kRegsCtl <= 512, "register split");
 };
 
@@ -72,10 +74,11 @@ struct PrefillBars {
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t twin_full, twin_done;
   uint64_t raw_full[2][4][4];    // [keys, values][slot][copy warp]
+  uint64_t spare_free;           // a single tile's unit is done with the second query tile's place
   uint64_t drain;
   PrefillItem item[2];
-  uint32_t there[kKeyRing][4];  // of a key tile's 128 keys, which are in the cache
-  uint32_t bad[kKeyRing][4];    // of an edge tile's, whose values are not finite
+  alignas(16) uint32_t there[kKeyRing][4];  // of a key tile's 128 keys, which are in the cache
+  alignas(16) uint32_t bad[kKeyRing][4];    // of an edge tile's, whose values are not finite
   float2 twin[2][kTile];         // (m, l) of a single tile's rows, by warpgroup
   uint32_t tmem_base;
   int abort_flag;
@@ -173,6 +176,14 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
+// Whether a word of two bf16 or four e4m3 values holds one that is not finite (all exponent bits
+// set; all seven bits of an e4m3 value, whose NaN that is).
+template <bool E4M3>
+__device__ __forceinline__ bool not_finite(uint32_t x) {
+  if constexpr (E4M3) return (((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+  return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+}
+
 // Four e4m3 values as two words of bf16 pairs (exact: a bf16 has every e4m3 value).
 __device__ __forceinline__ void e4m3_to_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
   uint32_t h0, h1;
@@ -186,12 +197,72 @@ __device__ __forceinline__ void e4m3_to_bf16(uint32_t x, uint32_t& lo, uint32_t&
   hi = pack_bf16(b.x, b.y);
 }
 
-// Whether a word of two bf16 or four e4m3 values holds one that is not finite (all exponent bits
-// set; all seven bits of an e4m3 value, whose NaN that is).
-template <bool E4M3>
-__device__ __forceinline__ bool not_finite(uint32_t x) {
-  if constexpr (E4M3) return (((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-  return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+// Rows of a warp's 32 of a tile, by the warp: lane l takes chunk C0 + l % CH (of 16 bytes of the
+// cache) of rows l / CH, l / CH + 32 / CH, ..., four at a time.  What varies from one of the four to
+// the next is known when this is compiled: unrolled throughout, the addresses spilled.
+//
+// bf16 rows, as they are, by asynchronous copies.  o: the lane's row's offset in the cache (-1: zeros).
+template <int CH, int C0>
+__device__ __forceinline__ void copy_rows(uint32_t tile, int mw, int lane, const char* base,
+                                          long long o) {
+  constexpr int kStep = 32 / CH;  // rows side by side
+  const int row0 = lane / CH, c = C0 + lane % CH;
+  const uint32_t dst = tile + (c >> 3) * kPrefillPanel + (mw * 32 + row0) * 128;
+  const char* src = base + c * 16;
+#pragma unroll 1
+  for (int p = 0; p < CH; p += 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const long long from = __shfl_sync(0xffffffffu, o, (p + i) * kStep + row0);
+      const uint32_t in8 = (i * kStep & 7) + row0;  // the row's place in the swizzle's period
+      cp_async16_or_zero(dst + (p + i) * kStep * 128 + (((c & 7) ^ in8) << 4),
+                         from < 0 ? base : src + from, from >= 0);
+    }
+  }
+}
+// e4m3 rows, widened: from the ring (raw: the warp's rows there, D bytes each) or from the cache.
+// Two chunks at a time: what one loads covers the other's latency, and a longer loop ran slower in
+// the kernel.  (Bits moved by hand and one product instead of the conversions, with NaN looked for,
+// took up to three times as long.)  The eight lanes of a row write to eight places of the swizzle's
+// period at once: those of the odd panel their second half first.
+template <int CH, int C0, int D, typename Behind>
+__device__ __forceinline__ void widen_rows(uint32_t tile, int mw, int lane, bool ring, uint32_t raw,
+                                           const char* base, long long o, const Behind& behind) {
+  constexpr int kStep = 32 / CH;
+  const int row0 = lane / CH, c = C0 + lane % CH;
+  const bool odd = (c & 4) != 0;
+  const uint32_t dst = tile + (c >> 2) * kPrefillPanel + (mw * 32 + row0) * 128;
+  raw += row0 * D + c * 16;
+  base += c * 16;
+#pragma unroll 1
+  for (int p = 0; p < CH; p += 2) {
+    uint4 v[2];
+    if (ring) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) v[i] = lds128(raw + (p + i) * kStep * D);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const long long from = __shfl_sync(0xffffffffu, o, (p + i) * kStep + row0);
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (from >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(base + from));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t in8 = ((p + i) * kStep & 7) + row0, at = dst + (p + i) * kStep * 128;
+      uint32_t a[4], b[4];
+      e4m3_to_bf16(odd ? v[i].z : v[i].x, a[0], a[1]);
+      e4m3_to_bf16(odd ? v[i].w : v[i].y, a[2], a[3]);
+      e4m3_to_bf16(odd ? v[i].x : v[i].z, b[0], b[1]);
+      e4m3_to_bf16(odd ? v[i].y : v[i].w, b[2], b[3]);
+      const uint32_t x = 2 * c & 7;
+      st_shared_v4(at + (((odd ? x + 1 : x) ^ in8) << 4), a[0], a[1], a[2], a[3]);
+      st_shared_v4(at + (((odd ? x : x + 1) ^ in8) << 4), b[0], b[1], b[2], b[3]);
+    }
+  }
+  __syncwarp();
+  behind();  // (the rows have been read)
 }
 
 template <int DQK, int DV, bool E4M3, typename Offsets>
@@ -207,18 +278,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const PrefillShape& sh = P.sh;
   if (threadIdx.x == 0) P.desc[blockIdx.x].parts = 0;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (sQ & 1023u) {  // the swizzled panels need a 1024-byte aligned window
     if (threadIdx.x == 0) atomicCAS(P.status, 0, kStatusInternal);
     return;
   }
 
-  // ---- the line: every thread counts the tiles of some consecutive units
-  long long* before = reinterpret_cast<long long*>(smem);  // [512] tiles in front of a thread's
+  // ---- the line: every thread counts the cost of some consecutive units
+  long long* before = reinterpret_cast<long long*>(smem);  // [512] cost in front of a thread's
   long long* warp_sum = before + kPrefillThreads;
   const int per = (sh.units + kPrefillThreads - 1) / kPrefillThreads;
   const int u0 = min(sh.units, (int)threadIdx.x * per), u1 = min(sh.units, u0 + per);
   long long mine = 0;
-  for (int i = u0; i < u1; ++i) mine += unit_at(P, off, i).tiles;
+  for (int i = u0; i < u1; ++i) mine += unit_cost(unit_at(P, off, i).tiles);
   long long upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
@@ -259,6 +331,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     }
     mbar_init(smem_u32(&bars->twin_full), 8);
     mbar_init(smem_u32(&bars->twin_done), 8);
+    mbar_init(smem_u32(&bars->spare_free), 4);
     for (int i = 0; i < 2 * 4 * 4; ++i) mbar_init(smem_u32(&bars->raw_full[0][0][0] + i), 1);
     mbar_init(smem_u32(&bars->drain), 1);
     fence_barrier_init();
@@ -308,6 +381,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       };
       auto unit = [&](int i) { return unit_at(P, off, i); };
       uint32_t q_loads = 0;
+      [[maybe_unused]] uint32_t twins = 0;  // units of a single tile so far
       PrefillItem it;
       walk.begin(unit);
       while (walk.next(unit, &it)) {
@@ -316,6 +390,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         if (!(ok = mbar_wait(smem_u32(&bars->q_empty), (n & 1) ^ 1, ab))) break;
         // rows past the sequence's tokens hold the next one's queries (or zeros): never stored
         const int tiles = it.tokens <= sh.per_tile ? 1 : 2;
+        if constexpr (C::kSpareQ) {  // (the copy warps may still use the second tile's place)
+          if (tiles == 1) ++twins;
+          else if (twins > 0 &&
+                   !(ok = mbar_wait(smem_u32(&bars->spare_free), (twins - 1) & 1, ab)))
+            break;
+        }
         const uint32_t qf = smem_u32(&bars->q_full);
         mbar_arrive_expect_tx(qf, (uint32_t)(tiles * (DQK / 64) * sh.per_tile * sh.group * 128));
         q_loads = n + 1;
@@ -416,25 +496,33 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     constexpr int kAhead = C::kKStages + C::kVStages - 1;
     static_assert(kAhead < 32, "a bit each");
     uint32_t issued = 0, told = 0, by_rows = 0;
-    auto tell = [&]() {
-      if (by_rows >> (told & 31) & 1u) {
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          const uint32_t s = told >> 1;
+    // e4m3: slots of the ring (bit 4 side + slot) that are on their way, and their barriers' parity
+    constexpr int kRaw = C::kRaw > 0 ? C::kRaw : 1;
+    [[maybe_unused]] uint32_t raw_on = 0, raw_parity = 0;
+    auto raw_at = [&](int side, uint32_t slot) -> uint32_t {  // this warp's rows there
+      if (C::kSpareQ && slot == C::kRaw)
+        return sQ + C::kQTile + (side ? kTile * DQK + mw * 32 * DV : mw * 32 * DQK);
+      return sQ + (side ? C::kOffRawV + slot * kTile * DV + mw * 32 * DV
+                        : C::kOffRawK + slot * kTile * DQK + mw * 32 * DQK);
+    };
+    [[maybe_unused]] bool was_pair = false;
+    auto tell = [&](uint32_t upto) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      for (; told != upto; ++told) {
+        const uint32_t bit = 1u << (told & 31), s = told >> 1;
+        if (lane == 0 && (by_rows & bit) != 0)
           mbar_arrive(told & 1 ? smem_u32(&bars->v_full[s % C::kVStages])
                                : smem_u32(&bars->k_full[s % C::kKStages]));
-        }
-        by_rows &= ~(1u << (told & 31));
+        by_rows &= ~bit;
       }
-      ++told;
     };
     // Waits; where that takes time, what is under way is announced first: it may be what the
     // others wait for.
     auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
       if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&bar), parity))) return true;
       cp_wait<0>();
-      while (told != issued) tell();
+      if (told != issued) tell(issued);
       return mbar_wait_warp(smem_u32(&bar), parity, ab);
     };
     for (uint32_t n = 0;; ++n) {
@@ -450,6 +538,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       // some row does not see
       const int right = min(item.pos0, end - 1);
       const int left = sh.window >= 0 ? item.pos0 + item.tokens - 1 - sh.window : 0;
+      // slots of the ring: one more, in the second query tile's place, where this unit has none and
+      // the one in front of it, whose products may still read it, had none either
+      const bool twin = item.tokens <= sh.per_tile;
+      [[maybe_unused]] const int slots = kRaw + (C::kSpareQ && twin && !was_pair ? 1 : 0);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
       auto edge = [&](int t) {
@@ -475,125 +567,174 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
                           in, page, P.heads_inner);
         }
       };
-      int page = look_up(0);
-      for (int t = 0; t < tiles && ok; ++t, ++step) {
-        const int key = (tile0 + t) * kTile + mw * 32 + lane;
-        const bool seen = key >= first && key < end;
-        const bool there = seen && page_in(P.cache, page);
-        if (seen && !there) atomicCAS(P.status, 0, kStatusBadPage);
-        const int in = key - div_page(P.cache, key) * P.cache.page_size;
-        // (-1: zeros)
-        const long long ko = there ? token_at(P.cache.k, page, in) : -1;
-        const long long vo = there ? token_at(P.cache.v, page, in) : -1;
-        const uint32_t bits = __ballot_sync(0xffffffffu, there);
-        const int here = page;
-        page = look_up(t + 1);
-        // Where some row does not see some key, values that are not finite may not reach the
-        // product (0 times them is NaN): they are looked for before the tile is handed on, zeros
-        // take their place, and the rows that see them become NaN by their sum.
-        uint32_t bad = 0;
-        const bool is_edge = edge(t);
-        if (is_edge) {
-          constexpr int kChunks = DV / (E4M3 ? 16 : 8), kRows = 32 / kChunks;
-#pragma unroll 1
-          for (int i0 = 0; i0 < kChunks; i0 += 4) {
-            uint4 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int at = (i0 + i) * 32 + lane, row = at / kChunks, c = at - row * kChunks;
-              const long long from = __shfl_sync(0xffffffffu, vo, row);
-              v[i] = make_uint4(0, 0, 0, 0);
-              if (from >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(vbase + from + c * 16));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t found = __ballot_sync(
-                  0xffffffffu, not_finite<E4M3>(v[i].x) || not_finite<E4M3>(v[i].y) ||
-                                   not_finite<E4M3>(v[i].z) || not_finite<E4M3>(v[i].w));
-#pragma unroll
-              for (int k = 0; k < kRows; ++k)
-                if (found >> (k * kChunks) & ((1u << kChunks) - 1u))
-                  bad |= 1u << ((i0 + i) * kRows + k);
-            }
-          }
+      // e4m3: this warp's rows of tile t on their way to the ring, where all are there and every
+      // query sees them
+      [[maybe_unused]] auto load_raw = [&](int side, int t, int page) {
+        if constexpr (E4M3) {
+          if (P.box == 0 || t >= tiles || edge(t)) return;
+          if (__ballot_sync(0xffffffffu, page_in(P.cache, page)) != ~0u) return;
+          const uint32_t slot = t % slots, bar = smem_u32(&bars->raw_full[side][slot][mw]);
+          __syncwarp();  // (what every lane has read there is behind it)
+          if (lane == 0) mbar_arrive_expect_tx(bar, 32 * (side ? DV : DQK));
+          __syncwarp();
+          if (leader) load_box(side, t, page, raw_at(side, slot), bar);
+          raw_on |= 1u << (side * 4 + slot);
         }
-        // all 32 rows by TMA (a page that is not in the cache: by rows, as zeros)
-        const bool boxes = P.box > 0 && !is_edge && bits == ~0u;
-#pragma unroll
+      };
+      int page = look_up(0);
+      int page_far = -1;  // of the tile that goes to the ring next
+      if constexpr (E4M3) {
+        for (int t = 0; t < slots; ++t) {
+          const int p = t == 0 ? page : look_up(t);
+          load_raw(0, t, p);
+          load_raw(1, t, p);
+        }
+        page_far = look_up(slots);
+      }
+      for (int t = 0; t < tiles && ok; ++t, ++step) {
+        // all 32 rows by TMA (a page that is not in the cache: by rows, as zeros); those that go
+        // through the ring are on their way
+        const bool is_edge = edge(t);
+        const uint32_t on = E4M3 ? 0x11u << (t % slots) : 0u;
+        const bool in_ring = E4M3 && (raw_on & on) == on;
+        const int here = page;
+        uint32_t bits = ~0u;
+        long long ko = -1, vo = -1;  // (-1: zeros)
+        if (!in_ring) {
+          const int key = (tile0 + t) * kTile + mw * 32 + lane;
+          const bool seen = key >= first && key < end;
+          const bool there = seen && page_in(P.cache, page);
+          if (seen && !there) atomicCAS(P.status, 0, kStatusBadPage);
+          const int in = key - div_page(P.cache, key) * P.cache.page_size;
+          if (there) ko = token_at(P.cache.k, page, in), vo = token_at(P.cache.v, page, in);
+          bits = __ballot_sync(0xffffffffu, there);
+        }
+        page = E4M3 && slots == 1 ? page_far : look_up(t + 1);
+        const bool boxes = !E4M3 && P.box > 0 && !is_edge && bits == ~0u;
+#pragma unroll 1
         for (int side = 0; side < 2; ++side) {
+          const int d = side ? DV : DQK;
           const uint32_t st = step % (side ? C::kVStages : C::kKStages);
           const uint32_t parity = ((step / (side ? C::kVStages : C::kKStages)) & 1) ^ 1;
           if (!(ok = wait(side ? bars->v_empty[st] : bars->k_empty[st], parity))) break;
-          if (side == 0 && lane == 0) {
-            bars->there[step % kKeyRing][mw] = bits;
-            bars->bad[step % kKeyRing][mw] = bad;
-          }
-          const uint32_t dst = (side ? sV + st * C::kVBytes : sK + st * C::kKBytes);
+          const uint32_t dst = side ? sV + st * C::kVBytes : sK + st * C::kKBytes;
           const char* base = side ? vbase : kbase;
-          const long long o = side ? (bad >> lane & 1u ? -1 : vo) : ko;
-          if constexpr (!E4M3) {
-            if (boxes) {
-              const uint32_t bar = smem_u32(side ? &bars->v_full[st] : &bars->k_full[st]);
-              if (lane == 0) mbar_arrive_expect_tx(bar, 32 * (side ? DV : DQK) * 2);
-              __syncwarp();
-              if (leader) load_box(side, t, here, dst, bar);
-              ++issued;
-              if (told + 1 == issued) ++told;
-              continue;
+          if (boxes) {
+            const uint32_t bar = smem_u32(side ? &bars->v_full[st] : &bars->k_full[st]);
+            if (lane == 0) {
+              if (side == 0) {
+                bars->there[step % kKeyRing][mw] = ~0u;
+                bars->bad[step % kKeyRing][mw] = 0;
+              }
+              mbar_arrive_expect_tx(bar, 32 * d * 2);
             }
-            constexpr int kMost = DQK > DV ? DQK : DV;
-            const int chunks = (side ? DV : DQK) / 8;  // of 16 bytes, of a row
-#pragma unroll
-            for (int i = 0; i < kMost / 8; ++i) {
-              if (i >= chunks) break;
-              const int at = i * 32 + lane, row = at / chunks, c = at - row * chunks;
-              const long long from = __shfl_sync(0xffffffffu, o, row);
-              const int r = mw * 32 + row;
-              cp_async16_or_zero(dst + (c >> 3) * kPrefillPanel + sw128_offset(r, c & 7),
-                                 base + (from < 0 ? 0 : from + c * 16), from >= 0);
+            __syncwarp();
+            if (leader) load_box(side, t, here, dst, bar);
+            ++issued;
+            if (told + 1 == issued) ++told;
+            continue;
+          }
+          const long long o = side ? vo : ko;
+          if constexpr (!E4M3) {
+            if constexpr (DQK == 64) {
+              copy_rows<8, 0>(dst, mw, lane, base, o);
+            } else {
+              copy_rows<16, 0>(dst, mw, lane, base, o);
+              if (d == 192) copy_rows<8, 16>(dst, mw, lane, base, o);
             }
           } else {
-            constexpr int kMost = DQK > DV ? DQK : DV;
-            const int chunks = (side ? DV : DQK) / 16;  // of 16 bytes, of a row
-            uint4 w[kMost / 16];
-#pragma unroll
-            for (int i = 0; i < kMost / 16; ++i) {
-              if (i >= chunks) break;
-              const int at = i * 32 + lane, row = at / chunks, c = at - row * chunks;
-              const long long from = __shfl_sync(0xffffffffu, o, row);
-              w[i] = make_uint4(0, 0, 0, 0);
-              if (from >= 0) w[i] = __ldg(reinterpret_cast<const uint4*>(base + from + c * 16));
+            const uint32_t slot = t % slots, bit = 1u << (side * 4 + slot);
+            const bool ring = in_ring;
+            if (ring) {
+              if (!(ok = mbar_wait_warp(smem_u32(&bars->raw_full[side][slot][mw]),
+                                        (raw_parity & bit) != 0, ab)))
+                break;
+              raw_on ^= bit;
+              raw_parity ^= bit;
             }
-#pragma unroll
-            for (int i = 0; i < kMost / 16; ++i) {
-              if (i >= chunks) break;
-              const int at = i * 32 + lane, row = at / chunks, c = at - row * chunks;
-              const int r = mw * 32 + row;
-              const uint32_t panel = dst + (c >> 2) * kPrefillPanel;
-              uint32_t a[4], b[4];
-              e4m3_to_bf16(w[i].x, a[0], a[1]);
-              e4m3_to_bf16(w[i].y, a[2], a[3]);
-              e4m3_to_bf16(w[i].z, b[0], b[1]);
-              e4m3_to_bf16(w[i].w, b[2], b[3]);
-              st_shared_v4(panel + sw128_offset(r, (2 * c) & 7), a[0], a[1], a[2], a[3]);
-              st_shared_v4(panel + sw128_offset(r, (2 * c + 1) & 7), b[0], b[1], b[2], b[3]);
+            const uint32_t raw = raw_at(side, slot);
+            auto nothing = [] {};
+            auto next = [&] { load_raw(side, t + slots, page_far); };
+            if constexpr (DQK == 64) {
+              widen_rows<4, 0, 64>(dst, mw, lane, ring, raw, base, o, next);
+            } else if (DQK == 128 || d == 128) {
+              widen_rows<8, 0, 128>(dst, mw, lane, ring, raw, base, o, next);
+            } else {
+              widen_rows<8, 0, 192>(dst, mw, lane, ring, raw, base, o, nothing);
+              widen_rows<4, 8, 192>(dst, mw, lane, ring, raw, base, o, next);
             }
           }
           cp_commit();
+          if (side == 0) {
+            // Where some row does not see some key, values that are not finite may not reach the
+            // product (0 times them is NaN): they are looked for before the tile's keys are handed
+            // on, zeros take their place, and the rows that see them become NaN by their sum.
+            uint32_t bad = 0;
+            if (is_edge) {
+              constexpr int kChunks = DV / (E4M3 ? 16 : 8), kRows = 32 / kChunks;
+              constexpr int kBatch = kChunks < 8 ? kChunks : 8;
+#pragma unroll 1
+              for (int i0 = 0; i0 < kChunks; i0 += kBatch) {
+                uint4 v[kBatch];
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                  const int at = (i0 + i) * 32 + lane, row = at / kChunks, c = at - row * kChunks;
+                  const long long from = __shfl_sync(0xffffffffu, vo, row);
+                  v[i] = make_uint4(0, 0, 0, 0);
+                  if (from >= 0)
+                    v[i] = __ldg(reinterpret_cast<const uint4*>(vbase + from + c * 16));
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                  const uint32_t found = __ballot_sync(
+                      0xffffffffu, not_finite<E4M3>(v[i].x) || not_finite<E4M3>(v[i].y) ||
+                                       not_finite<E4M3>(v[i].z) || not_finite<E4M3>(v[i].w));
+#pragma unroll
+                  for (int k = 0; k < kRows; ++k)
+                    if (found >> (k * kChunks) & ((1u << kChunks) - 1u))
+                      bad |= 1u << ((i0 + i) * kRows + k);
+                }
+              }
+              if (bad >> lane & 1u) vo = -1;
+            }
+            if (lane == 0) {
+              bars->there[step % kKeyRing][mw] = bits;
+              bars->bad[step % kKeyRing][mw] = bad;
+            }
+          }
           by_rows |= 1u << (issued & 31);
           ++issued;
           if (E4M3) {
-            while (told != issued) tell();
+            if (side == 1) tell(issued);  // (the tile's keys too, unless the values had to wait)
           } else if (issued - told > kAhead) {
             cp_wait<kAhead>();
-            while (issued - told > kAhead) tell();
+            tell(issued - kAhead);
           }
         }
+        if constexpr (E4M3) page_far = look_up(t + 1 + slots);
+      }
+      if constexpr (C::kSpareQ) {
+        if (ok && twin) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&bars->spare_free));
+        }
+        was_pair = !twin;
       }
       if (!ok) break;
     }
     cp_wait<0>();
-    while (ok && told != issued) tell();
+    if (ok && told != issued) tell(issued);
+    if (!ok && lane == 0) {
+      // let every copy already issued land before the CTA's memory is released
+      for (uint32_t s = step + 1 > C::kKStages ? step + 1 - C::kKStages : 0; s <= step; ++s)
+        mbar_wait_drain(smem_u32(&bars->k_full[s % C::kKStages]), (s / C::kKStages) & 1);
+      for (uint32_t s = step + 1 > C::kVStages ? step + 1 - C::kVStages : 0; s <= step; ++s)
+        mbar_wait_drain(smem_u32(&bars->v_full[s % C::kVStages]), (s / C::kVStages) & 1);
+      for (uint32_t b = raw_on; b != 0; b &= b - 1) {
+        const int i = __ffs(b) - 1;
+        mbar_wait_drain(smem_u32(&bars->raw_full[i >> 2][i & 3][mw]), raw_parity >> i & 1);
+      }
+    }
   } else {
     regs_inc<C::kRegsSoftmax>();
     // -------------------------------------------------------------- softmax
@@ -836,9 +977,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
 }
 
 // ----------------------------------------------------------------------------
-// Join of the units that were cut: a warp per row, the parts in order.
+// Join of the units that were cut.  One warp for up to eight parts of a row, two, four or eight for
+// more (a unit's parts are as many for each of its rows): a lane has DV / 32 columns of a part on
+// their way for each of the warp's, and the warps' sums meet in shared memory, in order.
 // ----------------------------------------------------------------------------
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 struct PrefillJoin {
   const PrefillDesc* desc;
   const float2* ml;
@@ -847,18 +990,28 @@ struct PrefillJoin {
   float* lse;
   int shares, group, per_tile, Hq;
 };
+__device__ __forceinline__ int join_team(int parts) {  // warps of a row
+  return parts <= 8 ? 1 : parts <= 16 ? 2 : parts <= 32 ? 4 : 8;
+}
 
 template <int DV>
 __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const PrefillJoin P) {
-  __shared__ int upto[kMaxPrefillCtas + 1];  // rows in front of each share's unit
-  __shared__ int sums[kJoinThreads / 32];
+  constexpr int kV = DV / 32;      // columns of a lane
+  constexpr int kFlight = 10;      // parts on their way at a time
+  __shared__ int upto[kMaxPrefillCtas + 1];  // groups of rows in front of each share's unit
+  __shared__ int sums[kJoinWarps];
+  __shared__ float2 met_ml[kJoinWarps];
+  __shared__ float met[kJoinWarps][DV];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int rows = 0;
+  // (every thread: this kernel may not end in front of the one that it is launched behind)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  int groups = 0;
   if (tid < P.shares) {
     const PrefillDesc d = P.desc[tid];
-    rows = d.parts > 0 ? d.tokens * P.group : 0;
+    const int rows = kJoinWarps / join_team(d.parts);  // of a block at a time
+    groups = d.parts > 0 ? (d.tokens * P.group + rows - 1) / rows : 0;
   }
-  int x = rows;
+  int x = groups;
 #pragma unroll
   for (int k = 1; k < 32; k <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, x, k);
@@ -868,56 +1021,87 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const Prefil
   __syncthreads();
   int front = 0, total = 0;
 #pragma unroll
-  for (int i = 0; i < kJoinThreads / 32; ++i) {
+  for (int i = 0; i < kJoinWarps; ++i) {
     if (i < warp) front += sums[i];
     total += sums[i];
   }
-  if (tid <= P.shares) upto[tid] = front + x - rows;
+  if (tid <= P.shares) upto[tid] = front + x - groups;
   __syncthreads();
-  constexpr int kV = DV / 32;  // columns of a lane
-  for (int i = blockIdx.x * (kJoinThreads / 32) + warp; i < total;
-       i += gridDim.x * (kJoinThreads / 32)) {
+  for (int i = blockIdx.x; i < total; i += gridDim.x) {
     int lo = 0, hi = P.shares - 1;  // the last share with upto <= i (those without rows passed over)
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (upto[mid] <= i) lo = mid; else hi = mid - 1;
     }
     const PrefillDesc d = P.desc[lo];
-    const int row = i - upto[lo];
+    const int team = join_team(d.parts), member = warp % team;
+    const int row = (i - upto[lo]) * (kJoinWarps / team) + warp / team;
+    const bool there = row < d.tokens * P.group;
     const int tok = row / P.group, h = row - tok * P.group;
     // the row's place among the slot's: two tiles of per_tile tokens
     const int w = tok / P.per_tile;
     const int place = w * kTile + (tok - w * P.per_tile) * P.group + h;
     auto at = [&](int p) { return (int64_t)prefill_slot(lo, p) * kPrefillRows + place; };
-    float top = -INFINITY;
-    for (int p = lane; p < d.parts; p += 32) top = fmaxf(top, P.ml[at(p)].x);
-#pragma unroll
-    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-    float sum = 0.f, acc[kV];
+    // this warp's parts: member, member + team, ...
+    float top = -INFINITY, sum = 0.f, acc[kV];
 #pragma unroll
     for (int k = 0; k < kV; ++k) acc[k] = 0.f;
-    for (int p0 = 0; p0 < d.parts; p0 += 8) {
+    if (there) {
+      for (int p = member + lane * team; p < d.parts; p += 32 * team)
+        top = fmaxf(top, P.ml[at(p)].x);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        if (p0 + q >= d.parts) break;
-        const int64_t s = at(p0 + q);
-        const float2 ml = P.ml[s];
-        // (NaN stays: a part whose sums are not finite makes the row not finite)
-        const float weight = ml.x == top ? (top == -INFINITY ? 0.f : 1.f) : ex2(ml.x - top);
-        const float* src = P.acc + s * DV + lane * kV;
-        float v[kV];
-        if constexpr (kV == 4) {
-          const float4 f = *reinterpret_cast<const float4*>(src);
-          v[0] = f.x, v[1] = f.y, v[2] = f.z, v[3] = f.w;
-        } else {
-          const float2 f = *reinterpret_cast<const float2*>(src);
-          v[0] = f.x, v[1] = f.y;
+      for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+      for (int p0 = member; p0 < d.parts; p0 += kFlight * team) {
+        float v[kFlight][kV];
+        float2 ml[kFlight];
+#pragma unroll
+        for (int q = 0; q < kFlight; ++q) {
+          const int64_t s = at(min(p0 + q * team, d.parts - 1));
+          ml[q] = P.ml[s];
+          const float* src = P.acc + s * DV + lane * kV;
+          if constexpr (kV == 4) {
+            const float4 f = *reinterpret_cast<const float4*>(src);
+            v[q][0] = f.x, v[q][1] = f.y, v[q][2] = f.z, v[q][3] = f.w;
+          } else {
+            const float2 f = *reinterpret_cast<const float2*>(src);
+            v[q][0] = f.x, v[q][1] = f.y;
+          }
         }
-        sum += ml.y * weight;
 #pragma unroll
-        for (int k = 0; k < kV; ++k) acc[k] += v[k] * weight;
+        for (int q = 0; q < kFlight; ++q) {
+          if (p0 + q * team >= d.parts) break;
+          // (NaN stays: a part whose sums are not finite makes the row not finite)
+          const float weight =
+              ml[q].x == top ? (top == -INFINITY ? 0.f : 1.f) : ex2(ml[q].x - top);
+          sum += ml[q].y * weight;
+#pragma unroll
+          for (int k = 0; k < kV; ++k) acc[k] += v[q][k] * weight;
+        }
       }
     }
+    if (team > 1) {  // (the same for the whole block)
+      if (lane == 0) met_ml[warp] = make_float2(top, sum);
+#pragma unroll
+      for (int k = 0; k < kV; ++k) met[warp][lane * kV + k] = acc[k];
+      __syncthreads();
+      if (member == 0) {
+        float t2 = top;
+        for (int q = 1; q < team; ++q) t2 = fmaxf(t2, met_ml[warp + q].x);
+        sum = 0.f;
+#pragma unroll
+        for (int k = 0; k < kV; ++k) acc[k] = 0.f;
+        for (int q = 0; q < team; ++q) {
+          const float2 ml = met_ml[warp + q];
+          const float weight = ml.x == t2 ? (t2 == -INFINITY ? 0.f : 1.f) : ex2(ml.x - t2);
+          sum += ml.y * weight;
+#pragma unroll
+          for (int k = 0; k < kV; ++k) acc[k] += met[warp + q][lane * kV + k] * weight;
+        }
+        top = t2;
+      }
+      __syncthreads();
+    }
+    if (!there || member != 0) continue;
     const bool no_key = sum == 0.f;
     const float inv = no_key ? 0.f : 1.0f / sum;
     const int64_t out = (int64_t)(d.tok0 + tok) * P.Hq + d.head * P.group + h;
@@ -966,8 +1150,17 @@ cudaError_t launch_prefill_typed(const PrefillLaunch& L, const Offsets& off) {
   J.group = L.sh.group;
   J.per_tile = L.sh.per_tile;
   J.Hq = L.Hq;
-  prefill_join_kernel<DV><<<grid * 4, kJoinThreads, 0, L.stream>>>(J);
-  return cudaGetLastError();
+  // on its way while the main kernel runs; it waits for that one's end before it reads
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid * 4);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefill_join_kernel<DV>, J);
 }
 
 template <int DQK, int DV, bool E4M3>

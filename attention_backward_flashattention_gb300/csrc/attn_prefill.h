@@ -69,25 +69,26 @@ __host__ __device__ inline PrefillUnit make_prefill_unit(const PrefillShape& sh,
 }
 
 // ---- shares -----------------------------------------------------------------
-// The key tiles of all units lie on one line, key head by key head, and each CTA takes an
-// equal share of it: the work is split over the keys as far as it has to be for every SM to
-// have some, whatever the lengths are, which only the device knows.  A cut within `tol` tiles of
-// a unit's end is moved there.  Cuts depend on the lengths alone.
-constexpr int kPrefillMinTiles = 3;  // of a share, where there are more CTAs than units
+// The units lie on one line, key head by key head, each as long as it takes, and each CTA
+// takes an equal share of it: the work is split over the keys as far as it has to be for every
+// SM to have some, whatever the lengths are, which only the device knows.  A cut within `tol`
+// tiles of a unit's end is moved there.  Cuts depend on the lengths alone.
+constexpr int kPrefillMinCost = 5;   // of a share, where there are more CTAs than units
 constexpr int kPrefillTol = 4;       // a unit's parts cost about as much as two tiles
+constexpr int kPrefillUnitCost = 2;  // of a unit besides its tiles
+__host__ __device__ inline int unit_cost(int tiles) { return tiles + kPrefillUnitCost; }
 struct PrefillLine {
-  long long total;  // tiles of the line
+  long long total;  // cost of all units
   int n;            // shares
   int tol;
 };
-__host__ __device__ inline PrefillLine make_prefill_line(long long tiles_per_head, int units,
+__host__ __device__ inline PrefillLine make_prefill_line(long long cost_per_head, int units,
                                                          int heads, int grid) {
   PrefillLine l;
-  l.total = tiles_per_head * heads;
-  long long n = l.total / kPrefillMinTiles;
+  l.total = cost_per_head * heads;
+  long long n = l.total / kPrefillMinCost;
   if (n < (long long)units * heads) n = (long long)units * heads;
-  if (n > l.total) n = l.total;
-  l.n = n < grid ? (int)n : grid;
+  l.n = n < grid ? (int)n : grid;  // (at most total)
   const long long share = l.total / l.n;
   l.tol = share / 6 < kPrefillTol ? (int)(share / 6) : kPrefillTol;
   return l;
@@ -95,17 +96,22 @@ __host__ __device__ inline PrefillLine make_prefill_line(long long tiles_per_hea
 __host__ __device__ inline long long prefill_cut(const PrefillLine& l, int c) {
   return div_line(l.total * c, l.n);
 }
-// Where a cut at x, inside the unit of tiles at .. at + tiles - 1, is made.
-__host__ __device__ inline long long prefill_snap(const PrefillLine& l, long long x, long long at,
-                                                  int tiles) {
-  if (x - at <= l.tol) return at;
-  if (at + tiles - x <= l.tol) return at + tiles;
-  return x;
+// The tile in front of which a cut at x, inside the unit at `at`, is made: 0: in front of the
+// unit, `tiles`: behind it.
+__host__ __device__ inline int prefill_snap(const PrefillLine& l, long long x, long long at,
+                                            int tiles) {
+  if (x <= at) return 0;
+  const int t = (int)div_line((x - at) * tiles, unit_cost(tiles));
+  if (t <= l.tol) return 0;
+  if (tiles - t <= l.tol) return tiles;
+  return t;
 }
 // Parts of the unit at `at` whose first part share c has, when cut c + 1 is inside it: a part for
-// each further share that starts inside.  cut(i) < e exactly for i < e n / total.
+// each further share that starts inside.  A cut at x is made at the unit's end from x >= e on, and
+// cut(i) < e exactly for i < e n / total.
 __host__ __device__ inline int prefill_parts(const PrefillLine& l, long long at, int tiles, int c) {
-  const long long e = at + tiles - l.tol;
+  const long long e =
+      at + ((long long)(tiles - l.tol) * unit_cost(tiles) + tiles - 1) / tiles;
   const long long past = (e * l.n + l.total - 1) / l.total;  // first i with cut(i) >= e
   return (int)(past - 1 - c) + 1;
 }
@@ -129,15 +135,17 @@ struct PrefillWalk {
   PrefillLine line;
   int c, units, heads;
   int head, index;   // the unit at hand
-  long long at;      // tiles in front of it
-  long long x, x1;   // where the share goes on, and its back cut
+  long long at;      // cost in front of it
+  long long x1;      // the share's back cut
+  int tile;          // the unit's tile from which on the share goes on
   PrefillUnit u;
   bool over;
 
 #pragma nv_exec_check_disable
   template <typename UnitAt>
   __host__ __device__ void next_unit(const UnitAt& unit) {
-    at += u.tiles;
+    at += unit_cost(u.tiles);
+    tile = 0;
     if (++index == units) {
       index = 0;
       ++head;
@@ -151,20 +159,19 @@ struct PrefillWalk {
     const long long x0 = prefill_cut(line, c);
     x1 = c + 1 < line.n ? prefill_cut(line, c + 1) : line.total;
     u = unit(index);
-    while (x0 >= at + u.tiles) next_unit(unit);
-    x = prefill_snap(line, x0, at, u.tiles);
-    if (x >= at + u.tiles) next_unit(unit);
+    while (x0 >= at + unit_cost(u.tiles)) next_unit(unit);
+    tile = prefill_snap(line, x0, at, u.tiles);
+    if (tile == u.tiles) next_unit(unit);
   }
 #pragma nv_exec_check_disable
   template <typename UnitAt>
   __host__ __device__ bool next(const UnitAt& unit, PrefillItem* it) {
     if (over || head >= heads) return false;
-    const long long unit_end = at + u.tiles;
-    long long end = unit_end;
-    if (x1 < unit_end) {
+    int end = u.tiles;
+    if (x1 < at + unit_cost(u.tiles)) {
       over = true;
       end = prefill_snap(line, x1, at, u.tiles);
-      if (end <= x) return false;
+      if (end <= tile) return false;
     }
     it->head = head;
     it->seq = u.seq;
@@ -173,17 +180,16 @@ struct PrefillWalk {
     it->pos0 = u.pos0;
     it->first = u.first;
     it->end = u.end;
-    it->tile = u.tile0 + (int)(x - at);
-    it->tiles = (int)(end - x);
+    it->tile = u.tile0 + tile;
+    it->tiles = end - tile;
     it->slot = -1;
     it->parts = 0;
-    if (x > at) {
+    if (tile > 0) {
       it->slot = 2 * c;
-    } else if (end < unit_end) {
+    } else if (end < u.tiles) {
       it->slot = 2 * c + 1;
       it->parts = prefill_parts(line, at, u.tiles, c);
     }
-    x = unit_end;
     if (!over) next_unit(unit);
     return true;
   }

@@ -56,7 +56,7 @@ int main() {
     }
     if (units.empty()) continue;
     sh.units = (int)units.size();
-    long long per_head = 0;
+    long long per_head = 0, tiles_per_head = 0;
     int covered = 0;
     for (const PrefillUnit& u : units) {
       need(u.tiles >= 1 && u.tokens >= 1 && u.tokens <= 2 * sh.per_tile, "unit sizes");
@@ -74,13 +74,14 @@ int main() {
         need(u.tile0 * (long long)kTile <= lo && hi < (u.tile0 + (long long)u.tiles) * kTile,
              "seen keys in the tiles");
       }
-      per_head += u.tiles;
+      per_head += unit_cost(u.tiles);
+      tiles_per_head += u.tiles;
     }
     need(covered == row0, "all tokens");
     const PrefillLine line = make_prefill_line(per_head, sh.units, heads, grid);
     need(line.n >= 1 && line.n <= grid && line.total == per_head * heads, "line");
     const bool brute = per_head * heads < 300000;
-    std::vector<char> done(brute ? line.total : 0, 0);
+    std::vector<char> done(brute ? tiles_per_head * heads : 0, 0);
     long long sum = 0;
     std::map<long long, std::vector<int>> slots;  // unit -> slots in order
     std::map<long long, int> expected;
@@ -103,7 +104,7 @@ int main() {
       while (w.next(unit, &it)) {
         // which unit: by its first token row
         int i = 0;
-        long long at = it.head * per_head;
+        long long at = it.head * tiles_per_head;
         while (units[i].tok0 != it.tok0) at += units[i++].tiles;
         const PrefillUnit& u = units[i];
         need(it.tiles >= 1 && it.tile >= u.tile0 && it.tile + it.tiles <= u.tile0 + u.tiles,
@@ -154,7 +155,7 @@ int main() {
           }
       }
     }
-    need(sum == line.total, "every tile");
+    need(sum == tiles_per_head * heads, "every tile");
     for (auto& s : slots) {
       need(expected.count(s.first) && (int)s.second.size() == expected[s.first], "part count");
       for (int p = 0; p < (int)s.second.size(); ++p)
