@@ -61,9 +61,11 @@ struct PrefillCfg {
   static_assert(kSmemBytes <= kPrefillMaxSmem, "shared memory budget");
   static constexpr uint32_t kTmemO = 256;
   // Registers a thread after the split of 512 x 128: softmax, copies, MMA and walk.
-  static constexpr uint32_t kRegsSoftmax = E4M3 ? 176 : 184;
-  static constexpr uint32_t kRegsCopy = E4M3 ? 96 : 80;
-  static constexpr uint32_t kRegsCtl = 64;
+  // (64 single tokens over 8000, bf16: 377 us with 184, 80 and 64, 362 with 192, 64 and 64, 389 with
+  // 200, 56 and 56; 192 columns: 300, 300 and 319 where 184, 72 and 72 take 295)
+  static constexpr uint32_t kRegsSoftmax = E4M3 ? 176 : DQK == 192 ? 184 : 192;
+  static constexpr uint32_t kRegsCopy = E4M3 ? 96 : DQK == 192 ? 72 : 64;
+  static constexpr uint32_t kRegsCtl = E4M3 ? 64 : DQK == 192 ? 72 : 64;
   static_assert(2 * kRegsSoftmax + kRegsCopy + kRegsCtl <= 512, "register split");
 };
 
