@@ -45,7 +45,8 @@ EXPORTED = ("attn_fwd", "attn_bwd_workspace_size", "attn_bwd", "attn_bwd_status"
             "attn_bwd_ex", "attn_debug_cache_stats", "attn_debug_set_bwd_variant",
             "attn_rope_rates", "attn_rope", "attn_cache_append", "attn_cache_status",
             "attn_decode", "attn_decode_workspace_size", "attn_decode_workspace_init",
-            "attn_fwd_grouped", "attn_bwd_grouped", "attn_prefill",
+            "attn_fwd_grouped", "attn_bwd_grouped", "attn_bwd_grouped_workspace_size",
+            "attn_prefill",
             "attn_prefill_workspace_size", "attn_norm_rope", "attn_norm_rope_bwd",
             "attn_norm_rope_bwd_workspace_size", "attn_cache_append_norm")
 BLOCK = 128  # rows per block of a block-sparse mask
@@ -171,6 +172,8 @@ def load():
         lib.attn_fwd_grouped.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, P, I, I, I, F, P, P,
                                          P]
         lib.attn_fwd_grouped.restype = I
+        lib.attn_bwd_grouped_workspace_size.argtypes = [I, I, I, I, I, I, I, I, I]
+        lib.attn_bwd_grouped_workspace_size.restype = SZ
         lib.attn_bwd_grouped.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, I, I,
                                          I, F, P, P, I, P, SZ, P]
         lib.attn_bwd_grouped.restype = I
@@ -302,6 +305,12 @@ def attn_fwd_grouped(q, k, v, o, lse, B, Hq, Hk, Tq, Tk, dqk, dv, rows, causal, 
                                    Tk, dqk, dv, _struct(rows), int(causal), _c_int(window_left),
                                    _c_int(window_right), float(scale), cq.ptr, ck.ptr,
                                    _stream(stream))
+
+
+def attn_bwd_grouped_workspace_size(B, Hq, Hk, Tq, Tk, dqk, dv, varlen=False,
+                                    deterministic=False) -> int:
+    return int(load().attn_bwd_grouped_workspace_size(B, Hq, Hk, Tq, Tk, dqk, dv, int(varlen),
+                                                      int(deterministic)))
 
 
 def attn_bwd_grouped(q, k, v, o, dO, lse, dq, dk, dv_out, B, Hq, Hk, Tq, Tk, dqk, dv, rows,
@@ -953,7 +962,7 @@ def _backward_grouped(q, k, v, o, dO, lse, causal, scale, cu_seqlens, determinis
     dq, dk, dvt = grads
     if q.numel() == 0:  # (tensors without elements have no address; no query sees a key)
         return dq, dk.zero_(), dvt.zero_()
-    need = attn_bwd_workspace_size(B, Hq, Tq, Tk, dqk, dv, cu_seqlens is not None, deterministic)
+    need = attn_bwd_grouped_workspace_size(*dims, cu_seqlens is not None, deterministic)
     if workspace is None or workspace.nbytes < need:
         workspace = _empty((max(need, 1),), torch.uint8, device)
     rc = attn_bwd_grouped(q, k, v, o, dO, lse, dq, dk, dvt, *dims, rows, causal, wl, wr, scale,

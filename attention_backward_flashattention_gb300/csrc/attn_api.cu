@@ -299,6 +299,20 @@ int qtiles_bound(int B, int Tq, bool varlen) {
 
 int cuda_err(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : ATTN_ERR_CUDA; }
 
+// Parts that the query heads of a key head are cut into in the backward: the fewest (a divisor of
+// the group) that make an item for each of 152 SMs, from sizes alone (a variable-length batch: at
+// most one ragged tile a sequence).  Without: 1170 us for T 4096, 16 and 1 heads, 164 for T 1024, 16
+// and 2; with, 191 and 46.  Two or three items for each SM: 73 to 103 us for 8 x 1024, 12 and 4 heads
+// of 64, 205 to 231 for 2 x 2048, 32 and 8 (the parts' traffic).
+constexpr int64_t kSplitItems = 152;
+int group_split(int B, int H, int Hk, int Tk, bool varlen) {
+  const int group = H / Hk;
+  const int64_t tiles = varlen ? cdiv(Tk, kTile) + (int64_t)B : (int64_t)B * cdiv(Tk, kTile);
+  for (int s = 1; s < group; ++s)
+    if (group % s == 0 && tiles * Hk * s >= kSplitItems) return s;
+  return group;
+}
+
 // Block-mask fields of the kernels' shape (mask may be null).  Returns
 // ATTN_OK or ATTN_ERR_INVALID_ARG.
 int set_block_mask(SeqShape* sh, const unsigned char* mask, int mask_batches, int mask_heads,
@@ -377,6 +391,7 @@ int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, i
   L.sh.H = H;
   L.sh.Hk = Hk;
   L.sh.group = H / Hk;
+  L.sh.split = 1;
   L.sh.varlen = varlen ? 1 : 0;
   L.sh.Tq = Tq;
   L.sh.Tk = Tk;
@@ -450,7 +465,8 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* o, const v
                                 (mask_heads != 1 && mask_heads != H)))
     return ATTN_ERR_INVALID_ARG;
   const bool varlen = cu_seqlens != nullptr;
-  if (workspace_bytes < attn_bwd_workspace_size(B, H, Tq, Tk, dqk, dv, varlen, deterministic))
+  if (workspace_bytes <
+      attn_bwd_grouped_workspace_size(B, H, Hk, Tq, Tk, dqk, dv, varlen, deterministic))
     return ATTN_ERR_WORKSPACE_TOO_SMALL;
 
   BwdLaunch L;
@@ -466,8 +482,11 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* o, const v
     return ATTN_ERR_CUDA;
   L.sh.nseq = B;
   L.sh.H = H;
-  L.sh.Hk = Hk;
-  L.sh.group = H / Hk;
+  const int split = group_split(B, H, Hk, Tk, varlen);
+  const int Hv = Hk * split;  // parts of key heads, which items are of
+  L.sh.Hk = Hv;
+  L.sh.group = H / Hv;
+  L.sh.split = split;
   L.sh.varlen = varlen ? 1 : 0;
   L.sh.Tq = Tq;
   L.sh.Tk = Tk;
@@ -477,11 +496,10 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* o, const v
   L.sh.band_off = varlen ? 0 : Tk - Tq;
   set_window(&L.sh, causal, window_left, window_right);
   L.sh.descending = deterministic ? 1 : 0;
-  // Grouped heads: few items, each as long as its group; longest first over all heads where
-  // Q, dO and the fp32 dQ of the call fit in L2 together, by head otherwise.
-  constexpr int64_t kBwdL2FitBytes = 64ll << 20;
-  L.sh.rank_major =
-      H != Hk && rows_q * H * (dqk + dv + 2ll * dqk) * 2 <= kBwdL2FitBytes ? 1 : 0;
+  // Grouped heads: few items, each as long as its group, so the longest of all heads go first
+  // (T 8192, 32 and 8 heads of 128: 1369 us by head, 1162 this way).  In deterministic mode an
+  // item then waits for the head's next one, which began at the same time (1848 and 2042 us).
+  L.sh.rank_major = H != Hk && !deterministic ? 1 : 0;
   rc = set_block_mask(&L.sh, block_mask, mask_batches, mask_heads, B, H, Tq, Tk, cu_seqlens,
                       cuk);
   if (rc) return rc;
@@ -500,14 +518,14 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* o, const v
   int n_qtiles;
   if (varlen) {
     int n_items = 0;
-    hc.tables(cu_seqlens, cuk, B, Hk, L.pair ? kBwdPairTable : kBwdTable, &tables, &n_items,
+    hc.tables(cu_seqlens, cuk, B, Hv, L.pair ? kBwdPairTable : kBwdTable, &tables, &n_items,
               &n_qtiles);
     L.sh.n_items = n_items;
     L.tables = &tables;
     L.lse_head_stride = Tq;
     L.lse_seq_stride = 0;
   } else {
-    L.sh.n_items = B * Hk * (L.pair ? cdiv(L.sh.nk_tiles, 2) : L.sh.nk_tiles);
+    L.sh.n_items = B * Hv * (L.pair ? cdiv(L.sh.nk_tiles, 2) : L.sh.nk_tiles);
     n_qtiles = B * L.sh.nq_tiles;
     L.tables = nullptr;
     L.lse_head_stride = Tq;
@@ -522,6 +540,10 @@ int bwd_impl(const void* q, const void* k, const void* v, const void* o, const v
   L.ws.nlse2 = reinterpret_cast<float*>(base + w.header + w.sem);
   L.ws.ndsum = reinterpret_cast<float*>(base + w.header + w.sem + w.stat);
   L.ws.dq_acc = reinterpret_cast<float*>(base + w.header + w.sem + 2 * w.stat);
+  if (split > 1) {
+    L.ws.dk_part = reinterpret_cast<float*>(base + w.total);
+    L.ws.dv_part = L.ws.dk_part + rows_k * Hv * dqk;
+  }
   L.o = o;
   L.dout = dO;
   L.lse = lse;
@@ -580,6 +602,16 @@ size_t attn_bwd_workspace_size(int B, int H, int Tq, int Tk, int dqk, int dv, in
   (void)Tk;
   if (B <= 0 || H <= 0 || Tq <= 0 || !supported_dims(dqk, dv)) return 0;
   return ws_sizes(qtiles_bound(B, Tq, varlen != 0), H, dqk).total;
+}
+
+size_t attn_bwd_grouped_workspace_size(int B, int Hq, int Hk, int Tq, int Tk, int dqk, int dv,
+                                       int varlen, int deterministic) {
+  const size_t own = attn_bwd_workspace_size(B, Hq, Tq, Tk, dqk, dv, varlen, deterministic);
+  if (own == 0 || Hk <= 0 || Hq % Hk != 0 || Tk <= 0) return 0;
+  const int split = group_split(B, Hq, Hk, Tk, varlen != 0);
+  if (split == 1) return own;
+  const int64_t rows = varlen ? Tk : (int64_t)B * Tk;
+  return own + (size_t)rows * Hk * split * (dqk + dv) * sizeof(float);
 }
 
 int attn_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H,

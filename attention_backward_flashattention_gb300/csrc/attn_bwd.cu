@@ -427,7 +427,9 @@ struct MainArgs {
 // it carry none of the mask's walks.  kGroup: several query heads share a key head
 // (sh.group > 1, never with a block mask): an item's walk takes the q-tiles of its
 // key head's first query head, then those of the next, as one sequence of steps, so
-// dK and dV are summed over the group in tensor memory and stored once.
+// dK and dV are summed over the group in tensor memory and stored once.  Where that
+// leaves too few items, a group is split into parts with items of their own, whose sums
+// go to the workspace as fp32 and are added, in order, by a launch of their own.
 template <int DQK, int DV, typename Tables, bool kMask, bool kGroup>
 __global__ void __launch_bounds__(kMainThreads, 1)
     attn_bwd_main_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -528,10 +530,11 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         mbar_arrive_expect_tx(kvb, C::kKBytes + C::kVBytes);
         kv_issued = true;
         kq = k;
+        const int khead = kGroup ? it.head / sh.split : it.head;
         for (int p = 0; p < C::kQPanels; ++p)
-          tma_load_3d(sK + p * kPanelBytes, &tm_k, kvb, p * 64, it.head, krow);
+          tma_load_3d(sK + p * kPanelBytes, &tm_k, kvb, p * 64, khead, krow);
         for (int p = 0; p < C::kVPanels; ++p)
-          tma_load_3d(sV + p * kPanelBytes, &tm_v, kvb, p * 64, it.head, krow);
+          tma_load_3d(sV + p * kPanelBytes, &tm_v, kvb, p * 64, khead, krow);
         const int nq = cdiv(it.Lq, kTile);
         const int i0 = first_qtile(sh, it, it.tile), i1 = last_qtile(sh, it, it.tile, nq) + 1;
         const uint8_t* col = mask_col<kMask>(sh, it);
@@ -1053,6 +1056,39 @@ __global__ void __launch_bounds__(kMainThreads, 1)
       const bool key_ok = kidx < it.Lk;
       const int krow = key_row0(sh, it) + kidx;
       const bool nothing = ifirst >= i1;  // no query sees this kv tile: zeros
+      if constexpr (kGroup) {
+        if (sh.split > 1) {  // (32 columns at a time, as below, fp32 and not yet scaled)
+          auto put = [&](uint32_t taddr, float* dst, int n) {
+#pragma unroll 1
+            for (int c = 0; c < n; c += 32) {
+              uint32_t v[32];
+              if (nothing) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = 0u;
+              } else {
+                tmem_ld32(taddr + c, v);
+                tmem_ld_wait();
+              }
+              if (!key_ok) continue;
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                st_global_v8(dst + c + e, v[e], v[e + 1], v[e + 2], v[e + 3], v[e + 4], v[e + 5],
+                             v[e + 6], v[e + 7]);
+            }
+          };
+          const int64_t place = (int64_t)krow * sh.Hk + it.head;
+          put(tmem + lane_base + C::kTmemdK, a.ws.dk_part + place * DQK, DQK);
+          put(tmem + lane_base + C::kTmemdV, a.ws.dv_part + place * DV, DV);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&bars->accv_free));
+            mbar_arrive(smem_u32(&bars->acck_free));
+            mbar_arrive(smem_u32(&bars->item_empty[slot]));
+          }
+          continue;
+        }
+      }
       auto dk_row = [&]() { return a.dk + (int64_t)krow * a.dk_row_stride + (int64_t)it.head * DQK; };
       auto dv_row = [&]() { return a.dv + (int64_t)krow * a.dv_row_stride + (int64_t)it.head * DV; };
       if constexpr (C::kSharedSdP) {
@@ -1155,6 +1191,42 @@ __global__ void __launch_bounds__(256)
   }
 }
 
+// ---------------------------------------------------------------------------
+// 4. split groups: dK = bf16(s * sum of the parts), dV = bf16(sum), eight columns a thread
+// ---------------------------------------------------------------------------
+struct PartSums {
+  const float* part[2];  // dK, dV
+  __nv_bfloat16* out[2];
+  int64_t row_stride[2];
+  int d[2];
+  float scale[2];
+  int heads, split;
+  int64_t n[2];          // threads' worth of columns
+};
+__global__ void __launch_bounds__(256) attn_bwd_sum_kernel(const PartSums P) {
+  int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int side = i < P.n[0] ? 0 : 1;
+  if (side) i -= P.n[0];
+  if (i >= P.n[side]) return;
+  const int d8 = P.d[side] / 8;
+  const int64_t rh = i / d8;  // key row and key head
+  const int c = (int)(i - rh * d8) * 8;
+  const int64_t row = rh / P.heads;
+  const int head = (int)(rh - row * P.heads);
+  const float* src = P.part[side] + rh * P.split * P.d[side] + c;
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < P.split; ++p) {
+    const float4 x = *reinterpret_cast<const float4*>(src + (int64_t)p * P.d[side]);
+    const float4 y = *reinterpret_cast<const float4*>(src + (int64_t)p * P.d[side] + 4);
+    s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w;
+    s[4] += y.x, s[5] += y.y, s[6] += y.z, s[7] += y.w;
+  }
+  const float k = P.scale[side];
+  *reinterpret_cast<uint4*>(P.out[side] + row * P.row_stride[side] + (int64_t)head * P.d[side] + c) =
+      make_uint4(pack_bf16(s[0] * k, s[1] * k), pack_bf16(s[2] * k, s[3] * k),
+                 pack_bf16(s[4] * k, s[5] * k), pack_bf16(s[6] * k, s[7] * k));
+}
+
 #ifdef ATTN_TRACE
 unsigned long long* g_trace_buf = nullptr;
 #endif
@@ -1204,7 +1276,7 @@ cudaError_t launch_all(const BwdLaunch& L, const Tables& tb) {
       e = launch_bwd_pair_main(L);
     } else {
       auto* k = L.sh.blk != nullptr ? attn_bwd_main_kernel<DQK, DV, Tables, true, false>
-                : L.sh.group > 1    ? attn_bwd_main_kernel<DQK, DV, Tables, false, true>
+                : L.sh.group > 1 || L.sh.split > 1 ? attn_bwd_main_kernel<DQK, DV, Tables, false, true>
                                     : attn_bwd_main_kernel<DQK, DV, Tables, false, false>;
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                C::kSmemBytes + kTraceSmem);
@@ -1235,6 +1307,27 @@ cudaError_t launch_all(const BwdLaunch& L, const Tables& tb) {
                            reinterpret_cast<__nv_bfloat16*>(L.dq), L.dq_row_stride, L.scale, L.sh, tb);
     if (e != cudaSuccess) return e;
     if (L.prof_aux[3] && (e = cudaEventRecord(L.prof_aux[3], L.stream)) != cudaSuccess) return e;
+  }
+  if (L.sh.split > 1) {
+    PartSums P;
+    const int64_t rows =
+        (int64_t)(L.sh.varlen ? L.tables->cuk[L.sh.nseq] : L.sh.nseq * L.sh.Tk) * (L.sh.Hk / L.sh.split);
+    P.part[0] = L.ws.dk_part;
+    P.part[1] = L.ws.dv_part;
+    P.out[0] = reinterpret_cast<__nv_bfloat16*>(L.dk);
+    P.out[1] = reinterpret_cast<__nv_bfloat16*>(L.dv);
+    P.row_stride[0] = L.dk_row_stride;
+    P.row_stride[1] = L.dv_row_stride;
+    P.d[0] = DQK;
+    P.d[1] = DV;
+    P.scale[0] = L.scale;
+    P.scale[1] = 1.0f;
+    P.heads = L.sh.Hk / L.sh.split;
+    P.split = L.sh.split;
+    P.n[0] = rows * (DQK / 8);
+    P.n[1] = rows * (DV / 8);
+    attn_bwd_sum_kernel<<<(unsigned)((P.n[0] + P.n[1] + 255) / 256), 256, 0, L.stream>>>(P);
+    return cudaGetLastError();
   }
   return cudaSuccess;
 }

@@ -63,8 +63,10 @@ struct NoTables {};
 struct SeqShape {
   int nseq;        // B (number of sequences)
   int H;           // query heads
-  int Hk;          // key heads (H unless heads are grouped)
+  int Hk;          // key heads (H unless heads are grouped).  Backward: times `split`
   int group;       // query heads that share a key head: H / Hk
+  int split;       // backward: parts that a key head's query heads are cut into (1: one), each
+                   // with items of its own (key head `head` of an Item counts parts)
   int varlen;      // 1: lengths come from VarlenTables
   int Tq, Tk;      // fixed-length sequence lengths (varlen: total token counts)
   int nq_tiles;    // fixed-length: ceil(Tq/128)

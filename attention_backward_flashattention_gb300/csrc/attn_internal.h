@@ -36,6 +36,7 @@ struct BwdWorkspace {
   float* nlse2;     // per (q-tile, head, row): -LSE * log2(e); -inf past the sequence end
   float* ndsum;     // per (q-tile, head, row): -D = -rowsum(dO * O); 0 past the end
   float* dq_acc;    // per (q-tile, head): [dqk/4][128][4] fp32 partial dQ
+  float *dk_part, *dv_part;  // split groups: [key row][part of a key head][dqk or dv] fp32
 };
 
 struct BwdLaunch {

@@ -215,8 +215,10 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
  * q, o, dO, dq (.., Hq, d), k, v, dk, dv (.., Hk, d), the heads of a row
  * adjacent, rows evenly spaced over the whole batch.  dk and dv are sums over
  * the group's query heads, accumulated in fp32 and rounded once.  LSE has Hq
- * heads.  Workspace: attn_bwd_workspace_size() with H = Hq.
- * No counterpart on the pages.
+ * heads.  No counterpart on the pages.
+ * Workspace: attn_bwd_grouped_workspace_size() bytes (0 for invalid sizes):
+ * that of attn_bwd for Hq heads, and, where there are few key tiles and heads,
+ * the fp32 sums of parts of the groups.
  *
  * attn_rows: elements between token rows, a multiple of 8 and at least H*d (0:
  * dense, H*d); the slices of one projection (T, (Hq + 2 Hk) * d) have its
@@ -229,6 +231,8 @@ int attn_fwd_grouped(const void* q, const void* k, const void* v, void* o, float
                      int Hq, int Hk, int Tq, int Tk, int dqk, int dv, const attn_rows* rows,
                      int causal, int window_left, int window_right, float scale,
                      const int* cu_seqlens_q, const int* cu_seqlens_k, void* stream);
+size_t attn_bwd_grouped_workspace_size(int B, int Hq, int Hk, int Tq, int Tk, int dqk, int dv,
+                                       int varlen, int deterministic);
 int attn_bwd_grouped(const void* q, const void* k, const void* v, const void* o, const void* dO,
                      const float* lse, void* dq, void* dk, void* dv_out, int B, int Hq, int Hk,
                      int Tq, int Tk, int dqk, int dv, const attn_rows* rows, int causal,

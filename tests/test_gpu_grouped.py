@@ -79,7 +79,26 @@ CASES = [
     ([384, 384], 4, 4, (128, 128), True, True, None),
     ([1000], 32, 8, (128, 128), True, True, (200, 0)),
     ([260, 129], 6, 3, (192, 128), False, True, None),
+    # (the backward gives groups of few key tiles in parts; these keep them whole, or in two parts)
+    ([130] * 20, 8, 4, (64, 64), True, True, None),
+    ([70 + 9 * i for i in range(40)], 6, 2, (128, 128), False, True, (100, 0)),
+    ([640] * 16, 4, 1, (128, 128), True, True, None),
+    ([333] * 14, 8, 4, (192, 128), False, False, None),
+    ([200] * 20, 4, 2, (192, 128), False, True, None),
 ]
+
+
+def test_parts_of_the_cases():
+    """The cases above have groups whole, in several parts of several heads, and of one each."""
+    kinds = set()
+    for lens, hq, hk, (dqk, dv), fixed, _, _ in CASES:
+        B, T = len(lens), lens[0] if fixed else sum(lens)
+        need = binding.attn_bwd_grouped_workspace_size(B, hq, hk, T, T, dqk, dv, not fixed)
+        own = binding.attn_bwd_workspace_size(B, hq, T, T, dqk, dv, not fixed)
+        parts = (need - own) // ((B * T if fixed else T) * hk * (dqk + dv) * 4)
+        if hq > hk:
+            kinds.add("whole" if parts == 0 else "each" if parts == hq // hk else "several")
+    assert kinds == {"whole", "each", "several"}
 
 
 @pytest.mark.parametrize("packed", [False, True])
