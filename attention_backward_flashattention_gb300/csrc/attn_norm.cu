@@ -20,6 +20,9 @@ namespace attn {
 namespace {
 
 constexpr int kNormThreads = 256;
+// Heads of a group in a chunk, where there are enough (16384 tokens, 32 + 8 heads of 128, forward and
+// backward: 60.7 and 107 us with 4, 57.3 and 104 with 8, 56.9 and 103 with 16).
+constexpr int kNormRounds = 16;
 
 // Lanes of a head, and whether they are all used.
 template <int D>
@@ -79,7 +82,7 @@ struct NormParams {
   Rotation rot;
   float eps;
   int nseq, pos0;
-  int tokens;      // token rows of a chunk
+  int tokens[2];   // token rows of a chunk, by tensor
   int blocks[2];   // of each tensor; a block takes a chunk, and then the one `blocks` behind it
 };
 
@@ -110,10 +113,11 @@ norm_kernel(const __grid_constant__ NormParams P, const __grid_constant__ Offset
   }
   const int dt = L::kGroups / X.H, dh = L::kGroups - dt * X.H;  // from one head to the next
 
-  for (int64_t first = (int64_t)block * P.tokens; first < X.rows;
-       first += (int64_t)P.blocks[which] * P.tokens) {
+  const int per_chunk = P.tokens[which];
+  for (int64_t first = (int64_t)block * per_chunk; first < X.rows;
+       first += (int64_t)P.blocks[which] * per_chunk) {
     const int row0 = (int)first;
-    const int tokens = min(P.tokens, X.rows - row0);
+    const int tokens = min(per_chunk, X.rows - row0);
     if (threadIdx.x < tokens) {
       const int r = row0 + threadIdx.x;
       if constexpr (sizeof(Offsets) > sizeof(RowOffsets)) {
@@ -228,28 +232,49 @@ norm_kernel(const __grid_constant__ NormParams P, const __grid_constant__ Offset
   }
 }
 
-// The weights' gradients from the blocks' rows of sums: 32 columns of one tensor a block.
+// The weights' gradients from the blocks' rows of sums: a cluster of eight blocks takes 32 columns of
+// one tensor, each block an eighth of the rows, whose sums meet in the first one, in order (one
+// block of each 32 columns took 17 us of 103).
 struct NormSums {
   const float* rows[2];
   float* dw[2];
   int blocks[2];
+  int d;
 };
-__global__ void __launch_bounds__(1024) norm_sums_kernel(const NormSums P, const int d) {
-  __shared__ float part[32][33];
-  const int per = d / 32, which = blockIdx.x / per;
-  if (P.dw[which] == nullptr) return;
+constexpr int kSumSlices = 8, kSumThreads = 512;
+__global__ void __cluster_dims__(kSumSlices, 1, 1) __launch_bounds__(kSumThreads)
+norm_sums_kernel(const NormSums P) {
+  __shared__ float part[kSumThreads / 32][32];
+  __shared__ float met[kSumSlices][32];
+  const int per = P.d / 32, which = blockIdx.y / per, slice = blockIdx.x;
   const int lane = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const int c = (blockIdx.x - which * per) * 32 + lane;
-  const float* rows = P.rows[which];
+  const int c = (blockIdx.y - which * per) * 32 + lane;
+  // (every thread: this kernel may not end in front of the one that it is launched behind)
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float s = 0.f;
+  if (P.dw[which] != nullptr) {
+    const float* rows = P.rows[which];
+    const int n = P.blocks[which], each = (n + kSumSlices - 1) / kSumSlices;
+    const int end = min(n, (slice + 1) * each);
 #pragma unroll 8
-  for (int i = y; i < P.blocks[which]; i += 32) s += __ldg(rows + (int64_t)i * d + c);
+    for (int i = slice * each + y; i < end; i += kSumThreads / 32) s += rows[(int64_t)i * P.d + c];
+  }
   part[y][lane] = s;
   __syncthreads();
   if (y == 0) {
     s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s += part[i][lane];
+    for (int i = 0; i < kSumThreads / 32; ++i) s += part[i][lane];
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(
+                     mapa_shared(smem_u32(&met[slice][lane]), 0)),
+                 "f"(s)
+                 : "memory");
+  }
+  cluster_sync();
+  if (slice == 0 && y == 0 && P.dw[which] != nullptr) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kSumSlices; ++i) s += met[i][lane];
     P.dw[which][c] = s;
   }
 }
@@ -423,26 +448,22 @@ template <int D, bool GRAD>
 cudaError_t norm_typed(const NormLaunch& L) {
   NormParams P;
   std::memset(&P, 0, sizeof(P));
-  // Token rows of a chunk: as many as the angles' memory holds, fewer where that left SMs without
-  // a block.
-  int64_t all = 0;
-  int most_heads = 1;
-  for (const NormTensor& t : L.t) {
-    all += (int64_t)t.rows * t.H;
-    if (t.rows > 0) most_heads = std::max(most_heads, t.H);
-  }
-  const int per_block = 8 * HeadLanes<D>::kGroups;  // heads, where there are many
-  int tokens = std::max(1, per_block / most_heads);
-  while (tokens > 1 && all / ((int64_t)tokens * most_heads) < 8ll * L.num_sms) tokens /= 2;
-  P.tokens = std::min(tokens, most_tokens(L.rot.dim));
+  // Token rows of a chunk: about kNormRounds heads a group, as far as the angles' memory goes,
+  // fewer where that left SMs without a block.
   int blocks = 0;
   for (int i = 0; i < 2; ++i) {
-    P.t[i] = L.t[i];
-    int n = cdiv(L.t[i].rows, P.tokens);
-    if (GRAD) n = std::min(n, i == 0 || L.t[0].rows == 0 ? kMaxNormBlocks : kMaxNormBlocks / 2);
-    P.blocks[i] = n;
-    if (GRAD && L.t[i].dw != nullptr) P.t[i].dw = L.workspace + (int64_t)i * kMaxNormBlocks * D;
-    blocks += n;
+    const NormTensor& t = L.t[i];
+    P.t[i] = t;
+    P.tokens[i] = 1;
+    if (t.rows == 0) continue;
+    int tokens = std::max(1, kNormRounds * HeadLanes<D>::kGroups / t.H);
+    tokens = std::min(tokens, most_tokens(L.rot.dim));
+    while (tokens > 1 && cdiv(t.rows, tokens) < 4 * L.num_sms) tokens /= 2;
+    P.tokens[i] = tokens;
+    P.blocks[i] = cdiv(t.rows, tokens);
+    if (GRAD) P.blocks[i] = std::min(P.blocks[i], kMaxNormBlocks);
+    if (GRAD && t.dw != nullptr) P.t[i].dw = L.workspace + (int64_t)i * kMaxNormBlocks * D;
+    blocks += P.blocks[i];
   }
   P.rot = L.rot;
   P.eps = L.eps;
@@ -465,8 +486,18 @@ cudaError_t norm_typed(const NormLaunch& L) {
     S.dw[i] = L.t[i].dw;
     S.blocks[i] = P.blocks[i];
   }
-  norm_sums_kernel<<<2 * (D / 32), 1024, 0, L.stream>>>(S, D);
-  return cudaGetLastError();
+  S.d = D;
+  // on its way while the main kernel runs; it waits for that one's end before it reads
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kSumSlices, 2 * (D / 32));
+  cfg.blockDim = dim3(kSumThreads);
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_sums_kernel, S);
 }
 
 template <int DQK, int DV, bool E4M3>
