@@ -12,10 +12,11 @@
 //                   each.  Tiles whose keys every row sees come by TMA, in boxes of rows that lie
 //                   in one page; the others, and pages that no box divides, row by row, where rows
 //                   that nothing sees, and values that are not finite, become zeros on the way.
-//                   e4m3 boxes land in a ring of their own, and the warp widens them
+//                   e4m3 boxes land in a ring of their own, and the warps widen them
 //   warp 12         MMA issuer: S_w = Q_w K^T, O_w += P_w V (tcgen05, accumulators in TMEM, P
 //                   in TMEM as the A operand)
 //   warp 13         walks over the share's units, loads their queries by TMA
+//   warp 14         e4m3: loads the ring
 // A unit has two query tiles, or one whose key tiles the warpgroups take in turn (each with
 // its own O, joined in tensor memory at the end): with few rows the chain S -> softmax -> PV of
 // one tile runs beside the other's.  Parts of a unit that is cut leave unnormalised sums in the
@@ -35,7 +36,7 @@ namespace attn {
 namespace {
 
 constexpr int kPrefillThreads = 512;
-constexpr int kCopyWarp = 8, kPrefillMmaWarp = 12, kWalkWarp = 13;
+constexpr int kCopyWarp = 8, kPrefillMmaWarp = 12, kWalkWarp = 13, kRingWarp = 14;
 constexpr int kPrefillPanel = kTile * 128;  // [128 rows][64] bf16
 constexpr int kPrefillMaxSmem = 232448;
 constexpr int kKeyRing = 8;  // key tiles whose bits are kept (more than are under way)
@@ -75,7 +76,8 @@ struct PrefillBars {
   uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t twin_full, twin_done;
-  uint64_t raw_full[2][4][4];    // [keys, values][slot][copy warp]
+  uint64_t raw_full[2][4], raw_empty[2][4];  // [keys, values][slot]
+  int raw_there[2][4];           // whether a slot holds its tile's rows (else they come by rows)
   uint64_t spare_free;           // a single tile's unit is done with the second query tile's place
   uint64_t drain;
   PrefillItem item[2];
@@ -316,7 +318,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     bars->abort_flag = 0;
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&bars->item_full[k]), 1);
-      mbar_init(smem_u32(&bars->item_empty[k]), 1 + 8 + 4);  // MMA, softmax warps, copy warps
+      // MMA, softmax warps, copy warps, ring
+      mbar_init(smem_u32(&bars->item_empty[k]), 1 + 8 + 4 + (E4M3 ? 1 : 0));
       mbar_init(smem_u32(&bars->s_full[k]), 1);
       mbar_init(smem_u32(&bars->p_full[k]), 4);
       mbar_init(smem_u32(&bars->o_done[k]), 1);
@@ -334,7 +337,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     mbar_init(smem_u32(&bars->twin_full), 8);
     mbar_init(smem_u32(&bars->twin_done), 8);
     mbar_init(smem_u32(&bars->spare_free), 4);
-    for (int i = 0; i < 2 * 4 * 4; ++i) mbar_init(smem_u32(&bars->raw_full[0][0][0] + i), 1);
+    for (int i = 0; i < 2 * 4; ++i) {
+      mbar_init(smem_u32(&bars->raw_full[0][0] + i), 1);
+      mbar_init(smem_u32(&bars->raw_empty[0][0] + i), 4);
+    }
     mbar_init(smem_u32(&bars->drain), 1);
     fence_barrier_init();
   }
@@ -367,6 +373,18 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     fence_proxy_async_smem();
   }
   __syncthreads();
+
+  // e4m3: the ring's slot `slot` of keys or values; slots of a unit: one more than the ring has, in
+  // the second query tile's place, where it has none and the unit in front of it, whose products may
+  // still read it, had none either
+  constexpr int kRaw = C::kRaw > 0 ? C::kRaw : 1;
+  [[maybe_unused]] auto raw_at = [&](int side, uint32_t slot) -> uint32_t {
+    if (C::kSpareQ && slot == C::kRaw) return sQ + C::kQTile + (side ? kTile * DQK : 0);
+    return sQ + (side ? C::kOffRawV + slot * kTile * DV : C::kOffRawK + slot * kTile * DQK);
+  };
+  [[maybe_unused]] auto slots_of = [&](bool twin, bool was_pair) -> uint32_t {
+    return kRaw + (C::kSpareQ && twin && !was_pair ? 1 : 0);
+  };
 
   if (warp >= kPrefillMmaWarp) {
     regs_dec<C::kRegsCtl>();
@@ -484,6 +502,68 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         mma_commit(smem_u32(&bars->drain));
         mbar_wait_drain(smem_u32(&bars->drain), 0);
       }
+    } else if (E4M3 && warp == kRingWarp) {
+      // ------------------------------------------------------------ e4m3: tiles to the ring
+      uint32_t parity = 0, loads = 0;  // by slot (bit 4 side + slot); slots that were loaded
+      bool ok = true, was_pair = false;
+      const int box = max(P.box, 8);
+      for (uint32_t n = 0;; ++n) {
+        if (!(ok = mbar_wait_warp(smem_u32(&bars->item_full[n & 1]), (n >> 1) & 1, ab))) break;
+        const PrefillItem& item = bars->item[n & 1];
+        const int khead = item.head;
+        if (khead < 0) break;
+        const int* table = P.cache.table + item.seq * P.cache.table_stride;
+        const int tile0 = item.tile, tiles = item.tiles;
+        // (as the copy warps have it)
+        const int right = min(item.pos0, item.end - 1);
+        const int left = sh.window >= 0 ? item.pos0 + item.tokens - 1 - sh.window : 0;
+        const bool twin = item.tokens <= sh.per_tile;
+        const uint32_t slots = slots_of(twin, was_pair);
+        was_pair = !twin;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
+        // lane l has box l of a tile; its page is looked up a tile ahead
+        const bool mine = P.box > 0 && lane < kTile / box;
+        auto key_of = [&](int t) { return (tile0 + t) * kTile + lane * box; };
+        auto look_up = [&](int t) -> int {
+          const int key0 = (tile0 + t) * kTile;
+          if (!mine || t >= tiles || key0 + kTile - 1 > right || key0 < left) return -1;
+          return __ldg(table + div_page(P.cache, key_of(t)));
+        };
+        int next = look_up(0);
+        for (int t = 0; t < tiles && ok; ++t) {
+          const int page = next;
+          next = look_up(t + 1);
+          const bool there = __all_sync(0xffffffffu, !mine || page_in(P.cache, page)) && P.box > 0;
+          const uint32_t slot = t % slots;
+          const int key = key_of(t), in = key - div_page(P.cache, key) * P.cache.page_size;
+#pragma unroll 1
+          for (int side = 0; side < 2; ++side) {
+            const uint32_t bit = 1u << (side * 4 + slot);
+            if (!(ok = mbar_wait_warp(smem_u32(&bars->raw_empty[side][slot]), (parity & bit) == 0,
+                                      ab)))
+              break;
+            parity ^= bit;
+            loads |= bit;
+            const uint32_t bar = smem_u32(&bars->raw_full[side][slot]);
+            if (lane == 0) {
+              bars->raw_there[side][slot] = there ? 1 : 0;
+              if (there) mbar_arrive_expect_tx(bar, kTile * (side ? DV : DQK));
+              else mbar_arrive(bar);
+            }
+            __syncwarp();
+            if (there && mine)
+              tma_load_page(raw_at(side, slot) + lane * box * (side ? DV : DQK),
+                            side ? &tm_v : &tm_k, bar, 0, khead, in, page, P.heads_inner);
+          }
+        }
+        if (!ok) break;
+      }
+      // (let every copy already issued land before the CTA's memory is released)
+      if (!ok && lane == 0)
+        for (int i = 0; i < 8; ++i)
+          if (loads >> i & 1u)
+            mbar_wait_drain(smem_u32(&bars->raw_full[i >> 2][i & 3]), (parity >> i & 1u) ^ 1u);
     }
   } else if (warp >= kCopyWarp) {
     if constexpr (C::kRegsCopy < 128) regs_dec<C::kRegsCopy>();
@@ -498,15 +578,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     constexpr int kAhead = C::kKStages + C::kVStages - 1;
     static_assert(kAhead < 32, "a bit each");
     uint32_t issued = 0, told = 0, by_rows = 0;
-    // e4m3: slots of the ring (bit 4 side + slot) that are on their way, and their barriers' parity
-    constexpr int kRaw = C::kRaw > 0 ? C::kRaw : 1;
-    [[maybe_unused]] uint32_t raw_on = 0, raw_parity = 0;
-    auto raw_at = [&](int side, uint32_t slot) -> uint32_t {  // this warp's rows there
-      if (C::kSpareQ && slot == C::kRaw)
-        return sQ + C::kQTile + (side ? kTile * DQK + mw * 32 * DV : mw * 32 * DQK);
-      return sQ + (side ? C::kOffRawV + slot * kTile * DV + mw * 32 * DV
-                        : C::kOffRawK + slot * kTile * DQK + mw * 32 * DQK);
-    };
+    // e4m3: parity of the ring's slots (bit 4 side + slot)
+    [[maybe_unused]] uint32_t raw_parity = 0;
     [[maybe_unused]] bool was_pair = false;
     auto tell = [&](uint32_t upto) {
       fence_proxy_async_smem();
@@ -540,10 +613,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       // some row does not see
       const int right = min(item.pos0, end - 1);
       const int left = sh.window >= 0 ? item.pos0 + item.tokens - 1 - sh.window : 0;
-      // slots of the ring: one more, in the second query tile's place, where this unit has none and
-      // the one in front of it, whose products may still read it, had none either
       const bool twin = item.tokens <= sh.per_tile;
-      [[maybe_unused]] const int slots = kRaw + (C::kSpareQ && twin && !was_pair ? 1 : 0);
+      [[maybe_unused]] const uint32_t slots = slots_of(twin, was_pair);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
       auto edge = [&](int t) {
@@ -556,53 +627,27 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         return t < tiles && key >= first && key < end ? __ldg(table + div_page(P.cache, key)) : -1;
       };
       // this lane's box of a tile, if the lane leads one, in the page that it has found
-      auto load_box = [&](int side, int t, int page, uint32_t dst, uint32_t bar) {
+      [[maybe_unused]] auto load_box = [&](int side, int t, int page, uint32_t dst, uint32_t bar) {
         const int key = (tile0 + t) * kTile + mw * 32 + lane;
         const int in = key - div_page(P.cache, key) * P.cache.page_size;
-        const CUtensorMap* map = side ? &tm_v : &tm_k;
-        if constexpr (E4M3) {
-          tma_load_page(dst + lane * (side ? DV : DQK), map, bar, 0, khead, in, page,
-                        P.heads_inner);
-        } else {
-          for (int p = 0; p < (side ? DV : DQK) / 64; ++p)
-            tma_load_page(dst + p * kPrefillPanel + (mw * 32 + lane) * 128, map, bar, p * 64, khead,
-                          in, page, P.heads_inner);
-        }
+        for (int p = 0; p < (side ? DV : DQK) / 64; ++p)
+          tma_load_page(dst + p * kPrefillPanel + (mw * 32 + lane) * 128, side ? &tm_v : &tm_k, bar,
+                        p * 64, khead, in, page, P.heads_inner);
       };
-      // e4m3: this warp's rows of tile t on their way to the ring, where all are there and every
-      // query sees them
-      [[maybe_unused]] auto load_raw = [&](int side, int t, int page) {
-        if constexpr (E4M3) {
-          if (P.box == 0 || t >= tiles || edge(t)) return;
-          if (__ballot_sync(0xffffffffu, page_in(P.cache, page)) != ~0u) return;
-          const uint32_t slot = t % slots, bar = smem_u32(&bars->raw_full[side][slot][mw]);
-          __syncwarp();  // (what every lane has read there is behind it)
-          if (lane == 0) mbar_arrive_expect_tx(bar, 32 * (side ? DV : DQK));
-          __syncwarp();
-          if (leader) load_box(side, t, page, raw_at(side, slot), bar);
-          raw_on |= 1u << (side * 4 + slot);
-        }
-      };
-      int page = look_up(0);
-      int page_far = -1;  // of the tile that goes to the ring next
-      if constexpr (E4M3) {
-        for (int t = 0; t < slots; ++t) {
-          const int p = t == 0 ? page : look_up(t);
-          load_raw(0, t, p);
-          load_raw(1, t, p);
-        }
-        page_far = look_up(slots);
-      }
+      int page = E4M3 ? -1 : look_up(0);
       for (int t = 0; t < tiles && ok; ++t, ++step) {
-        // all 32 rows by TMA (a page that is not in the cache: by rows, as zeros); those that go
-        // through the ring are on their way
         const bool is_edge = edge(t);
-        const uint32_t on = E4M3 ? 0x11u << (t % slots) : 0u;
-        const bool in_ring = E4M3 && (raw_on & on) == on;
-        const int here = page;
+        bool ring = false;
+        const uint32_t slot = E4M3 ? t % slots : 0;
+        if constexpr (E4M3) {  // (the values' slot says the same)
+          if (!(ok = wait(bars->raw_full[0][slot], raw_parity >> slot & 1u))) break;
+          ring = *static_cast<volatile int*>(&bars->raw_there[0][slot]) != 0;
+          if (!ring) page = look_up(t);
+        }
         uint32_t bits = ~0u;
         long long ko = -1, vo = -1;  // (-1: zeros)
-        if (!in_ring) {
+        const int here = page;
+        if (!ring) {
           const int key = (tile0 + t) * kTile + mw * 32 + lane;
           const bool seen = key >= first && key < end;
           const bool there = seen && page_in(P.cache, page);
@@ -611,7 +656,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           if (there) ko = token_at(P.cache.k, page, in), vo = token_at(P.cache.v, page, in);
           bits = __ballot_sync(0xffffffffu, there);
         }
-        page = E4M3 && slots == 1 ? page_far : look_up(t + 1);
+        if constexpr (!E4M3) page = look_up(t + 1);
+        // all 32 rows by TMA (a page that is not in the cache: by rows, as zeros)
         const bool boxes = !E4M3 && P.box > 0 && !is_edge && bits == ~0u;
 #pragma unroll 1
         for (int side = 0; side < 2; ++side) {
@@ -645,18 +691,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
               if (d == 192) copy_rows<8, 16>(dst, mw, lane, base, o);
             }
           } else {
-            const uint32_t slot = t % slots, bit = 1u << (side * 4 + slot);
-            const bool ring = in_ring;
-            if (ring) {
-              if (!(ok = mbar_wait_warp(smem_u32(&bars->raw_full[side][slot][mw]),
-                                        (raw_parity & bit) != 0, ab)))
-                break;
-              raw_on ^= bit;
-              raw_parity ^= bit;
-            }
-            const uint32_t raw = raw_at(side, slot);
+            if (side == 1 && !(ok = wait(bars->raw_full[1][slot], raw_parity >> (4 + slot) & 1u)))
+              break;
+            raw_parity ^= 1u << (side * 4 + slot);
+            const uint32_t raw = raw_at(side, slot) + mw * 32 * d;
             auto nothing = [] {};
-            auto next = [&] { load_raw(side, t + slots, page_far); };
+            auto next = [&] {  // (the slot's rows have been read)
+              if (lane == 0) mbar_arrive(smem_u32(&bars->raw_empty[side][slot]));
+            };
             if constexpr (DQK == 64) {
               widen_rows<4, 0, 64>(dst, mw, lane, ring, raw, base, o, next);
             } else if (DQK == 128 || d == 128) {
@@ -713,7 +755,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
             tell(issued - kAhead);
           }
         }
-        if constexpr (E4M3) page_far = look_up(t + 1 + slots);
       }
       if constexpr (C::kSpareQ) {
         if (ok && twin) {
@@ -732,10 +773,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         mbar_wait_drain(smem_u32(&bars->k_full[s % C::kKStages]), (s / C::kKStages) & 1);
       for (uint32_t s = step + 1 > C::kVStages ? step + 1 - C::kVStages : 0; s <= step; ++s)
         mbar_wait_drain(smem_u32(&bars->v_full[s % C::kVStages]), (s / C::kVStages) & 1);
-      for (uint32_t b = raw_on; b != 0; b &= b - 1) {
-        const int i = __ffs(b) - 1;
-        mbar_wait_drain(smem_u32(&bars->raw_full[i >> 2][i & 3][mw]), raw_parity >> i & 1);
-      }
     }
   } else {
     regs_inc<C::kRegsSoftmax>();
