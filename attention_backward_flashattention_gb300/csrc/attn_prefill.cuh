@@ -61,6 +61,11 @@ struct PrefillCfg {
   static constexpr int kSmemBytes = kOffBar + 3072;
   static_assert(kSmemBytes <= kPrefillMaxSmem, "shared memory budget");
   static constexpr uint32_t kTmemO = 256;
+  // Whether a step's products of P and V go in front of the wait for the next step's keys, or
+  // behind.  In front where keys come late (192 columns: 295 to 270 us for 2048 tokens over 8000;
+  // e4m3: 598 to 563 us for 64 single tokens over 8000); elsewhere the shorter code is faster
+  // (128 columns: 957 and 1008 us for 2048 over 30011).
+  static constexpr bool kLateKeys = E4M3 || DQK == 192;
   // Registers a thread after the split of 512 x 128: softmax, copies, MMA and walk.
   // (64 single tokens over 8000, bf16: 377 us with 184, 80 and 64, 362 with 192, 64 and 64, 389 with
   // 200, 56 and 56; 192 columns: 300, 300 and 319 where 184, 72 and 72 take 295)
@@ -456,7 +461,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         for (int t = -1; t < tiles; ++t, ++step) {
           // (`step` is that of t + 1)
           const bool next = t + 1 < tiles;
-          if (next && !(ok = W(bars->k_full[step % C::kKStages], (step / C::kKStages) & 1))) break;
+          [[maybe_unused]] bool k_here = false;
+          if constexpr (!C::kLateKeys)
+            if (next && !(ok = W(bars->k_full[step % C::kKStages], (step / C::kKStages) & 1)))
+              break;
           const uint32_t sv = (step - 1) % C::kVStages;
           if (t >= 0 && !(ok = W(bars->v_full[sv], ((step - 1) / C::kVStages) & 1))) break;
           int w = tile_used(use, 0, t) && !tile_used(use, 1, t) ? 1 : 0;
@@ -479,6 +487,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
               if (t == hi) mma_commit(smem_u32(&bars->o_done[w]));
             }
             if (used(t + 1)) {
+              if constexpr (C::kLateKeys) {
+                if (!k_here &&
+                    !(ok = W(bars->k_full[step % C::kKStages], (step / C::kKStages) & 1)))
+                  break;
+                k_here = true;
+              }
               const uint64_t q = bQ + (uint64_t)((use.twin ? 0 : w) * (C::kQTile >> 4));
               const uint64_t k = bK + (uint64_t)((step % C::kKStages) * (C::kKBytes >> 4));
 #pragma unroll
@@ -749,7 +763,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           by_rows |= 1u << (issued & 31);
           ++issued;
           if (E4M3) {
-            if (side == 1) tell(issued);  // (the tile's keys too, unless the values had to wait)
+            tell(issued);
           } else if (issued - told > kAhead) {
             cp_wait<kAhead>();
             tell(issued - kAhead);

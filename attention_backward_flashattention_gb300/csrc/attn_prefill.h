@@ -73,7 +73,10 @@ __host__ __device__ inline PrefillUnit make_prefill_unit(const PrefillShape& sh,
 // takes an equal share of it: the work is split over the keys as far as it has to be for every
 // SM to have some, whatever the lengths are, which only the device knows.  A cut within `tol`
 // tiles of a unit's end is moved there.  Cuts depend on the lengths alone.
-constexpr int kPrefillMinCost = 5;   // of a share, where there are more CTAs than units
+// Cost of a share at least, where there are more CTAs than units.  Measured, us, with 2, 3, 4, 6, 12:
+// 1 token over 1000, 8 key heads: 18.6, 18.4, 19.4, 19.8, 23.9; 64 tokens over 2000, 2 key heads of
+// 8: 28.5, 29.8, 31.8, 40.0, 47.1; 512 tokens over none: 24.6, 25.2, 24.5, 36.5, 22.1.
+constexpr int kPrefillMinCost = 3;
 constexpr int kPrefillTol = 4;       // a unit's parts cost about as much as two tiles
 constexpr int kPrefillUnitCost = 4;  // of a unit besides its tiles (8192 tokens of a prompt: 770 us
                                      // with 0, 658 with 2, 580 with 4, 590 with 6)
@@ -91,7 +94,7 @@ __host__ __device__ inline PrefillLine make_prefill_line(long long cost_per_head
   if (n < (long long)units * heads) n = (long long)units * heads;
   l.n = n < grid ? (int)n : grid;  // (at most total)
   const long long share = l.total / l.n;
-  l.tol = share / 6 < kPrefillTol ? (int)(share / 6) : kPrefillTol;
+  l.tol = share / 4 < 1 ? 1 : share / 4 < kPrefillTol ? (int)(share / 4) : kPrefillTol;
   return l;
 }
 __host__ __device__ inline long long prefill_cut(const PrefillLine& l, int c) {
