@@ -430,13 +430,8 @@ int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, i
   L.scale_log2 = scale * kLog2e;
   L.status = fwd_status_ptr();
   if (!L.status) return ATTN_ERR_CUDA;
-  // work-item counters of its own (the previous kernel on them left them at zero)
-  static std::atomic<unsigned> next_claim{0};
-  L.claim = fwd_claim_ptr((int)(next_claim.fetch_add(1) % kFwdClaimSlots));
-  if (!L.claim) return ATTN_ERR_CUDA;
-  const int sms = num_sms_current();
-  if (sms <= 0) return ATTN_ERR_CUDA;
-  L.grid = std::min(L.sh.n_items, sms);
+  // a CTA an item: the first ones on the SMs take over those that have not started
+  L.grid = L.sh.n_items;
   L.stream = static_cast<cudaStream_t>(stream);
   return cuda_err(launch_fwd(L, dqk, dv));
 }

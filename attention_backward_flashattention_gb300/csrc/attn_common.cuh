@@ -15,11 +15,11 @@
 // §3.2 "确定性执行实现": CTA order swizzled over heads/batches for L2 reuse,
 // longest-processing-time-first over batches, and shortest-first over causal
 // kv-tiles for the deterministic dQ reduction):
-//   forward   item = (sequence, head, 256-row unit m: two q-tiles), claimed
-//             dynamically (a per-call counter): all units of one (sequence,
+//   forward   item = (sequence, head, 256-row unit m: two q-tiles), taken as CTAs
+//             get done (cluster launch control): all units of one (sequence,
 //             head) are consecutive, the longest causal row range first (m
 //             descending), so one head's K and V stay in L2 while ~one SM count
-//             of its units run, and the last items claimed are the shortest.
+//             of its units run, and the last items taken are the shortest.
 //             When every head's K and V fit in L2 together (fixed length), the
 //             units go rank-major instead (longest of every head first), which
 //             balances better when each CTA gets only a few items.

@@ -10,13 +10,15 @@
 // division by the row sum happens once, after the loop).
 //
 // One CTA (384 threads) per SM, persistent over work items; an item is two
-// consecutive 128-row Q tiles of one (sequence, head).  The producer claims
-// items from a per-call counter (head-major, longest first within a head; see
+// consecutive 128-row Q tiles of one (sequence, head).  There is a CTA for each
+// item; the producer of a running one takes over CTAs that have not started
+// (cluster launch control; head-major, longest first within a head; see
 // attn_common.cuh) and hands each to the other roles through a 2-slot ring, so
-// the CTAs running at any moment share a few heads' K and V in L2:
+// the CTAs running at any moment share a few heads' K and V in L2.  No call
+// shares anything with another, captured or not:
 //   warps 0-3, 4-7  softmax warpgroup w owns Q tile w: thread r holds query
 //                   row r (TMEM lane r)
-//   warp 8          TMA producer and work claimer: the two Q tiles once per
+//   warp 8          TMA producer, and taker of items: the two Q tiles once per
 //                   item, K and V tiles into rings of their own
 //   warp 9          MMA issuer: S_w = Q_w K^T and O_w += P_w V
 // Tensor memory: S_0, S_1 at columns [0,128), [128,256), O_0, O_1 after them.
@@ -113,6 +115,8 @@ struct FwdBars {
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t drain;
+  uint64_t clc_full;       // the answer to the producer's question for a next item
+  alignas(16) uint64_t clc_answer[2];
   uint32_t tmem_base;
   int abort_flag;
   int item_slot[2];
@@ -205,26 +209,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     const __grid_constant__ CUtensorMap tm_v, __nv_bfloat16* __restrict__ out,
                     float* __restrict__ lse, const int64_t o_row_stride,
                     const int64_t lse_head_stride, const int64_t lse_seq_stride,
-                    const float scale_log2, int* status, int* claim, const SeqShape sh_in,
+                    const float scale_log2, int* status, const SeqShape sh_in,
                     const __grid_constant__ Tables tb) {
   using C = FwdCfg<DQK, DV>;
   SeqShape sh = sh_in;
   if constexpr (!kLeft) sh.wl = -1;
   extern __shared__ __align__(1024) uint8_t smem[];
-  // Every CTA counts out on claim[1] once it will claim no more items; the
-  // last one leaves both counters at zero for the next call that uses them.
-  auto count_out = [&]() {
-    __threadfence();  // this CTA's claims are ordered before its count-out
-    if (atomicAdd(&claim[1], 1) == (int)gridDim.x - 1) {
-      atomicExch(&claim[0], 0);
-      atomicExch(&claim[1], 0);
-    }
-  };
   if (smem_u32(smem) & 1023u) {  // the swizzled panels need a 1024-byte aligned window
-    if (threadIdx.x == 0) {
-      atomicCAS(status, 0, kStatusInternal);
-      count_out();
-    }
+    if (threadIdx.x == 0) atomicCAS(status, 0, kStatusInternal);
     return;
   }
   FwdBars* bars = reinterpret_cast<FwdBars*>(smem + C::kOffBar);
@@ -257,6 +249,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       mbar_init(smem_u32(&bars->o_done[w]), 1);
     }
     mbar_init(smem_u32(&bars->drain), 1);
+    mbar_init(smem_u32(&bars->clc_full), 1);
     fence_barrier_init();
   }
   if (warp == 9) {
@@ -280,15 +273,29 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     {
       uint32_t kv_it = 0, item_iter = 0, q_issued = 0, k_issued = 0;
       bool ok = true;
-      // claim the next work item (items are taken in order by all CTAs) and
-      // hand it to the MMA issuer and the softmax warps through a 2-slot ring
+      // The next work item, handed to the MMA issuer and the softmax warps through a 2-slot ring:
+      // this CTA's own first, then those of CTAs that have not started (in order), each asked
+      // for when the one in front of it is loaded (sooner, and a CTA held an item in reserve
+      // while others ended: 5 % more at T 32768).
+      const uint32_t answer = smem_u32(bars->clc_answer), clc = smem_u32(&bars->clc_full);
+      uint32_t asked = 0;
       auto claim_next = [&]() -> int {
         const uint32_t slot = item_iter & 1;
         if (!mbar_wait(smem_u32(&bars->item_empty[slot]), ((item_iter >> 1) & 1) ^ 1, ab)) {
           ok = false;
           return sh.n_items;
         }
-        const int item = atomicAdd(claim, 1);
+        int item = blockIdx.x;
+        if (item_iter > 0) {
+          mbar_arrive_expect_tx(clc, 16);
+          clc_ask(answer, clc);
+          ++asked;
+          if (!mbar_wait(clc, (asked - 1) & 1, ab)) {
+            ok = false;
+            return sh.n_items;
+          }
+          if (!clc_read(answer, &item)) item = sh.n_items;
+        }
         bars->item_slot[slot] = item;
         mbar_arrive(smem_u32(&bars->item_full[slot]));
         return item;
@@ -360,8 +367,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           ++kv_it;
         }
       }
-      count_out();
       if (!ok) {
+        if (asked > 0) mbar_wait_drain(clc, (asked - 1) & 1);
         // let every copy already issued land before the CTA's memory is released
         for (uint32_t t = k_issued > (uint32_t)C::kKStages ? k_issued - C::kKStages : 0;
              t < k_issued; ++t)
@@ -732,7 +739,7 @@ cudaError_t launch_kernel(const FwdLaunch& L) {
     if (e != cudaSuccess) return e;
     return cudaLaunchKernelEx(&cfg, k, L.tm_q, L.tm_k, L.tm_v,
                               reinterpret_cast<__nv_bfloat16*>(L.o), L.lse, L.o_row_stride,
-                              L.lse_head_stride, L.lse_seq_stride, L.scale_log2, L.status, L.claim,
+                              L.lse_head_stride, L.lse_seq_stride, L.scale_log2, L.status,
                               L.sh, *L.tables);
   }
   auto* k = attn_fwd_kernel<DQK, DV, NoTables, kMask, kLeft>;
@@ -740,7 +747,7 @@ cudaError_t launch_kernel(const FwdLaunch& L) {
   if (e != cudaSuccess) return e;
   return cudaLaunchKernelEx(&cfg, k, L.tm_q, L.tm_k, L.tm_v, reinterpret_cast<__nv_bfloat16*>(L.o),
                             L.lse, L.o_row_stride, L.lse_head_stride, L.lse_seq_stride,
-                            L.scale_log2, L.status, L.claim, L.sh, NoTables{});
+                            L.scale_log2, L.status, L.sh, NoTables{});
 }
 
 template <int DQK, int DV>
@@ -755,18 +762,6 @@ cudaError_t launch_typed(const FwdLaunch& L) {
 // Sticky status word of the forward kernels on each device (a bounded wait
 // that gave up writes its code here; attn_fwd_status reads and clears it).
 __device__ int g_fwd_status = 0;
-
-// Work-item counters of the forward: a pair (items claimed, CTAs done) per
-// call in flight, taken round-robin, so up to kFwdClaimSlots calls may
-// overlap on different streams.  A kernel leaves its pair at zero.
-__device__ int g_fwd_claim[2 * kFwdClaimSlots];
-
-int* fwd_claim_ptr(int slot) {
-  void* p = nullptr;
-  if (slot < 0 || slot >= kFwdClaimSlots) return nullptr;
-  if (cudaGetSymbolAddress(&p, g_fwd_claim) != cudaSuccess) return nullptr;
-  return static_cast<int*>(p) + 2 * slot;
-}
 
 int* fwd_status_ptr() {
   void* p = nullptr;

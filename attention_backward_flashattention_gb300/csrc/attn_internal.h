@@ -21,7 +21,6 @@ struct FwdLaunch {
   int64_t lse_seq_stride;        // fixed length: elements between sequences; varlen: 0
   float scale_log2;              // scale * log2(e)
   int* status;                   // device status word
-  int* claim;                    // device counters (items claimed, CTAs done), zero at launch
   SeqShape sh;
   const VarlenTables* tables;    // null for fixed-length batches
   int grid;
@@ -80,10 +79,6 @@ int* fwd_status_ptr();
 // Reads a sticky device status word and clears it, in one step on `stream`, which it
 // synchronises.  Returns the word, or ATTN_ERR_CUDA.
 int take_status(int* status, cudaStream_t stream);
-// Device address of forward work-item counter `slot` on the current device.
-constexpr int kFwdClaimSlots = 256;
-int* fwd_claim_ptr(int slot);
-
 // Dynamic shared memory the kernels need (for validation / tests).
 int fwd_smem_bytes(int dqk, int dv);
 int bwd_smem_bytes(int dqk, int dv);

@@ -123,6 +123,31 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Cluster launch control: a running CTA asks for one that has not started yet, which then never
+// does; the answer (16 bytes) arrives on the mbarrier.  After an answer without a CTA none may be
+// asked for again.
+__device__ __forceinline__ void clc_ask(uint32_t answer, uint32_t bar) {
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], "
+      "[%1];" ::"r"(answer),
+      "r"(bar)
+      : "memory");
+}
+// Whether the answer holds a CTA, and its blockIdx.x.
+__device__ __forceinline__ bool clc_read(uint32_t answer, int* x) {
+  uint32_t got, id;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\tld.shared.b128 a, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, a;\n\t}"
+      : "=r"(got), "=r"(id)
+      : "r"(answer)
+      : "memory");
+  *x = (int)id;
+  return got != 0;
+}
+
 // Named barrier among `count` threads (multiple of 32), id 1..15.
 __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t count) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
