@@ -386,7 +386,9 @@ append_norm_kernel(const __grid_constant__ AppendNormParams P, const __grid_cons
 #pragma unroll
       for (int e = 0; e < 16; e += 4) {
         const float4 q = *reinterpret_cast<const float4*>(w + (e < 8 ? ca + e : cb + e - 8));
-        f[e] *= r * q.x, f[e + 1] *= r * q.y, f[e + 2] *= r * q.z, f[e + 3] *= r * q.w;
+        // (in norm_kernel's order: the cache holds the bits that attn_norm_rope gives)
+        f[e] = f[e] * r * q.x, f[e + 1] = f[e + 1] * r * q.y;
+        f[e + 2] = f[e + 2] * r * q.z, f[e + 3] = f[e + 3] * r * q.w;
       }
       there = there && pos[min(t, tokens - 1)] >= 0;
       if (there) {

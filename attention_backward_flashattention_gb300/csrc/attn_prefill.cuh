@@ -818,9 +818,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       const bool row_ok = rt < tokens;
       const bool live = __any_sync(0xffffffffu, row_ok);  // (a warp without rows has no work)
       // a tile whose last key is past `right`, or whose first is in front of `left`, has keys that
-      // some row does not see; this row sees keys from `see0` to its own
-      const int right = first_pos;
-      const int left = sh.window >= 0 ? first_pos + tokens - 1 - sh.window : INT_MIN;
+      // some row of the unit does not see (the copy warps go by the same, and take values out of
+      // such a tile); this row sees keys from `see0` to its own
+      const int right = item.pos0;
+      const int left = sh.window >= 0 ? item.pos0 + item.tokens - 1 - sh.window : INT_MIN;
       const int see0 = sh.window >= 0 ? max(first_pos + rt, 0) - sh.window : 0;
       const int key0 = item.tile * kTile;
       // c in two factors, so that neither leaves fp32's range with the scale of an e4m3 cache
@@ -852,7 +853,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           const int kbase = key0 + t * kTile;
           tmem_ld_wait();
           // some row does not see some key of the tile: one that is not there, one after the
-          // first row's position, one in front of the last row's window
+          // unit's first position, one in front of its last one's window
           const bool edge = (there.x & there.y & there.z & there.w) != ~0u ||
                             kbase + kTile - 1 > right || kbase < left;
           float mx[8];
@@ -862,7 +863,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           if (edge) {
             const uint4 bad = *reinterpret_cast<const uint4*>(bars->bad[(step0 + t) % kKeyRing]);
             // the row's keys, relative to the tile: klo .. khi - 1
-            const int khi = right + rt + 1 - kbase, klo = see0 - kbase;
+            const int khi = first_pos + rt + 1 - kbase, klo = see0 - kbase;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const int a = min(32, max(0, klo - 32 * q)), b = min(32, max(0, khi - 32 * q));

@@ -210,6 +210,16 @@ def test_append(d, begin, dim, inter, kind, order, new, lens):
     ref, tol = forward64(q, wq, pos, freq, begin, inter)
     assert ((got.double() - ref).abs() <= tol)[live].all() and (got[~live] == 3).all()
     at = (table[seq, pos.clamp(min=0) // page].long()[live], pos[live] % page)
+    if cu is not None and all(m >= n for m, n in zip(lens, new)):  # the bits that norm_rope gives
+        shift = [m - n for m, n in zip(lens, new)]
+        for b in range(len(new)):
+            r = slice(cu[b], cu[b + 1])
+            if r.stop > r.start:
+                one, key = binding.norm_rope(q[None, r], k[None, r], norm, rot, pos0=shift[b])
+                assert torch.equal(got[r], one[0])
+                if kind == "bf16":
+                    j = torch.arange(shift[b], lens[b]).cuda()
+                    assert torch.equal(kc[table[b].long()[j // page], j % page], key[0])
     rk, tk = forward64(k, wk, pos, freq, begin, inter)
     for c, want, tol, raw in ((kc, rk, tk, before[0]), (vc, v.double(), None, before[1])):
         have = bits(c)[at].view(c.dtype).double()
