@@ -1068,9 +1068,13 @@ class HeadNorm:
         self.address = ctypes.addressof(self.struct)
 
     def check(self, d):
-        for w in (self.q_weight, self.k_weight):
-            if w is not None and w.shape[0] != d:
-                raise ValueError("the norm's weights must have one value per column of a head")
+        """For heads of d columns; the weights' memory is asked for anew, as a parameter's may move."""
+        for name in ("q_weight", "k_weight"):
+            w = getattr(self, name)
+            if w is not None:
+                if w.shape[0] != d:
+                    raise ValueError("the norm's weights must have one value per column of a head")
+                setattr(self.struct, name, w.data_ptr())
 
 
 def _norm_dims(q, k, cu_seqlens, cu_seqlens_k):

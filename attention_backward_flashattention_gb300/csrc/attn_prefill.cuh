@@ -39,6 +39,7 @@ constexpr int kPrefillThreads = 512;
 constexpr int kCopyWarp = 8, kPrefillMmaWarp = 12, kWalkWarp = 13, kRingWarp = 14;
 constexpr int kPrefillPanel = kTile * 128;  // [128 rows][64] bf16
 constexpr int kPrefillMaxSmem = 232448;
+constexpr int kBarBytes = 3 * 1024;  // barriers, items and the rest that is no tile
 constexpr int kKeyRing = 8;  // key tiles whose bits are kept (more than are under way)
 
 template <int DQK, int DV, bool E4M3>
@@ -58,7 +59,7 @@ struct PrefillCfg {
   static constexpr int kOffRawK = kOffV + kVStages * kVBytes;
   static constexpr int kOffRawV = kOffRawK + kRaw * kTile * DQK;
   static constexpr int kOffBar = kOffRawV + kRaw * kTile * DV;
-  static constexpr int kSmemBytes = kOffBar + 3072;
+  static constexpr int kSmemBytes = kOffBar + kBarBytes;
   static_assert(kSmemBytes <= kPrefillMaxSmem, "shared memory budget");
   static constexpr uint32_t kTmemO = 256;
   // Whether a step's products of P and V go in front of the wait for the next step's keys, or
@@ -92,7 +93,7 @@ struct PrefillBars {
   uint32_t tmem_base;
   int abort_flag;
 };
-static_assert(sizeof(PrefillBars) <= 3072, "barrier block size");
+static_assert(sizeof(PrefillBars) <= kBarBytes, "barrier block size");
 
 struct PrefillParams {
   CacheView cache;

@@ -175,6 +175,35 @@ def test_rows_of_zeros_and_extremes():
     assert torch.isnan(y[0, 3, 0]).all() and (y[0, 3, 1] == 0).all()
 
 
+def test_weights_that_move():
+    """A parameter whose memory is replaced: the next call reads the new one."""
+    x = torch.randn(1, 5, 2, 64, device="cuda").to(torch.bfloat16)
+    w = torch.nn.Parameter(torch.ones(64, device="cuda"))
+    norm = binding.HeadNorm(w, None)
+    one, _ = binding.norm_rope(x, None, norm)
+    w.data = torch.full((64,), 2.0, device="cuda")
+    two, _ = binding.norm_rope(x, None, norm)
+    assert torch.equal(two, one * 2)
+
+
+def test_append_keys_alone():
+    page, heads, d = 16, 3, 128
+    g = torch.Generator().manual_seed(1)
+    table, pages = make_table([40, 7], page, 3)
+    caches = [(make_cache(pages, page, heads, d, "bf16", "token", 4),
+               make_cache(pages, page, heads, d, "bf16", "token", 5)) for _ in range(2)]
+    lens = torch.tensor([40, 7], dtype=torch.int32).cuda()
+    q, k, v = (_rand(g, 10, h, d) for h in (6, heads, heads))
+    norm, rot = binding.HeadNorm(eps=EPS), binding.Rotation(inv_freq(d))
+    none = binding.cache_append(binding.PagedCache(*caches[0]), k, v, table, lens, rotation=rot,
+                                norm=norm)
+    binding.cache_append(binding.PagedCache(*caches[1]), k, v, table, lens, q=q, rotation=rot,
+                         norm=norm)
+    assert none is None
+    assert torch.equal(caches[0][0], caches[1][0]) and torch.equal(caches[0][1], caches[1][1])
+    assert binding.attn_cache_status() == binding.ATTN_OK
+
+
 @pytest.mark.parametrize("kind,order", [("bf16", "token"), ("bf16", "head"), ("e4m3", "token")])
 @pytest.mark.parametrize("d,begin,dim,inter", [((64, 64), 0, 64, False), ((128, 128), 0, 64, True),
                                                ((192, 128), 128, 64, True),

@@ -245,6 +245,35 @@ def test_windows_longer_than_anything(window):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_many_sequences(kind):
+    """More units than a CTA has threads, and more sequences than a table of offsets takes."""
+    heads, group, page, d = 1, 2, 16, 64
+    lens = [1 + 37 * i % 61 for i in range(1500)]
+    cache, q, kc, vc, ks, vs, table, lens_d = setup(8, heads, group, d, d, page, kind, "token",
+                                                    [1] * 1500, lens)
+    got = binding.prefill(cache, q, table, lens_d)
+    check(got, prefill64(q, kc, vc, table, lens, [1] * 1500, page, 0.125, -1, ks, vs))
+    assert binding.attn_cache_status() == binding.ATTN_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_sides_of_different_orders(kind):
+    """Keys token by token and values head by head, pages of 24 tokens."""
+    heads, group, page, d = 3, 2, 24, 128
+    new, lens = [40, 3], [500, 50]
+    table, pages = make_table(lens, page, 1)
+    kc = make_cache(pages, page, heads, d, kind, "token", 2)
+    vc = make_cache(pages, page, heads, d, kind, "head", 3)
+    unit = torch.full((heads,), 1 / 64).cuda() if kind == "e4m3" else None
+    q = torch.randn(43, heads * group, d, device="cuda").to(torch.bfloat16)
+    lens_d = torch.tensor(lens, dtype=torch.int32).cuda()
+    for k, v in ((kc, vc), (vc, kc)):
+        got = binding.prefill(binding.PagedCache(k, v, unit, unit), q, table, lens_d,
+                              cu_seqlens=_offsets(new))
+        check(got, prefill64(q, k, v, table, lens, new, page, 1 / math.sqrt(d), -1, unit, unit))
+
+
 def test_broadcast_caches():
     """A cache whose pages or heads share memory can be read (maps do not describe it: its tiles come
     by rows)."""
