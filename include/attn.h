@@ -216,6 +216,9 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
  * adjacent, rows evenly spaced over the whole batch.  dk and dv are sums over
  * the group's query heads, accumulated in fp32 and rounded once.  LSE has Hq
  * heads.  No counterpart on the pages.
+ * Values that are not finite: as in attn_fwd and attn_bwd, a row that does not see
+ * a key, or a neighbouring sequence's, meets it with a weight of zero wherever
+ * their tiles of 128 rows meet, so an infinity or a NaN there can reach it.
  * Workspace: attn_bwd_grouped_workspace_size() bytes (0 for invalid sizes):
  * that of attn_bwd for Hq heads, and, where there are few key tiles and heads,
  * the fp32 sums of parts of the groups.
