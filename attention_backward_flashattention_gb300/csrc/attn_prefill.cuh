@@ -35,8 +35,7 @@
 namespace attn {
 namespace {
 
-constexpr int kPrefillThreads = 512;
-constexpr int kCopyWarp = 8, kPrefillMmaWarp = 12, kWalkWarp = 13, kRingWarp = 14;
+constexpr int kCopyWarp = 8;
 constexpr int kPrefillPanel = kTile * 128;  // [128 rows][64] bf16
 constexpr int kPrefillMaxSmem = 232448;
 constexpr int kBarBytes = 3 * 1024;  // barriers, items and the rest that is no tile
@@ -44,6 +43,8 @@ constexpr int kKeyRing = 8;  // key tiles whose bits are kept (more than are und
 
 template <int DQK, int DV, bool E4M3>
 struct PrefillCfg {
+  static constexpr int kThreads = E4M3 ? 640 : 512;
+  static constexpr int kMmaWarp = kThreads / 32 - 4;
   static constexpr int kQTile = DQK / 64 * kPrefillPanel;
   static constexpr int kKBytes = DQK / 64 * kPrefillPanel;
   static constexpr int kVBytes = DV / 64 * kPrefillPanel;
@@ -70,21 +71,24 @@ struct PrefillCfg {
   // Registers a thread after the split of 512 x 128: softmax, copies, MMA and walk.
   // (64 single tokens over 8000, bf16: 377 us with 184, 80 and 64, 362 with 192, 64 and 64, 389 with
   // 200, 56 and 56; 192 columns: 300, 300 and 319 where 184, 72 and 72 take 295)
-  static constexpr uint32_t kRegsSoftmax = E4M3 ? 176 : DQK == 192 ? 184 : 192;
-  static constexpr uint32_t kRegsCopy = E4M3 ? 96 : DQK == 192 ? 72 : 64;
+  static constexpr uint32_t kRegs = E4M3 ? 96 : 128;
+  static constexpr uint32_t kRegsSoftmax = E4M3 ? 120 : DQK == 192 ? 184 : 192;
+  static constexpr uint32_t kRegsCopy = E4M3 ? 88 : DQK == 192 ? 72 : 64;
   static constexpr uint32_t kRegsCtl = E4M3 ? 64 : DQK == 192 ? 72 : 64;
-  static_assert(2 * kRegsSoftmax + kRegsCopy + kRegsCtl <= 512, "register split");
+  static_assert(2 * kRegsSoftmax + (E4M3 ? 2 : 1) * kRegsCopy + kRegsCtl <= kThreads / 128 * kRegs,
+                "register split");
 };
 
 struct PrefillBars {
   uint64_t item_full[2], item_empty[2];
   uint64_t q_full, q_empty;
+  uint64_t q_f16;  // e4m3: the queries are fp16
   uint64_t k_full[5], k_empty[5], v_full[5], v_empty[5];
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t twin_full, twin_done;
   uint64_t raw_full[2][4], raw_empty[2][4];  // [keys, values][slot]
   int raw_there[2][4];           // whether a slot holds its tile's rows (else they come by rows)
-  uint64_t spare_free;           // a single tile's unit is done with the second query tile's place
+  uint64_t spare_free[2];        // a single tile's unit is done with the second query tile's place
   uint64_t drain;
   PrefillItem item[2];
   alignas(16) uint32_t there[kKeyRing][4];  // of a key tile's 128 keys, which are in the cache
@@ -134,40 +138,43 @@ __device__ __forceinline__ PrefillUnit unit_at(const PrefillParams& P, const Off
   return make_prefill_unit(P.sh, P.room, b, row0, n, len, u);
 }
 
-// P = 2^(c (S - m)) of a row's 128 scores as bf16 pairs, and its sum.  kFar: the scores are so
-// large that c m, rounded, is off by more than 2^-8: differences first, and c in two factors.
-template <bool kFar>
-__device__ __forceinline__ float prefill_exp(const uint32_t (&sr)[4][32], float f1, float f2_,
-                                             float m, uint32_t (&pk0)[32], uint32_t (&pk1)[32]) {
-  const float c = f1 * f2_;
-  const uint64_t c2 = f2(c, c), nm2 = kFar ? f2(-m, -m) : f2(-m * c, -m * c);
-  uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) {
-      const uint64_t s2 = f2(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]));
-      float x0, x1;
-      if constexpr (kFar) {
-        const uint64_t d2 = add2(s2, nm2);
-        x0 = f2_lo(d2) * f1 * f2_;
-        x1 = f2_hi(d2) * f1 * f2_;
-      } else {
-        const uint64_t x2 = fma2(s2, c2, nm2);
-        x0 = f2_lo(x2);
-        x1 = f2_hi(x2);
-      }
-      const float p0 = ex2(x0), p1 = ex2(x1);
-      rs2[(e >> 1) & 3] = add2(rs2[(e >> 1) & 3], f2(p0, p1));
-      if (q < 2) pk0[q * 16 + e / 2] = pack_bf16(p0, p1);
-      else pk1[(q - 2) * 16 + e / 2] = pack_bf16(p0, p1);
-    }
-  }
-  const uint64_t s4 = add2(add2(rs2[0], rs2[1]), add2(rs2[2], rs2[3]));
-  return f2_lo(s4) + f2_hi(s4);
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
-// 16 bytes from global memory to shared, or zeros.
+// P = 2^(c (S - m)) of a row's 128 scores as bf16 pairs, and its sum; with kF16 as fp16 pairs,
+// times 2^kLift, which the largest weight of 2^8 leaves room for: 11 bits for weights down to 2^-21
+// of the maximum that they are taken by, and the least, below 2^-32, are zero.
+// kFar: the scores are so large that c m, rounded, is off by more than 2^-8: differences first, and
+// c in two factors.
+constexpr int kPart = 1;
+constexpr float kLift = 7.f;
+template <bool kF16>
+__device__ __forceinline__ void prefill_exp(const uint32_t (&sr)[32], bool far, float f1, float f2_,
+                                            float m, uint64_t (&rs2)[4], uint32_t (&pk)[16]) {
+  constexpr float lift = kF16 ? kLift : 0.f;
+  const float c = f1 * f2_;
+  const uint64_t c2 = f2(c, c), nm2 = far ? f2(-m, -m) : f2(lift - m * c, lift - m * c);
+  if (far) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const uint64_t d2 = add2(f2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), nm2);
+      const float p0 = ex2(f2_lo(d2) * f1 * f2_ + lift), p1 = ex2(f2_hi(d2) * f1 * f2_ + lift);
+      rs2[(e >> 1) & 3] = add2(rs2[(e >> 1) & 3], f2(p0, p1));
+      pk[e / 2] = kF16 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const uint64_t x2 = fma2(f2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, nm2);
+      const float p0 = ex2(f2_lo(x2)), p1 = ex2(f2_hi(x2));
+      rs2[(e >> 1) & 3] = add2(rs2[(e >> 1) & 3], f2(p0, p1));
+      pk[e / 2] = kF16 ? pack_f16(p0, p1) : pack_bf16(p0, p1);
+    }
+  }
+}
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                "r"(there ? 16 : 0)
@@ -194,17 +201,50 @@ __device__ __forceinline__ bool not_finite(uint32_t x) {
   return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
 }
 
-// Four e4m3 values as two words of bf16 pairs (exact: a bf16 has every e4m3 value).
-__device__ __forceinline__ void e4m3_to_bf16(uint32_t x, uint32_t& lo, uint32_t& hi) {
-  uint32_t h0, h1;
+// Four e4m3 values as two words of fp16 pairs (exact: an fp16 has every e4m3 value).
+__device__ __forceinline__ void e4m3_to_f16(uint32_t x, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(h0), "=r"(h1)
+      : "=r"(lo), "=r"(hi)
       : "r"(x));
-  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h0));
-  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-  lo = pack_bf16(a.x, a.y);
-  hi = pack_bf16(b.x, b.y);
+}
+
+// A row of a query tile (`row`: its place in the tile's first panel, r: its number) from bf16 to fp16
+// in place, times the power of two that puts its largest finite value into [2^14, 2^15): exact
+// but for elements below 2^-28 of that.  Returns the exponent.
+template <int D>
+__device__ __forceinline__ int query_to_f16(uint32_t row, int r) {
+  uint32_t top = 0;  // exponents of the row's finite values
+#pragma unroll 1
+  for (int p = 0; p < D / 64; ++p) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint4 v = lds128(row + p * kPrefillPanel + ((c ^ (r & 7)) << 4));
+      const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = x[i] & 0x7F80u, hi = (x[i] >> 16) & 0x7F80u;
+        top = max(top, max(lo == 0x7F80u ? 0u : lo, hi == 0x7F80u ? 0u : hi));
+      }
+    }
+  }
+  const int e = min(126, 141 - (int)(top >> 7));
+  const float by = __int_as_float((e + 127) << 23);
+#pragma unroll 1
+  for (int p = 0; p < D / 64; ++p) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint32_t at = row + p * kPrefillPanel + ((c ^ (r & 7)) << 4);
+      const uint4 v = lds128(at);
+      uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[i] = pack_f16(__uint_as_float(x[i] << 16) * by,
+                        __uint_as_float(x[i] & 0xFFFF0000u) * by);
+      st_shared_v4(at, x[0], x[1], x[2], x[3]);
+    }
+  }
+  return e;
 }
 
 // Rows of a warp's 32 of a tile, by the warp: lane l takes chunk C0 + l % CH (of 16 bytes of the
@@ -262,10 +302,10 @@ __device__ __forceinline__ void widen_rows(uint32_t tile, int mw, int lane, bool
     for (int i = 0; i < 2; ++i) {
       const uint32_t in8 = ((p + i) * kStep & 7) + row0, at = dst + (p + i) * kStep * 128;
       uint32_t a[4], b[4];
-      e4m3_to_bf16(odd ? v[i].z : v[i].x, a[0], a[1]);
-      e4m3_to_bf16(odd ? v[i].w : v[i].y, a[2], a[3]);
-      e4m3_to_bf16(odd ? v[i].x : v[i].z, b[0], b[1]);
-      e4m3_to_bf16(odd ? v[i].y : v[i].w, b[2], b[3]);
+      e4m3_to_f16(odd ? v[i].z : v[i].x, a[0], a[1]);
+      e4m3_to_f16(odd ? v[i].w : v[i].y, a[2], a[3]);
+      e4m3_to_f16(odd ? v[i].x : v[i].z, b[0], b[1]);
+      e4m3_to_f16(odd ? v[i].y : v[i].w, b[2], b[3]);
       const uint32_t x = 2 * c & 7;
       st_shared_v4(at + (((odd ? x + 1 : x) ^ in8) << 4), a[0], a[1], a[2], a[3]);
       st_shared_v4(at + (((odd ? x : x + 1) ^ in8) << 4), b[0], b[1], b[2], b[3]);
@@ -276,12 +316,14 @@ __device__ __forceinline__ void widen_rows(uint32_t tile, int mw, int lane, bool
 }
 
 template <int DQK, int DV, bool E4M3, typename Offsets>
-__global__ void __launch_bounds__(kPrefillThreads, 1)
+__global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
                    const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v,
                    const __grid_constant__ PrefillParams P, const __grid_constant__ Offsets off) {
   using C = PrefillCfg<DQK, DV, E4M3>;
+  constexpr int kPrefillThreads = C::kThreads, kMmaWarp = C::kMmaWarp;
+  constexpr int kWalkWarp = kMmaWarp + 1, kRingWarp = kMmaWarp + 2;  // (e4m3: two of these)
   extern __shared__ __align__(1024) uint8_t smem[];
   PrefillBars* bars = reinterpret_cast<PrefillBars*>(smem + C::kOffBar);
   const uint32_t sQ = smem_u32(smem), sK = sQ + C::kOffK, sV = sQ + C::kOffV;
@@ -311,7 +353,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   __syncthreads();
   long long in_front = 0, per_head = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < kPrefillThreads / 32; ++i) {
     if (i < warp) in_front += warp_sum[i];
     per_head += warp_sum[i];
   }
@@ -325,13 +367,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     for (int k = 0; k < 2; ++k) {
       mbar_init(smem_u32(&bars->item_full[k]), 1);
       // MMA, softmax warps, copy warps, ring
-      mbar_init(smem_u32(&bars->item_empty[k]), 1 + 8 + 4 + (E4M3 ? 1 : 0));
+      mbar_init(smem_u32(&bars->item_empty[k]), 1 + 8 + (E4M3 ? 8 + 2 : 4));
       mbar_init(smem_u32(&bars->s_full[k]), 1);
       mbar_init(smem_u32(&bars->p_full[k]), 4);
       mbar_init(smem_u32(&bars->o_done[k]), 1);
     }
     mbar_init(smem_u32(&bars->q_full), 1);
     mbar_init(smem_u32(&bars->q_empty), 1);
+    mbar_init(smem_u32(&bars->q_f16), 8);
     for (int s = 0; s < C::kKStages; ++s) {
       mbar_init(smem_u32(&bars->k_full[s]), 4);
       mbar_init(smem_u32(&bars->k_empty[s]), 1);
@@ -342,7 +385,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     }
     mbar_init(smem_u32(&bars->twin_full), 8);
     mbar_init(smem_u32(&bars->twin_done), 8);
-    mbar_init(smem_u32(&bars->spare_free), 4);
+    for (int side = 0; side < 2; ++side) mbar_init(smem_u32(&bars->spare_free[side]), 4);
     for (int i = 0; i < 2 * 4; ++i) {
       mbar_init(smem_u32(&bars->raw_full[0][0] + i), 1);
       mbar_init(smem_u32(&bars->raw_empty[0][0] + i), 4);
@@ -350,7 +393,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     mbar_init(smem_u32(&bars->drain), 1);
     fence_barrier_init();
   }
-  if (warp == kPrefillMmaWarp) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
   }
@@ -381,18 +424,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   __syncthreads();
 
   // e4m3: the ring's slot `slot` of keys or values; slots of a unit: one more than the ring has, in
-  // the second query tile's place, where it has none and the unit in front of it, whose products may
-  // still read it, had none either
+  // the second query tile's place, where it has none and the units in front of it, whose products may
+  // still read it, had none either.  since: units since one of two tiles.  (Behind as many as there
+  // are key stages its products are over: they have left the stages to other tiles.)
   constexpr int kRaw = C::kRaw > 0 ? C::kRaw : 1;
   [[maybe_unused]] auto raw_at = [&](int side, uint32_t slot) -> uint32_t {
     if (C::kSpareQ && slot == C::kRaw) return sQ + C::kQTile + (side ? kTile * DQK : 0);
     return sQ + (side ? C::kOffRawV + slot * kTile * DV : C::kOffRawK + slot * kTile * DQK);
   };
-  [[maybe_unused]] auto slots_of = [&](bool twin, bool was_pair) -> uint32_t {
-    return kRaw + (C::kSpareQ && twin && !was_pair ? 1 : 0);
+  [[maybe_unused]] auto slots_of = [&](bool twin, int since) -> uint32_t {
+    return kRaw + (C::kSpareQ && twin && since >= C::kKStages ? 1 : 0);
   };
 
-  if (warp >= kPrefillMmaWarp) {
+  if (warp >= kMmaWarp) {
     regs_dec<C::kRegsCtl>();
     if (warp == kWalkWarp && lane == 0) {
       // ------------------------------------------------------------ walk, queries
@@ -419,7 +463,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         if constexpr (C::kSpareQ) {  // (the copy warps may still use the second tile's place)
           if (tiles == 1) ++twins;
           else if (twins > 0 &&
-                   !(ok = mbar_wait(smem_u32(&bars->spare_free), (twins - 1) & 1, ab)))
+                   !(ok = mbar_wait(smem_u32(&bars->spare_free[0]), (twins - 1) & 1, ab) &&
+                          mbar_wait(smem_u32(&bars->spare_free[1]), (twins - 1) & 1, ab)))
             break;
         }
         const uint32_t qf = smem_u32(&bars->q_full);
@@ -436,10 +481,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         ok = give(it);
       }
       if (!ok && q_loads > 0) mbar_wait_drain(smem_u32(&bars->q_full), (q_loads - 1) & 1);
-    } else if (warp == kPrefillMmaWarp && lane == 0) {
+    } else if (warp == kMmaWarp && lane == 0) {
       // ------------------------------------------------------------ MMA issuer
-      constexpr uint32_t idS = idesc_bf16(128, 128, false, false);
-      constexpr uint32_t idO = idesc_bf16(128, DV, false, true);
+      constexpr uint32_t kTypes = E4M3 ? ~kIdescBf16 : ~0u;  // (without: fp16 operands)
+      constexpr uint32_t idS = idesc_bf16(128, 128, false, false) & kTypes;
+      constexpr uint32_t idO = idesc_bf16(128, DV, false, true) & kTypes;
       const uint64_t bQ = kmajor_base(sQ), bK = kmajor_base(sK), bV = mnmajor_base(sV, 128);
       uint32_t n = 0, step = 0, parity = 0;  // parity: of the next P of each warpgroup, by bit
       bool ok = true;
@@ -455,7 +501,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         const int tiles = item.tiles;
         const TileUse use = tile_use(sh, item);
         mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
-        if (!(ok = W(bars->q_full, n & 1))) break;
+        if (!(ok = W(E4M3 ? bars->q_f16 : bars->q_full, n & 1))) break;
         // After step t's P of a warpgroup: O += P V of step t, then S of step t + 1 (t = -1: the
         // first S).  A warpgroup that has no part in step t starts on the next at once.  One
         // place in the code for each product: unrolled over the warpgroups it spilled.
@@ -517,10 +563,12 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         mma_commit(smem_u32(&bars->drain));
         mbar_wait_drain(smem_u32(&bars->drain), 0);
       }
-    } else if (E4M3 && warp == kRingWarp) {
+    } else if (E4M3 && warp >= kRingWarp) {
       // ------------------------------------------------------------ e4m3: tiles to the ring
-      uint32_t parity = 0, loads = 0;  // by slot (bit 4 side + slot); slots that were loaded
-      bool ok = true, was_pair = false;
+      const int side = warp - kRingWarp;  // 0: keys, 1: values
+      uint32_t parity = 0, loads = 0;  // by slot; slots that were loaded
+      int since = C::kKStages;
+      bool ok = true;
       const int box = max(P.box, 8);
       for (uint32_t n = 0;; ++n) {
         if (!(ok = mbar_wait_warp(smem_u32(&bars->item_full[n & 1]), (n >> 1) & 1, ab))) break;
@@ -533,8 +581,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         const int right = min(item.pos0, item.end - 1);
         const int left = sh.window >= 0 ? item.pos0 + item.tokens - 1 - sh.window : 0;
         const bool twin = item.tokens <= sh.per_tile;
-        const uint32_t slots = slots_of(twin, was_pair);
-        was_pair = !twin;
+        const uint32_t slots = slots_of(twin, since);
+        since = twin ? min(since + 1, C::kKStages) : 0;
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
         // lane l has box l of a tile; its page is looked up a tile ahead
@@ -552,38 +600,37 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           const bool there = __all_sync(0xffffffffu, !mine || page_in(P.cache, page)) && P.box > 0;
           const uint32_t slot = t % slots;
           const int key = key_of(t), in = key - div_page(P.cache, key) * P.cache.page_size;
-#pragma unroll 1
-          for (int side = 0; side < 2; ++side) {
-            const uint32_t bit = 1u << (side * 4 + slot);
-            if (!(ok = mbar_wait_warp(smem_u32(&bars->raw_empty[side][slot]), (parity & bit) == 0,
-                                      ab)))
-              break;
-            parity ^= bit;
-            loads |= bit;
-            const uint32_t bar = smem_u32(&bars->raw_full[side][slot]);
-            if (lane == 0) {
-              bars->raw_there[side][slot] = there ? 1 : 0;
-              if (there) mbar_arrive_expect_tx(bar, kTile * (side ? DV : DQK));
-              else mbar_arrive(bar);
-            }
-            __syncwarp();
-            if (there && mine)
-              tma_load_page(raw_at(side, slot) + lane * box * (side ? DV : DQK),
-                            side ? &tm_v : &tm_k, bar, 0, khead, in, page, P.heads_inner);
+          const uint32_t bit = 1u << slot;
+          if (!(ok = mbar_wait_warp(smem_u32(&bars->raw_empty[side][slot]), (parity & bit) == 0,
+                                    ab)))
+            break;
+          parity ^= bit;
+          loads |= bit;
+          const uint32_t bar = smem_u32(&bars->raw_full[side][slot]);
+          if (lane == 0) {
+            bars->raw_there[side][slot] = there ? 1 : 0;
+            if (there) mbar_arrive_expect_tx(bar, kTile * (side ? DV : DQK));
+            else mbar_arrive(bar);
           }
+          __syncwarp();
+          if (there && mine)
+            tma_load_page(raw_at(side, slot) + lane * box * (side ? DV : DQK),
+                          side ? &tm_v : &tm_k, bar, 0, khead, in, page, P.heads_inner);
         }
         if (!ok) break;
       }
       // (let every copy already issued land before the CTA's memory is released)
       if (!ok && lane == 0)
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 4; ++i)
           if (loads >> i & 1u)
-            mbar_wait_drain(smem_u32(&bars->raw_full[i >> 2][i & 3]), (parity >> i & 1u) ^ 1u);
+            mbar_wait_drain(smem_u32(&bars->raw_full[side][i]), (parity >> i & 1u) ^ 1u);
     }
   } else if (warp >= kCopyWarp) {
-    if constexpr (C::kRegsCopy < 128) regs_dec<C::kRegsCopy>();
+    if constexpr (C::kRegsCopy < C::kRegs) regs_dec<C::kRegsCopy>();
     // -------------------------------------------------------------- keys and values
-    const int mw = warp - kCopyWarp;  // rows 32 mw .. 32 mw + 31 of every tile
+    const int mw = (warp - kCopyWarp) & 3;  // rows 32 mw .. 32 mw + 31 of every tile
+    // e4m3: the first four have the keys, the others the values
+    [[maybe_unused]] const int team = (warp - kCopyWarp) >> 2;
     const bool leader = P.box > 0 && lane % max(P.box, 1) == 0;  // of a box, at its first row
     uint32_t step = 0;
     bool ok = true;
@@ -593,9 +640,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     constexpr int kAhead = C::kKStages + C::kVStages - 1;
     static_assert(kAhead < 32, "a bit each");
     uint32_t issued = 0, told = 0, by_rows = 0;
-    // e4m3: parity of the ring's slots (bit 4 side + slot)
+    // e4m3: parity of the ring's slots
     [[maybe_unused]] uint32_t raw_parity = 0;
-    [[maybe_unused]] bool was_pair = false;
+    [[maybe_unused]] int since = C::kKStages;
     auto tell = [&](uint32_t upto) {
       fence_proxy_async_smem();
       __syncwarp();
@@ -610,6 +657,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     // Waits; where that takes time, what is under way is announced first: it may be what the
     // others wait for.
     auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
+      if constexpr (E4M3) return mbar_wait_warp(smem_u32(&bar), parity, ab);
       if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&bar), parity))) return true;
       cp_wait<0>();
       if (told != issued) tell(issued);
@@ -629,7 +677,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       const int right = min(item.pos0, end - 1);
       const int left = sh.window >= 0 ? item.pos0 + item.tokens - 1 - sh.window : 0;
       const bool twin = item.tokens <= sh.per_tile;
-      [[maybe_unused]] const uint32_t slots = slots_of(twin, was_pair);
+      [[maybe_unused]] const uint32_t slots = slots_of(twin, since);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
       auto edge = [&](int t) {
@@ -654,9 +702,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         const bool is_edge = edge(t);
         bool ring = false;
         const uint32_t slot = E4M3 ? t % slots : 0;
-        if constexpr (E4M3) {  // (the values' slot says the same)
-          if (!(ok = wait(bars->raw_full[0][slot], raw_parity >> slot & 1u))) break;
-          ring = *static_cast<volatile int*>(&bars->raw_there[0][slot]) != 0;
+        if constexpr (E4M3) {
+          if (!(ok = wait(bars->raw_full[team][slot], raw_parity >> slot & 1u))) break;
+          raw_parity ^= 1u << slot;
+          ring = *static_cast<volatile int*>(&bars->raw_there[team][slot]) != 0;
           if (!ring) page = look_up(t);
         }
         uint32_t bits = ~0u;
@@ -674,8 +723,39 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         if constexpr (!E4M3) page = look_up(t + 1);
         // all 32 rows by TMA (a page that is not in the cache: by rows, as zeros)
         const bool boxes = !E4M3 && P.box > 0 && !is_edge && bits == ~0u;
+        // Where some row does not see some key, values that are not finite may not reach the
+        // product (0 times them is NaN): they are looked for before the tile's keys are handed
+        // on, zeros take their place, and the rows that see them become NaN by their sum.
+        uint32_t bad = 0;
+        auto take_out = [&] {
+          constexpr int kChunks = DV / (E4M3 ? 16 : 8), kRows = 32 / kChunks;
+          constexpr int kBatch = kChunks < 8 ? kChunks : 8;
 #pragma unroll 1
-        for (int side = 0; side < 2; ++side) {
+          for (int i0 = 0; i0 < kChunks; i0 += kBatch) {
+            uint4 v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const int at = (i0 + i) * 32 + lane, row = at / kChunks, c = at - row * kChunks;
+              const long long from = __shfl_sync(0xffffffffu, vo, row);
+              v[i] = make_uint4(0, 0, 0, 0);
+              if (from >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(vbase + from + c * 16));
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+              const uint32_t found = __ballot_sync(
+                  0xffffffffu, not_finite<E4M3>(v[i].x) || not_finite<E4M3>(v[i].y) ||
+                                   not_finite<E4M3>(v[i].z) || not_finite<E4M3>(v[i].w));
+#pragma unroll
+              for (int k = 0; k < kRows; ++k)
+                if (found >> (k * kChunks) & ((1u << kChunks) - 1u))
+                  bad |= 1u << ((i0 + i) * kRows + k);
+            }
+          }
+          if (bad >> lane & 1u) vo = -1;
+        };
+        if (E4M3 && is_edge) take_out();  // (for the keys' warps too, which hand the bits on)
+#pragma unroll 1
+        for (int side = E4M3 ? team : 0; side < (E4M3 ? team + 1 : 2); ++side) {
           const int d = side ? DV : DQK;
           const uint32_t st = step % (side ? C::kVStages : C::kKStages);
           const uint32_t parity = ((step / (side ? C::kVStages : C::kKStages)) & 1) ^ 1;
@@ -706,9 +786,6 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
               if (d == 192) copy_rows<8, 16>(dst, mw, lane, base, o);
             }
           } else {
-            if (side == 1 && !(ok = wait(bars->raw_full[1][slot], raw_parity >> (4 + slot) & 1u)))
-              break;
-            raw_parity ^= 1u << (side * 4 + slot);
             const uint32_t raw = raw_at(side, slot) + mw * 32 * d;
             auto nothing = [] {};
             auto next = [&] {  // (the slot's rows have been read)
@@ -723,49 +800,23 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
               widen_rows<4, 8, 192>(dst, mw, lane, ring, raw, base, o, next);
             }
           }
-          cp_commit();
-          if (side == 0) {
-            // Where some row does not see some key, values that are not finite may not reach the
-            // product (0 times them is NaN): they are looked for before the tile's keys are handed
-            // on, zeros take their place, and the rows that see them become NaN by their sum.
-            uint32_t bad = 0;
-            if (is_edge) {
-              constexpr int kChunks = DV / (E4M3 ? 16 : 8), kRows = 32 / kChunks;
-              constexpr int kBatch = kChunks < 8 ? kChunks : 8;
-#pragma unroll 1
-              for (int i0 = 0; i0 < kChunks; i0 += kBatch) {
-                uint4 v[kBatch];
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                  const int at = (i0 + i) * 32 + lane, row = at / kChunks, c = at - row * kChunks;
-                  const long long from = __shfl_sync(0xffffffffu, vo, row);
-                  v[i] = make_uint4(0, 0, 0, 0);
-                  if (from >= 0)
-                    v[i] = __ldg(reinterpret_cast<const uint4*>(vbase + from + c * 16));
-                }
-#pragma unroll
-                for (int i = 0; i < kBatch; ++i) {
-                  const uint32_t found = __ballot_sync(
-                      0xffffffffu, not_finite<E4M3>(v[i].x) || not_finite<E4M3>(v[i].y) ||
-                                       not_finite<E4M3>(v[i].z) || not_finite<E4M3>(v[i].w));
-#pragma unroll
-                  for (int k = 0; k < kRows; ++k)
-                    if (found >> (k * kChunks) & ((1u << kChunks) - 1u))
-                      bad |= 1u << ((i0 + i) * kRows + k);
-                }
-              }
-              if (bad >> lane & 1u) vo = -1;
-            }
-            if (lane == 0) {
-              bars->there[step % kKeyRing][mw] = bits;
-              bars->bad[step % kKeyRing][mw] = bad;
-            }
+          if constexpr (!E4M3) {
+            cp_commit();
+            if (side == 0 && is_edge) take_out();
+          }
+          if (side == 0 && lane == 0) {
+            bars->there[step % kKeyRing][mw] = bits;
+            bars->bad[step % kKeyRing][mw] = bad;
+          }
+          if constexpr (E4M3) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(side ? &bars->v_full[st] : &bars->k_full[st]));
+            continue;
           }
           by_rows |= 1u << (issued & 31);
           ++issued;
-          if (E4M3) {
-            tell(issued);
-          } else if (issued - told > kAhead) {
+          if (issued - told > kAhead) {
             cp_wait<kAhead>();
             tell(issued - kAhead);
           }
@@ -774,15 +825,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       if constexpr (C::kSpareQ) {
         if (ok && twin) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->spare_free));
+          if (lane == 0) mbar_arrive(smem_u32(&bars->spare_free[team]));
         }
-        was_pair = !twin;
+        since = twin ? min(since + 1, C::kKStages) : 0;
       }
       if (!ok) break;
     }
     cp_wait<0>();
     if (ok && told != issued) tell(issued);
-    if (!ok && lane == 0) {
+    if (!E4M3 && !ok && lane == 0) {
       // let every copy already issued land before the CTA's memory is released
       for (uint32_t s = step + 1 > C::kKStages ? step + 1 - C::kKStages : 0; s <= step; ++s)
         mbar_wait_drain(smem_u32(&bars->k_full[s % C::kKStages]), (s / C::kKStages) & 1);
@@ -829,15 +880,29 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       float f1 = P.scale_log2, f2_ = 1.f;
       bool odd_c = false;
       if constexpr (E4M3) {
-        if (P.cache.k.scale != nullptr) {
-          int e1, e2;
-          const float a = frexpf(P.scale_log2, &e1);
-          const float b = frexpf(__ldg(P.cache.k.scale + item.head), &e2);
-          const int e = e1 + e2, h = e >> 1;
-          f1 = ldexpf(a * b, h);
-          f2_ = ldexpf(1.f, e - h);
-          odd_c = e < -120 || e > 120;
+        // the row's queries to fp16; of a single tile's unit by the first warpgroup for both
+        if (!(ok = mbar_wait_warp(smem_u32(&bars->q_full), n & 1, ab))) break;
+        int shift = 0;
+        if (live && !(twin && w == 1)) {
+          shift = query_to_f16<DQK>(sQ + w * C::kQTile + r * 128, r);
+          if (twin) bars->twin[1][r].x = __int_as_float(shift);  // (until the unit's end)
         }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->q_f16));
+        if (twin && w == 1) {
+          if (!(ok = mbar_wait_warp(smem_u32(&bars->q_f16), n & 1, ab))) break;
+          if (live) shift = __float_as_int(bars->twin[1][r].x);
+        }
+        int e1, e2;
+        const float a = frexpf(P.scale_log2, &e1);
+        const float b =
+            frexpf(P.cache.k.scale != nullptr ? __ldg(P.cache.k.scale + item.head) : 1.f, &e2);
+        // (beyond these ends every weight is 0 or 1 all the same)
+        const int e = min(250, max(-240, e1 + e2 - shift)), h = e >> 1;
+        f1 = ldexpf(a * b, h);
+        f2_ = ldexpf(1.f, e - h);
+        odd_c = e < -120 || e > 120;
       }
       const float c = f1 * f2_;
       float m = -INFINITY, l = 0.f;
@@ -846,47 +911,51 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         ++cnt;
         tc_fence_after();
         if (live) {
-          uint32_t sr[4][32];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) tmem_ld32(tS + q * 32, sr[q]);
           const uint4 there =
               *reinterpret_cast<const uint4*>(bars->there[(step0 + t) % kKeyRing]);
           const int kbase = key0 + t * kTile;
-          tmem_ld_wait();
           // some row does not see some key of the tile: one that is not there, one after the
           // unit's first position, one in front of its last one's window
           const bool edge = (there.x & there.y & there.z & there.w) != ~0u ||
                             kbase + kTile - 1 > right || kbase < left;
-          float mx[8];
+          uint4 see = make_uint4(~0u, ~0u, ~0u, ~0u);  // the keys that this row sees
           bool sees_bad = false;
-#pragma unroll
-          for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
           if (edge) {
             const uint4 bad = *reinterpret_cast<const uint4*>(bars->bad[(step0 + t) % kKeyRing]);
             // the row's keys, relative to the tile: klo .. khi - 1
             const int khi = first_pos + rt + 1 - kbase, klo = see0 - kbase;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            auto seen = [&](int q, uint32_t bits, uint32_t bads) -> uint32_t {
               const int a = min(32, max(0, klo - 32 * q)), b = min(32, max(0, khi - 32 * q));
-              uint32_t bits = q == 0 ? there.x : q == 1 ? there.y : q == 2 ? there.z : there.w;
               bits &= b >= 32 ? ~0u : (1u << b) - 1u;
               bits &= a >= 32 ? 0u : ~0u << a;
-              sees_bad |= (bits & (q == 0 ? bad.x : q == 1 ? bad.y : q == 2 ? bad.z : bad.w)) != 0;
+              sees_bad |= (bits & bads) != 0;
+              return bits;
+            };
+            see = make_uint4(seen(0, there.x, bad.x), seen(1, there.y, bad.y),
+                             seen(2, there.z, bad.z), seen(3, there.w, bad.w));
+          }
+          // 32 columns of the scores, those that the row does not see -inf
+          auto load = [&](int q, uint32_t (&s)[32]) {
+            tmem_ld32(tS + q * 32, s);
+            tmem_ld_wait();
+            if (edge) {
+              const uint32_t bits = q == 0 ? see.x : q == 1 ? see.y : q == 2 ? see.z : see.w;
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float x = (bits >> e) & 1u ? __uint_as_float(sr[q][e]) : -INFINITY;
-                sr[q][e] = __float_as_uint(x);
-                mx[e & 7] = fmaxf(mx[e & 7], x);
-              }
+              for (int e = 0; e < 32; ++e)
+                if (!(bits >> e & 1u)) s[e] = 0xFF800000u;
             }
-          } else {
+          };
+          float mx[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+          for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+#pragma unroll kPart
+          for (int q = 0; q < 4; ++q) {
+            uint32_t s[32];
+            load(q, s);
 #pragma unroll
-              for (int e = 0; e < 32; e += 2)
-                mx[(e >> 1) & 7] = max3(mx[(e >> 1) & 7], __uint_as_float(sr[q][e]),
-                                        __uint_as_float(sr[q][e + 1]));
-            }
+            for (int e = 0; e < 32; e += 2)
+              mx[(e >> 1) & 7] = max3(mx[(e >> 1) & 7], __uint_as_float(s[e]),
+                                      __uint_as_float(s[e + 1]));
           }
           const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                                   fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
@@ -896,11 +965,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           const bool resc = !none && (m_new - m) * f1 * f2_ > 8.0f;
           const float m_use = none ? 0.f : (resc ? m_new : m);
           const float alpha = resc ? ex2((m - m_use) * f1 * f2_) : 1.0f;
-          uint32_t pk0[32], pk1[32];
-          const bool far = row_ok && (odd_c || !(fabsf(m_use * c) <= 65536.f));
-          float sum;
-          if (__any_sync(0xffffffffu, far)) sum = prefill_exp<true>(sr, f1, f2_, m_use, pk0, pk1);
-          else sum = prefill_exp<false>(sr, f1, f2_, m_use, pk0, pk1);
+          const bool far = __any_sync(
+              0xffffffffu, row_ok && (odd_c || !(fabsf(m_use * c) <= 65536.f)));
           if (t > lo && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
             for (int q = 0; q < DV / 32; ++q) {
@@ -913,10 +979,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
               tmem_st32(tO + q * 32, ov);
             }
           }
-          l = sees_bad ? NAN : l * alpha + sum;
+          uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll kPart
+          for (int q = 0; q < 4; ++q) {  // (P's columns lie where scores have been read)
+            uint32_t s[32], p[16];
+            load(q, s);
+            prefill_exp<E4M3>(s, far, f1, f2_, m_use, rs2, p);
+            tmem_st16(tS + q * 16, p);
+          }
+          const uint64_t s4 = add2(add2(rs2[0], rs2[1]), add2(rs2[2], rs2[3]));
+          l = sees_bad ? NAN : l * alpha + (f2_lo(s4) + f2_hi(s4));
           m = none ? -INFINITY : m_use;
-          tmem_st32(tS, pk0);
-          tmem_st32(tS + 32, pk1);
           tmem_st_wait();
         }
         tc_fence_before();
@@ -931,6 +1004,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       done[0] += mine;
       float a_mine = 1.f, a_theirs = 0.f;
       float top = m * f1 * f2_;  // in base 2
+      if constexpr (E4M3) {  // scores beyond fp32, whose products with fp16 queries are within
+        if (top == INFINITY) l = NAN;
+        else if (top == -INFINITY && l > 0.f) l = 0.f;
+      }
       int q0 = 0, q1 = DV / 32;  // this warpgroup's columns, in 32s
       if (twin) {
         if (theirs && !(ok = mbar_wait_warp(smem_u32(&bars->o_done[w ^ 1]), done[1] & 1, ab)))
@@ -962,7 +1039,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
       const bool no_key = l == 0.f;
-      const float factor = (no_key ? 0.f : whole ? 1.0f / l : 1.0f) * v_scale;
+      constexpr float kUnlift = E4M3 ? 1.f / 128.f : 1.f;
+      l *= kUnlift;
+      const float factor = (no_key ? 0.f : whole ? 1.0f / l : 1.0f) * kUnlift * v_scale;
       const int64_t srow = (int64_t)slot * kPrefillRows + (twin ? 0 : w * kTile) + r;
       if (live) {
 #pragma unroll 1
@@ -1025,7 +1104,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == kPrefillMmaWarp) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
@@ -1193,7 +1272,7 @@ cudaError_t launch_prefill_typed(const PrefillLaunch& L, const Offsets& off) {
   cudaError_t e =
       cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return e;
-  k<<<grid, kPrefillThreads, C::kSmemBytes, L.stream>>>(L.tm_q, L.tm_k, L.tm_v, P, off);
+  k<<<grid, C::kThreads, C::kSmemBytes, L.stream>>>(L.tm_q, L.tm_k, L.tm_v, P, off);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   PrefillJoin J;
   J.desc = L.desc;

@@ -357,8 +357,9 @@ __host__ __device__ constexpr uint64_t mnmajor_step(int kk) {
 // Instruction descriptor, kind::f16: bf16 A and B, fp32 D, dense.
 // Bits: D format 4-5 (1 = f32), A format 7-9 (1 = bf16), B format 10-12,
 // A major 15 / B major 16 (1 = MN-major), N >> 3 in 17-22, M >> 4 in 24-28.
+constexpr uint32_t kIdescBf16 = (1u << 7) | (1u << 10);  // A and B bf16; without: both fp16
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major, bool b_mn_major) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | ((a_mn_major ? 1u : 0u) << 15) |
+  return (1u << 4) | kIdescBf16 | ((a_mn_major ? 1u : 0u) << 15) |
          ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) |
          ((uint32_t)(M >> 4) << 24);
 }
