@@ -193,12 +193,12 @@ __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-// Whether a word of two bf16 or four e4m3 values holds one that is not finite (all exponent bits
-// set; all seven bits of an e4m3 value, whose NaN that is).
+// Bits for the values of a word (two bf16, four e4m3) that are not finite: all exponent bits set; all
+// seven bits of an e4m3 value, whose NaN that is.
 template <bool E4M3>
-__device__ __forceinline__ bool not_finite(uint32_t x) {
-  if constexpr (E4M3) return (((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-  return (x & 0x7F80u) == 0x7F80u || (x & 0x7F800000u) == 0x7F800000u;
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  if constexpr (E4M3) return ((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+  return ((x & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
 }
 
 // Four e4m3 values as two words of fp16 pairs (exact: an fp16 has every e4m3 value).
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
     // others wait for.
     auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
       if constexpr (E4M3) return mbar_wait_warp(smem_u32(&bar), parity, ab);
-      if (__all_sync(0xffffffffu, mbar_try_wait(smem_u32(&bar), parity))) return true;
+      if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(&bar), parity))) return true;
       cp_wait<0>();
       if (told != issued) tell(issued);
       return mbar_wait_warp(smem_u32(&bar), parity, ab);
@@ -727,31 +727,25 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
         // product (0 times them is NaN): they are looked for before the tile's keys are handed
         // on, zeros take their place, and the rows that see them become NaN by their sum.
         uint32_t bad = 0;
+        // (A lane reads its own row: the little code matters, which is seldom in the cache.)
         auto take_out = [&] {
-          constexpr int kChunks = DV / (E4M3 ? 16 : 8), kRows = 32 / kChunks;
-          constexpr int kBatch = kChunks < 8 ? kChunks : 8;
+          constexpr int kChunks = DV / (E4M3 ? 16 : 8), kBatch = kChunks < 8 ? kChunks : 8;
+          uint32_t found = 0;
 #pragma unroll 1
           for (int i0 = 0; i0 < kChunks; i0 += kBatch) {
             uint4 v[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-              const int at = (i0 + i) * 32 + lane, row = at / kChunks, c = at - row * kChunks;
-              const long long from = __shfl_sync(0xffffffffu, vo, row);
               v[i] = make_uint4(0, 0, 0, 0);
-              if (from >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(vbase + from + c * 16));
+              if (vo >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(vbase + vo) + i0 + i);
             }
 #pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-              const uint32_t found = __ballot_sync(
-                  0xffffffffu, not_finite<E4M3>(v[i].x) || not_finite<E4M3>(v[i].y) ||
-                                   not_finite<E4M3>(v[i].z) || not_finite<E4M3>(v[i].w));
-#pragma unroll
-              for (int k = 0; k < kRows; ++k)
-                if (found >> (k * kChunks) & ((1u << kChunks) - 1u))
-                  bad |= 1u << ((i0 + i) * kRows + k);
-            }
+            for (int i = 0; i < kBatch; ++i)
+              found |= not_finite<E4M3>(v[i].x) | not_finite<E4M3>(v[i].y) |
+                       not_finite<E4M3>(v[i].z) | not_finite<E4M3>(v[i].w);
           }
-          if (bad >> lane & 1u) vo = -1;
+          bad = __ballot_sync(0xffffffffu, found != 0);
+          if (found != 0) vo = -1;
         };
         if (E4M3 && is_edge) take_out();  // (for the keys' warps too, which hand the bits on)
 #pragma unroll 1
@@ -802,7 +796,10 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
           }
           if constexpr (!E4M3) {
             cp_commit();
-            if (side == 0 && is_edge) take_out();
+            if (side == 0 && is_edge) {
+              take_out();
+              cp_wait<0>();  // (the keys came meanwhile)
+            }
           }
           if (side == 0 && lane == 0) {
             bars->there[step % kKeyRing][mw] = bits;
@@ -816,7 +813,9 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
           }
           by_rows |= 1u << (issued & 31);
           ++issued;
-          if (issued - told > kAhead) {
+          if (side == 0 && is_edge) {
+            tell(issued);
+          } else if (issued - told > kAhead) {
             cp_wait<kAhead>();
             tell(issued - kAhead);
           }
