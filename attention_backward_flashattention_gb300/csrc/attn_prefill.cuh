@@ -149,7 +149,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // of the maximum that they are taken by, and the least, below 2^-32, are zero.
 // kFar: the scores are so large that c m, rounded, is off by more than 2^-8: differences first, and
 // c in two factors.
-constexpr int kPart = 1;
 constexpr float kLift = 7.f;
 template <bool kF16>
 __device__ __forceinline__ void prefill_exp(const uint32_t (&sr)[32], bool far, float f1, float f2_,
@@ -271,9 +270,9 @@ __device__ __forceinline__ void copy_rows(uint32_t tile, int mw, int lane, const
   }
 }
 // e4m3 rows, widened: from the ring (raw: the warp's rows there, D bytes each) or from the cache.
-// Two chunks at a time: what one loads covers the other's latency, and a longer loop ran slower in
-// the kernel.  (Bits moved by hand and one product instead of the conversions, with NaN looked for,
-// took up to three times as long.)  The eight lanes of a row write to eight places of the swizzle's
+// Four chunks at a time (with two: 233 to 229 us for 64 x 5 tokens over 4000, 64 heads; 192 columns,
+// 2048 over 8000: 273 to 261; all eight, with the code that no longer stays in the cache: 1043 to
+// 1250).  The eight lanes of a row write to eight places of the swizzle's
 // period at once: those of the odd panel their second half first.
 template <int CH, int C0, int D, typename Behind>
 __device__ __forceinline__ void widen_rows(uint32_t tile, int mw, int lane, bool ring, uint32_t raw,
@@ -285,21 +284,21 @@ __device__ __forceinline__ void widen_rows(uint32_t tile, int mw, int lane, bool
   raw += row0 * D + c * 16;
   base += c * 16;
 #pragma unroll 1
-  for (int p = 0; p < CH; p += 2) {
-    uint4 v[2];
+  for (int p = 0; p < CH; p += 4) {
+    uint4 v[4];
     if (ring) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) v[i] = lds128(raw + (p + i) * kStep * D);
+      for (int i = 0; i < 4; ++i) v[i] = lds128(raw + (p + i) * kStep * D);
     } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const long long from = __shfl_sync(0xffffffffu, o, (p + i) * kStep + row0);
         v[i] = make_uint4(0, 0, 0, 0);
         if (from >= 0) v[i] = __ldg(reinterpret_cast<const uint4*>(base + from));
       }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const uint32_t in8 = ((p + i) * kStep & 7) + row0, at = dst + (p + i) * kStep * 128;
       uint32_t a[4], b[4];
       e4m3_to_f16(odd ? v[i].z : v[i].x, a[0], a[1]);
@@ -944,20 +943,36 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
                 if (!(bits >> e & 1u)) s[e] = 0xFF800000u;
             }
           };
-          float mx[8];
+          float top;
+          if (!edge) {
+            constexpr int kReds = E4M3 ? 2 : 4;  // columns in 32s at a time (registers)
+            float mx[kReds];
+            top = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < 4; q += kReds) {
+              uint32_t s[kReds][32];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
-#pragma unroll kPart
-          for (int q = 0; q < 4; ++q) {
-            uint32_t s[32];
-            load(q, s);
+              for (int i = 0; i < kReds; ++i) mx[i] = tmem_ld32_max(tS + (q + i) * 32, s[i]);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              mx[(e >> 1) & 7] = max3(mx[(e >> 1) & 7], __uint_as_float(s[e]),
-                                      __uint_as_float(s[e + 1]));
+              for (int i = 0; i < kReds; ++i) top = fmaxf(top, mx[i]);
+            }
+          } else {
+            float mx[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+              uint32_t s[32];
+              load(q, s);
+#pragma unroll
+              for (int e = 0; e < 32; e += 2)
+                mx[(e >> 1) & 7] = max3(mx[(e >> 1) & 7], __uint_as_float(s[e]),
+                                        __uint_as_float(s[e + 1]));
+            }
+            top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                        fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
           }
-          const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                  fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
           // the maximum moves (and O is rescaled) only when it grows by more than 2^8
           const float m_new = fmaxf(m, top);
           const bool none = m_new == -INFINITY;  // no key seen yet, or scores of -inf alone
@@ -979,7 +994,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
             }
           }
           uint64_t rs2[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll kPart
+#pragma unroll 1
           for (int q = 0; q < 4; ++q) {  // (P's columns lie where scores have been read)
             uint32_t s[32], p[16];
             load(q, s);
