@@ -587,8 +587,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (!(ok = mbar_wait_warp(smem_u32(&bars->s_full[w]), cnt & 1, ab))) break;
         tc_fence_after();
         uint32_t sr[4][32];
+        float top[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sr[c]);
+        for (int c = 0; c < 4; ++c) top[c] = tmem_ld32_max(tS + c * 32, sr[c]);
         tmem_ld_wait();
         const int kbase = j * kTile;
         // some row of the tile does not see all of its keys: the band's right
@@ -597,15 +598,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             (sh.wr >= 0 && kbase + kTile - 1 > qt * kTile + band_off(sh, it) + sh.wr) ||
             (sh.wl >= 0 && kbase < qt * kTile + kTile - 1 + band_off(sh, it) - sh.wl) ||
             (kbase + kTile > it.Lk);
-        // row maximum over 8 independent chains (a single chain is latency-bound)
-        float mx[8];
-#pragma unroll
-        for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
+        float rowmax = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         if (need_mask) {  // edge or ragged tile: keys outside the row's band -> -inf
           // this row's visible keys, relative to the tile: [klo, khi)
           const int klo = sh.wl >= 0 ? qidx + band_off(sh, it) - sh.wl - kbase : INT_MIN / 2;
           const int khi =
               min(it.Lk, sh.wr >= 0 ? qidx + band_off(sh, it) + sh.wr + 1 : it.Lk) - kbase;
+          // row maximum over 8 independent chains (a single chain is latency-bound)
+          float mx[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) mx[u] = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
 #pragma unroll
@@ -616,17 +618,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               mx[e & 7] = fmaxf(mx[e & 7], x);
             }
           }
-        } else {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              mx[(e >> 1) & 7] = max3(mx[(e >> 1) & 7], __uint_as_float(sr[c][e]),
-                                      __uint_as_float(sr[c][e + 1]));
-          }
+          rowmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                         fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
         }
-        const float rowmax = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
-                                   fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])));
         // all PV products of this warpgroup issued before this S are complete
         // (tensor-core work completes in issue order), so O is stable here
         const float m_new = fmaxf(m, rowmax * scale_log2);
