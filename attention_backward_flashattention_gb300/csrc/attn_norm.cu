@@ -10,7 +10,8 @@
 // (of 4, 8 or 16), a unit of 16 columns each: both of its sums are shuffles, a pair of columns is
 // always in one lane, and a lane keeps its columns' weights, and the sums of their gradients, from
 // head to head.  The sums over rows are taken in a fixed order: by lane, block, and then over the
-// blocks in a second launch.
+// blocks in a second launch.  Measured, 16384 tokens, 32 + 8 heads of 128 (device time): forward 57 us
+// (5.9 TB/s, 88 % of a copy), backward 90 us (5.6 TB/s, 83 %).
 #include <algorithm>
 #include <cstring>
 

@@ -5,22 +5,32 @@
 // 2^(c (s_j - m)), s_j = q . k_j, c = scale log2(e) (times the key head's scale of an e4m3 cache),
 // m a running maximum of the scores.  LSE = ln 2 (c m + log2 sum w).
 //
-// One CTA (512 threads) per SM, each with an equal share of the line of key tiles
+// One CTA per SM (512 threads; e4m3: 640), each with an equal share of the line of key tiles
 // (attn_prefill.h):
-//   warps 0-3, 4-7  softmax warpgroup w: thread = query row (TMEM lane) of query tile w
+//   warps 0-3, 4-7  softmax warpgroup w: thread = query row (TMEM lane) of query tile w.  e4m3: turns
+//                   its row of queries into fp16 first
 //   warps 8-11      key and value rows from their pages to shared memory, 32 rows of a tile
 //                   each.  Tiles whose keys every row sees come by TMA, in boxes of rows that lie
 //                   in one page; the others, and pages that no box divides, row by row, where rows
 //                   that nothing sees, and values that are not finite, become zeros on the way.
-//                   e4m3 boxes land in a ring of their own, and the warps widen them
-//   warp 12         MMA issuer: S_w = Q_w K^T, O_w += P_w V (tcgen05, accumulators in TMEM, P
+//   warps 8-15      e4m3: the same, four warps for the keys and four for the values.  The boxes land
+//                   in a ring of their own, and the warps widen them to fp16
+//   then one        MMA issuer: S_w = Q_w K^T, O_w += P_w V (tcgen05, accumulators in TMEM, P
 //                   in TMEM as the A operand)
-//   warp 13         walks over the share's units, loads their queries by TMA
-//   warp 14         e4m3: loads the ring
+//   one             walks over the share's units, loads their queries by TMA
+//   two             e4m3: load the ring, keys and values
 // A unit has two query tiles, or one whose key tiles the warpgroups take in turn (each with
 // its own O, joined in tensor memory at the end): with few rows the chain S -> softmax -> PV of
 // one tile runs beside the other's.  Parts of a unit that is cut leave unnormalised sums in the
 // workspace, and a second launch joins them in a fixed order.
+//
+// Bound, where there are many rows: the chain S -> softmax -> PV of the two tiles.  A pair of tiles
+// takes 4080 cycles, its products 2050, its exponentials 2050.  With few rows: memory (bf16), or
+// the widening (e4m3).  The roles run from one instruction cache: the softmax is a loop over
+// 32 columns, and its unrolled form took 234 us where the loop took 212 (8 x 256 tokens over 4096,
+// e4m3), through stalls for instructions.  Measured (32 query and 8 key heads of 128, device time): 2048 tokens over 30011
+// 927 us (1123 TFLOP/s; e4m3 1010), 8192 of a prompt 540, 32 x 5 tokens over 4000 109 (4.8 TB/s), 64
+// single tokens over 8000 351 (6.0 TB/s), 8 x 256 over 4096 181 (e4m3 195); the smallest call 15.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -64,16 +74,16 @@ struct PrefillCfg {
   static_assert(kSmemBytes <= kPrefillMaxSmem, "shared memory budget");
   static constexpr uint32_t kTmemO = 256;
   // Whether a step's products of P and V go in front of the wait for the next step's keys, or
-  // behind.  In front where keys come late (192 columns: 295 to 270 us for 2048 tokens over 8000;
-  // e4m3: 598 to 563 us for 64 single tokens over 8000); elsewhere the shorter code is faster
-  // (128 columns: 957 and 1008 us for 2048 over 30011).
-  static constexpr bool kLateKeys = E4M3 || DQK == 192;
-  // Registers a thread after the split of 512 x 128: softmax, copies, MMA and walk.
-  // (64 single tokens over 8000, bf16: 377 us with 184, 80 and 64, 362 with 192, 64 and 64, 389 with
-  // 200, 56 and 56; 192 columns: 300, 300 and 319 where 184, 72 and 72 take 295)
+  // behind.  In front where keys come late, with one or two stages of 192 columns (279 to 247 us for
+  // 2048 tokens over 8000); elsewhere the shorter code is faster (128 columns, 2048 over 30011: 927
+  // and 976 us, e4m3 1010 and 1039).
+  static constexpr bool kLateKeys = DQK == 192;
+  // Registers a thread at launch and after the split: softmax, copies, MMA and walk.  bf16 (64 single
+  // tokens over 8000): 351 us with 192, 64 and 64, 365 with 160, 96 and 96.  e4m3 (64 such, 64
+  // heads): 380 us with 112, 96 and 64, 388 with 120, 88 and 64.
   static constexpr uint32_t kRegs = E4M3 ? 96 : 128;
-  static constexpr uint32_t kRegsSoftmax = E4M3 ? 120 : DQK == 192 ? 184 : 192;
-  static constexpr uint32_t kRegsCopy = E4M3 ? 88 : DQK == 192 ? 72 : 64;
+  static constexpr uint32_t kRegsSoftmax = E4M3 ? 112 : DQK == 192 ? 184 : 192;
+  static constexpr uint32_t kRegsCopy = E4M3 ? 96 : DQK == 192 ? 72 : 64;
   static constexpr uint32_t kRegsCtl = E4M3 ? 64 : DQK == 192 ? 72 : 64;
   static_assert(2 * kRegsSoftmax + (E4M3 ? 2 : 1) * kRegsCopy + kRegsCtl <= kThreads / 128 * kRegs,
                 "register split");

@@ -78,8 +78,8 @@ __host__ __device__ inline PrefillUnit make_prefill_unit(const PrefillShape& sh,
 // 8: 28.5, 29.8, 31.8, 40.0, 47.1; 512 tokens over none: 24.6, 25.2, 24.5, 36.5, 22.1.
 constexpr int kPrefillMinCost = 3;
 constexpr int kPrefillTol = 4;       // a unit's parts cost about as much as two tiles
-constexpr int kPrefillUnitCost = 4;  // of a unit besides its tiles (8192 tokens of a prompt: 770 us
-                                     // with 0, 658 with 2, 580 with 4, 590 with 6)
+constexpr int kPrefillUnitCost = 3;  // of a unit besides its tiles (8192 tokens of a prompt: 551 us
+                                     // with 2, 540 with 3, 553 with 4; 4 x 512: 38.6, 36.4, 36.2)
 __host__ __device__ inline int unit_cost(int tiles) { return tiles + kPrefillUnitCost; }
 struct PrefillLine {
   long long total;  // cost of all units

@@ -592,7 +592,9 @@ int attn_decode(const attn_paged_cache* cache, const int* block_table, int max_p
  * be finite), and so does a largest score beyond fp32.
  * Weights enter the second product rounded to bf16 (their sum is of unrounded
  * ones): O is off by at most 2^-8 of the sum of |w_j v_j| besides its own
- * rounding.
+ * rounding.  Over an e4m3 cache the operands are fp16: each row of queries times
+ * a power of two, exact but for elements below 2^-28 of the row's largest, and
+ * weights of 11 bits down to 2^-21 of the largest so far, zero below 2^-32.
  *
  * The work is cut into equal shares of key tiles, at places that depend on the
  * lengths alone, and parts of a row are joined in a fixed order by a second
