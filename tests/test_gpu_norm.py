@@ -175,6 +175,26 @@ def test_rows_of_zeros_and_extremes():
     assert torch.isnan(y[0, 3, 0]).all() and (y[0, 3, 1] == 0).all()
 
 
+def test_captured_step():
+    """Norms and their gradients in a graph, replayed, have the bits of the calls in turn."""
+    g = torch.Generator().manual_seed(2)
+    q, k, dq, dk = (_rand(g, 2, 700, h, 128) for h in (8, 2, 8, 2))
+    w = torch.rand(128, generator=g).cuda() + 0.5
+    norm, rot = binding.HeadNorm(w, w, EPS), binding.Rotation(inv_freq(128))
+    call = lambda: (*binding.norm_rope(q, k, norm, rot),
+                    *binding.norm_rope_backward(q, k, dq, dk, norm, rot))
+    want = call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for t in got:
+        t.fill_(7)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_weights_that_move():
     """A parameter whose memory is replaced: the next call reads the new one."""
     x = torch.randn(1, 5, 2, 64, device="cuda").to(torch.bfloat16)

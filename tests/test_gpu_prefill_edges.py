@@ -246,6 +246,30 @@ def test_windows_longer_than_anything(window):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d,group,new,lens", [((128, 128), 2, [9], [400]), ((64, 64), 1, [300], [700]),
+                                              ((192, 128), 4, [70, 1], [200, 900])])
+def test_queries_of_many_sizes(kind, d, group, new, lens):
+    """Rows from zero to large, and one element far above the others in a column without keys."""
+    heads, page = 2, 16
+    cache, q, kc, vc, ks, vs, table, lens_d = setup(3, heads, group, *d, page, kind, "token", new,
+                                                    lens, poison=False)
+    bits(kc)[..., 5] = 0
+    sizes = torch.tensor([0.0, 2.0 ** -133, 2.0 ** -110, 2.0 ** -40, 2.0 ** -3, 1.0, 2.0])
+    rows = sum(new) * heads * group
+    of = sizes[torch.arange(rows) % len(sizes)].view(sum(new), heads * group, 1).cuda()
+    q = (q.float() * of).to(torch.bfloat16)
+    for spike in (None, 2.0 ** 16, 3e38):
+        if spike is not None:
+            q[..., 5] = spike
+            if spike > 1e30:  # (the others' exact value no longer counts beside it)
+                q[..., :5], q[..., 6:] = 0, 0
+        got = binding.prefill(cache, q, table, lens_d, cu_seqlens=_offsets(new))
+        check(got, prefill64(q, kc, vc, table, lens, new, page, 1 / math.sqrt(d[0]), -1, ks, vs),
+              f"spike {spike}")
+    assert binding.attn_cache_status() == binding.ATTN_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 def test_many_sequences(kind):
     """More units than a CTA has threads, and more sequences than a table of offsets takes."""
     heads, group, page, d = 1, 2, 16, 64
