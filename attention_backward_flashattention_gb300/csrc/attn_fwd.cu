@@ -287,6 +287,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         int item = blockIdx.x;
         if (item_iter > 0) {
+          fence_proxy_async_smem();  // (the answer in front of this one has been read)
           mbar_arrive_expect_tx(clc, 16);
           clc_ask(answer, clc);
           ++asked;
