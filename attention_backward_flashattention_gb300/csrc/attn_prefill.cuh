@@ -29,14 +29,15 @@
 // the widening (e4m3).  The roles run from one instruction cache: the softmax is a loop over
 // 32 columns, and its unrolled form took 234 us where the loop took 212 (8 x 256 tokens over 4096,
 // e4m3), through stalls for instructions.  Measured (32 query and 8 key heads of 128, device time): 2048 tokens over 30011
-// 927 us (1123 TFLOP/s; e4m3 1010), 8192 of a prompt 540, 32 x 5 tokens over 4000 109 (4.8 TB/s), 64
-// single tokens over 8000 351 (6.0 TB/s), 8 x 256 over 4096 181 (e4m3 195); the smallest call 15.
+// 905 us (1151 TFLOP/s; e4m3 992), 8192 of a prompt 528, 32 x 5 tokens over 4000 111 (4.7 TB/s), 64
+// single tokens over 8000 352 (6.0 TB/s), 8 x 256 over 4096 164 (e4m3 180); the smallest call 15.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <climits>
+#include <type_traits>
 
 #include "attn_internal.h"
 #include "attn_prefill.h"
@@ -1137,7 +1138,10 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
 // ----------------------------------------------------------------------------
 // Join of the units that were cut.  One warp for up to eight parts of a row, two, four or eight for
 // more (a unit's parts are as many for each of its rows): a lane has DV / 32 columns of a part on
-// their way for each of the warp's, and the warps' sums meet in shared memory, in order.
+// their way for each of the warp's, and the warps' sums meet in shared memory, in order.  With two
+// parts, as most units have that are cut, a warp has four rows on their way, with up to four
+// parts two (8 x 256 tokens over 4096, 32 and 8 heads: 181 us with one row, 164 so, 172 with twice as
+// many, whose registers leave an SM one block).  Units of few rows: one, 110 and 112 us for 32 x 5.
 // ----------------------------------------------------------------------------
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 struct PrefillJoin {
@@ -1150,6 +1154,12 @@ struct PrefillJoin {
 };
 __device__ __forceinline__ int join_team(int parts) {  // warps of a row
   return parts <= 8 ? 1 : parts <= 16 ? 2 : parts <= 32 ? 4 : 8;
+}
+__device__ __forceinline__ int join_rows(int parts, int rows) {  // rows of a warp at a time
+  return rows <= 32 ? 1 : parts <= 2 ? 4 : parts <= 4 ? 2 : 1;
+}
+__device__ __forceinline__ float join_weight(float m, float top) {
+  return m == top ? (top == -INFINITY ? 0.f : 1.f) : ex2(m - top);
 }
 
 template <int DV>
@@ -1166,8 +1176,9 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const Prefil
   int groups = 0;
   if (tid < P.shares) {
     const PrefillDesc d = P.desc[tid];
-    const int rows = kJoinWarps / join_team(d.parts);  // of a block at a time
-    groups = d.parts > 0 ? (d.tokens * P.group + rows - 1) / rows : 0;
+    const int all = d.tokens * P.group;
+    const int rows = kJoinWarps / join_team(d.parts) * join_rows(d.parts, all);  // of a block at a time
+    groups = d.parts > 0 ? (all + rows - 1) / rows : 0;
   }
   int x = groups;
 #pragma unroll
@@ -1192,13 +1203,85 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const Prefil
       if (upto[mid] <= i) lo = mid; else hi = mid - 1;
     }
     const PrefillDesc d = P.desc[lo];
+    const int rows = d.tokens * P.group;
+    // a row's place among the slot's: two tiles of per_tile tokens
+    auto place_of = [&](int row) {
+      const int tok = row / P.group, w = tok / P.per_tile;
+      return w * kTile + row - w * P.per_tile * P.group;
+    };
+    auto load = [&](int64_t s, float (&x)[kV]) {
+      const float* src = P.acc + s * DV + lane * kV;
+      if constexpr (kV == 4) {
+        const float4 y = *reinterpret_cast<const float4*>(src);
+        x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
+      } else {
+        const float2 y = *reinterpret_cast<const float2*>(src);
+        x[0] = y.x, x[1] = y.y;
+      }
+    };
+    auto store = [&](int row, float top, float sum, const float (&x)[kV]) {
+      const bool no_key = sum == 0.f;
+      const float inv = no_key ? 0.f : 1.0f / sum;
+      const int tok = row / P.group;
+      const int64_t out =
+          (int64_t)(d.tok0 + tok) * P.Hq + d.head * P.group + (row - tok * P.group);
+      uint32_t pk[kV / 2];
+#pragma unroll
+      for (int k = 0; k < kV / 2; ++k) pk[k] = pack_bf16(x[2 * k] * inv, x[2 * k + 1] * inv);
+      __nv_bfloat16* dst = P.o + out * DV + lane * kV;
+      if constexpr (kV == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+      else *reinterpret_cast<uint32_t*>(dst) = pk[0];
+      if (lane == 0 && P.lse != nullptr)
+        P.lse[out] = no_key ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+    };
+    // ROWS rows of PARTS parts at most, at once
+    auto few = [&](auto rows_of, auto parts_of) {
+      constexpr int kRows = decltype(rows_of)::value, kParts = decltype(parts_of)::value;
+      const int row0 = ((i - upto[lo]) * kJoinWarps + warp) * kRows;
+      if (row0 >= rows) return;
+      float v[kRows][kParts][kV];
+      float2 ml[kRows][kParts];
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int place = place_of(min(row0 + r, rows - 1));
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+          const int64_t s = (int64_t)prefill_slot(lo, min(p, d.parts - 1)) * kPrefillRows + place;
+          ml[r][p] = P.ml[s];
+          load(s, v[r][p]);
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        float top = ml[r][0].x, sum = 0.f, x[kV];
+#pragma unroll
+        for (int p = 1; p < kParts; ++p) top = fmaxf(top, ml[r][p].x);
+#pragma unroll
+        for (int k = 0; k < kV; ++k) x[k] = 0.f;
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) {
+          if (p >= d.parts) break;
+          const float weight = join_weight(ml[r][p].x, top);
+          sum += ml[r][p].y * weight;
+#pragma unroll
+          for (int k = 0; k < kV; ++k) x[k] += v[r][p][k] * weight;
+        }
+        if (row0 + r < rows) store(row0 + r, top, sum, x);
+      }
+    };
+    const int at_once = join_rows(d.parts, rows);
+    if (at_once == 4) {
+      few(std::integral_constant<int, 4>{}, std::integral_constant<int, 2>{});
+      continue;
+    }
+    if (at_once == 2) {
+      few(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+      continue;
+    }
     const int team = join_team(d.parts), member = warp % team;
     const int row = (i - upto[lo]) * (kJoinWarps / team) + warp / team;
-    const bool there = row < d.tokens * P.group;
-    const int tok = row / P.group, h = row - tok * P.group;
-    // the row's place among the slot's: two tiles of per_tile tokens
-    const int w = tok / P.per_tile;
-    const int place = w * kTile + (tok - w * P.per_tile) * P.group + h;
+    const bool there = row < rows;
+    const int place = place_of(row);
     auto at = [&](int p) { return (int64_t)prefill_slot(lo, p) * kPrefillRows + place; };
     // this warp's parts: member, member + team, ...
     float top = -INFINITY, sum = 0.f, acc[kV];
@@ -1216,21 +1299,13 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const Prefil
         for (int q = 0; q < kFlight; ++q) {
           const int64_t s = at(min(p0 + q * team, d.parts - 1));
           ml[q] = P.ml[s];
-          const float* src = P.acc + s * DV + lane * kV;
-          if constexpr (kV == 4) {
-            const float4 f = *reinterpret_cast<const float4*>(src);
-            v[q][0] = f.x, v[q][1] = f.y, v[q][2] = f.z, v[q][3] = f.w;
-          } else {
-            const float2 f = *reinterpret_cast<const float2*>(src);
-            v[q][0] = f.x, v[q][1] = f.y;
-          }
+          load(s, v[q]);
         }
 #pragma unroll
         for (int q = 0; q < kFlight; ++q) {
           if (p0 + q * team >= d.parts) break;
           // (NaN stays: a part whose sums are not finite makes the row not finite)
-          const float weight =
-              ml[q].x == top ? (top == -INFINITY ? 0.f : 1.f) : ex2(ml[q].x - top);
+          const float weight = join_weight(ml[q].x, top);
           sum += ml[q].y * weight;
 #pragma unroll
           for (int k = 0; k < kV; ++k) acc[k] += v[q][k] * weight;
@@ -1250,7 +1325,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const Prefil
         for (int k = 0; k < kV; ++k) acc[k] = 0.f;
         for (int q = 0; q < team; ++q) {
           const float2 ml = met_ml[warp + q];
-          const float weight = ml.x == t2 ? (t2 == -INFINITY ? 0.f : 1.f) : ex2(ml.x - t2);
+          const float weight = join_weight(ml.x, t2);
           sum += ml.y * weight;
 #pragma unroll
           for (int k = 0; k < kV; ++k) acc[k] += met[warp + q][lane * kV + k] * weight;
@@ -1260,17 +1335,7 @@ __global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const Prefil
       __syncthreads();
     }
     if (!there || member != 0) continue;
-    const bool no_key = sum == 0.f;
-    const float inv = no_key ? 0.f : 1.0f / sum;
-    const int64_t out = (int64_t)(d.tok0 + tok) * P.Hq + d.head * P.group + h;
-    uint32_t pk[kV / 2];
-#pragma unroll
-    for (int k = 0; k < kV / 2; ++k) pk[k] = pack_bf16(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-    __nv_bfloat16* dst = P.o + out * DV + lane * kV;
-    if constexpr (kV == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
-    else *reinterpret_cast<uint32_t*>(dst) = pk[0];
-    if (lane == 0 && P.lse != nullptr)
-      P.lse[out] = no_key ? -INFINITY : (top + log2f(sum)) * 0.69314718055994530942f;
+    store(row, top, sum, acc);
   }
 }
 
