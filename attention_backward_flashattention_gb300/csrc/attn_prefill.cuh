@@ -30,7 +30,7 @@
 // 32 columns, and its unrolled form took 234 us where the loop took 212 (8 x 256 tokens over 4096,
 // e4m3), through stalls for instructions.  Measured (32 query and 8 key heads of 128, device time): 2048 tokens over 30011
 // 905 us (1151 TFLOP/s; e4m3 992), 8192 of a prompt 528, 32 x 5 tokens over 4000 111 (4.7 TB/s), 64
-// single tokens over 8000 352 (6.0 TB/s), 8 x 256 over 4096 164 (e4m3 180); the smallest call 15.
+// single tokens over 8000 352 (6.0 TB/s), 8 x 256 over 4096 162 (e4m3 178); the smallest call 15.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -1140,8 +1140,8 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
 // more (a unit's parts are as many for each of its rows): a lane has DV / 32 columns of a part on
 // their way for each of the warp's, and the warps' sums meet in shared memory, in order.  With two
 // parts, as most units have that are cut, a warp has four rows on their way, with up to four
-// parts two (8 x 256 tokens over 4096, 32 and 8 heads: 181 us with one row, 164 so, 172 with twice as
-// many, whose registers leave an SM one block).  Units of few rows: one, 110 and 112 us for 32 x 5.
+// parts two (8 x 256 tokens over 4096, 32 and 8 heads: 181 us with one row, 162 so, 172 with twice as
+// many, whose registers leave an SM one block).  Units of few rows: one, 111 and 112 us for 32 x 5.
 // ----------------------------------------------------------------------------
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 struct PrefillJoin {
@@ -1163,7 +1163,7 @@ __device__ __forceinline__ float join_weight(float m, float top) {
 }
 
 template <int DV>
-__global__ void __launch_bounds__(kJoinThreads) prefill_join_kernel(const PrefillJoin P) {
+__global__ void __launch_bounds__(kJoinThreads, 3) prefill_join_kernel(const PrefillJoin P) {
   constexpr int kV = DV / 32;      // columns of a lane
   constexpr int kFlight = 10;      // parts on their way at a time
   __shared__ int upto[kMaxPrefillCtas + 1];  // groups of rows in front of each share's unit
@@ -1375,7 +1375,7 @@ cudaError_t launch_prefill_typed(const PrefillLaunch& L, const Offsets& off) {
   J.Hq = L.Hq;
   // on its way while the main kernel runs; it waits for that one's end before it reads
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid * 4);
+  cfg.gridDim = dim3(grid * 3);  // (as many as an SM takes at a time)
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = L.stream;
   cudaLaunchAttribute attr = {};

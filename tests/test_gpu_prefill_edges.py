@@ -1,6 +1,7 @@
 """Prefill where it can go wrong: values that are not finite in slots that a row does not see,
 scores at the ends of their range, bad pages and lengths, long caches, captured calls, workspaces."""
 import math
+import random
 
 import pytest
 import torch
@@ -278,6 +279,23 @@ def test_many_sequences(kind):
                                                     [1] * 1500, lens)
     got = binding.prefill(cache, q, table, lens_d)
     check(got, prefill64(q, kc, vc, table, lens, [1] * 1500, page, 0.125, -1, ks, vs))
+    assert binding.attn_cache_status() == binding.ATTN_OK
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [(64, 64), (128, 128), (192, 128)])
+def test_short_and_long_chunks_in_turn(kind, d):
+    """Units of one query tile and of two behind each other on every SM, with one key tile or more."""
+    heads, group, page = 2, 4, 64
+    rng = random.Random(5)
+    new = [rng.choice([1, 1, 3, 40, 64, 33, 2]) for _ in range(450)]
+    lens = [n + rng.choice([0, 5, 100, 130, 300, 517]) for n in new]
+    cache, q, kc, vc, ks, vs, table, lens_d = setup(11, heads, group, *d, page, kind, "token", new,
+                                                    lens)
+    ref = prefill64(q, kc, vc, table, lens, new, page, 1 / math.sqrt(d[0]), -1, ks, vs)
+    for _ in range(3):
+        got = binding.prefill(cache, q, table, lens_d, cu_seqlens=_offsets(new))
+        check(got, ref)
     assert binding.attn_cache_status() == binding.ATTN_OK
 
 
