@@ -325,6 +325,30 @@ __device__ __forceinline__ void widen_rows(uint32_t tile, int mw, int lane, bool
   behind();  // (the rows have been read)
 }
 
+// What a copy warp's account (TileAccount) stands on: its lanes' asynchronous copies, and the barriers of
+// the tiles.
+template <typename C>
+struct CopyOps {
+  PrefillBars* bars;
+  int lane;
+  __device__ __forceinline__ void close_group() const { cp_commit(); }
+  __device__ __forceinline__ void wait_all() const { cp_wait<0>(); }
+  template <int N>
+  __device__ __forceinline__ void wait_but_newest() const {
+    cp_wait<N>();
+  }
+  __device__ __forceinline__ void about_to_announce() const {
+    fence_proxy_async_smem();
+    __syncwarp();
+  }
+  __device__ __forceinline__ void announce(uint32_t tile) const {
+    const uint32_t s = tile >> 1;
+    if (lane == 0)
+      mbar_arrive(tile & 1 ? smem_u32(&bars->v_full[s % C::kVStages])
+                           : smem_u32(&bars->k_full[s % C::kKStages]));
+  }
+};
+
 template <int DQK, int DV, bool E4M3, typename Offsets>
 __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -644,33 +668,18 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
     const bool leader = P.box > 0 && lane % max(P.box, 1) == 0;  // of a box, at its first row
     uint32_t step = 0;
     bool ok = true;
-    // Copies by rows on their way that have not been announced yet.  `issued` counts the key and
-    // value tiles in turn (key tile of step s: 2 s), `told` those of them up to which all are
-    // announced; by_rows has a bit for each that has to be.
-    constexpr int kAhead = C::kKStages + C::kVStages - 1;
-    static_assert(kAhead < 32, "a bit each");
-    uint32_t issued = 0, told = 0, by_rows = 0;
+    // bf16: copies by rows on their way that have not been announced yet
+    [[maybe_unused]] const CopyOps<C> copies{bars, lane};
+    [[maybe_unused]] TileAccount<C::kKStages + C::kVStages - 1> account;
     // e4m3: parity of the ring's slots
     [[maybe_unused]] uint32_t raw_parity = 0;
     [[maybe_unused]] int since = C::kKStages;
-    auto tell = [&](uint32_t upto) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      for (; told != upto; ++told) {
-        const uint32_t bit = 1u << (told & 31), s = told >> 1;
-        if (lane == 0 && (by_rows & bit) != 0)
-          mbar_arrive(told & 1 ? smem_u32(&bars->v_full[s % C::kVStages])
-                               : smem_u32(&bars->k_full[s % C::kKStages]));
-        by_rows &= ~bit;
-      }
-    };
     // Waits; where that takes time, what is under way is announced first: it may be what the
     // others wait for.
     auto wait = [&](uint64_t& bar, uint32_t parity) -> bool {
       if constexpr (E4M3) return mbar_wait_warp(smem_u32(&bar), parity, ab);
       if (__all_sync(0xffffffffu, mbar_test_wait(smem_u32(&bar), parity))) return true;
-      cp_wait<0>();
-      if (told != issued) tell(issued);
+      account.flush(copies);
       return mbar_wait_warp(smem_u32(&bar), parity, ab);
     };
     for (uint32_t n = 0;; ++n) {
@@ -777,8 +786,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
             }
             __syncwarp();
             if (leader) load_box(side, t, here, dst, bar);
-            ++issued;
-            if (told + 1 == issued) ++told;
+            account.boxes(copies);
             continue;
           }
           const long long o = side ? vo : ko;
@@ -804,13 +812,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
               widen_rows<4, 8, 192>(dst, mw, lane, ring, raw, base, o, next);
             }
           }
-          if constexpr (!E4M3) {
-            cp_commit();
-            if (side == 0 && is_edge) {
-              take_out();
-              cp_wait<0>();  // (the keys came meanwhile)
-            }
-          }
+          if (!E4M3 && side == 0 && is_edge) take_out();  // (the keys come meanwhile)
           if (side == 0 && lane == 0) {
             bars->there[step % kKeyRing][mw] = bits;
             bars->bad[step % kKeyRing][mw] = bad;
@@ -821,14 +823,7 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
             if (lane == 0) mbar_arrive(smem_u32(side ? &bars->v_full[st] : &bars->k_full[st]));
             continue;
           }
-          by_rows |= 1u << (issued & 31);
-          ++issued;
-          if (side == 0 && is_edge) {
-            tell(issued);
-          } else if (issued - told > kAhead) {
-            cp_wait<kAhead>();
-            tell(issued - kAhead);
-          }
+          account.rows(copies, side == 0 && is_edge);
         }
       }
       if constexpr (C::kSpareQ) {
@@ -840,8 +835,10 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
       }
       if (!ok) break;
     }
-    cp_wait<0>();
-    if (ok && told != issued) tell(issued);
+    if constexpr (!E4M3) {
+      if (ok) account.flush(copies);
+      else cp_wait<0>();
+    }
     if (!E4M3 && !ok && lane == 0) {
       // let every copy already issued land before the CTA's memory is released
       for (uint32_t s = step + 1 > C::kKStages ? step + 1 - C::kKStages : 0; s <= step; ++s)

@@ -235,6 +235,62 @@ __host__ __device__ inline bool tile_used(const TileUse& u, int w, int t) {
   return t >= u.lo[w] && t <= u.hi[w] && (!u.twin || ((t ^ w) & 1) == 0);
 }
 
+// ---- copies under way (bf16) ----------------------------------------------------
+// A copy warp's account of its tiles, key and value tiles in turn (key tile of step s: 2 s).  One
+// comes by boxes, which announce themselves, or by rows: asynchronous copies, which the warp announces
+// when they have landed.  Every tile closes a group of copies, an empty one where it came by boxes:
+// the copies can only be waited for but for the newest `kAhead` groups, and those have to be the
+// newest tiles.
+//
+// Ops: close_group(), wait_all(), wait_but_newest<n>() of the groups, then about_to_announce() and
+// announce(tile).
+template <int kAhead>
+struct TileAccount {
+  static_assert(kAhead < 32, "a bit each");
+  uint32_t issued = 0;   // tiles so far
+  uint32_t told = 0;     // those up to which all are announced
+  uint32_t by_rows = 0;  // a bit for each that has to be
+
+#pragma nv_exec_check_disable
+  template <typename Ops>
+  __host__ __device__ void tell(const Ops& ops, uint32_t upto) {
+    ops.about_to_announce();
+    for (; told != upto; ++told) {
+      const uint32_t bit = 1u << (told & 31);
+      if ((by_rows & bit) != 0) ops.announce(told);
+      by_rows &= ~bit;
+    }
+  }
+  // A tile by boxes.
+#pragma nv_exec_check_disable
+  template <typename Ops>
+  __host__ __device__ void boxes(const Ops& ops) {
+    ops.close_group();
+    ++issued;
+    if (told + 1 == issued) ++told;
+  }
+  // A tile by rows; now: it is waited for and announced at once.
+#pragma nv_exec_check_disable
+  template <typename Ops>
+  __host__ __device__ void rows(const Ops& ops, bool now) {
+    ops.close_group();
+    by_rows |= 1u << (issued & 31);
+    ++issued;
+    if (now) {
+      flush(ops);
+    } else if (issued - told > kAhead) {
+      ops.template wait_but_newest<kAhead>();
+      tell(ops, issued - kAhead);
+    }
+  }
+#pragma nv_exec_check_disable
+  template <typename Ops>
+  __host__ __device__ void flush(const Ops& ops) {
+    ops.wait_all();
+    if (told != issued) tell(ops, issued);
+  }
+};
+
 // ---- workspace ----------------------------------------------------------------
 constexpr int kMaxPrefillCtas = 160;
 struct PrefillDesc {  // of a unit that is joined from parts, one place per share
