@@ -72,3 +72,17 @@ def test_bad_pages_between_whole_tiles(kind, d, page, new):
         ref = prefill64(q[rows], k1, v1, torch.zeros(1, 1, dtype=torch.int32).cuda(), [n], [new], n,
                         scale, -1, ks, vs)
         check((o[rows], lse[rows]), ref, f"sequence {b}")
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("length", [-5, 0])
+def test_neighbours_of_an_empty_sequence(kind, length):
+    """A length of 0 or below changes where the work is cut: the other sequences keep the bounds."""
+    heads, group, page, d = 2, 2, 16, 64
+    new, lens = [5, 5, 5], [100, 100, 300]
+    cache, q, kc, vc, ks, vs, table, lens_d = setup(4, heads, group, d, d, page, kind, "token", new,
+                                                    lens, poison=False)
+    lens_d[0] = length
+    got = binding.prefill(cache, q, table, lens_d)
+    assert binding.attn_cache_status() == binding.ATTN_OK
+    check(got, prefill64(q, kc, vc, table, [length] + lens[1:], new, page, 0.125, -1, ks, vs))
