@@ -494,7 +494,10 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
         if (!(ok = mbar_wait(smem_u32(&bars->q_empty), (n & 1) ^ 1, ab))) break;
         // rows past the sequence's tokens hold the next one's queries (or zeros): never stored
         const int tiles = it.tokens <= sh.per_tile ? 1 : 2;
-        if constexpr (C::kSpareQ) {  // (the copy warps may still use the second tile's place)
+        // The copy warps may still use the second tile's place.  By parity: of the phases in front only
+        // that of the unit just in front of this one may be open (this item's slot was let go of by
+        // the copy warps two units ago, and by then they were done with the place).
+        if constexpr (C::kSpareQ) {
           if (tiles == 1) ++twins;
           else if (twins > 0 &&
                    !(ok = mbar_wait(smem_u32(&bars->spare_free[0]), (twins - 1) & 1, ab) &&
@@ -697,8 +700,10 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
       const int left = sh.window >= 0 ? item.pos0 + item.tokens - 1 - sh.window : 0;
       const bool twin = item.tokens <= sh.per_tile;
       [[maybe_unused]] const uint32_t slots = slots_of(twin, since);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
+      if constexpr (!C::kSpareQ) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
+      }
       auto edge = [&](int t) {
         const int key0 = (tile0 + t) * kTile;
         return key0 + kTile - 1 > right || key0 < left;
@@ -827,9 +832,15 @@ __global__ void __launch_bounds__(PrefillCfg<DQK, DV, E4M3>::kThreads, 1)
         }
       }
       if constexpr (C::kSpareQ) {
-        if (ok && twin) {
+        // The item is let go of behind the place, so that the walk, which waits for an item's slot two
+        // units later, has seen all phases of spare_free but the last: it can tell them by parity.
+        // (The softmax warps keep the item longer.)
+        if (ok) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&bars->spare_free[team]));
+          if (lane == 0) {
+            if (twin) mbar_arrive(smem_u32(&bars->spare_free[team]));
+            mbar_arrive(smem_u32(&bars->item_empty[n & 1]));
+          }
         }
         since = twin ? min(since + 1, C::kKStages) : 0;
       }
