@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
       }
       if (!ok) {
-        if (asked > 0) mbar_wait_drain(clc, (asked - 1) & 1);
+        clc_drop_rest(answer, clc, asked, sh.n_items);
         // let every copy already issued land before the CTA's memory is released
         for (uint32_t t = k_issued > (uint32_t)C::kKStages ? k_issued - C::kKStages : 0;
              t < k_issued; ++t)

@@ -114,12 +114,13 @@ __device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity, co
 }
 
 // Wait used only while tearing down after an abort: ignores the abort flag
-// and gives up after 100 ms.
-__device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity) {
+// and gives up after 100 ms (false).
+__device__ __forceinline__ bool mbar_wait_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = globaltimer();
   while (!mbar_try_wait(bar, parity)) {
-    if (globaltimer() - t0 > 100000000ull) break;
+    if (globaltimer() - t0 > 100000000ull) return false;
   }
+  return true;
 }
 
 // Per-warpgroup register budget (all 128 threads of the warpgroup execute it).
@@ -132,6 +133,11 @@ __device__ __forceinline__ void regs_inc() {
 template <uint32_t N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Generic-proxy shared-memory writes -> visible to the async proxy (MMA/TMA).
+__device__ __forceinline__ void fence_proxy_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // Cluster launch control: a running CTA asks for one that has not started yet, which then never
@@ -157,6 +163,19 @@ __device__ __forceinline__ bool clc_read(uint32_t answer, int* x) {
       : "memory");
   *x = (int)id;
   return got != 0;
+}
+// For a CTA that gives up, by one thread: takes over the CTAs that have not started, one after the
+// other, and leaves their work undone, so that none starts only to wait in vain as this one did.
+// asked: questions put so far, the last of which may be without its answer yet; most: CTAs of the launch.
+__device__ __forceinline__ void clc_drop_rest(uint32_t answer, uint32_t bar, uint32_t asked,
+                                              int most) {
+  for (int n = 0; n <= most; ++n, ++asked) {
+    int x;
+    if (asked > 0 && (!mbar_wait_drain(bar, (asked - 1) & 1) || !clc_read(answer, &x))) return;
+    fence_proxy_async_smem();  // (the answer has been read)
+    mbar_arrive_expect_tx(bar, 16);
+    clc_ask(answer, bar);
+  }
 }
 
 // Named barrier among `count` threads (multiple of 32), id 1..15.
@@ -198,11 +217,6 @@ __device__ __forceinline__ void st_global_v8(void* p, uint32_t w0, uint32_t w1, 
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w0),
                "r"(w1), "r"(w2), "r"(w3), "r"(w4), "r"(w5), "r"(w6), "r"(w7)
                : "memory");
-}
-
-// Generic-proxy shared-memory writes -> visible to the async proxy (MMA/TMA).
-__device__ __forceinline__ void fence_proxy_async_smem() {
-  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
 // ----------------------------------------------------------------------------
