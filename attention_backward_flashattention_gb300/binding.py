@@ -1060,18 +1060,24 @@ class HeadNorm:
 
     def __init__(self, q_weight=None, k_weight=None, eps=1e-6):
         for w in (q_weight, k_weight):
-            if w is not None and (w.dtype is not torch.float32 or w.dim() != 1
-                                  or not w.is_contiguous()):
-                raise ValueError("q_weight and k_weight must be contiguous fp32, one per column")
+            if w is not None:
+                self._check_kind(w)
         self.q_weight, self.k_weight, self.eps = q_weight, k_weight, float(eps)
         self.struct = _NormStruct(_ptr(q_weight), _ptr(k_weight), self.eps)
         self.address = ctypes.addressof(self.struct)
 
+    @staticmethod
+    def _check_kind(w):
+        if w.dtype is not torch.float32 or w.dim() != 1 or not w.is_contiguous():
+            raise ValueError("q_weight and k_weight must be contiguous fp32, one per column")
+
     def check(self, d):
-        """For heads of d columns; the weights' memory is asked for anew, as a parameter's may move."""
+        """For heads of d columns.  The weights are looked at anew, as a parameter's memory may move,
+        and its type may change with it (a module turned to bf16)."""
         for name in ("q_weight", "k_weight"):
             w = getattr(self, name)
             if w is not None:
+                self._check_kind(w)
                 if w.shape[0] != d:
                     raise ValueError("the norm's weights must have one value per column of a head")
                 setattr(self.struct, name, w.data_ptr())
