@@ -73,11 +73,12 @@ constexpr int kMmaWarp = 13;
 template <int DQK>
 struct RegSplit {
   static constexpr uint32_t kLaunch = 128;
-  static constexpr uint32_t kCompute = DQK > 128 ? 88 : (DQK > 64 ? 104 : 112);
+  // (a P/dS thread holds 64 P in fp32; 192 columns: 325 us for T 4096, 16 heads, 330 with 88 and 128)
+  static constexpr uint32_t kCompute = DQK > 128 ? 96 : (DQK > 64 ? 104 : 112);
   // the MMA issuer (control warpgroup) holds every staged descriptor base:
   // 136 at d <= 128 keeps it from spilling (raised with setmaxnreg.inc)
-  static constexpr uint32_t kCtl = DQK > 128 ? 128 : 136;
-  static constexpr uint32_t kDq = 4 * kLaunch - 2 * kCompute - kCtl;  // 152, 168, 208
+  static constexpr uint32_t kCtl = DQK > 128 ? 120 : 136;
+  static constexpr uint32_t kDq = 4 * kLaunch - 2 * kCompute - kCtl;  // 152, 168, 200
   static_assert(2 * kCompute + kCtl + kDq <= 4 * kLaunch, "register split");
   static_assert(kCompute % 8 == 0 && kCtl % 8 == 0 && kDq % 8 == 0 && kDq <= 256, "setmaxnreg");
   // the kernel lowers the P/dS and control warpgroups (setmaxnreg.dec) and
@@ -329,6 +330,9 @@ struct BwdCfg {
   static constexpr uint32_t kTmemdK = kTmemdV + DV;
   static constexpr uint32_t kTmemdQ = kSharedSdP ? 0 : (kDqOnDp ? 128 : kTmemdK + DQK);
   static constexpr uint32_t kTmemCols = 512;
+  // Columns of S and of dP that a P/dS thread has at hand at a time, beside its 64 P in fp32 (192
+  // columns have the fewest registers for it: 94 us for T 2048, 12 and 2 heads, 98 with 32 of S).
+  static constexpr int kScoreCols = DQK > 128 ? 16 : 32, kGradCols = 16;
   static_assert(kTmemdK + DQK <= kTmemCols, "tensor memory budget (dK)");
   static_assert(kTmemdQ + DQK <= kTmemCols, "tensor memory budget (dQ)");
 };
@@ -808,11 +812,11 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         const uint32_t st = q_it % C::kStages;
         const float* nlse2 = stat_f + st * (C::kStatBytes / 4) + grp * 64;  // -LSE * log2(e)
         const float* ndsum = nlse2 + kTile;                                  // -D
-        // ---- P^T = exp2(S^T * s*log2e - LSE2), masked; bf16 pairs -> TMEM
+        // ---- P^T = exp2(S^T * s*log2e - LSE2), masked; bf16 pairs -> TMEM (for dV)
         if (!(ok = mbar_wait_warp(smem_u32(&bars->s_full), gi & 1, ab))) break;
         tc_fence_after();
         if (lane == 0 && (warp & 3) == 0) ATTN_TRACE_EV(20, gi);
-        uint32_t pk[32];  // P^T of this thread's key row, 64 queries as bf16 pairs
+        float pf[64];  // P^T of this thread's key row, 64 queries
         // key kidx is visible to query q iff kidx - off - wr <= q <= kidx - off + wl
         // (band bounds; -1 = open): this group's visible query columns are
         // [qmin, qmax), none for a key past the sequence end
@@ -820,42 +824,45 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         const int qmin = !key_ok ? 64 : (sh.wr >= 0 ? min(64, max(0, qrel - band_off(sh, it) - sh.wr)) : 0);
         const int qmax = sh.wl >= 0 ? min(64, max(0, qrel - band_off(sh, it) + sh.wl + 1)) : 64;
         const uint64_t sc2 = f2(a.scale_log2, a.scale_log2);
+        constexpr int kS = C::kScoreCols;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t sr[32];
-          tmem_ld32(tmem + lane_base + C::kTmemS + grp * 64 + c * 32, sr);
+        for (int q0 = 0; q0 < 64; q0 += kS) {
+          uint32_t sr[kS], pk[kS / 2];
+          tmem_load(tmem + lane_base + C::kTmemS + grp * 64 + q0, sr);
           tmem_ld_wait();
           if (qmin > 0 || qmax < 64) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const int q = c * 32 + e;  // query column within this group
+            for (int e = 0; e < kS; e += 4) {
+              const int q = q0 + e;  // query column within this group
               const float4 l4 = *reinterpret_cast<const float4*>(nlse2 + q);
               const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
-              float pe[4];
 #pragma unroll
               for (int u = 0; u < 4; ++u)
-                pe[u] = (q + u >= qmin && q + u < qmax)
-                            ? ex2(fmaf(__uint_as_float(sr[e + u]), a.scale_log2, lv[u]))
-                            : 0.f;
-              pk[(q >> 1) + 0] = pack_bf16(pe[0], pe[1]);
-              pk[(q >> 1) + 1] = pack_bf16(pe[2], pe[3]);
+                pf[q + u] = (q + u >= qmin && q + u < qmax)
+                                ? ex2(fmaf(__uint_as_float(sr[e + u]), a.scale_log2, lv[u]))
+                                : 0.f;
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const int q = c * 32 + e;
+            for (int e = 0; e < kS; e += 4) {
+              const int q = q0 + e;
               const float4 l4 = *reinterpret_cast<const float4*>(nlse2 + q);
               // two scores per packed FMA: S * s*log2e - LSE2
               const uint64_t x01 = fma2(f2(__uint_as_float(sr[e + 0]), __uint_as_float(sr[e + 1])),
                                         sc2, f2(l4.x, l4.y));
               const uint64_t x23 = fma2(f2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])),
                                         sc2, f2(l4.z, l4.w));
-              pk[(q >> 1) + 0] = pack_bf16(ex2(f2_lo(x01)), ex2(f2_hi(x01)));
-              pk[(q >> 1) + 1] = pack_bf16(ex2(f2_lo(x23)), ex2(f2_hi(x23)));
+              pf[q + 0] = ex2(f2_lo(x01));
+              pf[q + 1] = ex2(f2_hi(x01));
+              pf[q + 2] = ex2(f2_lo(x23));
+              pf[q + 3] = ex2(f2_hi(x23));
             }
           }
+          // (P lies in columns whose scores have been read)
+#pragma unroll
+          for (int e = 0; e < kS / 2; ++e) pk[e] = pack_bf16(pf[q0 + 2 * e], pf[q0 + 2 * e + 1]);
+          tmem_store(tmem + lane_base + C::kTmemS + grp * 64 + q0 / 2, pk);
         }
-        tmem_st32(tmem + lane_base + C::kTmemS + grp * 64, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -871,26 +878,32 @@ __global__ void __launch_bounds__(kMainThreads, 1)
         if (lane == 0 && (warp & 3) == 0) ATTN_TRACE_EV(25, gi);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t dr[32];
-          tmem_ld32(tmem + lane_base + C::kTmemdP + grp * 64 + c * 32, dr);
-          tmem_ld_wait();
+          constexpr int kD = C::kGradCols;
 #pragma unroll
-          for (int ch = 4 * c; ch < 4 * c + 4; ++ch) {
-            const int e0 = (ch & 3) * 8;
-            const float4 da = *reinterpret_cast<const float4*>(ndsum + ch * 8);
-            const float4 db = *reinterpret_cast<const float4*>(ndsum + ch * 8 + 4);
-            const uint64_t nd2[4] = {f2(da.x, da.y), f2(da.z, da.w), f2(db.x, db.y), f2(db.z, db.w)};
-            // dS = P * (dP - D): the difference in fp32 (packed pairs), rounded
-            // to bf16, then multiplied by the bf16 P pair (the product is
-            // rounded to bf16 for the MMAs anyway)
-            uint32_t w[4];
+          for (int q0 = c * 32; q0 < c * 32 + 32; q0 += kD) {
+            uint32_t dr[kD];
+            tmem_load(tmem + lane_base + C::kTmemdP + grp * 64 + q0, dr);
+            tmem_ld_wait();
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const uint64_t d2 = add2(f2(__uint_as_float(dr[e0 + 2 * u]),
-                                          __uint_as_float(dr[e0 + 2 * u + 1])), nd2[u]);
-              w[u] = mul_bf16x2(pk[ch * 4 + u], pack_bf16(f2_lo(d2), f2_hi(d2)));
+            for (int ch = q0 / 8; ch < (q0 + kD) / 8; ++ch) {
+              const int e0 = ch * 8 - q0;
+              const float4 da = *reinterpret_cast<const float4*>(ndsum + ch * 8);
+              const float4 db = *reinterpret_cast<const float4*>(ndsum + ch * 8 + 4);
+              const uint64_t nd2[4] = {f2(da.x, da.y), f2(da.z, da.w), f2(db.x, db.y),
+                                       f2(db.z, db.w)};
+              // dS = P * (dP - D) in fp32 (packed pairs), rounded once, to bf16 for the MMAs: from
+              // P rounded to bf16 and a rounded difference dQ and dK were off by 3.4e-3 of their
+              // norm, so by 2.4e-3 (1.7e-3 is the rounding of dQ and dK themselves)
+              uint32_t w[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const uint64_t d2 = add2(f2(__uint_as_float(dr[e0 + 2 * u]),
+                                            __uint_as_float(dr[e0 + 2 * u + 1])), nd2[u]);
+                const uint64_t s2 = mul2(f2(pf[ch * 8 + 2 * u], pf[ch * 8 + 2 * u + 1]), d2);
+                w[u] = pack_bf16(f2_lo(s2), f2_hi(s2));
+              }
+              st_shared_v4(sdS + grp * kPanelBytes + sw128_offset(r, ch), w[0], w[1], w[2], w[3]);
             }
-            st_shared_v4(sdS + grp * kPanelBytes + sw128_offset(r, ch), w[0], w[1], w[2], w[3]);
           }
           // this half of the dS^T columns is ready for dK
           fence_proxy_async_smem();

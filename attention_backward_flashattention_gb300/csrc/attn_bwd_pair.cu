@@ -526,14 +526,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!(ok = mbar_wait_warp(smem_u32(&bars->s_full), gi & 1, ab))) break;
         tc_fence_after();
         if (lane == 0 && (warp & 3) == 0) PAIR_TRACE(20, gi);
-        uint32_t pk[32];
+        float pf[64];  // P^T of this thread's key row, 64 queries
         const int qrel = kidx0 - kTile * i - grp * 64;
         const int qmin = !key_ok ? 64 : (sh.wr >= 0 ? min(64, max(0, qrel - band_off(sh, it) - sh.wr)) : 0);
         const int qmax = sh.wl >= 0 ? min(64, max(0, qrel - band_off(sh, it) + sh.wl + 1)) : 64;
         const uint64_t sc2 = f2(a.scale_log2, a.scale_log2);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t sr[32];
+          uint32_t sr[32], pk[16];
           tmem_ld32(tmem + lane_base + C::kTmemS + grp * 64 + c * 32, sr);
           tmem_ld_wait();
           if (qmin > 0 || qmax < 64) {
@@ -542,14 +542,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               const int q = c * 32 + e;
               const float4 l4 = *reinterpret_cast<const float4*>(nlse2 + q);
               const float lv[4] = {l4.x, l4.y, l4.z, l4.w};
-              float pe[4];
 #pragma unroll
               for (int v = 0; v < 4; ++v)
-                pe[v] = (q + v >= qmin && q + v < qmax)
-                            ? ex2(fmaf(__uint_as_float(sr[e + v]), a.scale_log2, lv[v]))
-                            : 0.f;
-              pk[(q >> 1) + 0] = pack_bf16(pe[0], pe[1]);
-              pk[(q >> 1) + 1] = pack_bf16(pe[2], pe[3]);
+                pf[q + v] = (q + v >= qmin && q + v < qmax)
+                                ? ex2(fmaf(__uint_as_float(sr[e + v]), a.scale_log2, lv[v]))
+                                : 0.f;
             }
           } else {
 #pragma unroll
@@ -560,12 +557,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                         sc2, f2(l4.x, l4.y));
               const uint64_t x23 = fma2(f2(__uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3])),
                                         sc2, f2(l4.z, l4.w));
-              pk[(q >> 1) + 0] = pack_bf16(ex2(f2_lo(x01)), ex2(f2_hi(x01)));
-              pk[(q >> 1) + 1] = pack_bf16(ex2(f2_lo(x23)), ex2(f2_hi(x23)));
+              pf[q + 0] = ex2(f2_lo(x01));
+              pf[q + 1] = ex2(f2_hi(x01));
+              pf[q + 2] = ex2(f2_lo(x23));
+              pf[q + 3] = ex2(f2_hi(x23));
             }
           }
+          // (P lies in columns whose scores have been read)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = pack_bf16(pf[c * 32 + 2 * e], pf[c * 32 + 2 * e + 1]);
+          tmem_st16(tmem + lane_base + C::kTmemS + grp * 64 + c * 16, pk);
         }
-        tmem_st32(tmem + lane_base + C::kTmemS + grp * 64, pk);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -580,28 +582,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0 && (warp & 3) == 0) PAIR_TRACE(23, gi);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          uint32_t dr[32];
-          tmem_ld32(tmem + lane_base + C::kTmemdP + grp * 64 + c * 32, dr);
-          tmem_ld_wait();
 #pragma unroll
-          for (int ch = 4 * c; ch < 4 * c + 4; ++ch) {
-            const int e0 = (ch & 3) * 8;
-            const float4 da = *reinterpret_cast<const float4*>(ndsum + ch * 8);
-            const float4 db = *reinterpret_cast<const float4*>(ndsum + ch * 8 + 4);
-            const uint64_t nd2[4] = {f2(da.x, da.y), f2(da.z, da.w), f2(db.x, db.y), f2(db.z, db.w)};
-            uint32_t w[4];
+          for (int q0 = c * 32; q0 < c * 32 + 32; q0 += 16) {
+            uint32_t dr[16];
+            tmem_ld16(tmem + lane_base + C::kTmemdP + grp * 64 + q0, dr);
+            tmem_ld_wait();
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              const uint64_t d2 = add2(f2(__uint_as_float(dr[e0 + 2 * v]),
-                                          __uint_as_float(dr[e0 + 2 * v + 1])), nd2[v]);
-              w[v] = mul_bf16x2(pk[ch * 4 + v], pack_bf16(f2_lo(d2), f2_hi(d2)));
+            for (int ch = q0 / 8; ch < q0 / 8 + 2; ++ch) {
+              const int e0 = (ch & 1) * 8;
+              const float4 da = *reinterpret_cast<const float4*>(ndsum + ch * 8);
+              const float4 db = *reinterpret_cast<const float4*>(ndsum + ch * 8 + 4);
+              const uint64_t nd2[4] = {f2(da.x, da.y), f2(da.z, da.w), f2(db.x, db.y), f2(db.z, db.w)};
+              uint32_t w[4];
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                const uint64_t d2 = add2(f2(__uint_as_float(dr[e0 + 2 * v]),
+                                            __uint_as_float(dr[e0 + 2 * v + 1])), nd2[v]);
+                const uint64_t s2 = mul2(f2(pf[ch * 8 + 2 * v], pf[ch * 8 + 2 * v + 1]), d2);
+                w[v] = pack_bf16(f2_lo(s2), f2_hi(s2));  // (rounded once)
+              }
+              if (dsq_remote)
+                st_cluster_v4(dsq_dst + sw128_offset(r, ch), w[0], w[1], w[2], w[3]);
+              else
+                st_shared_v4(dsq_local + sw128_offset(r, ch), w[0], w[1], w[2], w[3]);
+              // dS^T over the dP^T columns this group has read (the packed layout of P^T)
+              tmem_st4(tmem + lane_base + C::kTmemdP + grp * 64 + ch * 4, w[0], w[1], w[2], w[3]);
             }
-            if (dsq_remote)
-              st_cluster_v4(dsq_dst + sw128_offset(r, ch), w[0], w[1], w[2], w[3]);
-            else
-              st_shared_v4(dsq_local + sw128_offset(r, ch), w[0], w[1], w[2], w[3]);
-            // dS^T over the dP^T columns this group has read (the packed layout of P^T)
-            tmem_st4(tmem + lane_base + C::kTmemdP + grp * 64 + ch * 4, w[0], w[1], w[2], w[3]);
           }
           tmem_st_wait();
           if (dsq_remote) fence_proxy_async_cluster(); else fence_proxy_async_smem();
