@@ -31,7 +31,7 @@
 //             order in which each dQ tile receives its contributions, so a CTA
 //             only ever waits on work that was claimed before its own.
 //             Grouped heads: h is the key head, whose tiles take the q-tiles of all of its
-//             query heads; rank-major where a call's operands fit in L2 together.
+//             query heads; rank-major but in deterministic mode, whatever the size.
 //   Variable-length batches run sequence by sequence, most work (Lq * Lk) first.
 #pragma once
 

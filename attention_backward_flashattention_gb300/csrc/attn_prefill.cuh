@@ -24,13 +24,15 @@
 // one tile runs beside the other's.  Parts of a unit that is cut leave unnormalised sums in the
 // workspace, and a second launch joins them in a fixed order.
 //
-// Bound, where there are many rows: the chain S -> softmax -> PV of the two tiles.  A pair of tiles
-// takes 4080 cycles, its products 2050, its exponentials 2050.  With few rows: memory (bf16), or
-// the widening (e4m3).  The roles run from one instruction cache: the softmax is a loop over
-// 32 columns, and its unrolled form took 234 us where the loop took 212 (8 x 256 tokens over 4096,
-// e4m3), through stalls for instructions.  Measured (32 query and 8 key heads of 128, device time): 2048 tokens over 30011
-// 905 us (1151 TFLOP/s; e4m3 992), 8192 of a prompt 528, 32 x 5 tokens over 4000 111 (4.7 TB/s), 64
-// single tokens over 8000 352 (6.0 TB/s), 8 x 256 over 4096 162 (e4m3 178); the smallest call 15.
+// Bound, where there are many rows: the latency of the chain S -> softmax -> PV of the two tiles, each
+// with one softmax warp a scheduler.  A pair of tiles takes 4080 cycles, its products 2050, its
+// exponentials 1030; no unit is full (tensor pipe 49 %, special functions 25 %, issue 38 %).  With few
+// rows: memory (bf16), or the widening (e4m3).  The roles run from one instruction cache: the softmax is
+// a loop over 32 columns, and its unrolled form took 234 us where the loop took 212 (8 x 256 tokens over
+// 4096, e4m3), through stalls for instructions.  Measured (32 query and 8 key heads of 128, device time):
+// 2048 tokens over 30011 903 us (1153 TFLOP/s; e4m3 988), 8192 of a prompt 527, 32 x 5 tokens over 4000
+// 111 (4.7 TB/s), 64 single tokens over 8000 354 (5.9 TB/s), 8 x 256 over 4096 163 (e4m3 180); the
+// smallest call 15.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -60,7 +62,8 @@ struct PrefillCfg {
   static constexpr int kKBytes = DQK / 64 * kPrefillPanel;
   static constexpr int kVBytes = DV / 64 * kPrefillPanel;
   // stages of key and of value tiles (bf16), and of an e4m3 cache's bytes in front of them
-  static constexpr int kKStages = E4M3 ? (DQK == 64 ? 3 : DQK == 128 ? 2 : 1) : DQK == 64 ? 5 : DQK == 128 ? 3 : 2;
+  static constexpr int kKStages = E4M3 ? (DQK == 64 ? 3 : DQK == 128 ? 2 : 1)
+                                       : DQK == 64 ? 5 : DQK == 128 ? 3 : 2;
   static constexpr int kVStages = E4M3 ? (DQK == 64 ? 3 : DQK == 128 ? 2 : 1)
                                        : DQK == 64 ? 5 : DQK == 128 ? 2 : 1;
   static constexpr int kRaw = !E4M3 ? 0 : DQK == 64 ? 4 : 1;

@@ -614,8 +614,9 @@ int attn_prefill(const attn_paged_cache* cache, const int* block_table, int max_
 /*
  * Synchronises `stream`, returns the sticky device status of attn_cache_append,
  * attn_decode and attn_prefill on the current device (ATTN_OK, ATTN_ERR_BAD_PAGE,
- * ATTN_ERR_WORKSPACE_NOT_READY or ATTN_ERR_TIMEOUT, a bounded wait that gave up; the first since the last read) and clears it, in
- * one step: what a call on another stream reports meanwhile is kept for the next read.
+ * ATTN_ERR_WORKSPACE_NOT_READY or ATTN_ERR_TIMEOUT, a bounded wait that gave up; the
+ * first since the last read) and clears it, in one step: what a call on another stream
+ * reports meanwhile is kept for the next read.
  */
 int attn_cache_status(void* stream);
 
