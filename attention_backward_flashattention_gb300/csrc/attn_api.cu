@@ -313,6 +313,14 @@ int group_split(int B, int H, int Hk, int Tk, bool varlen) {
   return group;
 }
 
+// Whether a sequence that others follow ends inside a tile: offsets cu, or B sequences of T.
+bool has_tails(const int* cu, int B, int T) {
+  if (cu == nullptr) return B > 1 && T % kTile != 0;
+  for (int b = 0; b < B; ++b)
+    if ((cu[b + 1] - cu[b]) % kTile != 0 && cu[b + 1] < cu[B]) return true;
+  return false;
+}
+
 // Block-mask fields of the kernels' shape (mask may be null).  Returns
 // ATTN_OK or ATTN_ERR_INVALID_ARG.
 int set_block_mask(SeqShape* sh, const unsigned char* mask, int mask_batches, int mask_heads,
@@ -407,6 +415,7 @@ int fwd_impl(const void* q, const void* k, const void* v, void* o, float* lse, i
   // head-major); head-major keeps a few heads' K and V in L2 otherwise.
   constexpr int64_t kL2FitBytes = 48ll << 20;
   L.sh.rank_major = !varlen && (int64_t)B * Tk * Hk * (dqk + dv) * 2 <= kL2FitBytes ? 1 : 0;
+  L.sh.tails = has_tails(varlen ? cuk : nullptr, B, Tk) ? 1 : 0;
   rc = set_block_mask(&L.sh, block_mask, mask_batches, mask_heads, B, H, Tq, Tk, cu_seqlens,
                       cuk);
   if (rc) return rc;

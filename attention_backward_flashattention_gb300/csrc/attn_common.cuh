@@ -84,6 +84,8 @@ struct SeqShape {
   int descending;  // backward only: 1 = kv-tiles n descending (deterministic mode)
   int rank_major;  // 1 = units or kv-tiles rank-major ((b, h) fastest; within each sequence of
                    // a variable-length batch, h fastest).  Backward: grouped heads only
+  int tails;       // forward: 1 where some sequence's last tile of keys has rows of the next
+                   // sequence behind its own
   // Block mask (null: every tile pair in the band takes part).  Byte
   // [b][h][qt][kt] of a (mask batches, mask heads, q-tiles, kv-tiles) array;
   // a zero byte drops the pair (query tile qt, key tile kt) of sequence b,
@@ -216,6 +218,14 @@ __device__ __forceinline__ bool tile_on(const SeqShape& sh, const Item& it, int 
   return sh.blk == nullptr ||
          __ldg(sh.blk + it.seq * sh.blk_bstride + it.head * sh.blk_hstride +
                (int64_t)qt * sh.blk_nk + kt) != 0;
+}
+
+// The tile of a sequence (rows row0 .. row0 + len - 1 of `rows`) that rows of the next one share, or -1.
+__device__ __forceinline__ int tail_tile(int row0, int len, int rows) {
+  return len % kTile != 0 && row0 + len < rows ? len / kTile : -1;
+}
+__device__ __forceinline__ int key_rows(const SeqShape& sh) {
+  return sh.varlen ? sh.Tk : sh.nseq * sh.Tk;
 }
 
 // First token row of the keys of a sequence.

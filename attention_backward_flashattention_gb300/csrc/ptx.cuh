@@ -502,6 +502,16 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                : "memory");
 }
 
+// Zeros to the rows from `keep` on of a tile of PANELS panels of 128 rows of 128 bytes, by THREADS
+// threads.
+template <int PANELS, int THREADS>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int keep, int thread) {
+  for (int row = keep + (thread >> 3); row < 128; row += THREADS / 8)
+#pragma unroll
+    for (int p = 0; p < PANELS; ++p)
+      st_shared_v4(tile + p * 128 * 128 + row * 128 + (thread & 7) * 16, 0, 0, 0, 0);
+}
+
 __device__ __forceinline__ void red_add_v4(float* gptr, float a, float b, float c, float d) {
   asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(gptr), "f"(a), "f"(b),
                "f"(c), "f"(d)

@@ -93,6 +93,10 @@ extern "C" {
  * B, H, Tq, Tk, dqk, dv: sizes (see Layouts); causal: 0/1; scale: the s in
  * S = s Q K^T, finite and > 0 (the pages use 1/sqrt(dqk)); cu_seqlens: NULL or
  * host offsets.
+ * Values that are not finite: a row that does not see a key of its sequence meets it
+ * with a weight of zero wherever their tiles of 128 rows meet, so an infinity or a NaN
+ * there can reach it.  Those of another sequence never reach it in the forward; in the
+ * backward they can, where the two share a tile.
  * "ops(8)..." §1.2-1.3 (sdpa returns [O, stats]; stats only when training),
  * §2.1 forward formulas.
  */
@@ -216,9 +220,7 @@ int attn_bwd_ex(const void* q, const void* k, const void* v, const void* o, cons
  * adjacent, rows evenly spaced over the whole batch.  dk and dv are sums over
  * the group's query heads, accumulated in fp32 and rounded once.  LSE has Hq
  * heads.  No counterpart on the pages.
- * Values that are not finite: as in attn_fwd and attn_bwd, a row that does not see
- * a key, or a neighbouring sequence's, meets it with a weight of zero wherever
- * their tiles of 128 rows meet, so an infinity or a NaN there can reach it.
+ * Values that are not finite: as in attn_fwd and attn_bwd (see there).
  * Workspace: attn_bwd_grouped_workspace_size() bytes (0 for invalid sizes):
  * that of attn_bwd for Hq heads, and, where there are few key tiles and heads,
  * the fp32 sums of parts of the groups.
