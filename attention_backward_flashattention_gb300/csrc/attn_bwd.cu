@@ -891,9 +891,9 @@ __global__ void __launch_bounds__(kMainThreads, 1)
               const float4 db = *reinterpret_cast<const float4*>(ndsum + ch * 8 + 4);
               const uint64_t nd2[4] = {f2(da.x, da.y), f2(da.z, da.w), f2(db.x, db.y),
                                        f2(db.z, db.w)};
-              // dS = P * (dP - D) in fp32 (packed pairs), rounded once, to bf16 for the MMAs: from
-              // P rounded to bf16 and a rounded difference dQ and dK were off by 3.4e-3 of their
-              // norm, so by 2.4e-3 (1.7e-3 is the rounding of dQ and dK themselves)
+              // dS = P * (dP - D) in fp32 (packed pairs), rounded once, to bf16 for the MMAs: dQ and
+              // dK are off by 2.4e-3 of their norm (1.7e-3 is their own rounding), and were by
+              // 3.4e-3 with P and dP - D rounded in front of the product as well
               uint32_t w[4];
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
